@@ -201,7 +201,8 @@ def _own_logits(s):
                               draft_tokens=s["drafts"], parent=s["parent"],
                               repetition=s["repetition"], presence=s["presence"],
                               frequency=s["frequency"], bias_ids=s["bias_ids"], bias=s["bias"],
-                              mask=s["mask"], fill=FILL, allowed=s["mask"] is not None)
+                              mask=s["mask"], fill=FILL, allowed=s["mask"] is not None,
+                              out=s["out"])
 
 
 def _exact_logits(s):
@@ -308,7 +309,7 @@ def _own_pages(s):
     import sampling_ssd_verify_gb300 as ssd
 
     o = ssd.page_plan(s["lens"], s["new"], s["held"], s["tables"], s["free_pages"],
-                      s["free_count"], s["page"], s["most"])
+                      s["free_count"], s["page"], s["most"], out=s["out"])
     return dict(o, tables=s["tables"], free_pages=s["free_pages"])
 
 
@@ -420,8 +421,10 @@ def _plain_attn(s):
 def _own_attn(s):
     import sampling_ssd_verify_gb300 as ssd
 
-    return ssd.prefix_attention(s["q"], s["k"], s["v"], s["prefix_tables"], s["prefix_len"],
-                                s["group_off"], s["tables"], s["lens"], scale=s["scale"])
+    o = ssd.prefix_attention(s["q"], s["k"], s["v"], s["prefix_tables"], s["prefix_len"],
+                             s["group_off"], s["tables"], s["lens"], scale=s["scale"],
+                             out=s["out"])
+    return {"out": o["out"], "lse": o["lse"]}
 
 
 def _exact_attn(s):
@@ -456,12 +459,10 @@ def _exact_attn(s):
 
 
 def prepare(case, seed):
+    """The inputs, and `out`: where a program that calls again and again keeps the outputs."""
     op = case["op"]
-    if op == "logits":
-        return dict(_prepare_logits(case, seed), op=op)
-    if op == "pages":
-        return dict(_prepare_pages(case, seed), op=op)
-    return dict(_prepare_attn(case, seed), op=op)
+    make = {"logits": _prepare_logits, "pages": _prepare_pages, "attn": _prepare_attn}[op]
+    return dict(make(case, seed), op=op, out={})
 
 
 def run(state):
