@@ -10,7 +10,11 @@
  *   - Saguaro sampling (cached tokens' draft probability times C, then
  *     renormalised);
  *   - the outcome-cache build and lookup keyed by (row, k accepted, bonus t);
- *   - the geometric fan-out allocation of the cache budget (host helper).
+ *   - the geometric fan-out allocation of the cache budget (host helper);
+ * and what surrounds a round in a serving loop:
+ *   - penalties, biases and grammar masks on the logits before it;
+ *   - the pages, slots and positions of the key/value cache after it;
+ *   - attention of rows that share a prefix (the branches of a sequence).
  *
  * Sources, cited by page title and section:
  *   [SSD-note] "论文阅读：Speculative Speculative Decoding — 消除推测解码的最后一个顺序瓶颈"
@@ -70,8 +74,12 @@ typedef enum {
 #define SSD_DEV_BAD_TEMPERATURE 0x20 /* a per-sequence temperature negative or not
                                         finite; that sequence is verified greedily */
 #define SSD_DEV_BAD_FANOUT 0x40    /* a per-row fan-out outside [0, Fmax]; clamped */
+#define SSD_DEV_BAD_PENALTY 0x80   /* a penalty not finite, or a repetition penalty <= 0; left out */
+#define SSD_DEV_BAD_LENGTH 0x100   /* a length or count out of range or inconsistent; see the call */
+#define SSD_DEV_NO_PAGES 0x200     /* the free pages did not suffice for every request */
+#define SSD_DEV_BAD_PAGE 0x400     /* a page id outside [0, num_pages); its tokens read as zeros */
 
-typedef enum { SSD_BF16 = 0, SSD_F32 = 1 } ssd_dtype;
+typedef enum { SSD_BF16 = 0, SSD_F32 = 1, SSD_F16 = 2 } ssd_dtype; /* SSD_F16: attention only */
 
 /* A batch of logit rows in device memory. */
 typedef struct {
@@ -414,6 +422,202 @@ ssd_status ssd_cache_lookup(const void* table, size_t table_bytes, const int32_t
  * F_out HOST [K+1] int32 out.  K >= 0, budget >= 0, a > 0, r >= 0.
  * ------------------------------------------------------------------------- */
 ssd_status ssd_fanout(int K, int budget, double a, double r, int32_t* F_out);
+
+/* ---------------------------------------------------------------------------
+ * ssd_process_logits -- penalties for repeated tokens, biases and grammar
+ * masks on the logit rows of a round, before they are verified or sampled.
+ * The pages have no counterpart: a serving setting, as T = 0 is.
+ *
+ * Sequence b has N rows: row 0 follows its last verified token, row u > 0
+ * the drafts on the path to node u (a chain of drafts: u - 1, ..., 1).  For
+ * token v of row (b, u), with
+ *   c    = how often v occurs in history[b, prompt_len[b] .. history_len[b])
+ *          and among the drafts on the path to u,
+ *   seen = c > 0, or v occurs in history[b, 0 .. prompt_len[b]):
+ *   z = in[b, u, v];
+ *   if seen:   z = z > 0 ? z / repetition[b] : z * repetition[b];
+ *   if c > 0:  z = z - frequency[b] * c - presence[b];
+ *   if v is in bias_ids[b, :]:  z = z + its bias;
+ *   if the grammar does not allow v:  z = fill;
+ *   out[b, u, v] = z, computed in float32 and rounded once to the row type.
+ * The grammar overrides every other rule, NaN logits included.
+ *
+ * in, out      [B, N, V] logits of one dtype, row (b, u) is row b*N + u; out
+ *              is in itself (same pointer and row stride) or does not overlap
+ *              it.
+ * history      device int32, sequence b's tokens start at b * history_stride
+ *              (or NULL: no history).  A token outside [0, V) is passed over
+ *              and sets SSD_DEV_BAD_TOKEN.
+ * history_len  device [B] int32 in [0, history_max] (a value outside is
+ *              clamped and sets SSD_DEV_BAD_LENGTH).
+ * prompt_len   device [B] int32, or NULL: 0 (every token counts).
+ * draft_tokens device int32: the token of node u >= 1 is
+ *              draft_tokens[b * draft_stride + u - 1] (or NULL: drafts do not
+ *              count).  Tokens outside [0, V): as for history.
+ * parent       HOST [N] int32 as in ssd_tree_verify, or NULL for a chain.
+ * repetition, frequency, presence   device [B] float, or NULL for none.
+ *              A value not finite, or a repetition <= 0, is left out and sets
+ *              SSD_DEV_BAD_PENALTY.
+ * bias_ids, bias  device [B, n_bias] (or NULL with n_bias = 0), n_bias <=
+ *              65535.  A negative id is padding, one >= V is passed over and
+ *              sets SSD_DEV_BAD_TOKEN; of a token listed twice the later
+ *              entry holds.
+ * mask         device int32 words, or NULL: bit v % 32 of word
+ *              mask[b * mask_seq_stride + u * mask_row_stride + v / 32] says
+ *              whether v is allowed (strides of 0 share a mask).
+ * fill         the value of tokens that are not allowed (rounded to the row
+ *              type), not NaN.  For
+ *              ssd_verify it must be finite: SSD_MASKED_LOGIT is exact in
+ *              every type and far below any logit.  A row that allows nothing
+ *              is fill throughout.
+ * allowed      device [B, N] int32 out (or NULL): how many tokens of the row
+ *              the grammar allows; 0 shows a dead end.
+ * N <= 256.  One launch, no workspace.
+ * ------------------------------------------------------------------------- */
+#define SSD_MASKED_LOGIT (-1048576.0f) /* -2^20 */
+typedef struct {
+  const int32_t* history;
+  int64_t history_stride;
+  int32_t history_max;
+  int32_t n_bias;
+  const int32_t* history_len;
+  const int32_t* prompt_len;
+  const int32_t* draft_tokens;
+  int64_t draft_stride;
+  const int32_t* parent; /* host */
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  const int32_t* bias_ids;
+  const float* bias;
+  const int32_t* mask;
+  int64_t mask_seq_stride;
+  int64_t mask_row_stride;
+  float fill;
+  int32_t pad_; /* must be 0 */
+} ssd_logit_rules;
+ssd_status ssd_process_logits(const ssd_logits* in, const ssd_logits* out, int B, int N, int V,
+                              const ssd_logit_rules* rules, int32_t* allowed,
+                              int32_t* dev_status, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ssd_page_plan -- the pages of a paged key/value cache after a round, and
+ * the slots of the tokens that come next.  [SD-blog]'s rollback after a
+ * rejection is a matter of lengths here: the pages of rejected drafts are
+ * kept for the next drafts, or go back.
+ *
+ * Request b has lens[b] tokens in the cache, will append new_tokens[b], and
+ * holds the pages tables[b, 0 .. held[b]).  need = ceil((lens + new) / page).
+ *   1. Every request with held > need gives back tables[b, need .. held): in
+ *      the order of b and of columns they are pushed on the stack of free
+ *      pages, free_pages[0 .. *free_count), whose top is its end.
+ *   2. In the order of b, every request with held < need takes need - held
+ *      pages from the top, into tables[b, held .. need).  A request whose
+ *      pages are more than are left takes none, and neither does any later
+ *      request that needs one (SSD_DEV_NO_PAGES): served[b] = 0.
+ *   3. Its tokens stand in rows cu[b] .. cu[b + 1) of the batch's new tokens
+ *      (cu: running sums of new_tokens): row cu[b] + i has owner b, position
+ *      lens[b] + i and slot tables[b, position / page] * page + position %
+ *      page (-1 when b was not served).
+ * The inputs are left as they are but for the entries of tables and
+ * free_pages named above, so a call repeated on the same inputs gives the
+ * same results; the next round passes kv_len (less the tokens rejected),
+ * held_out and free_out.
+ * A request is not served, and SSD_DEV_BAD_LENGTH set, when lens, new or held
+ * are negative, held > cols, lens + new > cols * page, or held pages do not
+ * hold lens tokens; it keeps its pages and has no rows.
+ *
+ * Outputs are not inputs: kv_len, held_out and free_out are arrays of their
+ * own.
+ *
+ * lens, new_tokens, held  device [B] int32.      B <= 8192.
+ * tables      device int32, request b's row starts at b * table_stride, cols
+ *             columns.
+ * free_pages  device [free_cap] int32; free_count device int32 in [0,
+ *             free_cap] (clamped otherwise, SSD_DEV_BAD_LENGTH).  Pages that
+ *             do not fit the array are lost, and set SSD_DEV_BAD_LENGTH.
+ * slots       device [max_rows] int64 out; positions, owner [max_rows] int32
+ *             out (each may be NULL).  Rows past the last token are -1; tokens
+ *             past max_rows have no row, and set SSD_DEV_BAD_LENGTH.
+ * cu          device [B + 1] int32 out; kv_len (lens + new if served, else
+ *             lens), held_out, served device [B] int32 out; free_out device
+ *             int32 out.
+ * One launch, no workspace.
+ * ------------------------------------------------------------------------- */
+ssd_status ssd_page_plan(const int32_t* lens, const int32_t* new_tokens, const int32_t* held, int B,
+                         int32_t* tables, int64_t table_stride, int cols, int32_t* free_pages,
+                         int free_cap, const int32_t* free_count, int page, int max_rows,
+                         int64_t* slots, int32_t* positions, int32_t* owner, int32_t* cu,
+                         int32_t* kv_len, int32_t* held_out, int32_t* served, int32_t* free_out,
+                         int32_t* dev_status, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ssd_prefix_attention -- attention of one query token per row over a paged
+ * cache, for rows that share prefixes: every group of rows reads its prefix
+ * once, and every row its own tokens after it.  [SSD-note] §"实现细节：缓存怎么建",
+ * §"两层 batch": the branches of a sequence (one per predicted outcome) are
+ * rows of one drafter batch, over the same prefix.
+ *
+ * Row r of group g (group_off[g] <= r < group_off[g + 1]) attends to the
+ * first prefix_len[g] tokens of pages prefix_tables[g, :] and the first
+ * lens[r] tokens of pages tables[r, :].  With s_j = scale * q . k_j over all
+ * of them, per query head, query head i reading key/value head i / (Hq/Hkv):
+ *   lse = log sum_j exp(s_j);   out = sum_j exp(s_j - lse) v_j.
+ * A row with no token at all, or of no group and no own token, gives out = 0
+ * and lse = -inf.  Several tokens of one branch are several rows over the
+ * same table, each with its own lens.
+ *
+ * q, out      [R, Hq, D] of dtype (SSD_BF16 or SSD_F16); D elements are
+ *             contiguous, strides are in elements and multiples of 8, bases
+ *             16-byte aligned.  D: 64, 128 or 256.  Hkv divides Hq.
+ * k, v        [num_pages, page_size, Hkv, D] of dtype, strides and bases as
+ *             for q, any order of the first three dimensions.  Bytes of a
+ *             page past the last token are not used, whatever they hold.
+ * prefix_tables, tables  device int32 page ids, rows of prefix_cols / cols
+ *             columns.  An id outside [0, num_pages) of a token that is read
+ *             sets SSD_DEV_BAD_PAGE; the token reads as zeros.
+ * prefix_len  device [G] int32 in [0, prefix_cols * page_size]; lens device
+ *             [R] int32 in [0, cols * page_size] (NULL tables and lens: no
+ *             own tokens).  Values outside are clamped and set
+ *             SSD_DEV_BAD_LENGTH.
+ * group_off   device [G + 1] int32, not falling, within [0, R]; otherwise
+ *             SSD_DEV_BAD_LENGTH is set and the rows concerned are undefined.
+ * lse         device [R, Hq] float out (or NULL).
+ * workspace   256-byte aligned, >= ssd_prefix_attention_workspace_size of the
+ *             same descriptor.
+ * Scores, their maxima and sums and the outputs' sums are held in float32;
+ * the weights exp(s_j - max) are rounded to dtype for the matrix product.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  const void* ptr;
+  int64_t page_stride;
+  int64_t token_stride;
+  int64_t head_stride;
+} ssd_paged;
+typedef struct {
+  int32_t dtype; /* ssd_dtype */
+  int32_t R, Hq, Hkv, D;
+  int32_t G;
+  int32_t num_pages, page_size;
+  const void* q;
+  int64_t q_row_stride, q_head_stride;
+  ssd_paged k, v;
+  const int32_t* prefix_tables;
+  const int32_t* prefix_len;
+  const int32_t* group_off;
+  const int32_t* tables;
+  const int32_t* lens;
+  int64_t prefix_table_stride, table_stride;
+  int32_t prefix_cols, cols;
+  void* out;
+  int64_t out_row_stride, out_head_stride;
+  float* lse;
+  float scale;
+  int32_t pad_; /* must be 0 */
+} ssd_attention;
+size_t ssd_prefix_attention_workspace_size(const ssd_attention* a);
+ssd_status ssd_prefix_attention(const ssd_attention* a, void* workspace, size_t workspace_bytes,
+                                int32_t* dev_status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -9,7 +9,9 @@ fallback: without the library, or without a GPU, every call raises.
 Entry points (same names as the C ABI):
   verify, topf_bonus, saguaro_sample, cache_build, cache_build_guesses,
   cache_lookup, fanout, plus verify_host (host tensors in, host results out,
-  copies included).
+  copies included); around a round: process_logits (penalties, biases and
+  grammar masks), page_plan (pages, slots and positions of a paged cache) and
+  prefix_attention (attention of rows that share prefixes).
 
 Sources (page title, section):
   [SSD-note] "论文阅读：Speculative Speculative Decoding — 消除推测解码的最后一个顺序瓶颈"
@@ -29,8 +31,10 @@ __all__ = [
     "SSDError", "build", "lib", "verify", "verify_round", "verify_host", "topf_bonus",
     "saguaro_sample", "tree_verify",
     "cache_bytes", "cache_build", "cache_build_guesses", "cache_lookup", "fanout",
+    "process_logits", "page_plan", "prefix_attention", "MASKED_LOGIT",
     "DEV_BAD_TOKEN", "DEV_ZERO_RESIDUAL", "DEV_TIMEOUT", "DEV_TABLE_FULL", "DEV_DUPLICATE_KEY",
-    "DEV_BAD_TEMPERATURE", "DEV_BAD_FANOUT",
+    "DEV_BAD_TEMPERATURE", "DEV_BAD_FANOUT", "DEV_BAD_PENALTY", "DEV_BAD_LENGTH",
+    "DEV_NO_PAGES", "DEV_BAD_PAGE",
 ]
 
 DEV_BAD_TOKEN = 0x1
@@ -40,8 +44,14 @@ DEV_TABLE_FULL = 0x8
 DEV_DUPLICATE_KEY = 0x10
 DEV_BAD_TEMPERATURE = 0x20
 DEV_BAD_FANOUT = 0x40
+DEV_BAD_PENALTY = 0x80
+DEV_BAD_LENGTH = 0x100
+DEV_NO_PAGES = 0x200
+DEV_BAD_PAGE = 0x400
 
-SSD_BF16, SSD_F32 = 0, 1
+MASKED_LOGIT = -1048576.0  # what a token outside the grammar gets: -2^20
+
+SSD_BF16, SSD_F32, SSD_F16 = 0, 1, 2
 _lib = None
 
 
@@ -52,6 +62,39 @@ class SSDError(RuntimeError):
 class _Logits(ctypes.Structure):
     _fields_ = [("ptr", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("pad_", ctypes.c_int32),
                 ("row_stride", ctypes.c_int64)]
+
+
+class _LogitRules(ctypes.Structure):
+    _fields_ = [("history", ctypes.c_void_p), ("history_stride", ctypes.c_int64),
+                ("history_max", ctypes.c_int32), ("n_bias", ctypes.c_int32),
+                ("history_len", ctypes.c_void_p), ("prompt_len", ctypes.c_void_p),
+                ("draft_tokens", ctypes.c_void_p), ("draft_stride", ctypes.c_int64),
+                ("parent", ctypes.c_void_p), ("repetition", ctypes.c_void_p),
+                ("frequency", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("bias_ids", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("mask", ctypes.c_void_p), ("mask_seq_stride", ctypes.c_int64),
+                ("mask_row_stride", ctypes.c_int64), ("fill", ctypes.c_float),
+                ("pad_", ctypes.c_int32)]
+
+
+class _Paged(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _Attention(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("R", ctypes.c_int32), ("Hq", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32), ("G", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("q", ctypes.c_void_p), ("q_row_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64), ("k", _Paged), ("v", _Paged),
+                ("prefix_tables", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p),
+                ("group_off", ctypes.c_void_p), ("tables", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("prefix_table_stride", ctypes.c_int64),
+                ("table_stride", ctypes.c_int64), ("prefix_cols", ctypes.c_int32),
+                ("cols", ctypes.c_int32), ("out", ctypes.c_void_p),
+                ("out_row_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("lse", ctypes.c_void_p), ("scale", ctypes.c_float), ("pad_", ctypes.c_int32)]
 
 
 _vp = ctypes.c_void_p
@@ -87,6 +130,12 @@ _SIGS = {
     "ssd_cache_build_guesses": ([_vp, _sz, _vp, _i, _i, _i, _vp, _vp], _i),
     "ssd_cache_lookup": ([_vp, _sz, _vp, _vp, _i, _vp, _vp, _vp], _i),
     "ssd_fanout": ([_i, _i, ctypes.c_double, ctypes.c_double, _vp], _i),
+    "ssd_process_logits": ([_LP, _LP, _i, _i, _i, ctypes.POINTER(_LogitRules), _vp, _vp, _vp],
+                           _i),
+    "ssd_page_plan": ([_vp, _vp, _vp, _i, _vp, ctypes.c_int64, _i, _vp, _i, _vp, _i, _i] +
+                      [_vp] * 10, _i),
+    "ssd_prefix_attention_workspace_size": ([ctypes.POINTER(_Attention)], _sz),
+    "ssd_prefix_attention": ([ctypes.POINTER(_Attention), _vp, _sz, _vp, _vp], _i),
 }
 
 
@@ -497,3 +546,239 @@ def fanout(K: int, budget: int, a: float = 0.7, r: float = 1.0) -> np.ndarray:
     _check(lib().ssd_fanout(int(K), int(budget), float(a), float(r),
                             F.ctypes.data_as(ctypes.c_void_p)), "ssd_fanout")
     return F
+
+
+# ---- around a round ---------------------------------------------------------------------
+def _tensor(t, name, dtype, shape, device):
+    """A device tensor's address, its type, shape and place checked; None: 0.
+    Its last dimension is contiguous; of the others, so is what follows the
+    first."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or t.device != device:
+        raise SSDError(f"{name}: expected {dtype} on {device}")
+    if t.shape != shape:
+        raise SSDError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise SSDError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _rows2d(t, name, rows, device):
+    """Address and row stride of an int32 [rows, n] tensor with contiguous
+    rows that do not overlap (one row: any stride)."""
+    torch = _torch()
+    if t.dtype != torch.int32 or t.device != device:
+        raise SSDError(f"{name}: expected int32 on {device}")
+    if t.dim() != 2 or t.shape[0] != rows:
+        raise SSDError(f"{name}: expected {rows} rows")
+    n = t.shape[1]
+    if n > 1 and t.stride(1) != 1:
+        raise SSDError(f"{name}: rows must be contiguous")
+    stride = t.stride(0) if rows > 1 else max(n, 1)
+    if stride < n:
+        raise SSDError(f"{name}: rows must not overlap")
+    return t.data_ptr(), stride
+
+
+def _use_stream(stream, tensors):
+    """The stream's handle; memory taken from the current stream's pool is
+    not given out again before `stream` is done with it."""
+    torch = _torch()
+    current = torch.cuda.current_stream()
+    if stream is None:
+        return current.cuda_stream
+    if stream != current:
+        for t in tensors:
+            t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def process_logits(logits, history=None, history_len=None, prompt_len=None, draft_tokens=None,
+                   parent=None, repetition=None, presence=None, frequency=None, bias_ids=None,
+                   bias=None, mask=None, fill=MASKED_LOGIT, allowed=False, dev_status=None,
+                   stream=None, out=None):
+    """ssd_process_logits: penalties, biases and a grammar on logits [B, N, V].
+
+    history int32 [B, H] with history_len [B] (its first prompt_len [B] tokens
+    count for the repetition penalty alone).  draft_tokens int32 [B, N-1], or
+    [B, N] with an entry for node 0 that is not looked at; parent: N ints (a
+    chain when None).  repetition, presence, frequency: float32 [B].  bias_ids
+    int32 [B, n] (negative: padding), bias float32 [B, n].  mask int32 words
+    [B or 1, N or 1, ceil(V / 32)], bit v % 32 of word v / 32 set where token v
+    is allowed; others get `fill`.
+    Returns a dict: ``logits`` [B, N, V], new unless `out` has it (it may be
+    the input itself), and with allowed=True ``allowed`` int32 [B, N], the
+    number of tokens that the mask allows."""
+    torch = _torch()
+    if logits.dim() != 3:
+        raise SSDError("expected logits [B, N, V]")
+    B, N, V = logits.shape
+    dev = logits.device
+    o = out if out is not None else {}
+    if "logits" not in o:
+        o["logits"] = torch.empty((B, N, V), dtype=logits.dtype, device=dev)
+    z = o["logits"]
+    if z.shape != logits.shape or z.dtype != logits.dtype or z.device != dev:
+        raise SSDError("out logits must have the input's shape, type and device")
+    count = None
+    if allowed:
+        if "allowed" not in o:
+            o["allowed"] = torch.empty((B, N), dtype=torch.int32, device=dev)
+        count = _tensor(o["allowed"], "allowed", torch.int32, (B, N), dev)
+    r = _LogitRules()
+    if history is not None:
+        if history_len is None:
+            raise SSDError("history needs history_len")
+        r.history, r.history_stride = _rows2d(history, "history", B, dev)
+        r.history_max = history.shape[1]
+        r.history_len = _tensor(history_len, "history_len", torch.int32, (B,), dev)
+        r.prompt_len = _tensor(prompt_len, "prompt_len", torch.int32, (B,), dev)
+    par = None
+    if parent is not None:
+        par = np.ascontiguousarray(parent, dtype=np.int32)
+        if par.shape != (N,):
+            raise SSDError("parent must have N entries")
+        r.parent = par.ctypes.data
+    if draft_tokens is not None and N > 1:
+        ptr, r.draft_stride = _rows2d(draft_tokens, "draft_tokens", B, dev)
+        n = draft_tokens.shape[1]
+        if n not in (N - 1, N):
+            raise SSDError("draft_tokens must have N - 1 or N columns")
+        r.draft_tokens = ptr + 4 * (n - (N - 1))
+    r.repetition = _tensor(repetition, "repetition", torch.float32, (B,), dev)
+    r.presence = _tensor(presence, "presence", torch.float32, (B,), dev)
+    r.frequency = _tensor(frequency, "frequency", torch.float32, (B,), dev)
+    if (bias_ids is None) != (bias is None):
+        raise SSDError("bias_ids and bias go together")
+    if bias_ids is not None:
+        if bias_ids.dim() != 2:
+            raise SSDError("bias_ids: expected [B, n]")
+        r.n_bias = n = bias_ids.shape[1]
+        r.bias_ids = _tensor(bias_ids, "bias_ids", torch.int32, (B, n), dev)
+        r.bias = _tensor(bias, "bias", torch.float32, (B, n), dev)
+    if mask is not None:
+        W = (V + 31) // 32
+        if mask.dtype != torch.int32 or mask.device != dev or mask.dim() != 3 or \
+                mask.shape[0] not in (1, B) or mask.shape[1] not in (1, N) or \
+                mask.shape[2] != W or (W > 1 and mask.stride(2) != 1):
+            raise SSDError("mask: expected int32 words [B or 1, N or 1, ceil(V / 32)]")
+        r.mask = mask.data_ptr()
+        r.mask_seq_stride = mask.stride(0) if mask.shape[0] > 1 else 0
+        r.mask_row_stride = mask.stride(1) if mask.shape[1] > 1 else 0
+    r.fill = fill
+    st = lib().ssd_process_logits(ctypes.byref(_logits(logits)), ctypes.byref(_logits(z)), B, N, V,
+                                  ctypes.byref(r), count, _dev_ptr(dev_status),
+                                  _use_stream(stream, o.values()))
+    _check(st, "ssd_process_logits")
+    return o
+
+
+def page_plan(lens, new, held, tables, free_pages, free_count, page_size, max_rows,
+              dev_status=None, stream=None, out=None):
+    """ssd_page_plan: the pages of a paged key/value cache after a round, and
+    where the next tokens go.
+
+    lens, new, held int32 [B]: tokens in the cache, tokens to append, pages
+    held; tables int32 [B, W] and the stack free_pages int32 [n] with
+    free_count int32 [1] (entries of both are written, free_count is not).
+    Returns a dict of device tensors: slots int64, positions and owner int32
+    [max_rows]; cu int32 [B + 1]; kv_len, held, served int32 [B]; free_count
+    int32 [1].  `out`: the dict of an earlier call, to use its tensors again
+    (not while its kv_len, held or free_count are this call's inputs)."""
+    torch = _torch()
+    B = lens.shape[0] if lens.dim() == 1 else 0
+    dev, i32 = lens.device, torch.int32
+    T = int(max_rows)
+    o = out if out is not None else {}
+    if "slots" not in o:
+        o["slots"] = torch.empty(T, dtype=torch.int64, device=dev)
+        for name, n in (("positions", T), ("owner", T), ("cu", B + 1), ("kv_len", B),
+                        ("held", B), ("served", B), ("free_count", 1)):
+            o[name] = torch.empty(n, dtype=i32, device=dev)
+    table_ptr, table_stride = _rows2d(tables, "tables", B, dev)
+    if not lens.is_cuda:
+        raise SSDError("expected CUDA tensors")
+    st = lib().ssd_page_plan(
+        _tensor(lens, "lens", i32, (B,), dev), _tensor(new, "new", i32, (B,), dev),
+        _tensor(held, "held", i32, (B,), dev), B, table_ptr, table_stride, tables.shape[1],
+        _tensor(free_pages, "free_pages", i32, free_pages.shape, dev), free_pages.numel(),
+        _tensor(free_count, "free_count", i32, (1,), dev), int(page_size), T,
+        _tensor(o["slots"], "slots", torch.int64, (T,), dev),
+        _tensor(o["positions"], "positions", i32, (T,), dev),
+        _tensor(o["owner"], "owner", i32, (T,), dev), _tensor(o["cu"], "cu", i32, (B + 1,), dev),
+        _tensor(o["kv_len"], "kv_len", i32, (B,), dev), _tensor(o["held"], "held", i32, (B,), dev),
+        _tensor(o["served"], "served", i32, (B,), dev),
+        _tensor(o["free_count"], "free_count", i32, (1,), dev), _dev_ptr(dev_status),
+        _use_stream(stream, o.values()))
+    _check(st, "ssd_page_plan")
+    return o
+
+
+def _paged(t):
+    if t.stride(3) != 1:
+        raise SSDError("the head dimension of the cache must be contiguous")
+    return _Paged(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+
+
+def prefix_attention(q, k_cache, v_cache, prefix_tables, prefix_len, group_off, tables=None,
+                     lens=None, scale=None, lse=True, workspace=None, dev_status=None,
+                     stream=None, out=None):
+    """ssd_prefix_attention: one query token per row, q [R, Hq, D] (bf16 or
+    fp16), over caches [pages, page_size, Hkv, D] of its type (any strides
+    with a contiguous head dimension).
+
+    Rows group_off[g] .. group_off[g+1] (int32 [G+1]) read the first
+    prefix_len[g] (int32 [G]) tokens of pages prefix_tables[g, :] (int32
+    [G, W]), and each row the first lens[r] (int32 [R]) tokens of its own
+    pages tables[r, :] (int32 [R, W']).  scale: 1 / sqrt(D) when None.
+    Returns a dict: ``out`` [R, Hq, D] and, unless lse=False, ``lse`` float32
+    [R, Hq].  `out`: the dict of an earlier call of these shapes, to use its
+    tensors and workspace again."""
+    torch = _torch()
+    if q.dim() != 3 or k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise SSDError("expected q [R, Hq, D] and caches [pages, page_size, Hkv, D]")
+    R, Hq, D = q.shape
+    pages, page, Hkv, Dk = k_cache.shape
+    dev = q.device
+    dt = {torch.bfloat16: SSD_BF16, torch.float16: SSD_F16}.get(q.dtype)
+    if dt is None or k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
+        raise SSDError("q and the caches must share bfloat16 or float16")
+    if not q.is_cuda or k_cache.device != dev or v_cache.device != dev:
+        raise SSDError("q and the caches must be on one GPU")
+    if Dk != D or q.stride(2) != 1:
+        raise SSDError("q and the caches must share a contiguous head dimension")
+    o = out if out is not None else {}
+    if "out" not in o:
+        o["out"] = torch.empty((R, Hq, D), dtype=q.dtype, device=dev)
+        if lse:
+            o["lse"] = torch.empty((R, Hq), dtype=torch.float32, device=dev)
+    y = o["out"]
+    if y.shape != q.shape or y.dtype != q.dtype or y.device != dev or y.stride(2) != 1:
+        raise SSDError("out must have q's shape, type and device")
+    G = prefix_len.shape[0]
+    i32 = torch.int32
+    a = _Attention(dt, R, Hq, Hkv, D, G, pages, page, q.data_ptr(), q.stride(0), q.stride(1),
+                   _paged(k_cache), _paged(v_cache))
+    a.prefix_tables, a.prefix_table_stride = _rows2d(prefix_tables, "prefix_tables", G, dev)
+    a.prefix_cols = prefix_tables.shape[1]
+    a.prefix_len = _tensor(prefix_len, "prefix_len", i32, (G,), dev)
+    a.group_off = _tensor(group_off, "group_off", i32, (G + 1,), dev)
+    if (tables is None) != (lens is None):
+        raise SSDError("tables and lens go together")
+    if tables is not None:
+        a.tables, a.table_stride = _rows2d(tables, "tables", R, dev)
+        a.cols = tables.shape[1]
+        a.lens = _tensor(lens, "lens", i32, (R,), dev)
+    a.out, a.out_row_stride, a.out_head_stride = y.data_ptr(), y.stride(0), y.stride(1)
+    a.lse = _tensor(o["lse"], "lse", torch.float32, (R, Hq), dev) if lse else None
+    a.scale = D ** -0.5 if scale is None else scale
+    L = lib()
+    ws = workspace if workspace is not None else o.get("workspace")
+    if ws is None:
+        need = L.ssd_prefix_attention_workspace_size(ctypes.byref(a))
+        ws = o["workspace"] = _workspace(need, dev)
+    st = L.ssd_prefix_attention(ctypes.byref(a), ws.data_ptr(), ws.numel(), _dev_ptr(dev_status),
+                                _use_stream(stream, (*o.values(), ws)))
+    _check(st, "ssd_prefix_attention")
+    return o

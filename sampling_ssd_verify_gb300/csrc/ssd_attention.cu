@@ -1,0 +1,579 @@
+// ssd_attention.cu -- attention over shared prefixes and own tokens of a
+// paged cache (ssd_prefix_attention): the kernel of few rows, the join of
+// partial results, and the entry point.
+//
+// out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m), with m the running
+// maximum, over any stretch of tokens; two stretches join by weighting each
+// with exp(m_i - max m).
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "ssd_attention_dev.cuh"
+
+namespace ssd {
+namespace {
+
+// ---- a stretch of tokens by one warp -----------------------------------------------
+// 16 (row, head) pairs are the M of the matrix instructions, 16 tokens a step.
+// Each warp keeps its own ring of steps in shared memory, filled by 16-byte
+// asynchronous copies, so warps never wait for one another.
+constexpr int kWarpsPerCta = 4;
+constexpr int kStep = 16;           // tokens of a step
+constexpr int kRing = 3;            // steps of the ring
+constexpr int kTileTokens = 64;     // tokens of a tile (the unit of the split)
+constexpr int kBlockRows = 16;
+
+template <int D>
+__host__ __device__ constexpr int step_bytes() { return 2 * kStep * D * 2; }  // K and V
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  const __half2 x = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4],
+                                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (&a)[4],
+                                                 uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <bool TRANS>
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  if constexpr (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// 16 bytes global -> shared; zeros when !ok (src is then not read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(ok ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Where a stretch's partial goes: pair i of the block at o + i * o_step.
+struct Partial {
+  float* o;
+  int64_t o_step;
+  float2* ml;
+  int64_t ml_step;
+};
+
+// Pairs [pair0, min(pair0 + 16, npairs)) of the rows from row0 on, key/value
+// head h, tokens [t0, t1) of `table`.
+template <typename T, int D>
+__device__ __forceinline__ void warp_stretch(const AttnParams& p, uint32_t ring, int row0,
+                                             int pair0, int npairs, int h, const int32_t* table,
+                                             int t0, int t1, const Partial& out) {
+  constexpr int KK = D / 16;        // k-steps of the scores, 16-dimension groups of the output
+  constexpr int CH = D / 8;         // 16-byte chunks of a token
+  const int lane = threadIdx.x & 31, quad = lane & 3, gid = lane >> 2;
+  const ssd_attention& a = p.a;
+
+  // the queries as A fragments; pairs past the end are zeros
+  uint32_t qf[KK][4];
+  {
+    const T* q0 = nullptr;
+    const T* q1 = nullptr;
+    const int i0 = pair0 + gid, i1 = i0 + 8;
+    if (i0 < npairs)
+      q0 = static_cast<const T*>(a.q) + (int64_t)(row0 + i0 / p.gqa) * a.q_row_stride +
+           (int64_t)(h * p.gqa + i0 % p.gqa) * a.q_head_stride;
+    if (i1 < npairs)
+      q1 = static_cast<const T*>(a.q) + (int64_t)(row0 + i1 / p.gqa) * a.q_row_stride +
+           (int64_t)(h * p.gqa + i1 % p.gqa) * a.q_head_stride;
+#pragma unroll
+    for (int k = 0; k < KK; ++k) {
+      const int c = k * 16 + quad * 2;
+      qf[k][0] = q0 ? *reinterpret_cast<const uint32_t*>(q0 + c) : 0u;
+      qf[k][1] = q1 ? *reinterpret_cast<const uint32_t*>(q1 + c) : 0u;
+      qf[k][2] = q0 ? *reinterpret_cast<const uint32_t*>(q0 + c + 8) : 0u;
+      qf[k][3] = q1 ? *reinterpret_cast<const uint32_t*>(q1 + c + 8) : 0u;
+    }
+  }
+
+  float o[2 * KK][4];
+#pragma unroll
+  for (int n = 0; n < 2 * KK; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+  const int steps = (t1 - t0 + kStep - 1) / kStep;
+  // lane i (and i + 16) looks up the page of token i of a step, one step
+  // before its copies are issued
+  auto page_of = [&](int step) {
+    const int t = t0 + step * kStep + (lane & 15);
+    return t < t1 ? table[t / a.page_size] : -1;
+  };
+  auto issue = [&](int step, int page) {
+    const int t = t0 + step * kStep + (lane & 15);
+    bool ok = t < t1;
+    if (ok && (unsigned)page >= (unsigned)a.num_pages) {
+      ok = false;
+      flag(p, SSD_DEV_BAD_PAGE);
+    }
+    const int in_page = ok ? t % a.page_size : 0;
+    const int64_t pg = ok ? page : 0;
+    // a token that is not there: a negative offset, no read
+    const int64_t ko = ok ? pg * a.k.page_stride + in_page * a.k.token_stride : -1;
+    const int64_t vo = ok ? pg * a.v.page_stride + in_page * a.v.token_stride : -1;
+    const T* kb = static_cast<const T*>(a.k.ptr) + h * a.k.head_stride;
+    const T* vb = static_cast<const T*>(a.v.ptr) + h * a.v.head_stride;
+    const uint32_t ks = ring + (step % kRing) * step_bytes<D>();
+    const uint32_t vs = ks + kStep * D * 2;
+#pragma unroll
+    for (int i = 0; i < kStep * CH / 32; ++i) {
+      const int idx = i * 32 + lane, tok = idx / CH, c = idx % CH;
+      const int64_t k_at = __shfl_sync(0xffffffffu, ko, tok);
+      const int64_t v_at = __shfl_sync(0xffffffffu, vo, tok);
+      const uint32_t d = tok * (D * 2) + ((c ^ (tok & 7)) << 4);
+      copy16(ks + d, kb + (k_at < 0 ? 0 : k_at + c * 8), k_at >= 0);
+      copy16(vs + d, vb + (v_at < 0 ? 0 : v_at + c * 8), v_at >= 0);
+    }
+  };
+
+  __syncwarp();  // the ring's last readers are done
+  int page = page_of(0);
+#pragma unroll
+  for (int s = 0; s < kRing - 1; ++s) {
+    if (s < steps) issue(s, page);
+    copies_commit();
+    page = s + 1 < steps ? page_of(s + 1) : -1;
+  }
+  for (int s = 0; s < steps; ++s) {
+    copies_wait<kRing - 2>();
+    __syncwarp();
+    if (s + kRing - 1 < steps) issue(s + kRing - 1, page);
+    copies_commit();
+    if (s + kRing < steps) page = page_of(s + kRing);
+
+    const uint32_t ks = ring + (s % kRing) * step_bytes<D>();
+    const uint32_t vs = ks + kStep * D * 2;
+    float sc[2][4] = {};
+    {
+      const int tok = (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+#pragma unroll
+      for (int k = 0; k < KK; ++k) {
+        uint32_t b[4];
+        ldsm4<false>(b, ks + tok * (D * 2) + (((2 * k + half) ^ (tok & 7)) << 4));
+        mma16816<T>(sc[0], qf[k], b[0], b[1]);
+        mma16816<T>(sc[1], qf[k], b[2], b[3]);
+      }
+    }
+    const int left = t1 - (t0 + s * kStep);  // tokens of this step that are there
+    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int col = n * 8 + quad * 2 + (i & 1);
+        sc[n][i] = col < left ? sc[n][i] * p.scale_log2 : -INFINITY;
+        top[i >> 1] = fmaxf(top[i >> 1], sc[n][i]);
+      }
+    float keep[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+      const float m1 = fmaxf(m[r], top[r]);
+      const float off = m1 == -INFINITY ? 0.f : m1;
+      keep[r] = exp2_fast(m[r] - off);
+      m[r] = m1;
+      float sum = 0.f;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          sc[n][2 * r + i] = exp2_fast(sc[n][2 * r + i] - off);
+          sum += sc[n][2 * r + i];
+        }
+      l[r] = l[r] * keep[r] + sum;
+    }
+    const uint32_t pf[4] = {pack2<T>(sc[0][0], sc[0][1]), pack2<T>(sc[0][2], sc[0][3]),
+                            pack2<T>(sc[1][0], sc[1][1]), pack2<T>(sc[1][2], sc[1][3])};
+    const int tok = (lane & 7) + (((lane >> 3) & 1) << 3);
+#pragma unroll
+    for (int k = 0; k < KK; ++k) {
+      uint32_t b[4];
+      ldsm4<true>(b, vs + tok * (D * 2) + (((2 * k + (lane >> 4)) ^ (tok & 7)) << 4));
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        float(&c)[4] = o[2 * k + n];
+        c[0] *= keep[0];
+        c[1] *= keep[0];
+        c[2] *= keep[1];
+        c[3] *= keep[1];
+        mma16816<T>(c, pf, b[2 * n], b[2 * n + 1]);
+      }
+    }
+  }
+  copies_wait<0>();
+
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    const int i = gid + 8 * r;
+    if (pair0 + i >= npairs) continue;
+    if (quad == 0) out.ml[i * out.ml_step] = make_float2(m[r], l[r]);
+    float* to = out.o + i * out.o_step + quad * 2;
+#pragma unroll
+    for (int n = 0; n < 2 * KK; ++n)
+      *reinterpret_cast<float2*>(to + n * 8) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarpsPerCta * 32)
+    prefix_kernel(const __grid_constant__ AttnParams p) {
+  extern __shared__ __align__(128) unsigned char s_ring[];
+  __shared__ Start s_start[kWarpsPerCta];
+  __shared__ int2 s_warp[kWarpsPerCta];
+  const int w0 = blockIdx.x * kWarpsPerCta, warp = threadIdx.x >> 5, w = w0 + warp;
+  const int total = find_starts<kWarpsPerCta * 32, kWarpsPerCta>(p, w0, s_start, s_warp);
+  const uint32_t ring = smem_addr(s_ring) + warp * kRing * step_bytes<D>();
+  Walk k;
+  k.u = first_unit(p, w, total);
+  k.u1 = first_unit(p, w + 1, total);
+  if (k.u >= k.u1) return;
+  k.g = s_start[warp].g;
+  k.unit = s_start[warp].unit;
+  k.item = s_start[warp].item;
+  k.w = w;
+  Stretch s;
+  while (next_stretch(p, k, s)) {
+    if (s.slot >= p.nslots) break;  // cannot happen: the host sized the slots for every split
+    const Partial out{p.po + (int64_t)s.slot * kBlockRows * D, D, p.pml + (int64_t)s.slot * kBlockRows,
+                      1};
+    warp_stretch<T, D>(p, ring, s.q.row0, s.mb * kBlockRows, s.q.rows * p.gqa, s.h,
+                       p.a.prefix_tables + (int64_t)s.g * p.a.prefix_table_stride,
+                       s.tile0 * kTileTokens, min(s.q.len, s.tile1 * kTileTokens), out);
+  }
+}
+
+// Tokens of row r's own cache, clamped into range.
+__device__ __forceinline__ int own_len(const AttnParams& p, int r) {
+  if (!p.a.lens) return 0;
+  const long long most = (long long)p.a.cols * p.a.page_size;
+  const int n = p.a.lens[r];
+  return n < 0 ? 0 : n > most ? (int)most : n;
+}
+// Tokens of one of the nsplit stretches, whole steps.
+__device__ __forceinline__ int own_stretch(const AttnParams& p, int len) {
+  return ((len + p.nsplit - 1) / p.nsplit + kStep - 1) / kStep * kStep;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarpsPerCta * 32)
+    own_kernel(const __grid_constant__ AttnParams p, int blocks) {
+  extern __shared__ __align__(128) unsigned char s_ring[];
+  const int warp = threadIdx.x >> 5;
+  int64_t task = (int64_t)blockIdx.x * kWarpsPerCta + warp;
+  if (task >= (int64_t)p.a.R * p.a.Hkv * blocks * p.nsplit) return;
+  const int split = (int)(task % p.nsplit);
+  task /= p.nsplit;
+  const int mb = (int)(task % blocks);
+  task /= blocks;
+  const int h = (int)(task % p.a.Hkv), r = (int)(task / p.a.Hkv);
+  const int len = own_len(p, r), n = own_stretch(p, len);
+  const int t0 = min(len, split * n), t1 = min(len, t0 + n);
+  if (h == 0 && mb == 0 && split == 0 && (threadIdx.x & 31) == 0 && len != p.a.lens[r])
+    flag(p, SSD_DEV_BAD_LENGTH);
+  if (t0 >= t1) return;  // the join does not look at it
+  const int64_t at = ((int64_t)r * p.a.Hq + h * p.gqa + mb * kBlockRows) * p.nsplit + split;
+  const Partial out{p.so + at * D, (int64_t)p.nsplit * D, p.sml + at, p.nsplit};
+  warp_stretch<T, D>(p, smem_addr(s_ring) + warp * kRing * step_bytes<D>(), r, mb * kBlockRows,
+                     p.gqa, h, p.a.tables + (int64_t)r * p.a.table_stride, t0, t1, out);
+}
+
+// ---- the join ------------------------------------------------------------------------
+// One warp per (row, head): the largest score of all its partials, then their
+// sums weighted by it.
+constexpr int kJoinWarps = 8;
+
+// The group of row r: the last one that starts at or before it.
+__device__ __forceinline__ int group_of_row(const int32_t* off, int G, int r) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = G;  // the answer is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32, i = lo + lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, i < lo + n && off[i] <= r);
+    const int k = le ? 31 - __clz(le) : 0;
+    n = min(step, n - k * step);
+    lo += k * step;
+  }
+  return lo;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t pair = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  if (pair >= (int64_t)p.a.R * p.a.Hq) return;
+  const int r = (int)(pair / p.a.Hq), head = (int)(pair % p.a.Hq);
+
+  // partials [0, np) are the prefix's, the others the own tokens'
+  int np = 0, ns = 0;
+  int64_t slot0 = 0;
+  if (p.a.G > 0) {
+    const int g = group_of_row(p.a.group_off, p.a.G, r);
+    const Group q = group_of(p, g);
+    const int unit0 = p.unit_base[g], total = p.unit_base[p.a.G];
+    if (r >= q.row0 && r < q.row0 + q.rows && q.tiles > 0 && total > 0) {
+      const int i = (r - q.row0) * p.gqa + head % p.gqa;
+      const int local = head / p.gqa * q.blocks + i / p.mt;
+      const int u = unit0 + local * q.tiles;
+      const int w0 = worker_of(p, u, total);
+      np = worker_of(p, u + q.tiles - 1, total) - w0 + 1;
+      slot0 = ((int64_t)p.item_base[g] + local + w0) * p.mt + i % p.mt;
+      if (slot0 + (int64_t)(np - 1) * p.mt >= (int64_t)p.nslots * p.mt) np = 0;
+    }
+  }
+  const int len = own_len(p, r);
+  if (len > 0) ns = (len + own_stretch(p, len) - 1) / own_stretch(p, len);
+
+  auto ml_of = [&](int i) {
+    return i < np ? p.pml[slot0 + (int64_t)i * p.mt] : p.sml[pair * p.nsplit + (i - np)];
+  };
+  float m = -INFINITY;
+  for (int i = lane; i < np + ns; i += 32) m = fmaxf(m, ml_of(i).x);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const float off = m == -INFINITY ? 0.f : m;
+
+  float acc[E] = {};
+  float l = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < np + ns; ++i) {
+    const float2 ml = ml_of(i);
+    const float wgt = exp2_fast(ml.x - off);
+    l += ml.y * wgt;
+    const float* o = (i < np ? p.po + (slot0 + (int64_t)i * p.mt) * D
+                             : p.so + (pair * p.nsplit + (i - np)) * D) + lane * E;
+    float x[E];
+    if constexpr (E == 2) {
+      *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(o);
+    } else {
+#pragma unroll
+      for (int k = 0; k < E; k += 4)
+        *reinterpret_cast<float4*>(x + k) = *reinterpret_cast<const float4*>(o + k);
+    }
+#pragma unroll
+    for (int k = 0; k < E; ++k) acc[k] += x[k] * wgt;
+  }
+  // no token at all: zeros and -inf
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  T* to = static_cast<T*>(p.a.out) + (int64_t)r * p.a.out_row_stride +
+          (int64_t)head * p.a.out_head_stride + lane * E;
+  uint32_t y[E / 2];
+#pragma unroll
+  for (int k = 0; k < E / 2; ++k) y[k] = pack2<T>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+  if constexpr (E == 2) *reinterpret_cast<uint32_t*>(to) = y[0];
+  if constexpr (E == 4) *reinterpret_cast<uint2*>(to) = make_uint2(y[0], y[1]);
+  if constexpr (E == 8) *reinterpret_cast<uint4*>(to) = make_uint4(y[0], y[1], y[2], y[3]);
+  if (lane == 0 && p.a.lse)
+    p.a.lse[pair] = np + ns > 0 ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+// ---- set-up ---------------------------------------------------------------------------
+struct Layout {
+  int own_blocks;
+  size_t po, pml, unit, item, so, sml, total;
+};
+
+bool strides_ok(const void* ptr, std::initializer_list<int64_t> strides) {
+  if (!ptr || (uintptr_t)ptr % 16 != 0) return false;
+  for (int64_t s : strides)
+    if (s < 0 || s % 8 != 0) return false;
+  return true;
+}
+
+ssd_status check(const ssd_attention* a) {
+  if (!a || (a->dtype != SSD_BF16 && a->dtype != SSD_F16) || a->pad_ != 0)
+    return SSD_ERR_INVALID_ARG;
+  if (a->R < 1 || a->Hq < 1 || a->Hkv < 1 || a->Hq % a->Hkv != 0 || a->G < 0 ||
+      a->num_pages < 1 || a->page_size < 1 || !std::isfinite(a->scale))
+    return SSD_ERR_INVALID_ARG;
+  if (a->D != 64 && a->D != 128 && a->D != 256) return SSD_ERR_UNSUPPORTED;
+  if (a->prefix_cols < 0 || a->cols < 0 || (a->tables == nullptr) != (a->lens == nullptr))
+    return SSD_ERR_INVALID_ARG;
+  if (a->G > 0 && (!a->prefix_tables || !a->prefix_len || !a->group_off ||
+                   a->prefix_table_stride < a->prefix_cols))
+    return SSD_ERR_INVALID_ARG;
+  if (a->tables && a->table_stride < a->cols) return SSD_ERR_INVALID_ARG;
+  if ((int64_t)a->prefix_cols * a->page_size > 0x7fffffff ||
+      (int64_t)a->cols * a->page_size > 0x7fffffff || (int64_t)a->R * a->Hq > 0x7fffffff)
+    return SSD_ERR_UNSUPPORTED;
+  return SSD_OK;
+}
+
+int ctas_per_sm(int D) { return D == 256 ? 1 : D == 128 ? 2 : 4; }  // by shared memory
+
+// The split and the workspace of a call; false when its work is beyond 32-bit
+// counts.
+bool plan(const ssd_attention& a, AttnParams& p, Layout& L) {
+  const int sms = std::max(num_sms(), 1);
+  p.a = a;
+  p.gqa = a.Hq / a.Hkv;
+  p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
+  p.mt = kBlockRows;
+  p.tn = kTileTokens;
+  p.workers = sms * ctas_per_sm(a.D) * kWarpsPerCta;
+  const int64_t items =
+      a.Hkv * ((int64_t)a.R * p.gqa / p.mt + std::min<int64_t>(a.G, a.R));
+  const int64_t tiles = ((int64_t)a.prefix_cols * a.page_size + p.tn - 1) / p.tn;
+  if (items * std::max<int64_t>(tiles, 1) > 0x7fffffff) return false;
+  p.nslots = a.G > 0 ? (int)(items + p.workers) : 0;
+  // own tokens: stretches of at least a tile, as many as give each resident
+  // warp one
+  L.own_blocks = (p.gqa + kBlockRows - 1) / kBlockRows;
+  const int64_t own = (int64_t)a.R * a.Hkv * L.own_blocks;
+  const int64_t most = a.lens ? ((int64_t)a.cols * a.page_size + p.tn - 1) / p.tn : 0;
+  p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(most, p.workers / own));
+  if (own * p.nsplit / kWarpsPerCta >= 0x7fffffff) return false;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align256(bytes);
+    return here;
+  };
+  L.po = take((size_t)p.nslots * p.mt * a.D * 4);
+  L.pml = take((size_t)p.nslots * p.mt * 8);
+  L.unit = take((size_t)(a.G + 1) * 4);
+  L.item = take((size_t)(a.G + 1) * 4);
+  const size_t rows = a.lens ? (size_t)a.R * a.Hq * p.nsplit : 0;
+  L.so = take(rows * a.D * 4);
+  L.sml = take(rows * 8);
+  L.total = std::max<size_t>(at, 256);
+  return true;
+}
+
+template <typename T, int D>
+cudaError_t launch(const AttnParams& p, const Layout& L, cudaStream_t s) {
+  const int smem = kWarpsPerCta * kRing * step_bytes<D>();
+  cudaError_t e;
+  if (p.a.G > 0) {
+    e = cudaFuncSetAttribute(prefix_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    prefix_kernel<T, D><<<p.workers / kWarpsPerCta, kWarpsPerCta * 32, smem, s>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  if (p.a.lens && p.a.cols > 0) {
+    e = cudaFuncSetAttribute(own_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t tasks = (int64_t)p.a.R * p.a.Hkv * L.own_blocks * p.nsplit;
+    own_kernel<T, D><<<(unsigned)((tasks + kWarpsPerCta - 1) / kWarpsPerCta), kWarpsPerCta * 32,
+                       smem, s>>>(p, L.own_blocks);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t pairs = (int64_t)p.a.R * p.a.Hq;
+  join_kernel<T, D><<<(unsigned)((pairs + kJoinWarps - 1) / kJoinWarps), kJoinWarps * 32, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_d(const AttnParams& p, const Layout& L, cudaStream_t s) {
+  switch (p.a.D) {
+    case 64: return launch<T, 64>(p, L, s);
+    case 128: return launch<T, 128>(p, L, s);
+    default: return launch<T, 256>(p, L, s);
+  }
+}
+
+}  // namespace
+}  // namespace ssd
+
+using namespace ssd;
+
+extern "C" {
+
+size_t ssd_prefix_attention_workspace_size(const ssd_attention* a) {
+  AttnParams p{};
+  Layout L;
+  if (check(a) != SSD_OK || !plan(*a, p, L)) return 0;
+  return L.total;
+}
+
+ssd_status ssd_prefix_attention(const ssd_attention* a, void* workspace, size_t workspace_bytes,
+                                int32_t* dev_status, void* stream) {
+  const ssd_status st = check(a);
+  if (st != SSD_OK) return st;
+  if (!strides_ok(a->q, {a->q_row_stride, a->q_head_stride}) ||
+      !strides_ok(a->out, {a->out_row_stride, a->out_head_stride}) ||
+      !strides_ok(a->k.ptr, {a->k.page_stride, a->k.token_stride, a->k.head_stride}) ||
+      !strides_ok(a->v.ptr, {a->v.page_stride, a->v.token_stride, a->v.head_stride}))
+    return SSD_ERR_INVALID_ARG;
+  AttnParams p{};
+  Layout L;
+  if (!plan(*a, p, L)) return SSD_ERR_UNSUPPORTED;
+  if (!workspace || (uintptr_t)workspace % 256 != 0 || workspace_bytes < L.total)
+    return SSD_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  p.po = reinterpret_cast<float*>(ws + L.po);
+  p.pml = reinterpret_cast<float2*>(ws + L.pml);
+  p.unit_base = reinterpret_cast<int*>(ws + L.unit);
+  p.item_base = reinterpret_cast<int*>(ws + L.item);
+  p.so = reinterpret_cast<float*>(ws + L.so);
+  p.sml = reinterpret_cast<float2*>(ws + L.sml);
+  p.status = dev_status;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = a->dtype == SSD_BF16 ? launch_d<__nv_bfloat16>(p, L, s)
+                                             : launch_d<__half>(p, L, s);
+  if (e == cudaSuccess) return SSD_OK;
+  cudaGetLastError();
+  return SSD_ERR_CUDA;
+}
+
+}  // extern "C"

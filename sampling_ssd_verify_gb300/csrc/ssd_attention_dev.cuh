@@ -1,0 +1,184 @@
+// ssd_attention_dev.cuh -- what the attention kernels share: parameters, the
+// split of the prefixes' work over workers, and the layout of partial results.
+//
+// A prefix is attended to by all rows of its group.  The rows' query heads
+// that read one key/value head, (row, head) in row-major order, are cut into
+// blocks of MT; an item is (group, key/value head, block), and costs the tiles
+// of TN tokens of the group's prefix.  All tiles of all items, in order, are
+// divided evenly among the workers, so every worker has the same share however
+// the lengths differ; a worker that gets a stretch of an item leaves a partial
+// result (unnormalised sums, their largest score and weight), and the rows'
+// partials are joined afterwards.  The partial of item i by worker w has slot
+// i + w: along the sequence of stretches one of the two steps up each time,
+// so slots are never shared, and need no counter.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "ssd.h"
+#include "ssd_device.cuh"
+#include "ssd_internal.cuh"
+
+namespace ssd {
+
+struct AttnParams {
+  ssd_attention a;
+  float scale_log2;       // scale * log2(e): scores in base 2
+  int gqa;                // query heads per key/value head
+  // prefixes: items, partials
+  int mt, tn;             // rows of a block, tokens of a tile
+  int workers;
+  int nslots;
+  float* po;              // [nslots, mt, D] unnormalised sums
+  float2* pml;            // [nslots, mt] largest score (base 2), weight
+  int* unit_base;         // [G + 1] tiles of all items before group g
+  int* item_base;         // [G + 1] items before group g
+  // own tokens: nsplit stretches per row, each with its partial
+  int nsplit;
+  float* so;              // [R, Hq, nsplit, D]
+  float2* sml;            // [R, Hq, nsplit]
+  int32_t* status;
+};
+
+__device__ __forceinline__ void flag(const AttnParams& p, int bit) {
+  if (p.status) atomicOr(p.status, bit);
+}
+
+// Group g: its rows and tokens, clamped into range.
+struct Group {
+  int row0, rows, len;
+  int blocks, tiles;      // blocks of its (row, head) pairs, tiles of its prefix
+  bool torn;              // its rows are no range within [0, R]
+  bool bad;               // that, or its length was clamped
+};
+__device__ __forceinline__ Group group_of(const AttnParams& p, int g) {
+  Group q;
+  const int o0 = p.a.group_off[g], o1 = p.a.group_off[g + 1];
+  const int len = p.a.prefix_len[g];
+  q.row0 = min(max(o0, 0), p.a.R);
+  q.rows = min(max(o1, 0), p.a.R) - q.row0;
+  const long long most = (long long)p.a.prefix_cols * p.a.page_size;
+  q.len = len < 0 ? 0 : len > most ? (int)most : len;
+  q.torn = q.row0 != o0 || q.rows < 0 || q.row0 + q.rows != o1;
+  q.bad = q.torn || q.len != len;
+  q.rows = max(q.rows, 0);
+  q.blocks = (q.rows * p.gqa + p.mt - 1) / p.mt;
+  q.tiles = (q.len + p.tn - 1) / p.tn;
+  return q;
+}
+
+// First tile of worker w when `total` tiles are shared, and the worker that
+// has tile u.  At most one worker per tile takes part, so that each of those
+// has a tile, and the partials of an item are by consecutive workers.
+__device__ __forceinline__ int first_unit(const AttnParams& p, int w, int total) {
+  const int n = min(p.workers, total);
+  return w >= n ? total : (int)((long long)w * total / n);
+}
+__device__ __forceinline__ int worker_of(const AttnParams& p, int u, int total) {
+  return (int)((((long long)u + 1) * min(p.workers, total) - 1) / total);
+}
+
+// Running sums over the groups, by the whole CTA (NT threads), which finds for
+// each of its NW workers w0 .. w0 + NW - 1 the group that holds its first
+// tile.  CTA 0 leaves the sums for the join.  Returns the number of tiles.
+struct Start {
+  int g, unit, item;      // the group, and the sums before it
+};
+template <int NT, int NW>
+__device__ __forceinline__ int find_starts(const AttnParams& p, int w0, Start* s_start,
+                                           int2* s_warp) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = p.a.G;
+  int total = 0, torn = 0;
+  // pass 0 forms the total, pass 1 the starts that it determines (one pass
+  // over the groups each; the lengths of pass 1 come from L1)
+  for (int pass = 0; pass < 2; ++pass) {
+    int2 base = make_int2(0, 0);
+    for (int g0 = 0; g0 < G; g0 += NT) {
+      const int g = g0 + tid;
+      int2 mine = make_int2(0, 0);
+      if (g < G) {
+        const Group q = group_of(p, g);
+        torn |= q.torn;
+        mine = torn ? mine : make_int2(p.a.Hkv * q.blocks * q.tiles, p.a.Hkv * q.blocks);
+        if (pass == 0 && blockIdx.x == 0 && q.bad) flag(p, SSD_DEV_BAD_LENGTH);
+      }
+      int2 x = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, x.x, d);
+        const int b = __shfl_up_sync(0xffffffffu, x.y, d);
+        if (lane >= d) { x.x += a; x.y += b; }
+      }
+      if (lane == 31) s_warp[warp] = x;
+      __syncthreads();
+      int2 before = base;
+      for (int w = 0; w < NT / 32; ++w) {
+        const int2 y = s_warp[w];
+        if (w < warp) { before.x += y.x; before.y += y.y; }
+        base.x += y.x;
+        base.y += y.y;
+      }
+      __syncthreads();
+      if (pass == 1 && g < G) {
+        const int u = before.x + x.x - mine.x, i = before.y + x.y - mine.y;
+        if (blockIdx.x == 0) {
+          p.unit_base[g] = torn ? 0 : u;
+          p.item_base[g] = torn ? 0 : i;
+        }
+#pragma unroll
+        for (int k = 0; k < NW; ++k) {
+          const int f = first_unit(p, w0 + k, total);
+          if (!torn && f >= u && f < u + mine.x) s_start[k] = Start{g, u, i};
+        }
+      }
+    }
+    if (pass == 0 && __syncthreads_or(torn)) torn = 1;
+    total = torn ? 0 : base.x;
+    if (pass == 1 && blockIdx.x == 0 && tid == 0) {
+      p.unit_base[G] = total;
+      p.item_base[G] = torn ? 0 : base.y;
+    }
+  }
+  __syncthreads();
+  return total;
+}
+
+// A worker's stretches, one after the other.
+struct Stretch {
+  int g, h, mb;           // the item
+  int slot;
+  Group q;
+  int tile0, tile1;       // tiles of the prefix
+};
+struct Walk {
+  int u, u1;              // tiles still to do
+  int g, unit, item;
+  int w;
+};
+__device__ __forceinline__ bool next_stretch(const AttnParams& p, Walk& k, Stretch& s) {
+  if (k.u >= k.u1) return false;
+  Group q = group_of(p, k.g);
+  int n = p.a.Hkv * q.blocks * q.tiles;
+  while (k.u >= k.unit + n) {  // ends: u < u1 <= total
+    k.unit += n;
+    k.item += p.a.Hkv * q.blocks;
+    q = group_of(p, ++k.g);
+    n = p.a.Hkv * q.blocks * q.tiles;
+  }
+  const int local = (k.u - k.unit) / q.tiles;  // item within the group
+  s.q = q;
+  s.g = k.g;
+  s.h = local / q.blocks;
+  s.mb = local - s.h * q.blocks;
+  s.tile0 = (k.u - k.unit) - local * q.tiles;
+  s.tile1 = min(q.tiles, s.tile0 + (k.u1 - k.u));
+  s.slot = k.item + local + k.w;
+  k.u += s.tile1 - s.tile0;
+  return true;
+}
+
+}  // namespace ssd

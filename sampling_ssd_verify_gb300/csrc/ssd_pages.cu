@@ -1,0 +1,235 @@
+// ssd_pages.cu -- pages, slots and positions of a paged key/value cache from
+// request lengths (ssd_page_plan).
+//
+// All arithmetic is running sums over the requests: of their new tokens, of
+// the pages they give back and of the pages they take.  The i-th page taken
+// is entry top - 1 - i of the stack with the returned pages on it, so every
+// page and every slot follows from the sums by itself.  Each CTA therefore
+// forms the sums of all requests again in its shared memory (a few KB of
+// lengths from L2) and writes its share of the outputs; no CTA waits for
+// another, and nothing that the launch writes is read by it: table entries
+// taken lie at columns >= held, those read below it; stack entries written
+// lie at >= *free_count, those read below it.  Bound by the latency of the
+// launch, the loads of the lengths and the scan; bytes count from about a
+// hundred thousand new tokens on (16 bytes each).
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "ssd.h"
+#include "ssd_internal.cuh"
+
+namespace ssd {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxRequests = 8192;  // three sums each in shared memory
+constexpr int kRowsPerCta = 2048;   // new tokens per CTA before another one is added
+
+struct PageParams {
+  const int32_t *lens, *add, *held;
+  int B;
+  int32_t* tables;
+  int64_t table_stride;
+  int cols;
+  int32_t* free_pages;
+  int free_cap;
+  const int32_t* free_count;
+  int page, max_rows;
+  int64_t* slots;
+  int32_t *positions, *owner, *cu, *kv_len, *held_out, *served, *free_out, *status;
+};
+
+struct Request {
+  int len, add, held, need;
+  bool ok;  // its lengths are consistent
+};
+
+__device__ __forceinline__ Request request(const PageParams& p, int b) {
+  Request q;
+  q.len = p.lens[b];
+  q.add = p.add[b];
+  q.held = p.held[b];
+  const int64_t end = (int64_t)q.len + q.add;
+  q.ok = q.len >= 0 && q.add >= 0 && q.held >= 0 && q.held <= p.cols &&
+         end <= min((int64_t)p.cols * p.page, (int64_t)0x7fffffff) && q.len <= (int64_t)q.held * p.page;
+  q.need = q.ok ? (int)((end + p.page - 1) / p.page) : q.held;
+  if (!q.ok) q.add = 0;
+  return q;
+}
+
+__device__ __forceinline__ int clamp32(int64_t x) {
+  return (int)(x < 0x7fffffff ? x : 0x7fffffff);
+}
+
+// The largest b in [0, n) with sum[b] <= i (sum[0] = 0 <= i).
+__device__ __forceinline__ int find(const int* sum, int n, int i) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sum[mid] <= i) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kThreads) page_plan_kernel(const PageParams p) {
+  extern __shared__ int s_sums[];
+  int* s_cu = s_sums;                   // [B + 1] new tokens before request b
+  int* s_back = s_cu + p.B + 1;         // [B + 1] pages given back before it
+  int* s_ask = s_back + p.B + 1;        // [B + 1] pages asked for before it
+  __shared__ int64_t s_warp[3][kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n0 = *p.free_count;
+  int bad = 0;
+
+  // ---- running sums: consecutive requests per thread, then over the threads ------
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  int64_t sum[3] = {0, 0, 0};
+  for (int b = b0; b < b1; ++b) {
+    const Request q = request(p, b);
+    if (!q.ok) bad = SSD_DEV_BAD_LENGTH;
+    sum[0] += q.add;
+    sum[1] += max(q.held - q.need, 0);
+    sum[2] += max(q.need - q.held, 0);
+  }
+  int64_t inc[3];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    int64_t x = sum[k];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    inc[k] = x;
+    if (lane == 31) s_warp[k][warp] = x;
+  }
+  __syncthreads();
+  int64_t run[3];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    int64_t before = 0;
+    for (int w = 0; w < warp; ++w) before += s_warp[k][w];
+    run[k] = before + inc[k] - sum[k];
+  }
+  for (int b = b0; b < b1; ++b) {
+    const Request q = request(p, b);
+    s_cu[b] = clamp32(run[0]);
+    s_back[b] = clamp32(run[1]);
+    s_ask[b] = clamp32(run[2]);
+    run[0] += q.add;
+    run[1] += max(q.held - q.need, 0);
+    run[2] += max(q.need - q.held, 0);
+  }
+  if (b1 == p.B && b0 < p.B) {  // the thread of the last request
+    s_cu[p.B] = clamp32(run[0]);
+    s_back[p.B] = clamp32(run[1]);
+    s_ask[p.B] = clamp32(run[2]);
+  }
+  __syncthreads();
+
+  const int n = min(max(n0, 0), p.free_cap);
+  const int total = s_cu[p.B], back = s_back[p.B], ask = s_ask[p.B];
+  const int64_t top = (int64_t)n + back;
+
+  // entry i of the stack with the returned pages on it, 0 <= i < top
+  auto stack = [&](int64_t i) {
+    if (i < n) return p.free_pages[i];
+    const int k = (int)(i - n);
+    const int b = find(s_back, p.B, k);
+    return p.tables[b * p.table_stride + request(p, b).need + (k - s_back[b])];
+  };
+  auto is_served = [&](const Request& q, int b) {
+    return q.ok && (q.need <= q.held || (int64_t)s_ask[b + 1] <= top);
+  };
+
+  const int gtid = blockIdx.x * kThreads + tid, nthreads = gridDim.x * kThreads;
+  // ---- rows of the new tokens ----------------------------------------------------
+  for (int t = gtid; t < p.max_rows; t += nthreads) {
+    int64_t slot = -1;
+    int pos = -1, own = -1;
+    if (t < total) {
+      own = find(s_cu, p.B, t);
+      const Request q = request(p, own);
+      pos = q.len + (t - s_cu[own]);
+      if (is_served(q, own)) {
+        const int col = pos / p.page;
+        const int pg = col < q.held ? p.tables[own * p.table_stride + col]
+                                    : stack(top - 1 - (s_ask[own] + (col - q.held)));
+        slot = (int64_t)pg * p.page + (pos - col * p.page);
+      }
+    }
+    p.slots[t] = slot;
+    if (p.positions) p.positions[t] = pos;
+    if (p.owner) p.owner[t] = own;
+  }
+  // ---- pages taken, pages given back ---------------------------------------------
+  for (int64_t i = gtid; i < min((int64_t)ask, top); i += nthreads) {
+    const int b = find(s_ask, p.B, (int)i);
+    if ((int64_t)s_ask[b + 1] <= top)
+      p.tables[b * p.table_stride + p.held[b] + ((int)i - s_ask[b])] = stack(top - 1 - i);
+  }
+  for (int k = gtid; k < back; k += nthreads)
+    if (n + (int64_t)k < p.free_cap) p.free_pages[n + k] = stack(n + (int64_t)k);
+  // ---- the requests ----------------------------------------------------------------
+  for (int b = gtid; b < p.B; b += nthreads) {
+    const Request q = request(p, b);
+    const bool ok = is_served(q, b);
+    p.cu[b] = s_cu[b];
+    p.kv_len[b] = ok ? q.len + q.add : q.len;
+    p.held_out[b] = ok ? q.need : q.held;
+    p.served[b] = ok;
+    if (q.ok && !ok) bad |= SSD_DEV_NO_PAGES;
+    // the pages left after the last request that got what it asked for
+    if (s_ask[b] < s_ask[b + 1] && s_ask[b] <= top && s_ask[b + 1] > top)
+      *p.free_out = (int)min(top - s_ask[b], (int64_t)p.free_cap);
+  }
+  if (gtid == 0) {
+    p.cu[p.B] = total;
+    if (ask <= top) *p.free_out = (int)min(top - ask, (int64_t)p.free_cap);
+    if (n != n0 || top > p.free_cap || total > p.max_rows) bad |= SSD_DEV_BAD_LENGTH;
+  }
+  if (bad && p.status) atomicOr(p.status, bad);
+}
+
+}  // namespace
+}  // namespace ssd
+
+using namespace ssd;
+
+extern "C" ssd_status ssd_page_plan(const int32_t* lens, const int32_t* new_tokens,
+                                    const int32_t* held, int B, int32_t* tables,
+                                    int64_t table_stride, int cols, int32_t* free_pages,
+                                    int free_cap, const int32_t* free_count, int page,
+                                    int max_rows, int64_t* slots, int32_t* positions,
+                                    int32_t* owner, int32_t* cu, int32_t* kv_len,
+                                    int32_t* held_out, int32_t* served, int32_t* free_out,
+                                    int32_t* dev_status, void* stream) {
+  if (!lens || !new_tokens || !held || !tables || !free_count || !cu || !kv_len || !held_out ||
+      !served || !free_out || free_out == free_count || kv_len == lens || held_out == held)
+    return SSD_ERR_INVALID_ARG;
+  if (B < 1 || cols < 1 || page < 1 || free_cap < 0 || max_rows < 0 || table_stride < cols)
+    return SSD_ERR_INVALID_ARG;
+  if ((free_cap > 0 && !free_pages) || (max_rows > 0 && !slots)) return SSD_ERR_INVALID_ARG;
+  if (B > kMaxRequests) return SSD_ERR_UNSUPPORTED;
+  const PageParams p{lens,     new_tokens, held,  B, tables, table_stride, cols,
+                     free_pages, free_cap, free_count, page,    max_rows, slots, positions,
+                     owner,    cu,         kv_len, held_out,   served, free_out,     dev_status};
+  const size_t smem = (size_t)3 * (B + 1) * sizeof(int);
+  const int64_t work = std::max<int64_t>(max_rows / kRowsPerCta, B / kThreads);
+  const int grid = (int)std::min<int64_t>(std::max(num_sms(), 1), 1 + work);
+  cudaError_t e = cudaFuncSetAttribute(
+      page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess) {
+    page_plan_kernel<<<grid, kThreads, smem, static_cast<cudaStream_t>(stream)>>>(p);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess) return SSD_OK;
+  cudaGetLastError();
+  return SSD_ERR_CUDA;
+}
