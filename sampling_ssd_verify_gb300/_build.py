@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(PKG, "libssd.so")
 CHECKS_LIB_PATH = os.path.join(PKG, "libssd_checks.so")
 SOURCES = ["ssd_stream_bf16.cu", "ssd_stream_f32.cu", "ssd_cache.cu", "ssd_api.cu",
            "ssd_noalloc.cu", "ssd_tree.cu", "ssd_logits.cu", "ssd_pages.cu",
-           "ssd_attention.cu"]
+           "ssd_attention.cu", "ssd_attention_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

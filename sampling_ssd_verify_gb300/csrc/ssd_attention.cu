@@ -427,6 +427,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
 
 // ---- set-up ---------------------------------------------------------------------------
 struct Layout {
+  bool tc;                  // the prefixes' kernel is the tensor-core one
   int own_blocks;
   size_t po, pml, unit, item, so, sml, total;
 };
@@ -466,9 +467,11 @@ bool plan(const ssd_attention& a, AttnParams& p, Layout& L) {
   p.a = a;
   p.gqa = a.Hq / a.Hkv;
   p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
-  p.mt = kBlockRows;
-  p.tn = kTileTokens;
-  p.workers = sms * ctas_per_sm(a.D) * kWarpsPerCta;
+  L.tc = prefix_tc_fits(a);
+  p.mt = L.tc ? kTcBlock : kBlockRows;
+  p.tn = L.tc ? kTcTile : kTileTokens;
+  const int warps = sms * ctas_per_sm(a.D) * kWarpsPerCta;  // resident at once
+  p.workers = L.tc ? sms : warps;
   const int64_t items =
       a.Hkv * ((int64_t)a.R * p.gqa / p.mt + std::min<int64_t>(a.G, a.R));
   const int64_t tiles = ((int64_t)a.prefix_cols * a.page_size + p.tn - 1) / p.tn;
@@ -478,8 +481,9 @@ bool plan(const ssd_attention& a, AttnParams& p, Layout& L) {
   // warp one
   L.own_blocks = (p.gqa + kBlockRows - 1) / kBlockRows;
   const int64_t own = (int64_t)a.R * a.Hkv * L.own_blocks;
-  const int64_t most = a.lens ? ((int64_t)a.cols * a.page_size + p.tn - 1) / p.tn : 0;
-  p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(most, p.workers / own));
+  const int64_t most =
+      a.lens ? ((int64_t)a.cols * a.page_size + kTileTokens - 1) / kTileTokens : 0;
+  p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(most, warps / own));
   if (own * p.nsplit / kWarpsPerCta >= 0x7fffffff) return false;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -502,7 +506,10 @@ template <typename T, int D>
 cudaError_t launch(const AttnParams& p, const Layout& L, cudaStream_t s) {
   const int smem = kWarpsPerCta * kRing * step_bytes<D>();
   cudaError_t e;
-  if (p.a.G > 0) {
+  if (p.a.G > 0 && L.tc) {
+    e = launch_prefix_tc(p, s);
+    if (e != cudaSuccess) return e;
+  } else if (p.a.G > 0) {
     e = cudaFuncSetAttribute(prefix_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     prefix_kernel<T, D><<<p.workers / kWarpsPerCta, kWarpsPerCta * 32, smem, s>>>(p);

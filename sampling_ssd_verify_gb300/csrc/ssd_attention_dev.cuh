@@ -181,4 +181,10 @@ __device__ __forceinline__ bool next_stretch(const AttnParams& p, Walk& k, Stret
   return true;
 }
 
+// The tensor-core kernel (ssd_attention_tc.cu): blocks of kTcBlock pairs, tiles
+// of kTcTile tokens, one worker per SM.
+constexpr int kTcBlock = 128, kTcTile = 128;
+bool prefix_tc_fits(const ssd_attention& a);
+cudaError_t launch_prefix_tc(const AttnParams& p, cudaStream_t s);
+
 }  // namespace ssd
