@@ -99,10 +99,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// Where a stretch's partial goes: pair i of the block at o + i * o_step.
+// Where a stretch's partial goes: dimension d of pair i of the block at
+// o + i * o_step + (d / 4) * d_step + d % 4.
 struct Partial {
   float* o;
-  int64_t o_step;
+  int64_t o_step, d_step;
   float2* ml;
   int64_t ml_step;
 };
@@ -265,10 +266,11 @@ __device__ __forceinline__ void warp_stretch(const AttnParams& p, uint32_t ring,
     const int i = gid + 8 * r;
     if (pair0 + i >= npairs) continue;
     if (quad == 0) out.ml[i * out.ml_step] = make_float2(m[r], l[r]);
-    float* to = out.o + i * out.o_step + quad * 2;
+    float* to = out.o + i * out.o_step + (quad >> 1) * out.d_step + (quad & 1) * 2;
 #pragma unroll
     for (int n = 0; n < 2 * KK; ++n)
-      *reinterpret_cast<float2*>(to + n * 8) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
+      *reinterpret_cast<float2*>(to + 2 * n * out.d_step) =
+          make_float2(o[n][2 * r], o[n][2 * r + 1]);
   }
 }
 
@@ -292,8 +294,8 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32)
   Stretch s;
   while (next_stretch(p, k, s)) {
     if (s.slot >= p.nslots) break;  // cannot happen: the host sized the slots for every split
-    const Partial out{p.po + (int64_t)s.slot * kBlockRows * D, D, p.pml + (int64_t)s.slot * kBlockRows,
-                      1};
+    const Partial out{p.po + part_at<D>(s.slot, kBlockRows, 0, 0), 4, kBlockRows * 4,
+                      p.pml + (int64_t)s.slot * kBlockRows, 1};
     warp_stretch<T, D>(p, ring, s.q.row0, s.mb * kBlockRows, s.q.rows * p.gqa, s.h,
                        p.a.prefix_tables + (int64_t)s.g * p.a.prefix_table_stride,
                        s.tile0 * kTileTokens, min(s.q.len, s.tile1 * kTileTokens), out);
@@ -330,15 +332,24 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32)
     flag(p, SSD_DEV_BAD_LENGTH);
   if (t0 >= t1) return;  // the join does not look at it
   const int64_t at = ((int64_t)r * p.a.Hq + h * p.gqa + mb * kBlockRows) * p.nsplit + split;
-  const Partial out{p.so + at * D, (int64_t)p.nsplit * D, p.sml + at, p.nsplit};
+  const Partial out{p.so + at * D, (int64_t)p.nsplit * D, 4, p.sml + at, p.nsplit};
   warp_stretch<T, D>(p, smem_addr(s_ring) + warp * kRing * step_bytes<D>(), r, mb * kBlockRows,
                      p.gqa, h, p.a.tables + (int64_t)r * p.a.table_stride, t0, t1, out);
 }
 
 // ---- the join ------------------------------------------------------------------------
-// One warp per (row, head): the largest score of all its partials, then their
-// sums weighted by it.
+// One warp per (row, key/value head, up to four of its query heads): the row's
+// own tokens, or their partials, then the prefix's partials, then the output.
+//
+// Own tokens are few in the calls that this kernel is made for (a branch's
+// drafts), and such a task is a chain of loads: length, page, token beside
+// group, sums, partials.  It is bound by that latency, so it has few registers
+// and many warps: a token is spread over D / 8 lanes of 16 bytes, and the
+// products run on the ordinary units.  Long own caches go through own_kernel,
+// split over many warps.
 constexpr int kJoinWarps = 8;
+constexpr int kJoinHeads = 4;
+constexpr int kShortOwn = 64;  // tokens of an own cache up to which the join reads it
 
 // The group of row r: the last one that starts at or before it.
 __device__ __forceinline__ int group_of_row(const int32_t* off, int G, int r) {
@@ -354,80 +365,214 @@ __device__ __forceinline__ int group_of_row(const int32_t* off, int G, int r) {
   return lo;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t pair = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-  if (pair >= (int64_t)p.a.R * p.a.Hq) return;
-  const int r = (int)(pair / p.a.Hq), head = (int)(pair % p.a.Hq);
+// The prefix's partials of a pair: np of them, from `slot` on, at row `i`.
+struct Parts {
+  int np, slot, i;
+};
+__device__ __forceinline__ Parts parts_of(const AttnParams& p, const Group& q, int unit0,
+                                          int item0, int total, int r, int h, int head) {
+  Parts s{0, 0, 0};
+  if (r < q.row0 || r >= q.row0 + q.rows || q.tiles == 0 || total == 0) return s;
+  const int i = (r - q.row0) * p.gqa + head;
+  const int local = h * q.blocks + i / p.mt;
+  const int u = unit0 + local * q.tiles;
+  const int w0 = worker_of(p, u, total);
+  s.np = worker_of(p, u + q.tiles - 1, total) - w0 + 1;
+  s.slot = item0 + local + w0;
+  s.i = i % p.mt;
+  if (s.slot + s.np > p.nslots) s.np = 0;  // cannot happen: see the layout
+  return s;
+}
 
-  // partials [0, np) are the prefix's, the others the own tokens'
-  int np = 0, ns = 0;
-  int64_t slot0 = 0;
-  if (p.a.G > 0) {
-    const int g = group_of_row(p.a.group_off, p.a.G, r);
-    const Group q = group_of(p, g);
-    const int unit0 = p.unit_base[g], total = p.unit_base[p.a.G];
-    if (r >= q.row0 && r < q.row0 + q.rows && q.tiles > 0 && total > 0) {
-      const int i = (r - q.row0) * p.gqa + head % p.gqa;
-      const int local = head / p.gqa * q.blocks + i / p.mt;
-      const int u = unit0 + local * q.tiles;
-      const int w0 = worker_of(p, u, total);
-      np = worker_of(p, u + q.tiles - 1, total) - w0 + 1;
-      slot0 = ((int64_t)p.item_base[g] + local + w0) * p.mt + i % p.mt;
-      if (slot0 + (int64_t)(np - 1) * p.mt >= (int64_t)p.nslots * p.mt) np = 0;
-    }
+template <typename T>
+__device__ __forceinline__ void widen(float (&f)[8], const uint4& x) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 y;
+    if constexpr (__is_same(T, __half))
+      y = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    else
+      y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+    f[2 * i] = y.x;
+    f[2 * i + 1] = y.y;
   }
+}
+
+// Weighted sums of one more stretch: o, l at maximum m take x, its weight and
+// maximum in ml.
+__device__ __forceinline__ void add_part(float (&o)[8], float& m, float& l, float2 ml,
+                                         const float4& x0, const float4& x1) {
+  const float m1 = fmaxf(m, ml.x), off = m1 == -INFINITY ? 0.f : m1;
+  const float a = exp2_fast(m - off), b = exp2_fast(ml.x - off);
+  m = m1;
+  l = l * a + ml.y * b;
+  const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] = o[e] * a + x[e] * b;
+}
+
+template <typename T, int D, bool SHORT_OWN>
+__global__ void __launch_bounds__(kJoinWarps * 32, SHORT_OWN ? 2 : 3)
+    join_kernel(const __grid_constant__ AttnParams p, int head_blocks) {
+  constexpr int LT = D / 8;          // lanes of a token
+  constexpr int TS = 32 / LT;        // tokens at a time
+  constexpr int HS = kJoinHeads / TS;  // heads that a lane's share finishes
+  static_assert(HS * TS == kJoinHeads, "heads are dealt to the tokens' lanes");
+  const int lane = threadIdx.x & 31, sub = lane / LT, d0 = lane % LT * 8;
+  int64_t task = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  if (task >= (int64_t)p.a.R * p.a.Hkv * head_blocks) return;
+  const int hb = (int)(task % head_blocks) * kJoinHeads;
+  task /= head_blocks;
+  const int h = (int)(task % p.a.Hkv), r = (int)(task / p.a.Hkv);
+  const int heads = min(kJoinHeads, p.gqa - hb);
+  const ssd_attention& a = p.a;
+
   const int len = own_len(p, r);
-  if (len > 0) ns = (len + own_stretch(p, len) - 1) / own_stretch(p, len);
+  Group q{};
+  int unit0 = 0, item0 = 0, total = 0;
+  if (a.G > 0) {
+    const int g = group_of_row(a.group_off, a.G, r);
+    q = group_of(p, g);
+    unit0 = p.unit_base[g];
+    item0 = p.item_base[g];
+    total = p.unit_base[a.G];
+  }
 
-  auto ml_of = [&](int i) {
-    return i < np ? p.pml[slot0 + (int64_t)i * p.mt] : p.sml[pair * p.nsplit + (i - np)];
-  };
-  float m = -INFINITY;
-  for (int i = lane; i < np + ns; i += 32) m = fmaxf(m, ml_of(i).x);
+  float o[kJoinHeads][8] = {};
+  float m[kJoinHeads], l[kJoinHeads];
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  const float off = m == -INFINITY ? 0.f : m;
-
-  float acc[E] = {};
-  float l = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < np + ns; ++i) {
-    const float2 ml = ml_of(i);
-    const float wgt = exp2_fast(ml.x - off);
-    l += ml.y * wgt;
-    const float* o = (i < np ? p.po + (slot0 + (int64_t)i * p.mt) * D
-                             : p.so + (pair * p.nsplit + (i - np)) * D) + lane * E;
-    float x[E];
-    if constexpr (E == 2) {
-      *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(o);
-    } else {
+  for (int i = 0; i < kJoinHeads; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+  }
+  if (SHORT_OWN && a.lens && h == 0 && hb == 0 && lane == 0 && len != a.lens[r])
+    flag(p, SSD_DEV_BAD_LENGTH);
+  if (SHORT_OWN && len > 0) {
+    uint4 qx[kJoinHeads];
 #pragma unroll
-      for (int k = 0; k < E; k += 4)
-        *reinterpret_cast<float4*>(x + k) = *reinterpret_cast<const float4*>(o + k);
+    for (int i = 0; i < kJoinHeads; ++i)
+      qx[i] = i < heads ? *reinterpret_cast<const uint4*>(
+                              static_cast<const T*>(a.q) + (int64_t)r * a.q_row_stride +
+                              (int64_t)(h * p.gqa + hb + i) * a.q_head_stride + d0)
+                        : make_uint4(0u, 0u, 0u, 0u);
+    const int32_t* table = a.tables + (int64_t)r * a.table_stride;
+    for (int t0 = 0; t0 < len; t0 += 2 * TS) {
+      uint4 kx[2], vx[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int t = t0 + j * TS + sub;
+        kx[j] = vx[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (t < len) {
+          const int page = table[t / a.page_size];
+          if ((unsigned)page < (unsigned)a.num_pages) {
+            const int in_page = t % a.page_size;
+            kx[j] = *reinterpret_cast<const uint4*>(
+                static_cast<const T*>(a.k.ptr) + (int64_t)page * a.k.page_stride +
+                (int64_t)in_page * a.k.token_stride + (int64_t)h * a.k.head_stride + d0);
+            vx[j] = *reinterpret_cast<const uint4*>(
+                static_cast<const T*>(a.v.ptr) + (int64_t)page * a.v.page_stride +
+                (int64_t)in_page * a.v.token_stride + (int64_t)h * a.v.head_stride + d0);
+          } else {
+            flag(p, SSD_DEV_BAD_PAGE);
+          }
+        }
+      }
+      float sc[2][kJoinHeads];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float kf[8];
+        widen<T>(kf, kx[j]);
+#pragma unroll
+        for (int i = 0; i < kJoinHeads; ++i) {
+          float qf[8], x = 0.f;
+          widen<T>(qf, qx[i]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x = fmaf(qf[e], kf[e], x);
+#pragma unroll
+          for (int d = LT / 2; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+          sc[j][i] = t0 + j * TS + sub < len ? x * p.scale_log2 : -INFINITY;
+        }
+      }
+      float vf[2][8];
+      widen<T>(vf[0], vx[0]);
+      widen<T>(vf[1], vx[1]);
+#pragma unroll
+      for (int i = 0; i < kJoinHeads; ++i) {
+        float top = fmaxf(sc[0][i], sc[1][i]);
+#pragma unroll
+        for (int d = LT; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float m1 = fmaxf(m[i], top), off = m1 == -INFINITY ? 0.f : m1;
+        const float keep = exp2_fast(m[i] - off);
+        const float w0 = exp2_fast(sc[0][i] - off), w1 = exp2_fast(sc[1][i] - off);
+        m[i] = m1;
+        l[i] = l[i] * keep + w0 + w1;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          o[i][e] = fmaf(w1, vf[1][e], fmaf(w0, vf[0][e], o[i][e] * keep));
+      }
     }
 #pragma unroll
-    for (int k = 0; k < E; ++k) acc[k] += x[k] * wgt;
-  }
-  // no token at all: zeros and -inf
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  T* to = static_cast<T*>(p.a.out) + (int64_t)r * p.a.out_row_stride +
-          (int64_t)head * p.a.out_head_stride + lane * E;
-  uint32_t y[E / 2];
+    for (int i = 0; i < kJoinHeads; ++i)
 #pragma unroll
-  for (int k = 0; k < E / 2; ++k) y[k] = pack2<T>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-  if constexpr (E == 2) *reinterpret_cast<uint32_t*>(to) = y[0];
-  if constexpr (E == 4) *reinterpret_cast<uint2*>(to) = make_uint2(y[0], y[1]);
-  if constexpr (E == 8) *reinterpret_cast<uint4*>(to) = make_uint4(y[0], y[1], y[2], y[3]);
-  if (lane == 0 && p.a.lse)
-    p.a.lse[pair] = np + ns > 0 ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      for (int d = LT; d < 32; d <<= 1) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[i][e] += __shfl_xor_sync(0xffffffffu, o[i][e], d);
+      }
+  }
+
+  // each token's lanes finish heads sub, sub + TS, ..
+#pragma unroll
+  for (int k = 0; k < HS; ++k) {
+    const int i = k * TS + sub;
+    float y[8], my = m[k * TS], ly = l[k * TS];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = o[k * TS][e];
+#pragma unroll
+    for (int z = 1; z < TS; ++z)
+      if (sub == z) {
+        my = m[k * TS + z];
+        ly = l[k * TS + z];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = o[k * TS + z][e];
+      }
+    if (i >= heads) continue;
+    const int head = h * p.gqa + hb + i;
+    const int64_t pair = (int64_t)r * a.Hq + head;
+    if (!SHORT_OWN && len > 0) {
+      const int ns = (len + own_stretch(p, len) - 1) / own_stretch(p, len);
+      for (int j = 0; j < ns; ++j) {
+        const int64_t at = pair * p.nsplit + j;
+        const float4* x = reinterpret_cast<const float4*>(p.so + at * D + d0);
+        add_part(y, my, ly, p.sml[at], x[0], x[1]);
+      }
+    }
+    const Parts s = parts_of(p, q, unit0, item0, total, r, h, hb + i);
+#pragma unroll 2
+    for (int j = 0; j < s.np; ++j) {
+      const float2 ml = p.pml[(int64_t)(s.slot + j) * p.mt + s.i];
+      const float* x = p.po + part_at<D>(s.slot + j, p.mt, s.i, d0);
+      add_part(y, my, ly, ml, *reinterpret_cast<const float4*>(x),
+               *reinterpret_cast<const float4*>(x + 4 * p.mt));
+    }
+    // no token at all: zeros and -inf
+    const float inv = ly == 0.f ? 0.f : 1.f / ly;
+    uint4 out;
+    out.x = pack2<T>(y[0] * inv, y[1] * inv);
+    out.y = pack2<T>(y[2] * inv, y[3] * inv);
+    out.z = pack2<T>(y[4] * inv, y[5] * inv);
+    out.w = pack2<T>(y[6] * inv, y[7] * inv);
+    *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (int64_t)r * a.out_row_stride +
+                              (int64_t)head * a.out_head_stride + d0) = out;
+    if (d0 == 0 && a.lse) a.lse[pair] = (my + log2f(ly)) * 0.6931471805599453f;
+  }
 }
 
 // ---- set-up ---------------------------------------------------------------------------
 struct Layout {
   bool tc;                  // the prefixes' kernel is the tensor-core one
+  bool short_own;           // the join reads own tokens itself
   int own_blocks;
   size_t po, pml, unit, item, so, sml, total;
 };
@@ -477,13 +622,14 @@ bool plan(const ssd_attention& a, AttnParams& p, Layout& L) {
   const int64_t tiles = ((int64_t)a.prefix_cols * a.page_size + p.tn - 1) / p.tn;
   if (items * std::max<int64_t>(tiles, 1) > 0x7fffffff) return false;
   p.nslots = a.G > 0 ? (int)(items + p.workers) : 0;
-  // own tokens: stretches of at least a tile, as many as give each resident
-  // warp one
+  // own tokens: read by the join where they are few; else in stretches of two
+  // tiles or more, four for each resident warp, which evens out their lengths
+  const int64_t most = a.lens ? (int64_t)a.cols * a.page_size : 0;
+  L.short_own = most <= kShortOwn;
   L.own_blocks = (p.gqa + kBlockRows - 1) / kBlockRows;
   const int64_t own = (int64_t)a.R * a.Hkv * L.own_blocks;
-  const int64_t most =
-      a.lens ? ((int64_t)a.cols * a.page_size + kTileTokens - 1) / kTileTokens : 0;
-  p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(most, warps / own));
+  p.nsplit = (int)std::max<int64_t>(
+      1, std::min<int64_t>((most + 2 * kTileTokens - 1) / (2 * kTileTokens), 4 * warps / own));
   if (own * p.nsplit / kWarpsPerCta >= 0x7fffffff) return false;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -495,7 +641,7 @@ bool plan(const ssd_attention& a, AttnParams& p, Layout& L) {
   L.pml = take((size_t)p.nslots * p.mt * 8);
   L.unit = take((size_t)(a.G + 1) * 4);
   L.item = take((size_t)(a.G + 1) * 4);
-  const size_t rows = a.lens ? (size_t)a.R * a.Hq * p.nsplit : 0;
+  const size_t rows = L.short_own ? 0 : (size_t)a.R * a.Hq * p.nsplit;
   L.so = take(rows * a.D * 4);
   L.sml = take(rows * 8);
   L.total = std::max<size_t>(at, 256);
@@ -516,7 +662,7 @@ cudaError_t launch(const AttnParams& p, const Layout& L, cudaStream_t s) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  if (p.a.lens && p.a.cols > 0) {
+  if (!L.short_own) {
     e = cudaFuncSetAttribute(own_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int64_t tasks = (int64_t)p.a.R * p.a.Hkv * L.own_blocks * p.nsplit;
@@ -525,8 +671,13 @@ cudaError_t launch(const AttnParams& p, const Layout& L, cudaStream_t s) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  const int64_t pairs = (int64_t)p.a.R * p.a.Hq;
-  join_kernel<T, D><<<(unsigned)((pairs + kJoinWarps - 1) / kJoinWarps), kJoinWarps * 32, 0, s>>>(p);
+  const int head_blocks = (p.gqa + kJoinHeads - 1) / kJoinHeads;
+  const int64_t tasks = (int64_t)p.a.R * p.a.Hkv * head_blocks;
+  const unsigned grid = (unsigned)((tasks + kJoinWarps - 1) / kJoinWarps);
+  if (L.short_own)
+    join_kernel<T, D, true><<<grid, kJoinWarps * 32, 0, s>>>(p, head_blocks);
+  else
+    join_kernel<T, D, false><<<grid, kJoinWarps * 32, 0, s>>>(p, head_blocks);
   return cudaGetLastError();
 }
 

@@ -32,7 +32,7 @@ struct AttnParams {
   int mt, tn;             // rows of a block, tokens of a tile
   int workers;
   int nslots;
-  float* po;              // [nslots, mt, D] unnormalised sums
+  float* po;              // [nslots, D / 4, mt, 4] unnormalised sums (part_at)
   float2* pml;            // [nslots, mt] largest score (base 2), weight
   int* unit_base;         // [G + 1] tiles of all items before group g
   int* item_base;         // [G + 1] items before group g
@@ -42,6 +42,15 @@ struct AttnParams {
   float2* sml;            // [R, Hq, nsplit]
   int32_t* status;
 };
+
+// Place of dimension d (a multiple of 4, or within one) of row i of a prefix's
+// partial: the rows of four dimensions stand together, so that a kernel with a
+// row per thread writes whole lines, and the rows of a key/value head's query
+// heads are read as one piece.
+template <int D>
+__device__ __forceinline__ int64_t part_at(int slot, int mt, int i, int d) {
+  return (((int64_t)slot * (D / 4) + d / 4) * mt + i) * 4 + d % 4;
+}
 
 __device__ __forceinline__ void flag(const AttnParams& p, int bit) {
   if (p.status) atomicOr(p.status, bit);

@@ -35,8 +35,8 @@ namespace {
 constexpr int kBlock = kTcBlock;  // pairs of a block (M)
 constexpr int kTile = kTcTile;    // tokens of a tile
 constexpr int kSoftmax = 256;     // threads of the two warpgroups
-constexpr int kThreads = kSoftmax + 128;  // a third warpgroup: copies, products, two idle warps
-constexpr int kCopyWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = kSoftmax + 128;  // a third warpgroup: copies, products, hints
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kHintWarp = 10;
 // Registers per thread: launched with 168 (12 warps), of which the third
 // warpgroup gives up 80 and the others take 40 each: 8 * 208 + 4 * 88 = 12 * 168.
 constexpr int kRegsSoftmax = 208, kRegsOther = 88;
@@ -169,6 +169,13 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) 
   return *reinterpret_cast<const uint32_t*>(&x);
 }
 
+// Ring positions of K and V of tile j of a stretch of n tiles, counted from the
+// stretch's first: in the order in which the products take them (K0, K1, V0, K2,
+// V1, ..), so that slots fall free in order and the copies in flight are the
+// next ones needed.
+__device__ __forceinline__ uint32_t at_k(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ uint32_t at_v(int j, int n) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
+
 struct Bars {
   uint64_t full[12], empty[12];   // ring slots
   uint64_t q_full;                // queries of a stretch are in place, its sums' columns free
@@ -252,30 +259,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return page;
         };
-        int page = page_at(s.tile0);
-        for (int tile = s.tile0; tile < s.tile1; ++tile) {
-          const int next = page_at(tile + 1);
+        // one K or V tile: wait for its slot, announce its bytes, copy its boxes
+        auto load = [&](const CUtensorMap* map, int tile, int page) {
           const int here = min(kTile, s.q.len - tile * kTile);
           const int n = (here + rows - 1) / rows;  // boxes with tokens
-          const int in_page = (tile * kTile) % P * (boxes == 1);
-  #pragma unroll
-          for (int kv = 0; kv < 2; ++kv, ++c) {
-            const int slot = c % S::kSlots;
-            const uint32_t use = c / S::kSlots;
-            if (use > 0) mbar_wait(&bars.empty[slot], (use - 1) & 1, &s_err, p.status);
-            if (lane == 0)
-              mbar_arrive_expect_tx(&bars.full[slot], (uint32_t)(n * rows * 128 * S::kPanels));
-            __syncwarp();
-            if (lane < n) {
-              const uint32_t dst = ring + slot * S::kSlot + lane * rows * 128;
-  #pragma unroll
-              for (int d = 0; d < S::kPanels; ++d)
-                tma_box(dst + d * kPanel, kv ? &vmap : &kmap, d * 64, s.h, in_page, page,
-                        &bars.full[slot]);
-            }
+          const int in_page = boxes == 1 ? tile * kTile % P : 0;
+          const int slot = c % S::kSlots;
+          const uint32_t use = c / S::kSlots;
+          ++c;
+          if (use > 0) mbar_wait(&bars.empty[slot], (use - 1) & 1, &s_err, p.status);
+          if (lane == 0)
+            mbar_arrive_expect_tx(&bars.full[slot], (uint32_t)(n * rows * 128 * S::kPanels));
+          __syncwarp();
+          if (lane < n) {
+            const uint32_t dst = ring + slot * S::kSlot + lane * rows * 128;
+#pragma unroll
+            for (int d = 0; d < S::kPanels; ++d)
+              tma_box(dst + d * kPanel, map, d * 64, s.h, in_page, page, &bars.full[slot]);
           }
+        };
+        // pages are looked up one tile ahead of their copies
+        int page = page_at(s.tile0), last = -1;
+        for (int tile = s.tile0; tile < s.tile1; ++tile) {
+          const int next = page_at(tile + 1);
+          load(&kmap, tile, page);
+          if (tile > s.tile0) load(&vmap, tile - 1, last);
+          last = page;
           page = next;
         }
+        load(&vmap, s.tile1 - 1, last);
       }
       if (s_err) {  // let the copies in flight land before the memory is given up
         for (uint32_t i = c > S::kSlots ? c - S::kSlots : 0; i < c; ++i) {
@@ -294,12 +306,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_after();
           for (int j = 0; j <= n; ++j) {
             if (j < n) {
-              const uint32_t at = c + 2 * j;
+              const uint32_t at = c + at_k(j);
               const int slot = at % S::kSlots;
               mbar_wait(&bars.full[slot], (at / S::kSlots) & 1, &s_err, p.status);
               fence_after();
               const uint32_t ks = ring + slot * S::kSlot;
-  #pragma unroll
+#pragma unroll
               for (int i = 0; i < D / 16; ++i) {
                 const uint32_t off = (i / 4) * kPanel + (i % 4) * 32;
                 mma_ss(tmem + kColS + (j & 1) * kColStep, operand(qs + off, 16),
@@ -310,13 +322,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (j > 0) {
               const int b = (j - 1) & 1;
-              const uint32_t at = c + 2 * (j - 1) + 1;
+              const uint32_t at = c + at_v(j - 1, n);
               const int slot = at % S::kSlots;
               mbar_wait(&bars.p_full[b], done[b]++ & 1, &s_err, p.status);
               mbar_wait(&bars.full[slot], (at / S::kSlots) & 1, &s_err, p.status);
               fence_after();
               const uint32_t vs = ring + slot * S::kSlot;
-  #pragma unroll
+#pragma unroll
               for (int i = 0; i < kTile / 16; ++i)
                 mma_ts(tmem + kColO + b * kColStep, tmem + kColS + b * kColStep + i * 8,
                        operand(vs + i * 16 * 128, kPanel), sum, j > 2 || i > 0);
@@ -329,6 +341,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit(&bars.drained);
         int none = 0;
         mbar_wait(&bars.drained, 0, &none, p.status);
+      }
+    } else if (warp == kHintWarp) {
+      // ---- queries of all stretches into L2, so that a stretch starts without a
+      // trip to memory (stretches are few: this runs far ahead) -----------------------
+      while (next_stretch(p, k, s)) {
+        const int n = min(kBlock, s.q.rows * p.gqa - s.mb * kBlock);
+        for (int i = lane; i < n; i += 32) {
+          const int pair = s.mb * kBlock + i;
+          const char* q = reinterpret_cast<const char*>(
+              static_cast<const T*>(p.a.q) +
+              (int64_t)(s.q.row0 + pair / p.gqa) * p.a.q_row_stride +
+              (int64_t)(s.h * p.gqa + pair % p.gqa) * p.a.q_head_stride);
+#pragma unroll
+          for (int d = 0; d < D * 2; d += 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(q + d));
+        }
       }
     }
   } else {
@@ -431,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (here < kTile) {
           // rows of V past the last token: whatever the page or the slot held
           // must not meet the zero weights (0 * NaN)
-          const uint32_t at = c + 2 * j + 1;
+          const uint32_t at = c + at_v(j, n);
           const int slot = at % S::kSlots;
           mbar_wait(&bars.full[slot], (at / S::kSlots) & 1, &s_err, p.status);
           const uint32_t vs = ring + slot * S::kSlot;
@@ -463,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool mine = pair0 + m < npairs && s.slot < p.nslots;
       const int64_t row = (int64_t)s.slot * kBlock + m;
       if (mine && b == 0) p.pml[row] = make_float2(mx, m0.y * f0 + m1.y * f1);
-      float* out = p.po + row * D + b * (D / 2);
+      float* out = p.po + part_at<D>(s.slot, kBlock, m, b * (D / 2));
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
         uint32_t y0[32], y1[32];
@@ -479,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (mine) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<uint4*>(out + i * 32 + e) =
+            *reinterpret_cast<uint4*>(out + (i * 32 + e) * kBlock) =
                 make_uint4(y0[e], y0[e + 1], y0[e + 2], y0[e + 3]);
         }
       }
