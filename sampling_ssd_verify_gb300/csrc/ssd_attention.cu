@@ -31,19 +31,6 @@ template <int D>
 __host__ __device__ constexpr int step_bytes() { return 2 * kStep * D * 2; }  // K and V
 
 template <typename T>
-__device__ __forceinline__ uint32_t pack2(float a, float b);
-template <>
-__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
-  const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&x);
-}
-template <>
-__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
-  const __half2 x = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&x);
-}
-
-template <typename T>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1);
 template <>
@@ -79,26 +66,6 @@ __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
                  : "memory");
 }
 
-// 16 bytes global -> shared; zeros when !ok (src is then not read).
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(ok ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void copies_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Where a stretch's partial goes: dimension d of pair i of the block at
 // o + i * o_step + (d / 4) * d_step + d % 4.
 struct Partial {
@@ -125,12 +92,15 @@ __device__ __forceinline__ void warp_stretch(const AttnParams& p, uint32_t ring,
     const T* q0 = nullptr;
     const T* q1 = nullptr;
     const int i0 = pair0 + gid, i1 = i0 + 8;
+    auto query = [&](int i) {
+      const int r = p.by_gqa.quotient(i);
+      return static_cast<const T*>(a.q) + (int64_t)(row0 + r) * a.q_row_stride +
+             (int64_t)(h * p.gqa + i - r * p.gqa) * a.q_head_stride;
+    };
     if (i0 < npairs)
-      q0 = static_cast<const T*>(a.q) + (int64_t)(row0 + i0 / p.gqa) * a.q_row_stride +
-           (int64_t)(h * p.gqa + i0 % p.gqa) * a.q_head_stride;
+      q0 = query(i0);
     if (i1 < npairs)
-      q1 = static_cast<const T*>(a.q) + (int64_t)(row0 + i1 / p.gqa) * a.q_row_stride +
-           (int64_t)(h * p.gqa + i1 % p.gqa) * a.q_head_stride;
+      q1 = query(i1);
 #pragma unroll
     for (int k = 0; k < KK; ++k) {
       const int c = k * 16 + quad * 2;
@@ -153,7 +123,7 @@ __device__ __forceinline__ void warp_stretch(const AttnParams& p, uint32_t ring,
   // before its copies are issued
   auto page_of = [&](int step) {
     const int t = t0 + step * kStep + (lane & 15);
-    return t < t1 ? table[t / a.page_size] : -1;
+    return t < t1 ? table[p.by_page.quotient(t)] : -1;
   };
   auto issue = [&](int step, int page) {
     const int t = t0 + step * kStep + (lane & 15);
@@ -162,7 +132,7 @@ __device__ __forceinline__ void warp_stretch(const AttnParams& p, uint32_t ring,
       ok = false;
       flag(p, SSD_DEV_BAD_PAGE);
     }
-    const int in_page = ok ? t % a.page_size : 0;
+    const int in_page = ok ? t - p.by_page.quotient(t) * a.page_size : 0;
     const int64_t pg = ok ? page : 0;
     // a token that is not there: a negative offset, no read
     const int64_t ko = ok ? pg * a.k.page_stride + in_page * a.k.token_stride : -1;
@@ -294,6 +264,7 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32)
   Stretch s;
   while (next_stretch(p, k, s)) {
     if (s.slot >= p.nslots) break;  // cannot happen: the host sized the slots for every split
+    if ((threadIdx.x & 31) == 0) leave_worker(p, s, w);
     const Partial out{p.po + part_at<D>(s.slot, kBlockRows, 0, 0), 4, kBlockRows * 4,
                       p.pml + (int64_t)s.slot * kBlockRows, 1};
     warp_stretch<T, D>(p, ring, s.q.row0, s.mb * kBlockRows, s.q.rows * p.gqa, s.h,
@@ -369,18 +340,16 @@ __device__ __forceinline__ int group_of_row(const int32_t* off, int G, int r) {
 struct Parts {
   int np, slot, i;
 };
-__device__ __forceinline__ Parts parts_of(const AttnParams& p, const Group& q, int unit0,
-                                          int item0, int total, int r, int h, int head) {
+__device__ __forceinline__ Parts parts_of(const AttnParams& p, const Group& q, int item0, int r,
+                                          int h, int head) {
   Parts s{0, 0, 0};
-  if (r < q.row0 || r >= q.row0 + q.rows || q.tiles == 0 || total == 0) return s;
-  const int i = (r - q.row0) * p.gqa + head;
-  const int local = h * q.blocks + i / p.mt;
-  const int u = unit0 + local * q.tiles;
-  const int w0 = worker_of(p, u, total);
-  s.np = worker_of(p, u + q.tiles - 1, total) - w0 + 1;
-  s.slot = item0 + local + w0;
-  s.i = i % p.mt;
-  if (s.slot + s.np > p.nslots) s.np = 0;  // cannot happen: see the layout
+  if (r < q.row0 || r >= q.row0 + q.rows || q.tiles == 0 || item0 < 0) return s;
+  const int i = (r - q.row0) * p.gqa + head, mb = p.mt == kTcBlock ? i / kTcBlock : i / kBlockRows;
+  const int item = item0 + h * q.blocks + mb;
+  const int2 w = p.item_workers[item];
+  s.np = w.y - w.x + 1;
+  s.slot = item + w.x;
+  s.i = i - mb * p.mt;
   return s;
 }
 
@@ -420,152 +389,150 @@ __global__ void __launch_bounds__(kJoinWarps * 32, SHORT_OWN ? 2 : 3)
   constexpr int HS = kJoinHeads / TS;  // heads that a lane's share finishes
   static_assert(HS * TS == kJoinHeads, "heads are dealt to the tokens' lanes");
   const int lane = threadIdx.x & 31, sub = lane / LT, d0 = lane % LT * 8;
-  int64_t task = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-  if (task >= (int64_t)p.a.R * p.a.Hkv * head_blocks) return;
-  const int hb = (int)(task % head_blocks) * kJoinHeads;
-  task /= head_blocks;
-  const int h = (int)(task % p.a.Hkv), r = (int)(task / p.a.Hkv);
-  const int heads = min(kJoinHeads, p.gqa - hb);
+  // a CTA per row: its warps meet the same lengths, tables and sums
+  const int r = blockIdx.x;
   const ssd_attention& a = p.a;
-
   const int len = own_len(p, r);
   Group q{};
-  int unit0 = 0, item0 = 0, total = 0;
+  int item0 = -1;
   if (a.G > 0) {
     const int g = group_of_row(a.group_off, a.G, r);
     q = group_of(p, g);
-    unit0 = p.unit_base[g];
     item0 = p.item_base[g];
-    total = p.unit_base[a.G];
   }
+  for (int task = threadIdx.x >> 5; task < a.Hkv * head_blocks; task += blockDim.x >> 5) {
+    const int h = head_blocks == 1 ? task : task / head_blocks;
+    const int hb = (task - h * head_blocks) * kJoinHeads;
+    const int heads = min(kJoinHeads, p.gqa - hb);
 
-  float o[kJoinHeads][8] = {};
-  float m[kJoinHeads], l[kJoinHeads];
+    float o[kJoinHeads][8] = {};
+    float m[kJoinHeads], l[kJoinHeads];
 #pragma unroll
-  for (int i = 0; i < kJoinHeads; ++i) {
-    m[i] = -INFINITY;
-    l[i] = 0.f;
-  }
-  if (SHORT_OWN && a.lens && h == 0 && hb == 0 && lane == 0 && len != a.lens[r])
-    flag(p, SSD_DEV_BAD_LENGTH);
-  if (SHORT_OWN && len > 0) {
-    uint4 qx[kJoinHeads];
+    for (int i = 0; i < kJoinHeads; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+    }
+    if (SHORT_OWN && a.lens && h == 0 && hb == 0 && lane == 0 && len != a.lens[r])
+      flag(p, SSD_DEV_BAD_LENGTH);
+    if (SHORT_OWN && len > 0) {
+      uint4 qx[kJoinHeads];
 #pragma unroll
-    for (int i = 0; i < kJoinHeads; ++i)
-      qx[i] = i < heads ? *reinterpret_cast<const uint4*>(
-                              static_cast<const T*>(a.q) + (int64_t)r * a.q_row_stride +
-                              (int64_t)(h * p.gqa + hb + i) * a.q_head_stride + d0)
-                        : make_uint4(0u, 0u, 0u, 0u);
-    const int32_t* table = a.tables + (int64_t)r * a.table_stride;
-    for (int t0 = 0; t0 < len; t0 += 2 * TS) {
-      uint4 kx[2], vx[2];
+      for (int i = 0; i < kJoinHeads; ++i)
+        qx[i] = i < heads ? *reinterpret_cast<const uint4*>(
+                                static_cast<const T*>(a.q) + (int64_t)r * a.q_row_stride +
+                                (int64_t)(h * p.gqa + hb + i) * a.q_head_stride + d0)
+                          : make_uint4(0u, 0u, 0u, 0u);
+      const int32_t* table = a.tables + (int64_t)r * a.table_stride;
+      for (int t0 = 0; t0 < len; t0 += 2 * TS) {
+        uint4 kx[2], vx[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int t = t0 + j * TS + sub;
-        kx[j] = vx[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (t < len) {
-          const int page = table[t / a.page_size];
-          if ((unsigned)page < (unsigned)a.num_pages) {
-            const int in_page = t % a.page_size;
-            kx[j] = *reinterpret_cast<const uint4*>(
-                static_cast<const T*>(a.k.ptr) + (int64_t)page * a.k.page_stride +
-                (int64_t)in_page * a.k.token_stride + (int64_t)h * a.k.head_stride + d0);
-            vx[j] = *reinterpret_cast<const uint4*>(
-                static_cast<const T*>(a.v.ptr) + (int64_t)page * a.v.page_stride +
-                (int64_t)in_page * a.v.token_stride + (int64_t)h * a.v.head_stride + d0);
-          } else {
-            flag(p, SSD_DEV_BAD_PAGE);
+        for (int j = 0; j < 2; ++j) {
+          const int t = t0 + j * TS + sub;
+          kx[j] = vx[j] = make_uint4(0u, 0u, 0u, 0u);
+          if (t < len) {
+            const int col = p.by_page.quotient(t), page = table[col];
+            if ((unsigned)page < (unsigned)a.num_pages) {
+              const int in_page = t - col * a.page_size;
+              kx[j] = *reinterpret_cast<const uint4*>(
+                  static_cast<const T*>(a.k.ptr) + (int64_t)page * a.k.page_stride +
+                  (int64_t)in_page * a.k.token_stride + (int64_t)h * a.k.head_stride + d0);
+              vx[j] = *reinterpret_cast<const uint4*>(
+                  static_cast<const T*>(a.v.ptr) + (int64_t)page * a.v.page_stride +
+                  (int64_t)in_page * a.v.token_stride + (int64_t)h * a.v.head_stride + d0);
+            } else {
+              flag(p, SSD_DEV_BAD_PAGE);
+            }
           }
         }
-      }
-      float sc[2][kJoinHeads];
+        float sc[2][kJoinHeads];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float kf[8];
-        widen<T>(kf, kx[j]);
+        for (int j = 0; j < 2; ++j) {
+          float kf[8];
+          widen<T>(kf, kx[j]);
+#pragma unroll
+          for (int i = 0; i < kJoinHeads; ++i) {
+            float qf[8], x = 0.f;
+            widen<T>(qf, qx[i]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x = fmaf(qf[e], kf[e], x);
+#pragma unroll
+            for (int d = LT / 2; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+            sc[j][i] = t0 + j * TS + sub < len ? x * p.scale_log2 : -INFINITY;
+          }
+        }
+        float vf[2][8];
+        widen<T>(vf[0], vx[0]);
+        widen<T>(vf[1], vx[1]);
 #pragma unroll
         for (int i = 0; i < kJoinHeads; ++i) {
-          float qf[8], x = 0.f;
-          widen<T>(qf, qx[i]);
+          float top = fmaxf(sc[0][i], sc[1][i]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x = fmaf(qf[e], kf[e], x);
+          for (int d = LT; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+          const float m1 = fmaxf(m[i], top), off = m1 == -INFINITY ? 0.f : m1;
+          const float keep = exp2_fast(m[i] - off);
+          const float w0 = exp2_fast(sc[0][i] - off), w1 = exp2_fast(sc[1][i] - off);
+          m[i] = m1;
+          l[i] = l[i] * keep + w0 + w1;
 #pragma unroll
-          for (int d = LT / 2; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-          sc[j][i] = t0 + j * TS + sub < len ? x * p.scale_log2 : -INFINITY;
+          for (int e = 0; e < 8; ++e)
+            o[i][e] = fmaf(w1, vf[1][e], fmaf(w0, vf[0][e], o[i][e] * keep));
         }
       }
-      float vf[2][8];
-      widen<T>(vf[0], vx[0]);
-      widen<T>(vf[1], vx[1]);
 #pragma unroll
-      for (int i = 0; i < kJoinHeads; ++i) {
-        float top = fmaxf(sc[0][i], sc[1][i]);
+      for (int i = 0; i < kJoinHeads; ++i)
 #pragma unroll
-        for (int d = LT; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const float m1 = fmaxf(m[i], top), off = m1 == -INFINITY ? 0.f : m1;
-        const float keep = exp2_fast(m[i] - off);
-        const float w0 = exp2_fast(sc[0][i] - off), w1 = exp2_fast(sc[1][i] - off);
-        m[i] = m1;
-        l[i] = l[i] * keep + w0 + w1;
+        for (int d = LT; d < 32; d <<= 1) {
+          l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          o[i][e] = fmaf(w1, vf[1][e], fmaf(w0, vf[0][e], o[i][e] * keep));
-      }
+          for (int e = 0; e < 8; ++e) o[i][e] += __shfl_xor_sync(0xffffffffu, o[i][e], d);
+        }
     }
-#pragma unroll
-    for (int i = 0; i < kJoinHeads; ++i)
-#pragma unroll
-      for (int d = LT; d < 32; d <<= 1) {
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[i][e] += __shfl_xor_sync(0xffffffffu, o[i][e], d);
-      }
-  }
 
-  // each token's lanes finish heads sub, sub + TS, ..
+    // each token's lanes finish heads sub, sub + TS, ..
 #pragma unroll
-  for (int k = 0; k < HS; ++k) {
-    const int i = k * TS + sub;
-    float y[8], my = m[k * TS], ly = l[k * TS];
+    for (int k = 0; k < HS; ++k) {
+      const int i = k * TS + sub;
+      float y[8], my = m[k * TS], ly = l[k * TS];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = o[k * TS][e];
+      for (int e = 0; e < 8; ++e) y[e] = o[k * TS][e];
 #pragma unroll
-    for (int z = 1; z < TS; ++z)
-      if (sub == z) {
-        my = m[k * TS + z];
-        ly = l[k * TS + z];
+      for (int z = 1; z < TS; ++z)
+        if (sub == z) {
+          my = m[k * TS + z];
+          ly = l[k * TS + z];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = o[k * TS + z][e];
+          for (int e = 0; e < 8; ++e) y[e] = o[k * TS + z][e];
+        }
+      if (i >= heads) continue;
+      const int head = h * p.gqa + hb + i;
+      const int64_t pair = (int64_t)r * a.Hq + head;
+      if (!SHORT_OWN && len > 0) {
+        const int ns = (len + own_stretch(p, len) - 1) / own_stretch(p, len);
+        for (int j = 0; j < ns; ++j) {
+          const int64_t at = pair * p.nsplit + j;
+          const float4* x = reinterpret_cast<const float4*>(p.so + at * D + d0);
+          add_part(y, my, ly, p.sml[at], x[0], x[1]);
+        }
       }
-    if (i >= heads) continue;
-    const int head = h * p.gqa + hb + i;
-    const int64_t pair = (int64_t)r * a.Hq + head;
-    if (!SHORT_OWN && len > 0) {
-      const int ns = (len + own_stretch(p, len) - 1) / own_stretch(p, len);
-      for (int j = 0; j < ns; ++j) {
-        const int64_t at = pair * p.nsplit + j;
-        const float4* x = reinterpret_cast<const float4*>(p.so + at * D + d0);
-        add_part(y, my, ly, p.sml[at], x[0], x[1]);
-      }
-    }
-    const Parts s = parts_of(p, q, unit0, item0, total, r, h, hb + i);
+      const Parts s = parts_of(p, q, item0, r, h, hb + i);
 #pragma unroll 2
-    for (int j = 0; j < s.np; ++j) {
-      const float2 ml = p.pml[(int64_t)(s.slot + j) * p.mt + s.i];
-      const float* x = p.po + part_at<D>(s.slot + j, p.mt, s.i, d0);
-      add_part(y, my, ly, ml, *reinterpret_cast<const float4*>(x),
-               *reinterpret_cast<const float4*>(x + 4 * p.mt));
+      for (int j = 0; j < s.np; ++j) {
+        const float2 ml = p.pml[(int64_t)(s.slot + j) * p.mt + s.i];
+        const float* x = p.po + part_at<D>(s.slot + j, p.mt, s.i, d0);
+        add_part(y, my, ly, ml, *reinterpret_cast<const float4*>(x),
+                 *reinterpret_cast<const float4*>(x + 4 * p.mt));
+      }
+      // no token at all: zeros and -inf
+      const float inv = ly == 0.f ? 0.f : 1.f / ly;
+      uint4 out;
+      out.x = pack2<T>(y[0] * inv, y[1] * inv);
+      out.y = pack2<T>(y[2] * inv, y[3] * inv);
+      out.z = pack2<T>(y[4] * inv, y[5] * inv);
+      out.w = pack2<T>(y[6] * inv, y[7] * inv);
+      *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (int64_t)r * a.out_row_stride +
+                                (int64_t)head * a.out_head_stride + d0) = out;
+      if (d0 == 0 && a.lse) a.lse[pair] = (my + log2f(ly)) * 0.6931471805599453f;
     }
-    // no token at all: zeros and -inf
-    const float inv = ly == 0.f ? 0.f : 1.f / ly;
-    uint4 out;
-    out.x = pack2<T>(y[0] * inv, y[1] * inv);
-    out.y = pack2<T>(y[2] * inv, y[3] * inv);
-    out.z = pack2<T>(y[4] * inv, y[5] * inv);
-    out.w = pack2<T>(y[6] * inv, y[7] * inv);
-    *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (int64_t)r * a.out_row_stride +
-                              (int64_t)head * a.out_head_stride + d0) = out;
-    if (d0 == 0 && a.lse) a.lse[pair] = (my + log2f(ly)) * 0.6931471805599453f;
   }
 }
 
@@ -574,7 +541,7 @@ struct Layout {
   bool tc;                  // the prefixes' kernel is the tensor-core one
   bool short_own;           // the join reads own tokens itself
   int own_blocks;
-  size_t po, pml, unit, item, so, sml, total;
+  size_t po, pml, item, workers, so, sml, total;
 };
 
 bool strides_ok(const void* ptr, std::initializer_list<int64_t> strides) {
@@ -611,6 +578,8 @@ bool plan(const ssd_attention& a, AttnParams& p, Layout& L) {
   const int sms = std::max(num_sms(), 1);
   p.a = a;
   p.gqa = a.Hq / a.Hkv;
+  p.by_page = divisor(a.page_size);
+  p.by_gqa = divisor(p.gqa);
   p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
   L.tc = prefix_tc_fits(a);
   p.mt = L.tc ? kTcBlock : kBlockRows;
@@ -620,7 +589,7 @@ bool plan(const ssd_attention& a, AttnParams& p, Layout& L) {
   const int64_t items =
       a.Hkv * ((int64_t)a.R * p.gqa / p.mt + std::min<int64_t>(a.G, a.R));
   const int64_t tiles = ((int64_t)a.prefix_cols * a.page_size + p.tn - 1) / p.tn;
-  if (items * std::max<int64_t>(tiles, 1) > 0x7fffffff) return false;
+  if (items * (tiles + 1) > 0x7fffffff) return false;
   p.nslots = a.G > 0 ? (int)(items + p.workers) : 0;
   // own tokens: read by the join where they are few; else in stretches of two
   // tiles or more, four for each resident warp, which evens out their lengths
@@ -639,8 +608,8 @@ bool plan(const ssd_attention& a, AttnParams& p, Layout& L) {
   };
   L.po = take((size_t)p.nslots * p.mt * a.D * 4);
   L.pml = take((size_t)p.nslots * p.mt * 8);
-  L.unit = take((size_t)(a.G + 1) * 4);
-  L.item = take((size_t)(a.G + 1) * 4);
+  L.item = take((size_t)a.G * 4);
+  L.workers = take((size_t)items * 8);
   const size_t rows = L.short_own ? 0 : (size_t)a.R * a.Hq * p.nsplit;
   L.so = take(rows * a.D * 4);
   L.sml = take(rows * 8);
@@ -672,12 +641,11 @@ cudaError_t launch(const AttnParams& p, const Layout& L, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   const int head_blocks = (p.gqa + kJoinHeads - 1) / kJoinHeads;
-  const int64_t tasks = (int64_t)p.a.R * p.a.Hkv * head_blocks;
-  const unsigned grid = (unsigned)((tasks + kJoinWarps - 1) / kJoinWarps);
+  const int threads = std::min(kJoinWarps, p.a.Hkv * head_blocks) * 32;
   if (L.short_own)
-    join_kernel<T, D, true><<<grid, kJoinWarps * 32, 0, s>>>(p, head_blocks);
+    join_kernel<T, D, true><<<p.a.R, threads, 0, s>>>(p, head_blocks);
   else
-    join_kernel<T, D, false><<<grid, kJoinWarps * 32, 0, s>>>(p, head_blocks);
+    join_kernel<T, D, false><<<p.a.R, threads, 0, s>>>(p, head_blocks);
   return cudaGetLastError();
 }
 
@@ -721,8 +689,8 @@ ssd_status ssd_prefix_attention(const ssd_attention* a, void* workspace, size_t 
   char* ws = static_cast<char*>(workspace);
   p.po = reinterpret_cast<float*>(ws + L.po);
   p.pml = reinterpret_cast<float2*>(ws + L.pml);
-  p.unit_base = reinterpret_cast<int*>(ws + L.unit);
   p.item_base = reinterpret_cast<int*>(ws + L.item);
+  p.item_workers = reinterpret_cast<int2*>(ws + L.workers);
   p.so = reinterpret_cast<float*>(ws + L.so);
   p.sml = reinterpret_cast<float2*>(ws + L.sml);
   p.status = dev_status;

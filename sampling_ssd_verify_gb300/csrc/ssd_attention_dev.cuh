@@ -3,10 +3,11 @@
 //
 // A prefix is attended to by all rows of its group.  The rows' query heads
 // that read one key/value head, (row, head) in row-major order, are cut into
-// blocks of MT; an item is (group, key/value head, block), and costs the tiles
-// of TN tokens of the group's prefix.  All tiles of all items, in order, are
-// divided evenly among the workers, so every worker has the same share however
-// the lengths differ; a worker that gets a stretch of an item leaves a partial
+// blocks of MT; an item is (group, key/value head, block), and costs one unit
+// for its start and end (queries, partial) and one for each tile of TN tokens of
+// the group's prefix.  The units of all items, in order, are divided evenly
+// among the workers, so every worker has the same share however the lengths
+// differ; a worker that gets a stretch of an item leaves a partial
 // result (unnormalised sums, their largest score and weight), and the rows'
 // partials are joined afterwards.  The partial of item i by worker w has slot
 // i + w: along the sequence of stretches one of the two steps up each time,
@@ -24,8 +25,57 @@
 
 namespace ssd {
 
+// 16 bytes global -> shared; zeros when !ok (src is then not read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(ok ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  const __half2 x = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+
+// Division of numbers below 2^31 by a divisor known to the host: with
+// 2^s >= d, m = ceil(2^(32 + s) / d) - 2^32 gives n / d = (n + (n * m >> 32)) >> s.
+struct Divisor {
+  uint32_t d, m, s;
+  __device__ __forceinline__ int quotient(int n) const {
+    return (int)(((uint64_t)__umulhi((uint32_t)n, m) + (uint32_t)n) >> s);
+  }
+};
+inline Divisor divisor(int d) {
+  Divisor v{(uint32_t)d, 0, 0};
+  while ((1ull << v.s) < (uint64_t)d) ++v.s;
+  v.m = (uint32_t)(((1ull << (32 + v.s)) + d - 1) / (uint64_t)d - (1ull << 32));
+  return v;
+}
+
 struct AttnParams {
   ssd_attention a;
+  Divisor by_page, by_gqa;
   float scale_log2;       // scale * log2(e): scores in base 2
   int gqa;                // query heads per key/value head
   // prefixes: items, partials
@@ -34,8 +84,8 @@ struct AttnParams {
   int nslots;
   float* po;              // [nslots, D / 4, mt, 4] unnormalised sums (part_at)
   float2* pml;            // [nslots, mt] largest score (base 2), weight
-  int* unit_base;         // [G + 1] tiles of all items before group g
-  int* item_base;         // [G + 1] items before group g
+  int* item_base;         // [G] items before group g; -1 throughout when group_off is torn
+  int2* item_workers;     // [items] first and last worker of an item with tokens
   // own tokens: nsplit stretches per row, each with its partial
   int nsplit;
   float* so;              // [R, Hq, nsplit, D]
@@ -60,6 +110,7 @@ __device__ __forceinline__ void flag(const AttnParams& p, int bit) {
 struct Group {
   int row0, rows, len;
   int blocks, tiles;      // blocks of its (row, head) pairs, tiles of its prefix
+  int cost;               // units of an item
   bool torn;              // its rows are no range within [0, R]
   bool bad;               // that, or its length was clamped
 };
@@ -76,23 +127,20 @@ __device__ __forceinline__ Group group_of(const AttnParams& p, int g) {
   q.rows = max(q.rows, 0);
   q.blocks = (q.rows * p.gqa + p.mt - 1) / p.mt;
   q.tiles = (q.len + p.tn - 1) / p.tn;
+  q.cost = q.tiles > 0 ? q.tiles + 1 : 0;
   return q;
 }
 
-// First tile of worker w when `total` tiles are shared, and the worker that
-// has tile u.  At most one worker per tile takes part, so that each of those
-// has a tile, and the partials of an item are by consecutive workers.
+// First unit of worker w when `total` units are shared.  At most one worker per
+// unit takes part, so that the partials of an item are by consecutive workers.
 __device__ __forceinline__ int first_unit(const AttnParams& p, int w, int total) {
   const int n = min(p.workers, total);
   return w >= n ? total : (int)((long long)w * total / n);
 }
-__device__ __forceinline__ int worker_of(const AttnParams& p, int u, int total) {
-  return (int)((((long long)u + 1) * min(p.workers, total) - 1) / total);
-}
 
 // Running sums over the groups, by the whole CTA (NT threads), which finds for
 // each of its NW workers w0 .. w0 + NW - 1 the group that holds its first
-// tile.  CTA 0 leaves the sums for the join.  Returns the number of tiles.
+// tile.  CTA 0 leaves the items' sums for the join.  Returns the number of tiles.
 struct Start {
   int g, unit, item;      // the group, and the sums before it
 };
@@ -101,9 +149,9 @@ __device__ __forceinline__ int find_starts(const AttnParams& p, int w0, Start* s
                                            int2* s_warp) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.a.G;
+  // pass 0 forms the total, pass 1 the starts that it determines; up to NT
+  // groups, the sums of pass 0 serve for pass 1
   int total = 0, torn = 0;
-  // pass 0 forms the total, pass 1 the starts that it determines (one pass
-  // over the groups each; the lengths of pass 1 come from L1)
   for (int pass = 0; pass < 2; ++pass) {
     int2 base = make_int2(0, 0);
     for (int g0 = 0; g0 < G; g0 += NT) {
@@ -112,7 +160,7 @@ __device__ __forceinline__ int find_starts(const AttnParams& p, int w0, Start* s
       if (g < G) {
         const Group q = group_of(p, g);
         torn |= q.torn;
-        mine = torn ? mine : make_int2(p.a.Hkv * q.blocks * q.tiles, p.a.Hkv * q.blocks);
+        mine = torn ? mine : make_int2(p.a.Hkv * q.blocks * q.cost, p.a.Hkv * q.blocks);
         if (pass == 0 && blockIdx.x == 0 && q.bad) flag(p, SSD_DEV_BAD_LENGTH);
       }
       int2 x = mine;
@@ -123,7 +171,7 @@ __device__ __forceinline__ int find_starts(const AttnParams& p, int w0, Start* s
         if (lane >= d) { x.x += a; x.y += b; }
       }
       if (lane == 31) s_warp[warp] = x;
-      __syncthreads();
+      const int any_torn = __syncthreads_or(torn);
       int2 before = base;
       for (int w = 0; w < NT / 32; ++w) {
         const int2 y = s_warp[w];
@@ -131,35 +179,34 @@ __device__ __forceinline__ int find_starts(const AttnParams& p, int w0, Start* s
         base.x += y.x;
         base.y += y.y;
       }
-      __syncthreads();
+      if (G <= NT) {
+        torn = any_torn;
+        total = torn ? 0 : base.x;
+        pass = 1;
+      }
       if (pass == 1 && g < G) {
         const int u = before.x + x.x - mine.x, i = before.y + x.y - mine.y;
-        if (blockIdx.x == 0) {
-          p.unit_base[g] = torn ? 0 : u;
-          p.item_base[g] = torn ? 0 : i;
-        }
+        if (blockIdx.x == 0) p.item_base[g] = torn ? -1 : i;
 #pragma unroll
         for (int k = 0; k < NW; ++k) {
           const int f = first_unit(p, w0 + k, total);
           if (!torn && f >= u && f < u + mine.x) s_start[k] = Start{g, u, i};
         }
       }
+      __syncthreads();
     }
-    if (pass == 0 && __syncthreads_or(torn)) torn = 1;
-    total = torn ? 0 : base.x;
-    if (pass == 1 && blockIdx.x == 0 && tid == 0) {
-      p.unit_base[G] = total;
-      p.item_base[G] = torn ? 0 : base.y;
+    if (pass == 0) {
+      torn = __syncthreads_or(torn);
+      total = torn ? 0 : base.x;
     }
   }
-  __syncthreads();
   return total;
 }
 
 // A worker's stretches, one after the other.
 struct Stretch {
-  int g, h, mb;           // the item
-  int slot;
+  int g, h, mb;           // the item,
+  int item, slot;         // its number, and the partial's
   Group q;
   int tile0, tile1;       // tiles of the prefix
 };
@@ -169,25 +216,37 @@ struct Walk {
   int w;
 };
 __device__ __forceinline__ bool next_stretch(const AttnParams& p, Walk& k, Stretch& s) {
-  if (k.u >= k.u1) return false;
-  Group q = group_of(p, k.g);
-  int n = p.a.Hkv * q.blocks * q.tiles;
-  while (k.u >= k.unit + n) {  // ends: u < u1 <= total
-    k.unit += n;
-    k.item += p.a.Hkv * q.blocks;
-    q = group_of(p, ++k.g);
-    n = p.a.Hkv * q.blocks * q.tiles;
+  while (k.u < k.u1) {
+    Group q = group_of(p, k.g);
+    int n = p.a.Hkv * q.blocks * q.cost;
+    while (k.u >= k.unit + n) {  // ends: u < u1 <= total
+      k.unit += n;
+      k.item += p.a.Hkv * q.blocks;
+      q = group_of(p, ++k.g);
+      n = p.a.Hkv * q.blocks * q.cost;
+    }
+    const int local = (k.u - k.unit) / q.cost;   // item within the group
+    const int at = (k.u - k.unit) - local * q.cost;
+    const int take = min(q.cost - at, k.u1 - k.u);
+    k.u += take;
+    s.q = q;
+    s.g = k.g;
+    s.h = local / q.blocks;
+    s.mb = local - s.h * q.blocks;
+    s.tile0 = max(at - 1, 0);
+    s.tile1 = at + take - 1;
+    s.item = k.item + local;
+    s.slot = s.item + k.w;
+    if (s.tile1 > s.tile0) return true;  // not only the unit of the item's start
   }
-  const int local = (k.u - k.unit) / q.tiles;  // item within the group
-  s.q = q;
-  s.g = k.g;
-  s.h = local / q.blocks;
-  s.mb = local - s.h * q.blocks;
-  s.tile0 = (k.u - k.unit) - local * q.tiles;
-  s.tile1 = min(q.tiles, s.tile0 + (k.u1 - k.u));
-  s.slot = k.item + local + k.w;
-  k.u += s.tile1 - s.tile0;
-  return true;
+  return false;
+}
+
+// One thread per stretch tells the join which workers have the item.
+__device__ __forceinline__ void leave_worker(const AttnParams& p, const Stretch& s, int w) {
+  if (s.slot >= p.nslots) return;
+  if (s.tile0 == 0) p.item_workers[s.item].x = w;
+  if (s.tile1 == s.q.tiles) p.item_workers[s.item].y = w;
 }
 
 // The tensor-core kernel (ssd_attention_tc.cu): blocks of kTcBlock pairs, tiles

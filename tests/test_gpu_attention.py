@@ -169,6 +169,17 @@ def test_long_prefixes(page):
     check(s, call(s), rows=list(range(0, 193, 7)) + [39, 40, 42, 43, 192])
 
 
+@pytest.mark.parametrize("page", [16, 128, 20])
+def test_many_short_groups(page):
+    """Every worker has many items, most of them of one tile."""
+    rng = np.random.default_rng(page)
+    n = 700
+    s = make(rng.integers(0, 4, n), rng.integers(0, 400, n), None, 8, 4, 128, page,
+             dtype_of("bfloat16"), seed=page, own=False)
+    poison(s)
+    check(s, call(s), rows=range(0, s["q"].shape[0], 9))
+
+
 def test_long_own_tokens():
     """Few rows with long own caches: their stretches are split too."""
     torch, dev = torch_dev()
