@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32)
   extern __shared__ __align__(128) unsigned char s_ring[];
   __shared__ Start s_start[kWarpsPerCta];
   __shared__ int2 s_warp[kWarpsPerCta];
+  start_next();
   const int w0 = blockIdx.x * kWarpsPerCta, warp = threadIdx.x >> 5, w = w0 + warp;
   const int total = find_starts<kWarpsPerCta * 32, kWarpsPerCta>(p, w0, s_start, s_warp);
   const uint32_t ring = smem_addr(s_ring) + warp * kRing * step_bytes<D>();
@@ -286,12 +287,8 @@ __device__ __forceinline__ int own_stretch(const AttnParams& p, int len) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarpsPerCta * 32)
-    own_kernel(const __grid_constant__ AttnParams p, int blocks) {
-  extern __shared__ __align__(128) unsigned char s_ring[];
-  const int warp = threadIdx.x >> 5;
-  int64_t task = (int64_t)blockIdx.x * kWarpsPerCta + warp;
-  if (task >= (int64_t)p.a.R * p.a.Hkv * blocks * p.nsplit) return;
+__device__ __forceinline__ void own_task(const AttnParams& p, uint32_t ring, int64_t task,
+                                         int blocks) {
   const int split = (int)(task % p.nsplit);
   task /= p.nsplit;
   const int mb = (int)(task % blocks);
@@ -304,234 +301,256 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32)
   if (t0 >= t1) return;  // the join does not look at it
   const int64_t at = ((int64_t)r * p.a.Hq + h * p.gqa + mb * kBlockRows) * p.nsplit + split;
   const Partial out{p.so + at * D, (int64_t)p.nsplit * D, 4, p.sml + at, p.nsplit};
-  warp_stretch<T, D>(p, smem_addr(s_ring) + warp * kRing * step_bytes<D>(), r, mb * kBlockRows,
-                     p.gqa, h, p.a.tables + (int64_t)r * p.a.table_stride, t0, t1, out);
+  warp_stretch<T, D>(p, ring, r, mb * kBlockRows, p.gqa, h, p.a.tables + (int64_t)r * p.a.table_stride, t0, t1, out);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarpsPerCta * 32)
+    own_kernel(const __grid_constant__ AttnParams p, int blocks) {
+  extern __shared__ __align__(128) unsigned char s_ring[];
+  start_next();
+  const int warp = threadIdx.x >> 5;
+  int64_t task = (int64_t)blockIdx.x * kWarpsPerCta + warp;
+  if (task < (int64_t)p.a.R * p.a.Hkv * blocks * p.nsplit)
+    own_task<T, D>(p, smem_addr(s_ring) + warp * kRing * step_bytes<D>(), task, blocks);
+  // It needs nothing of the prefixes' kernel; the join that waits for this one
+  // must find that one done too.
+  wait_previous();
 }
 
 // ---- the join ------------------------------------------------------------------------
-// One warp per (row, key/value head, up to four of its query heads): the row's
+// One warp per (row, key/value head, up to eight of its query heads): the row's
 // own tokens, or their partials, then the prefix's partials, then the output.
 //
 // Own tokens are few in the calls that this kernel is made for (a branch's
-// drafts), and such a task is a chain of loads: length, page, token beside
-// group, sums, partials.  It is bound by that latency, so it has few registers
-// and many warps: a token is spread over D / 8 lanes of 16 bytes, and the
-// products run on the ordinary units.  Long own caches go through own_kernel,
-// split over many warps.
+// drafts), and such a task is a chain of loads: page, tokens, partials.  It is
+// bound by their latency and by what it issues around them, so the operands of
+// the products come straight from global memory, in an order of the dimensions
+// that needs no exchange between lanes and in which every load of a warp takes
+// whole sectors (the cache of an SM that still runs the kernel before is small).
+// In 16-byte chunks of 8 dimensions: lane (gid, quad) holds chunks quad + 4 i of
+// query head gid and of token gid, whose elements 4 s .. 4 s + 3 are the k of
+// product s of Q K^T; and chunks gid + 8 i of tokens 2 quad and 2 quad + 1, whose
+// element e is column gid of product 8 i + e of the sums: so it receives, of head
+// gid, dimensions 64 i + 16 quad + e and + 8.  Long own caches go through
+// own_kernel, split over many warps.
 constexpr int kJoinWarps = 8;
-constexpr int kJoinHeads = 4;
+constexpr int kJoinHeads = 8;
+template <int D> constexpr int kJoinCtas = D == 256 ? 1 : 2;  // per SM, by registers
 constexpr int kShortOwn = 64;  // tokens of an own cache up to which the join reads it
-
-// The group of row r: the last one that starts at or before it.
-__device__ __forceinline__ int group_of_row(const int32_t* off, int G, int r) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, n = G;  // the answer is in [lo, lo + n)
-  while (n > 1) {
-    const int step = (n + 31) / 32, i = lo + lane * step;
-    const unsigned le = __ballot_sync(0xffffffffu, i < lo + n && off[i] <= r);
-    const int k = le ? 31 - __clz(le) : 0;
-    n = min(step, n - k * step);
-    lo += k * step;
-  }
-  return lo;
-}
 
 // The prefix's partials of a pair: np of them, from `slot` on, at row `i`.
 struct Parts {
   int np, slot, i;
 };
-__device__ __forceinline__ Parts parts_of(const AttnParams& p, const Group& q, int item0, int r,
-                                          int h, int head) {
-  Parts s{0, 0, 0};
-  if (r < q.row0 || r >= q.row0 + q.rows || q.tiles == 0 || item0 < 0) return s;
-  const int i = (r - q.row0) * p.gqa + head, mb = p.mt == kTcBlock ? i / kTcBlock : i / kBlockRows;
-  const int item = item0 + h * q.blocks + mb;
+__device__ __forceinline__ Parts parts_of(const AttnParams& p, const int4& row, int h, int head) {
+  if (row.x < 0) return Parts{0, 0, 0};
+  const int i = row.y + head, mb = p.mt == kTcBlock ? i / kTcBlock : i / kBlockRows;
+  const int item = row.x + h * row.z + mb;
   const int2 w = p.item_workers[item];
-  s.np = w.y - w.x + 1;
-  s.slot = item + w.x;
-  s.i = i - mb * p.mt;
-  return s;
+  return Parts{w.y - w.x + 1, item + w.x, i - mb * p.mt};
 }
 
+// Eight rows (heads) of the 16 that an instruction has; the others are zeros.
 template <typename T>
-__device__ __forceinline__ void widen(float (&f)[8], const uint4& x) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float2 y;
-    if constexpr (__is_same(T, __half))
-      y = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    else
-      y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-    f[2 * i] = y.x;
-    f[2 * i + 1] = y.y;
-  }
+__device__ __forceinline__ void mma_k16(float& c0, float& c1, uint32_t a0, uint32_t a2,
+                                        uint32_t b0, uint32_t b1) {
+  float x[4] = {c0, c1, 0.f, 0.f};
+  const uint32_t a[4] = {a0, 0u, a2, 0u};
+  mma16816<T>(x, a, b0, b1);
+  c0 = x[0];
+  c1 = x[1];
+}
+template <typename T>
+__device__ __forceinline__ void mma_k8(float& c0, float& c1, uint32_t a0, uint32_t b0) {
+  float d2, d3;
+  if constexpr (__is_same(T, __half))
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
+        "{%0,%1,%7,%7};"
+        : "+f"(c0), "+f"(c1), "=f"(d2), "=f"(d3)
+        : "r"(a0), "r"(0), "r"(b0), "f"(0.f));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
+        "{%0,%1,%7,%7};"
+        : "+f"(c0), "+f"(c1), "=f"(d2), "=f"(d3)
+        : "r"(a0), "r"(0), "r"(b0), "f"(0.f));
 }
 
-// Weighted sums of one more stretch: o, l at maximum m take x, its weight and
-// maximum in ml.
-__device__ __forceinline__ void add_part(float (&o)[8], float& m, float& l, float2 ml,
-                                         const float4& x0, const float4& x1) {
-  const float m1 = fmaxf(m, ml.x), off = m1 == -INFINITY ? 0.f : m1;
-  const float a = exp2_fast(m - off), b = exp2_fast(ml.x - off);
-  m = m1;
-  l = l * a + ml.y * b;
-  const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+// Chunks 0, STEP, 2 STEP, .. of 16 bytes, or zeros.
+template <int STEP, int N>
+__device__ __forceinline__ void load_chunks(uint4 (&x)[N], const void* from, bool ok) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) o[e] = o[e] * a + x[e] * b;
+  for (int i = 0; i < N; ++i)
+    x[i] = ok ? static_cast<const uint4*>(from)[i * STEP] : make_uint4(0u, 0u, 0u, 0u);
+}
+__device__ __forceinline__ uint32_t word(const uint4& x, int i) {
+  return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
 }
 
 template <typename T, int D, bool SHORT_OWN>
-__global__ void __launch_bounds__(kJoinWarps * 32, SHORT_OWN ? 2 : 3)
+__global__ void __launch_bounds__(kJoinWarps * 32, kJoinCtas<D>)
     join_kernel(const __grid_constant__ AttnParams p, int head_blocks) {
-  constexpr int LT = D / 8;          // lanes of a token
-  constexpr int TS = 32 / LT;        // tokens at a time
-  constexpr int HS = kJoinHeads / TS;  // heads that a lane's share finishes
-  static_assert(HS * TS == kJoinHeads, "heads are dealt to the tokens' lanes");
-  const int lane = threadIdx.x & 31, sub = lane / LT, d0 = lane % LT * 8;
-  // a CTA per row: its warps meet the same lengths, tables and sums
-  const int r = blockIdx.x;
+  constexpr int EL = D / 4;          // dimensions of a lane
+  constexpr int NI = D / 64;         // its runs of 16 of the sums
+  const int lane = threadIdx.x & 31, gid = lane >> 2, quad = lane & 3;
+  // a row per CTA and turn: its warps meet the same lengths, tables and places,
+  // which are looked up one turn ahead
   const ssd_attention& a = p.a;
-  const int len = own_len(p, r);
-  Group q{};
-  int item0 = -1;
-  if (a.G > 0) {
-    const int g = group_of_row(a.group_off, a.G, r);
-    q = group_of(p, g);
-    item0 = p.item_base[g];
-  }
-  for (int task = threadIdx.x >> 5; task < a.Hkv * head_blocks; task += blockDim.x >> 5) {
-    const int h = head_blocks == 1 ? task : task / head_blocks;
-    const int hb = (task - h * head_blocks) * kJoinHeads;
-    const int heads = min(kJoinHeads, p.gqa - hb);
+  const int step = gridDim.x;
+  int page_col = p.by_page.quotient(gid);
+  if (page_col >= a.cols) page_col = -1;
+  auto page_of = [&](int r) {        // of token gid, before the length is known
+    return SHORT_OWN && page_col >= 0 && r < a.R ? a.tables[(int64_t)r * a.table_stride + page_col]
+                                                 : -1;
+  };
+  auto length_of = [&](int r) { return r < a.R ? own_len(p, r) : 0; };
+  auto items_of = [&](int r) {
+    return a.G > 0 && r < a.R ? p.row_items[r] : row_items_of(-1, 0, 0);
+  };
+  int r = blockIdx.x;
+  int next_len = length_of(r), next_first = page_of(r);
+  wait_previous();
+  int4 next_row = items_of(r);
+  for (; r < a.R; r += step) {
+    const int len = next_len, first = next_first;
+    const int4 row = next_row;
+    next_len = length_of(r + step);
+    next_first = page_of(r + step);
+    next_row = items_of(r + step);
+    const int32_t* table = a.tables + (int64_t)r * a.table_stride;
+    if (SHORT_OWN && a.lens && threadIdx.x == 0 && len != a.lens[r]) flag(p, SSD_DEV_BAD_LENGTH);
 
-    float o[kJoinHeads][8] = {};
-    float m[kJoinHeads], l[kJoinHeads];
+    for (int task = threadIdx.x >> 5; task < a.Hkv * head_blocks; task += blockDim.x >> 5) {
+      const int h = head_blocks == 1 ? task : task / head_blocks;
+      const int in_h = (task - h * head_blocks) * kJoinHeads + gid;  // this lane's query head
+      const bool mine = in_h < p.gqa;
+      const int head = h * p.gqa + in_h;
+
+      // where the partials are, on its way while the own tokens are read
+      const Parts s = mine ? parts_of(p, row, h, in_h) : Parts{0, 0, 0};
+
+      // sums at dimensions 64 i + 16 quad + e; the first partial is loaded into
+      // them, beside the own tokens
+      float o[NI][16] = {};
+      float m = -INFINITY, l = 0.f;
+      if (s.np > 0) {
+        const float2 ml = p.pml[(int64_t)s.slot * p.mt + s.i];
+        m = ml.x;
+        l = quad == 0 ? ml.y : 0.f;      // summed over the quad below
+        const float* x = p.po + part_at<D>(s.slot, p.mt, s.i, quad * 16);
 #pragma unroll
-    for (int i = 0; i < kJoinHeads; ++i) {
-      m[i] = -INFINITY;
-      l[i] = 0.f;
-    }
-    if (SHORT_OWN && a.lens && h == 0 && hb == 0 && lane == 0 && len != a.lens[r])
-      flag(p, SSD_DEV_BAD_LENGTH);
-    if (SHORT_OWN && len > 0) {
-      uint4 qx[kJoinHeads];
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int i = 0; i < kJoinHeads; ++i)
-        qx[i] = i < heads ? *reinterpret_cast<const uint4*>(
-                                static_cast<const T*>(a.q) + (int64_t)r * a.q_row_stride +
-                                (int64_t)(h * p.gqa + hb + i) * a.q_head_stride + d0)
-                          : make_uint4(0u, 0u, 0u, 0u);
-      const int32_t* table = a.tables + (int64_t)r * a.table_stride;
-      for (int t0 = 0; t0 < len; t0 += 2 * TS) {
-        uint4 kx[2], vx[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int t = t0 + j * TS + sub;
-          kx[j] = vx[j] = make_uint4(0u, 0u, 0u, 0u);
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<float4*>(&o[i][c * 4]) =
+                *reinterpret_cast<const float4*>(x + (i * 16 + c) * 4 * p.mt);
+      }
+      if (SHORT_OWN && len > 0) {
+        uint4 q[EL / 8];
+        load_chunks<4>(q, static_cast<const T*>(a.q) + (int64_t)r * a.q_row_stride +
+                        (int64_t)head * a.q_head_stride + quad * 8, mine);
+        for (int t0 = 0; t0 < len; t0 += 8) {
+          const int t = t0 + gid, col = p.by_page.quotient(t);
+          int page = -1, in_page = 0;
           if (t < len) {
-            const int col = p.by_page.quotient(t), page = table[col];
-            if ((unsigned)page < (unsigned)a.num_pages) {
-              const int in_page = t - col * a.page_size;
-              kx[j] = *reinterpret_cast<const uint4*>(
-                  static_cast<const T*>(a.k.ptr) + (int64_t)page * a.k.page_stride +
-                  (int64_t)in_page * a.k.token_stride + (int64_t)h * a.k.head_stride + d0);
-              vx[j] = *reinterpret_cast<const uint4*>(
-                  static_cast<const T*>(a.v.ptr) + (int64_t)page * a.v.page_stride +
-                  (int64_t)in_page * a.v.token_stride + (int64_t)h * a.v.head_stride + d0);
-            } else {
+            page = t0 == 0 ? first : table[col];
+            in_page = t - col * a.page_size;
+            if ((unsigned)page >= (unsigned)a.num_pages) {
               flag(p, SSD_DEV_BAD_PAGE);
+              page = -1;               // reads as zeros
             }
           }
-        }
-        float sc[2][kJoinHeads];
+          uint4 k[EL / 8], v0[NI], v1[NI];
+          load_chunks<4>(k, static_cast<const T*>(a.k.ptr) + (int64_t)page * a.k.page_stride +
+                          (int64_t)in_page * a.k.token_stride + (int64_t)h * a.k.head_stride + quad * 8,
+                   page >= 0);
+          const T* vh = static_cast<const T*>(a.v.ptr) + (int64_t)h * a.v.head_stride + gid * 8;
+          const int pg0 = __shfl_sync(0xffffffffu, page, quad * 8);
+          const int pg1 = __shfl_sync(0xffffffffu, page, quad * 8 + 4);
+          const int ip0 = __shfl_sync(0xffffffffu, in_page, quad * 8);
+          const int ip1 = __shfl_sync(0xffffffffu, in_page, quad * 8 + 4);
+          load_chunks<8>(v0, vh + (int64_t)pg0 * a.v.page_stride + (int64_t)ip0 * a.v.token_stride,
+                   pg0 >= 0);
+          load_chunks<8>(v1, vh + (int64_t)pg1 * a.v.page_stride + (int64_t)ip1 * a.v.token_stride,
+                   pg1 >= 0);
+          float s0 = 0.f, s1 = 0.f;    // scores of tokens t0 + 2 quad, + 1
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float kf[8];
-          widen<T>(kf, kx[j]);
+          for (int i = 0; i < EL / 4; ++i)
+            mma_k16<T>(s0, s1, word(q[i / 2], i % 2 * 2), word(q[i / 2], i % 2 * 2 + 1),
+                       word(k[i / 2], i % 2 * 2), word(k[i / 2], i % 2 * 2 + 1));
+          s0 = t0 + quad * 2 < len ? s0 * p.scale_log2 : -INFINITY;
+          s1 = t0 + quad * 2 + 1 < len ? s1 * p.scale_log2 : -INFINITY;
+          float top = fmaxf(s0, s1);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const float m1 = fmaxf(m, top), off = m1 == -INFINITY ? 0.f : m1;
+          const float keep = exp2_fast(m - off);
+          m = m1;
+          s0 = exp2_fast(s0 - off);
+          s1 = exp2_fast(s1 - off);
+          l = l * keep + s0 + s1;
+          const uint32_t pw = pack2<T>(s0, s1);
 #pragma unroll
-          for (int i = 0; i < kJoinHeads; ++i) {
-            float qf[8], x = 0.f;
-            widen<T>(qf, qx[i]);
+          for (int i = 0; i < NI; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x = fmaf(qf[e], kf[e], x);
-#pragma unroll
-            for (int d = LT / 2; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-            sc[j][i] = t0 + j * TS + sub < len ? x * p.scale_log2 : -INFINITY;
-          }
-        }
-        float vf[2][8];
-        widen<T>(vf[0], vx[0]);
-        widen<T>(vf[1], vx[1]);
-#pragma unroll
-        for (int i = 0; i < kJoinHeads; ++i) {
-          float top = fmaxf(sc[0][i], sc[1][i]);
-#pragma unroll
-          for (int d = LT; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-          const float m1 = fmaxf(m[i], top), off = m1 == -INFINITY ? 0.f : m1;
-          const float keep = exp2_fast(m[i] - off);
-          const float w0 = exp2_fast(sc[0][i] - off), w1 = exp2_fast(sc[1][i] - off);
-          m[i] = m1;
-          l[i] = l[i] * keep + w0 + w1;
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            o[i][e] = fmaf(w1, vf[1][e], fmaf(w0, vf[0][e], o[i][e] * keep));
+            for (int e = 0; e < 8; ++e) {
+              o[i][e] *= keep;
+              o[i][e + 8] *= keep;
+              mma_k8<T>(o[i][e], o[i][e + 8], pw,
+                        __byte_perm(word(v0[i], e / 2), word(v1[i], e / 2),
+                                    e & 1 ? 0x7632 : 0x5410));
+            }
         }
       }
-#pragma unroll
-      for (int i = 0; i < kJoinHeads; ++i)
-#pragma unroll
-        for (int d = LT; d < 32; d <<= 1) {
-          l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[i][e] += __shfl_xor_sync(0xffffffffu, o[i][e], d);
-        }
-    }
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      if (!mine) continue;
 
-    // each token's lanes finish heads sub, sub + TS, ..
+      // one more stretch: its sums of four dimensions 4 c .. of the lane's at
+      // x + (i * 16 + c) * step
+      auto add = [&](float2 ml, const float* x, int64_t step) {
+        const float m1 = fmaxf(m, ml.x), off = m1 == -INFINITY ? 0.f : m1;
+        const float f = exp2_fast(m - off), g = exp2_fast(ml.x - off);
+        m = m1;
+        l = l * f + ml.y * g;
 #pragma unroll
-    for (int k = 0; k < HS; ++k) {
-      const int i = k * TS + sub;
-      float y[8], my = m[k * TS], ly = l[k * TS];
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = o[k * TS][e];
-#pragma unroll
-      for (int z = 1; z < TS; ++z)
-        if (sub == z) {
-          my = m[k * TS + z];
-          ly = l[k * TS + z];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = o[k * TS + z][e];
-        }
-      if (i >= heads) continue;
-      const int head = h * p.gqa + hb + i;
+          for (int c = 0; c < 4; ++c) {
+            const float4 y = *reinterpret_cast<const float4*>(x + (i * 16 + c) * step);
+            o[i][c * 4] = fmaf(y.x, g, o[i][c * 4] * f);
+            o[i][c * 4 + 1] = fmaf(y.y, g, o[i][c * 4 + 1] * f);
+            o[i][c * 4 + 2] = fmaf(y.z, g, o[i][c * 4 + 2] * f);
+            o[i][c * 4 + 3] = fmaf(y.w, g, o[i][c * 4 + 3] * f);
+          }
+      };
       const int64_t pair = (int64_t)r * a.Hq + head;
       if (!SHORT_OWN && len > 0) {
         const int ns = (len + own_stretch(p, len) - 1) / own_stretch(p, len);
         for (int j = 0; j < ns; ++j) {
           const int64_t at = pair * p.nsplit + j;
-          const float4* x = reinterpret_cast<const float4*>(p.so + at * D + d0);
-          add_part(y, my, ly, p.sml[at], x[0], x[1]);
+          add(p.sml[at], p.so + at * D + quad * 16, 4);
         }
       }
-      const Parts s = parts_of(p, q, item0, r, h, hb + i);
-#pragma unroll 2
-      for (int j = 0; j < s.np; ++j) {
-        const float2 ml = p.pml[(int64_t)(s.slot + j) * p.mt + s.i];
-        const float* x = p.po + part_at<D>(s.slot + j, p.mt, s.i, d0);
-        add_part(y, my, ly, ml, *reinterpret_cast<const float4*>(x),
-                 *reinterpret_cast<const float4*>(x + 4 * p.mt));
-      }
+      for (int j = 1; j < s.np; ++j)
+        add(p.pml[(int64_t)(s.slot + j) * p.mt + s.i],
+            p.po + part_at<D>(s.slot + j, p.mt, s.i, quad * 16), 4 * p.mt);
       // no token at all: zeros and -inf
-      const float inv = ly == 0.f ? 0.f : 1.f / ly;
-      uint4 out;
-      out.x = pack2<T>(y[0] * inv, y[1] * inv);
-      out.y = pack2<T>(y[2] * inv, y[3] * inv);
-      out.z = pack2<T>(y[4] * inv, y[5] * inv);
-      out.w = pack2<T>(y[6] * inv, y[7] * inv);
-      *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (int64_t)r * a.out_row_stride +
-                                (int64_t)head * a.out_head_stride + d0) = out;
-      if (d0 == 0 && a.lse) a.lse[pair] = (my + log2f(ly)) * 0.6931471805599453f;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      T* to = static_cast<T*>(a.out) + (int64_t)r * a.out_row_stride +
+              (int64_t)head * a.out_head_stride + quad * 16;
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int c = 0; c < 16; c += 8)
+          *reinterpret_cast<uint4*>(to + i * 64 + c) =
+              make_uint4(pack2<T>(o[i][c] * inv, o[i][c + 1] * inv),
+                         pack2<T>(o[i][c + 2] * inv, o[i][c + 3] * inv),
+                         pack2<T>(o[i][c + 4] * inv, o[i][c + 5] * inv),
+                         pack2<T>(o[i][c + 6] * inv, o[i][c + 7] * inv));
+      if (quad == 0 && a.lse) a.lse[pair] = (m + log2f(l)) * 0.6931471805599453f;
     }
   }
 }
@@ -541,7 +560,7 @@ struct Layout {
   bool tc;                  // the prefixes' kernel is the tensor-core one
   bool short_own;           // the join reads own tokens itself
   int own_blocks;
-  size_t po, pml, item, workers, so, sml, total;
+  size_t po, pml, rows, workers, so, sml, total;
 };
 
 bool strides_ok(const void* ptr, std::initializer_list<int64_t> strides) {
@@ -608,19 +627,37 @@ bool plan(const ssd_attention& a, AttnParams& p, Layout& L) {
   };
   L.po = take((size_t)p.nslots * p.mt * a.D * 4);
   L.pml = take((size_t)p.nslots * p.mt * 8);
-  L.item = take((size_t)a.G * 4);
+  L.rows = take(a.G > 0 ? (size_t)a.R * 16 : 0);
   L.workers = take((size_t)items * 8);
-  const size_t rows = L.short_own ? 0 : (size_t)a.R * a.Hq * p.nsplit;
-  L.so = take(rows * a.D * 4);
-  L.sml = take(rows * 8);
+  const size_t owns = L.short_own ? 0 : (size_t)a.R * a.Hq * p.nsplit;
+  L.so = take(owns * a.D * 4);
+  L.sml = take(owns * 8);
   L.total = std::max<size_t>(at, 256);
   return true;
+}
+
+// The next kernel of a call, which may start before the one before is done.
+template <typename... A>
+cudaError_t launch_next(void (*kernel)(A...), int grid, int threads, int smem, cudaStream_t s,
+                        bool early_start, const AttnParams& p, int n) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)grid);
+  c.blockDim = dim3((unsigned)threads);
+  c.dynamicSmemBytes = (size_t)smem;
+  c.stream = s;
+  c.attrs = &early;
+  c.numAttrs = early_start ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kernel, p, n);
 }
 
 template <typename T, int D>
 cudaError_t launch(const AttnParams& p, const Layout& L, cudaStream_t s) {
   const int smem = kWarpsPerCta * kRing * step_bytes<D>();
   cudaError_t e;
+  bool first = p.a.G == 0;
   if (p.a.G > 0 && L.tc) {
     e = launch_prefix_tc(p, s);
     if (e != cudaSuccess) return e;
@@ -635,18 +672,22 @@ cudaError_t launch(const AttnParams& p, const Layout& L, cudaStream_t s) {
     e = cudaFuncSetAttribute(own_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int64_t tasks = (int64_t)p.a.R * p.a.Hkv * L.own_blocks * p.nsplit;
-    own_kernel<T, D><<<(unsigned)((tasks + kWarpsPerCta - 1) / kWarpsPerCta), kWarpsPerCta * 32,
-                       smem, s>>>(p, L.own_blocks);
-    e = cudaGetLastError();
+    e = launch_next(own_kernel<T, D>, (int)((tasks + kWarpsPerCta - 1) / kWarpsPerCta),
+                    kWarpsPerCta * 32, smem, s, !first, p, L.own_blocks);
     if (e != cudaSuccess) return e;
+    first = false;
   }
   const int head_blocks = (p.gqa + kJoinHeads - 1) / kJoinHeads;
   const int threads = std::min(kJoinWarps, p.a.Hkv * head_blocks) * 32;
-  if (L.short_own)
-    join_kernel<T, D, true><<<p.a.R, threads, 0, s>>>(p, head_blocks);
-  else
-    join_kernel<T, D, false><<<p.a.R, threads, 0, s>>>(p, head_blocks);
-  return cudaGetLastError();
+  const int resident = std::max(num_sms(), 1) * kJoinCtas<D> * kJoinWarps * 32 / threads;
+  const int grid = std::min(p.a.R, resident);
+  // Started early, the join finds the shared-memory split of the kernel before on
+  // its SM: 256 x 24 branches then take 52 us more (it has many turns, and lives
+  // on its cache), a call of one turn 2 us less.
+  const bool early = !first && p.a.R <= resident;
+  return L.short_own
+             ? launch_next(join_kernel<T, D, true>, grid, threads, 0, s, early, p, head_blocks)
+             : launch_next(join_kernel<T, D, false>, grid, threads, 0, s, early, p, head_blocks);
 }
 
 template <typename T>
@@ -689,7 +730,7 @@ ssd_status ssd_prefix_attention(const ssd_attention* a, void* workspace, size_t 
   char* ws = static_cast<char*>(workspace);
   p.po = reinterpret_cast<float*>(ws + L.po);
   p.pml = reinterpret_cast<float2*>(ws + L.pml);
-  p.item_base = reinterpret_cast<int*>(ws + L.item);
+  p.row_items = reinterpret_cast<int4*>(ws + L.rows);
   p.item_workers = reinterpret_cast<int2*>(ws + L.workers);
   p.so = reinterpret_cast<float*>(ws + L.so);
   p.sml = reinterpret_cast<float2*>(ws + L.sml);

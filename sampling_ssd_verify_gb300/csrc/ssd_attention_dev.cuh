@@ -84,7 +84,7 @@ struct AttnParams {
   int nslots;
   float* po;              // [nslots, D / 4, mt, 4] unnormalised sums (part_at)
   float2* pml;            // [nslots, mt] largest score (base 2), weight
-  int* item_base;         // [G] items before group g; -1 throughout when group_off is torn
+  int4* row_items;        // [R] row_items_of
   int2* item_workers;     // [items] first and last worker of an item with tokens
   // own tokens: nsplit stretches per row, each with its partial
   int nsplit;
@@ -100,6 +100,23 @@ struct AttnParams {
 template <int D>
 __device__ __forceinline__ int64_t part_at(int slot, int mt, int i, int d) {
   return (((int64_t)slot * (D / 4) + d / 4) * mt + i) * 4 + d % 4;
+}
+
+// The kernels of a call follow one another on the stream, each launched so that
+// its CTAs may start as soon as SMs fall free at the end of the one before:
+// `start_next` lets it, `wait_previous` waits until all of it is done and seen.
+__device__ __forceinline__ void start_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// What the join needs of a row's group: the number of the group's first item,
+// or -1 when there is no prefix to join; the row's first pair in the group; the
+// blocks of a key/value head.
+__device__ __forceinline__ int4 row_items_of(int item, int pair, int blocks) {
+  return make_int4(item, pair, blocks, 0);
 }
 
 __device__ __forceinline__ void flag(const AttnParams& p, int bit) {
@@ -140,7 +157,7 @@ __device__ __forceinline__ int first_unit(const AttnParams& p, int w, int total)
 
 // Running sums over the groups, by the whole CTA (NT threads), which finds for
 // each of its NW workers w0 .. w0 + NW - 1 the group that holds its first
-// tile.  CTA 0 leaves the items' sums for the join.  Returns the number of tiles.
+// tile.  Leaves each row's items for the join.  Returns the number of tiles.
 struct Start {
   int g, unit, item;      // the group, and the sums before it
 };
@@ -157,8 +174,9 @@ __device__ __forceinline__ int find_starts(const AttnParams& p, int w0, Start* s
     for (int g0 = 0; g0 < G; g0 += NT) {
       const int g = g0 + tid;
       int2 mine = make_int2(0, 0);
+      Group q{};
       if (g < G) {
-        const Group q = group_of(p, g);
+        q = group_of(p, g);
         torn |= q.torn;
         mine = torn ? mine : make_int2(p.a.Hkv * q.blocks * q.cost, p.a.Hkv * q.blocks);
         if (pass == 0 && blockIdx.x == 0 && q.bad) flag(p, SSD_DEV_BAD_LENGTH);
@@ -186,11 +204,24 @@ __device__ __forceinline__ int find_starts(const AttnParams& p, int w0, Start* s
       }
       if (pass == 1 && g < G) {
         const int u = before.x + x.x - mine.x, i = before.y + x.y - mine.y;
-        if (blockIdx.x == 0) p.item_base[g] = torn ? -1 : i;
 #pragma unroll
         for (int k = 0; k < NW; ++k) {
           const int f = first_unit(p, w0 + k, total);
           if (!torn && f >= u && f < u + mine.x) s_start[k] = Start{g, u, i};
+        }
+      }
+      // the groups that fall to this CTA, one at a time by their warp
+      if (pass == 1 && !torn) {
+        const int item = before.y + x.y - mine.y;
+        unsigned todo = __ballot_sync(0xffffffffu, g < G && g % (int)gridDim.x == (int)blockIdx.x);
+        for (; todo != 0; todo &= todo - 1) {
+          const int src = __ffs(todo) - 1;
+          const int first = __shfl_sync(0xffffffffu, q.tiles > 0 ? item : -1, src);
+          const int row0 = __shfl_sync(0xffffffffu, q.row0, src);
+          const int rows = __shfl_sync(0xffffffffu, q.rows, src);
+          const int blocks = __shfl_sync(0xffffffffu, q.blocks, src);
+          for (int r = lane; r < rows; r += 32)
+            p.row_items[row0 + r] = row_items_of(first, r * p.gqa, blocks);
         }
       }
       __syncthreads();
@@ -200,6 +231,11 @@ __device__ __forceinline__ int find_starts(const AttnParams& p, int w0, Start* s
       total = torn ? 0 : base.x;
     }
   }
+  // rows of no group
+  const int r0 = torn ? 0 : p.a.group_off[0], r1 = torn ? 0 : p.a.group_off[G];
+  const int step = gridDim.x * NT, at = blockIdx.x * NT + tid;
+  for (int r = at; r < r0; r += step) p.row_items[r] = row_items_of(-1, 0, 0);
+  for (int r = r1 + at; r < p.a.R; r += step) p.row_items[r] = row_items_of(-1, 0, 0);
   return total;
 }
 

@@ -150,11 +150,11 @@ __device__ __forceinline__ constexpr uint32_t product(int n, bool b_rows_are_k) 
 }
 
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int c0, int c1,
-                                        int c2, int c3, uint64_t* bar) {
+                                        int c2, int c3, uint64_t* bar, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar)), "l"(policy)
       : "memory");
 }
 __device__ __forceinline__ void fence_async() {
@@ -208,6 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t vring = kring + S::kSlots * S::kSlot;
   const uint32_t qs = vring + S::kSlots * S::kSlot;
 
+  start_next();
   if (warp == kMmaWarp) tmem_alloc(&sh.tmem);
   if (tid == 0) {
     sh.err = 0;
@@ -261,8 +262,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int P = p.a.page_size;
       const int rows = min(P, kTile);            // tokens of a box
       const int boxes = kTile / rows;            // boxes of a whole tile, at most 16
+      // A prefix that one block reads is not read again: it leaves L2 first, so
+      // that the partials stay there for the join.  With more blocks it stays.
+      uint64_t once, again;
+      asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+      asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(again));
       uint32_t c = 0;                            // tiles so far
       while (next_stretch(p, k, s)) {
+        const uint64_t policy = s.q.blocks == 1 ? once : again;
         const int32_t* table = p.a.prefix_tables + (int64_t)s.g * p.a.prefix_table_stride;
         auto page_at = [&](int tile) {  // not looked at here: the load stays in flight
           const int t = tile * kTile + lane * rows;
@@ -293,7 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t dst = slots + slot * S::kSlot + lane * rows * 128;
 #pragma unroll
             for (int d = 0; d < S::kPanels; ++d)
-              tma_box(dst + d * kPanel, map, d * 64, s.h, in_page, page, &full[slot]);
+              tma_box(dst + d * kPanel, map, d * 64, s.h, in_page, page, &full[slot],
+                      policy);
           }
           page = next;
           next = after;
