@@ -10,11 +10,17 @@
 // thousand tokens of a row.  A CTA owns a slice of the vocabulary of one
 // sequence: it counts the history's tokens of the slice once in shared
 // memory and streams that slice of the sequence's rows past the counts, so
-// the history is scanned once for all N rows.  From row to row only the
-// drafts that differ between the two paths are added or taken out.  A bitmap
-// of the touched tokens lets a 16-byte vector of untouched ones pass with one
-// look-up.
-
+// the history is scanned once for all N rows.  A token that is among the drafts
+// has a bit of its own in its count, and the few such tokens walk the path of
+// their row when they are met, so that the rows need no counts of their own.
+//
+// A warp streams its own vectors through its own part of a ring in shared
+// memory, filled by asynchronous copies, four vectors per thread a step.  A
+// bitmap tells which tokens of a vector are touched; the warp lists those of a
+// step and shares them out evenly, a token per lane (one in thirty is touched
+// after 4096 tokens: each lane by itself would take its hits one after the
+// other, with most lanes idle).  No barrier stands between the rows.
+//
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -23,16 +29,22 @@
 #include <cmath>
 
 #include "ssd.h"
+#include "ssd_device.cuh"
 #include "ssd_internal.cuh"
 
 namespace ssd {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxSlice = 8192;     // tokens of a slice: 32 KB of counts, 16 KB of bias entries
+constexpr int kMaxSlice = 4096;     // tokens of a slice: 16 KB of counts, 8 KB of bias entries
 constexpr int kMinSlice = 1024;
-constexpr int kBatch = 4;           // vectors in flight per thread
-constexpr uint32_t kPromptBit = 0x80000000u;  // counts word: token occurs in the prompt
+constexpr int kMaxRows = 16;        // rows of a CTA: 8 KB of mask bits
+constexpr int kVecs = 2;            // vectors of a thread and step: 8 KB per CTA
+constexpr int kStages = 2;          // steps of the ring
+constexpr int kBatch = 8;           // history tokens in flight per thread
+constexpr uint32_t kPromptBit = 0x80000000u;  // counts word: token occurs in the prompt,
+constexpr uint32_t kDraftBit = 0x40000000u;   // among the drafts of some row
+constexpr uint32_t kCountBits = kDraftBit - 1;
 
 struct LogitParams {
   const void* in;
@@ -62,27 +74,42 @@ template <> struct Elem<SSD_F32> {
 
 // What a rule needs of its sequence.
 struct Rules {
-  float rep, freq, pres;
+  float rep, inv, freq, pres;  // inv = 1 / rep: one more rounding than a division, 20 instructions less
   const float* bias;
+  const int* tok;           // draft token of each node
+  const int16_t* parent;
 };
 
+// Logit z of token v in row u, whose count word and bias entry are given.
 __device__ __forceinline__ float adjust(float z, uint32_t word, uint32_t bias_entry,
-                                        const Rules& ru) {
-  if (word != 0u) z = z > 0.f ? z / ru.rep : z * ru.rep;
-  const uint32_t c = word & ~kPromptBit;
+                                        const Rules& ru, int v, int u) {
+  uint32_t c = word & kCountBits;
+  if (word & kDraftBit)
+    for (int w = u; w > 0; w = ru.parent[w]) c += ru.tok[w] == v;
+  if (c != 0u || (word & kPromptBit)) z *= z > 0.f ? ru.inv : ru.rep;
   if (c != 0u) z = z - ru.freq * (float)c - ru.pres;
   if (bias_entry != 0u) z += ru.bias[bias_entry - 1];
   return z;
 }
 
-// The 32 mask bits from token v on (bits past the row are whatever the last
-// word repeats; callers use only tokens of the row).
-__device__ __forceinline__ uint32_t mask_bits(const int32_t* m, int v, int last_word) {
-  const int w = v >> 5;
-  const uint32_t lo = (uint32_t)m[w];
-  if ((v & 31) == 0) return lo;
-  const uint32_t hi = (uint32_t)m[min(w + 1, last_word)];
-  return __funnelshift_r(lo, hi, v & 31);
+// 16 bytes global -> shared, of this thread's own ring.
+__device__ __forceinline__ void fetch(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void fetch4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void fetch_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void fetch_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Bits k .. of a bitmap in shared memory with a word to spare.
+__device__ __forceinline__ uint32_t bits_at(const uint32_t* map, int k) {
+  return __funnelshift_r(map[k >> 5], map[(k >> 5) + 1], k & 31);
 }
 
 template <int DT>
@@ -91,10 +118,18 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
   constexpr int VE = 16 / (int)sizeof(E);  // tokens of a vector
   constexpr uint32_t kAll = (1u << VE) - 1u;
   extern __shared__ uint4 smem4[];
-  uint32_t* count = reinterpret_cast<uint32_t*>(smem4);             // [slice]
-  uint32_t* touched = count + p.slice;                              // [slice / 32 + 2]
-  uint16_t* bias_at = reinterpret_cast<uint16_t*>(touched + p.slice / 32 + 4);  // [slice] if biases
+  uint4* ring = smem4;                                              // [kStages][kVecs][kThreads]
+  constexpr int kHits = kVecs * 32 * VE;                            // tokens of a warp and step
+  uint16_t* list = reinterpret_cast<uint16_t*>(ring + kStages * kVecs * kThreads) +
+                   (threadIdx.x >> 5) * kHits;
+  uint32_t* count =                                                 // [slice]
+      reinterpret_cast<uint32_t*>(list + (kThreads / 32 - (threadIdx.x >> 5)) * kHits);
+  uint32_t* touched = count + p.slice;                              // [slice / 32 + 4]
+  const int words = p.slice / 32 + 4;
+  uint32_t* bits = touched + words;                                 // [rows][words] if a mask
+  uint16_t* bias_at = reinterpret_cast<uint16_t*>(bits + (p.r.mask ? p.rows * words : 0));
   __shared__ int s_tok[kMaxTreeNodes];
+  __shared__ int16_t s_parent[kMaxTreeNodes];
   __shared__ int s_sum[kThreads / 32];
 
   const int tid = threadIdx.x;
@@ -107,13 +142,65 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
   const int v0 = sl * p.slice, nv = min(p.slice, p.V - v0);
   const ssd_logit_rules& r = p.r;
 
+  // ---- the rows' vectors: steps of kVecs * kThreads, alike for the whole CTA ----------
+  constexpr int kStep = kVecs * kThreads;
+  struct Place {
+    int u, i;               // row, its first vector of the step
+    const E* in;            // the slice of the row
+    int head, nvec;         // tokens before its first whole vector, vectors
+  };
+  auto row_at = [&](Place& q) {
+    q.in = static_cast<const E*>(p.in) + (b * p.N + q.u) * p.in_stride + v0;
+    const E* out = static_cast<const E*>(p.out) + (b * p.N + q.u) * p.out_stride + v0;
+    const uint32_t mis = (uint32_t)(uintptr_t)q.in & 15u;
+    const bool vec = mis == ((uint32_t)(uintptr_t)out & 15u);
+    q.head = vec ? min(nv, (int)((16u - mis) & 15u) / (int)sizeof(E)) : nv;
+    q.nvec = (nv - q.head) / VE;
+    q.i = 0;
+  };
+  auto settle = [&](Place& q) {  // to the next row that has vectors
+    while (q.u < u1 && q.i >= q.nvec)
+      if (++q.u < u1) row_at(q);
+  };
+  Place ahead;
+  ahead.u = u0;
+  row_at(ahead);
+  settle(ahead);
+  Place at = ahead;
+  auto fetch_next = [&](int stage) {
+    if (ahead.u < u1) {
+      const uint4* in = reinterpret_cast<const uint4*>(ahead.in + ahead.head);
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) {
+        const int i = ahead.i + j * kThreads + tid;
+        if (i < ahead.nvec) fetch(smem_addr(ring + stage * kStep + j * kThreads + tid), in + i);
+      }
+      ahead.i += kStep;
+      settle(ahead);
+    }
+    fetch_commit();
+  };
+  // the rows' mask bits, then the first vectors: both arrive while the counts are made
+  if (r.mask) {
+    const int w0 = v0 >> 5, per = min(p.slice / 32 + 1, ((p.V - 1) >> 5) + 1 - w0);
+    const int32_t* m = r.mask + b * r.mask_seq_stride + w0;
+    for (int i = tid; i < (u1 - u0) * per; i += kThreads) {
+      const int u = i / per, w = i - u * per;
+      fetch4(smem_addr(bits + u * words + w), m + (u0 + u) * r.mask_row_stride + w);
+    }
+  }
+  fetch_commit();
+#pragma unroll
+  for (int d = 0; d < kStages - 1; ++d) fetch_next(d);
+
   // ---- the sequence's rules -----------------------------------------------------
-  Rules ru{1.f, 0.f, 0.f, r.bias + b * r.n_bias};
+  Rules ru{1.f, 1.f, 0.f, 0.f, r.bias + b * r.n_bias, s_tok, s_parent};
   int bad = 0;
   if (r.repetition) {
     ru.rep = r.repetition[b];
     if (!(ru.rep > 0.f) || isinf(ru.rep)) { ru.rep = 1.f; bad = SSD_DEV_BAD_PENALTY; }
   }
+  ru.inv = 1.f / ru.rep;
   if (r.frequency) {
     ru.freq = r.frequency[b];
     if (!isfinite(ru.freq)) { ru.freq = 0.f; bad = SSD_DEV_BAD_PENALTY; }
@@ -124,8 +211,8 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
   }
 
   // ---- counts of the slice's tokens ---------------------------------------------
-  for (int i = tid; i < (p.slice + p.slice / 32 + 4) / 4; i += kThreads)
-    smem4[i] = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = tid; i < (p.slice + words) / 4; i += kThreads)
+    reinterpret_cast<uint4*>(count)[i] = make_uint4(0u, 0u, 0u, 0u);
   if (r.n_bias)
     for (int i = tid; i < p.slice / 8; i += kThreads)
       reinterpret_cast<uint4*>(bias_at)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -133,6 +220,7 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
     for (int u = 1 + tid; u < p.N; u += kThreads) {
       const int t = r.draft_tokens[b * r.draft_stride + u - 1];
       s_tok[u] = t;
+      s_parent[u] = p.parent[u];
       if ((unsigned)t >= (unsigned)p.V) bad |= SSD_DEV_BAD_TOKEN;
     }
   __syncthreads();
@@ -144,17 +232,35 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
       len = min(max(len, 0), r.history_max);
     }
     const int32_t* h = r.history + b * r.history_stride;
-    for (int i = tid; i < len; i += kThreads) {
-      const int t = h[i], k = t - v0;
-      if ((unsigned)t >= (unsigned)p.V) {
-        bad |= SSD_DEV_BAD_TOKEN;
-      } else if ((unsigned)k < (unsigned)nv) {
-        if (i < prompt) atomicOr(&count[k], kPromptBit);
-        else atomicAdd(&count[k], 1u);
-        atomicOr(&touched[k >> 5], 1u << (k & 31));
+    for (int i0 = tid; i0 < len; i0 += kThreads * kBatch) {
+      int t[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = i0 + j * kThreads;
+        t[j] = i < len ? h[i] : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = i0 + j * kThreads, k = t[j] - v0;
+        if (i >= len) break;
+        if ((unsigned)t[j] >= (unsigned)p.V) {
+          bad |= SSD_DEV_BAD_TOKEN;
+        } else if ((unsigned)k < (unsigned)nv) {
+          if (i < prompt) atomicOr(&count[k], kPromptBit);
+          else atomicAdd(&count[k], 1u);
+          atomicOr(&touched[k >> 5], 1u << (k & 31));
+        }
       }
     }
   }
+  if (r.draft_tokens)
+    for (int u = 1 + tid; u < p.N; u += kThreads) {
+      const int t = s_tok[u], k = t - v0;
+      if ((unsigned)t < (unsigned)p.V && (unsigned)k < (unsigned)nv) {
+        atomicOr(&count[k], kDraftBit);
+        atomicOr(&touched[k >> 5], 1u << (k & 31));
+      }
+    }
   for (int i = tid; i < r.n_bias; i += kThreads) {
     const int t = r.bias_ids[b * r.n_bias + i], k = t - v0;
     if (t >= p.V) {
@@ -173,109 +279,94 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
   }
   if (bad && p.status) atomicOr(p.status, bad);
 
-  const int last_word = (p.V - 1) >> 5;
   const E fill = Elem<DT>::store(r.fill);
-  int at_node = 0;  // the node whose path the counts hold (thread 0)
-  for (int u = u0; u < u1; ++u) {
-    // ---- the drafts of this row's path -------------------------------------------
-    __syncthreads();
-    if (tid == 0 && r.draft_tokens) {
-      // from node a's path to node c's: parents have lower indices, so the
-      // larger index steps up until both meet
-      int a = at_node, c = u;
-      while (a != c) {
-        const bool drop = a > c;
-        const int node = drop ? a : c;
-        const int k = s_tok[node] - v0;
-        if ((unsigned)s_tok[node] < (unsigned)p.V && (unsigned)k < (unsigned)nv) {
-          count[k] += drop ? 0xffffffffu : 1u;
-          touched[k >> 5] |= 1u << (k & 31);
-        }
-        if (drop) a = p.parent[a];
-        else c = p.parent[c];
-      }
-      at_node = u;
-    }
-    __syncthreads();
+  fetch_wait<kStages - 1>();  // the mask bits
+  __syncthreads();
 
-    const int32_t* mask =
-        r.mask ? r.mask + b * r.mask_seq_stride + u * r.mask_row_stride : nullptr;
-    const int64_t row = b * p.N + u;
-    const E* in = static_cast<const E*>(p.in) + row * p.in_stride + v0;
-    E* out = static_cast<E*>(p.out) + row * p.out_stride + v0;
-
-    // one token, for the ends of rows that are not aligned
-    auto single = [&](int k) {
-      E e = in[k];
-      if ((touched[k >> 5] >> (k & 31)) & 1u)
-        e = Elem<DT>::store(adjust(Elem<DT>::load(e), count[k], r.n_bias ? bias_at[k] : 0u, ru));
-      if (mask) {
-        const int v = v0 + k;
-        if (!(((uint32_t)mask[v >> 5] >> (v & 31)) & 1u)) e = fill;
-      }
-      out[k] = e;
-    };
-    const uint32_t mis = (uint32_t)(uintptr_t)in & 15u;
-    const bool vec = mis == ((uint32_t)(uintptr_t)out & 15u);
-    const int head = vec ? min(nv, (int)((16u - mis) & 15u) / (int)sizeof(E)) : nv;
-    const int nvec = (nv - head) / VE;
-    for (int k = tid; k < head; k += kThreads) single(k);
-    for (int k = head + nvec * VE + tid; k < nv; k += kThreads) single(k);
-
-    const uint4* in4 = reinterpret_cast<const uint4*>(in + head);
-    uint4* out4 = reinterpret_cast<uint4*>(out + head);
-    for (int i0 = tid; i0 < nvec; i0 += kThreads * kBatch) {
-      uint4 x[kBatch];
-      uint32_t ok[kBatch];
+  const int lane = tid & 31;
+  for (int stage = 0; at.u < u1; stage = (stage + 1) % kStages) {
+    fetch_next((stage + kStages - 1) % kStages);
+    fetch_wait<kStages - 1>();
+    __syncwarp();  // the warp's copies are there for all its lanes
+    E* out = static_cast<E*>(p.out) + (b * p.N + at.u) * p.out_stride + v0;
+    const uint32_t* allow = bits + (at.u - u0) * words;
+    const int k0 = at.head + at.i * VE;  // the step's first token
+    uint32_t hit[kVecs];
+    int n = 0;
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int i = i0 + j * kThreads;
-        if (i < nvec) {
-          x[j] = __ldcs(in4 + i);
-          ok[j] = mask ? mask_bits(mask, v0 + head + i * VE, last_word) & kAll : kAll;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int i = i0 + j * kThreads;
-        if (i >= nvec) break;
-        const int k = head + i * VE;
-        uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-        const uint32_t hit =
-            __funnelshift_r(touched[k >> 5], touched[(k >> 5) + 1], k & 31) & ok[j];
-        if (ok[j] != kAll) {
+    for (int j = 0; j < kVecs; ++j) {
+      const int i = at.i + j * kThreads + tid, k = at.head + i * VE;
+      hit[j] = 0u;
+      if (i < at.nvec) {
+        const uint4 x = ring[stage * kStep + j * kThreads + tid];
+        uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        const uint32_t ok = r.mask ? bits_at(allow, k) & kAll : kAll;
+        hit[j] = bits_at(touched, k) & ok;
+        if (ok != kAll) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             if constexpr (DT == SSD_BF16) {
-              const uint32_t m = (ok[j] >> (2 * q) & 1u ? 0xffffu : 0u) |
-                                 (ok[j] >> (2 * q + 1) & 1u ? 0xffff0000u : 0u);
+              const uint32_t m = (ok >> (2 * q) & 1u ? 0xffffu : 0u) |
+                                 (ok >> (2 * q + 1) & 1u ? 0xffff0000u : 0u);
               w[q] = (w[q] & m) | (((uint32_t)fill * 0x10001u) & ~m);
             } else {
-              w[q] = ok[j] >> q & 1u ? w[q] : __float_as_uint(fill);
+              w[q] = ok >> q & 1u ? w[q] : __float_as_uint(fill);
             }
           }
         }
-        __stcs(out4 + i, make_uint4(w[0], w[1], w[2], w[3]));
-        // touched tokens: few, and written again by the same thread
-        for (uint32_t h = hit & kAll; h != 0u; h &= h - 1u) {
-          const int e = __ffs(h) - 1;
-          const int q = DT == SSD_BF16 ? e >> 1 : e;
-          const uint32_t word = q & 2 ? (q & 1 ? w[3] : w[2]) : (q & 1 ? w[1] : w[0]);
-          float z;
-          if constexpr (DT == SSD_BF16)
-            z = Elem<DT>::load((uint16_t)(word >> (16 * (e & 1))));
-          else
-            z = __uint_as_float(word);
-          z = adjust(z, count[k + e], r.n_bias ? bias_at[k + e] : 0u, ru);
-          out[k + e] = Elem<DT>::store(z);
-        }
+        __stcs(reinterpret_cast<uint4*>(out + k), make_uint4(w[0], w[1], w[2], w[3]));
+        n += __popc(hit[j]);
       }
     }
+    // the touched tokens of the warp's vectors, listed and then taken one per lane
+    int before = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, before, d);
+      if (lane >= d) before += y;
+    }
+    const int total = __shfl_sync(0xffffffffu, before, 31);
+    before -= n;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j)
+      for (uint32_t h = hit[j]; h != 0u; h &= h - 1u)
+        list[before++] = (uint16_t)((j * kThreads + tid) * VE + __ffs(h) - 1);
+    __syncwarp();
+    const E* raw = reinterpret_cast<const E*>(ring + stage * kStep);
+    for (int t = lane; t < total; t += 32) {
+      const int e = list[t], k = k0 + e;
+      const float z = adjust(Elem<DT>::load(raw[e]), count[k], r.n_bias ? bias_at[k] : 0u, ru,
+                             v0 + k, at.u);
+      out[k] = Elem<DT>::store(z);
+    }
+    __syncwarp();  // list and ring are read
+    at.i += kStep;
+    settle(at);
+  }
+
+  const int last_word = (p.V - 1) >> 5;
+  for (int u = u0; u < u1; ++u) {
+    // ---- the ends of rows that are not aligned, token by token -------------------------
+    Place q;
+    q.u = u;
+    row_at(q);
+    E* out = static_cast<E*>(p.out) + (b * p.N + u) * p.out_stride + v0;
+    auto single = [&](int k) {
+      E e = q.in[k];
+      if (touched[k >> 5] >> (k & 31) & 1u)
+        e = Elem<DT>::store(adjust(Elem<DT>::load(e), count[k], r.n_bias ? bias_at[k] : 0u, ru,
+                                   v0 + k, u));
+      if (r.mask && !(bits[(u - u0) * words + (k >> 5)] >> (k & 31) & 1u)) e = fill;
+      out[k] = e;
+    };
+    for (int k = tid; k < q.head; k += kThreads) single(k);
+    for (int k = q.head + q.nvec * VE + tid; k < nv; k += kThreads) single(k);
 
     // ---- allowed tokens: each row is counted whole by one of the slices' CTAs --------
     if (p.allowed && (u - u0) % p.nslice == sl) {
       int n = 0;
-      if (mask) {
+      if (r.mask) {
+        const int32_t* mask = r.mask + b * r.mask_seq_stride + u * r.mask_row_stride;
         for (int i = tid; i <= last_word; i += kThreads) {
           uint32_t m = (uint32_t)mask[i];
           if (i == last_word && (p.V & 31)) m &= (1u << (p.V & 31)) - 1u;
@@ -290,8 +381,9 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
       if (tid == 0) {
         int t = 0;
         for (int i = 0; i < kThreads / 32; ++i) t += s_sum[i];
-        p.allowed[row] = t;
+        p.allowed[b * p.N + u] = t;
       }
+      __syncthreads();  // s_sum is read
     }
   }
 }
@@ -351,7 +443,7 @@ extern "C" ssd_status ssd_process_logits(const ssd_logits* in, const ssd_logits*
   const int64_t want = 2 * (int64_t)std::max(num_sms(), 1);
   p.slice = kMaxSlice;
   while (p.slice > kMinSlice && p.slice / 2 >= V) p.slice /= 2;
-  p.rows = N;
+  p.rows = std::min(N, kMaxRows);
   auto ctas = [&] {
     p.nslice = (V + p.slice - 1) / p.slice;
     p.ngroup = (N + p.rows - 1) / p.rows;
@@ -361,7 +453,11 @@ extern "C" ssd_status ssd_process_logits(const ssd_logits* in, const ssd_logits*
   while (ctas() < want && p.slice > kMinSlice) p.slice /= 2;
   const int64_t grid = ctas();
   if (grid > 0x7fffffff) return SSD_ERR_UNSUPPORTED;
-  const size_t smem = (size_t)(p.slice + p.slice / 32 + 4) * 4 + (r.n_bias ? p.slice * 2 : 0);
+  const size_t words = p.slice / 32 + 4;
+  const int ve = in->dtype == SSD_BF16 ? 8 : 4;
+  const size_t smem = (size_t)kStages * kVecs * kThreads * 16 + kVecs * kThreads * ve * 2 +
+                      (p.slice + words) * 4 +
+                      (r.mask ? p.rows * words * 4 : 0) + (r.n_bias ? p.slice * 2 : 0);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = in->dtype == SSD_BF16 ? launch<SSD_BF16>(p, grid, smem, s)
                                               : launch<SSD_F32>(p, grid, smem, s);
