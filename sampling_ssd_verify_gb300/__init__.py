@@ -69,7 +69,7 @@ class _LogitRules(ctypes.Structure):
                 ("history_max", ctypes.c_int32), ("n_bias", ctypes.c_int32),
                 ("history_len", ctypes.c_void_p), ("prompt_len", ctypes.c_void_p),
                 ("draft_tokens", ctypes.c_void_p), ("draft_stride", ctypes.c_int64),
-                ("parent", ctypes.c_void_p), ("repetition", ctypes.c_void_p),
+                ("parent", ctypes.c_char_p), ("repetition", ctypes.c_void_p),
                 ("frequency", ctypes.c_void_p), ("presence", ctypes.c_void_p),
                 ("bias_ids", ctypes.c_void_p), ("bias", ctypes.c_void_p),
                 ("mask", ctypes.c_void_p), ("mask_seq_stride", ctypes.c_int64),
@@ -549,46 +549,44 @@ def fanout(K: int, budget: int, a: float = 0.7, r: float = 1.0) -> np.ndarray:
 
 
 # ---- around a round ---------------------------------------------------------------------
-def _tensor(t, name, dtype, shape, device):
-    """A device tensor's address, its type, shape and place checked; None: 0.
-    Its last dimension is contiguous; of the others, so is what follows the
-    first."""
-    if t is None:
-        return 0
-    if t.dtype != dtype or t.device != device:
-        raise SSDError(f"{name}: expected {dtype} on {device}")
-    if t.shape != shape:
-        raise SSDError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise SSDError(f"{name}: expected a contiguous tensor")
-    return t.data_ptr()
+# Calls of a few microseconds on the device: their checks are kept few and
+# cheap (a tensor's type, device, shape and layout, each asked for once).
+def _tensor(t, name, dtype, shape, dev):
+    """Address of a contiguous tensor of that type and shape on GPU `dev`."""
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    raise SSDError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on cuda:{dev}, "
+                   f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _rows2d(t, name, rows, device):
-    """Address and row stride of an int32 [rows, n] tensor with contiguous
-    rows that do not overlap (one row: any stride)."""
-    torch = _torch()
-    if t.dtype != torch.int32 or t.device != device:
-        raise SSDError(f"{name}: expected int32 on {device}")
-    if t.dim() != 2 or t.shape[0] != rows:
-        raise SSDError(f"{name}: expected {rows} rows")
-    n = t.shape[1]
-    if n > 1 and t.stride(1) != 1:
-        raise SSDError(f"{name}: rows must be contiguous")
-    stride = t.stride(0) if rows > 1 else max(n, 1)
-    if stride < n:
-        raise SSDError(f"{name}: rows must not overlap")
-    return t.data_ptr(), stride
+def _rows2d(t, name, rows, i32, dev):
+    """Address, row stride and columns of an int32 [rows, n] tensor with
+    contiguous rows that do not overlap."""
+    shape = t.shape
+    if t.dtype is not i32 or t.get_device() != dev or len(shape) != 2 or shape[0] != rows:
+        raise SSDError(f"{name}: expected an int32 tensor of {rows} rows on cuda:{dev}, "
+                       f"got {t.dtype} {tuple(shape)} on {t.device}")
+    n = shape[1]
+    if t.is_contiguous():
+        return t.data_ptr(), n, n
+    if (n > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < n):
+        raise SSDError(f"{name}: rows must be contiguous and must not overlap")
+    return t.data_ptr(), max(t.stride(0), n), n
 
 
-def _use_stream(stream, tensors):
+def _rows3d(t):
+    """ssd_logits of a [B, N, V] tensor whose rows are evenly spaced."""
+    return _Logits(t.data_ptr(), SSD_BF16 if t.element_size() == 2 else SSD_F32, 0,
+                   t.shape[2]) if t.is_contiguous() else _logits(t)
+
+
+def _use_stream(stream, dev, tensors):
     """The stream's handle; memory taken from the current stream's pool is
     not given out again before `stream` is done with it."""
     torch = _torch()
-    current = torch.cuda.current_stream()
     if stream is None:
-        return current.cuda_stream
-    if stream != current:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream != torch.cuda.current_stream(dev):
         for t in tensors:
             t.record_stream(stream)
     return stream.cuda_stream
@@ -611,66 +609,69 @@ def process_logits(logits, history=None, history_len=None, prompt_len=None, draf
     the input itself), and with allowed=True ``allowed`` int32 [B, N], the
     number of tokens that the mask allows."""
     torch = _torch()
-    if logits.dim() != 3:
-        raise SSDError("expected logits [B, N, V]")
-    B, N, V = logits.shape
-    dev = logits.device
+    i32, f32 = torch.int32, torch.float32
+    shape = logits.shape
+    dev = logits.get_device()
+    if len(shape) != 3 or dev < 0 or logits.dtype not in (torch.bfloat16, f32):
+        raise SSDError("expected bfloat16 or float32 logits [B, N, V] on the GPU")
+    B, N, V = shape
     o = out if out is not None else {}
-    if "logits" not in o:
-        o["logits"] = torch.empty((B, N, V), dtype=logits.dtype, device=dev)
-    z = o["logits"]
-    if z.shape != logits.shape or z.dtype != logits.dtype or z.device != dev:
+    z = o.get("logits")
+    if z is None:
+        z = o["logits"] = torch.empty(shape, dtype=logits.dtype, device=logits.device)
+    elif z.shape != shape or z.dtype is not logits.dtype or z.get_device() != dev:
         raise SSDError("out logits must have the input's shape, type and device")
     count = None
     if allowed:
         if "allowed" not in o:
-            o["allowed"] = torch.empty((B, N), dtype=torch.int32, device=dev)
-        count = _tensor(o["allowed"], "allowed", torch.int32, (B, N), dev)
-    r = _LogitRules()
+            o["allowed"] = torch.empty((B, N), dtype=i32, device=logits.device)
+        count = _tensor(o["allowed"], "allowed", i32, (B, N), dev)
+    row = (B,)
+    h = h_stride = h_max = h_len = p_len = 0
     if history is not None:
         if history_len is None:
             raise SSDError("history needs history_len")
-        r.history, r.history_stride = _rows2d(history, "history", B, dev)
-        r.history_max = history.shape[1]
-        r.history_len = _tensor(history_len, "history_len", torch.int32, (B,), dev)
-        r.prompt_len = _tensor(prompt_len, "prompt_len", torch.int32, (B,), dev)
-    par = None
-    if parent is not None:
-        par = np.ascontiguousarray(parent, dtype=np.int32)
-        if par.shape != (N,):
-            raise SSDError("parent must have N entries")
-        r.parent = par.ctypes.data
+        h, h_stride, h_max = _rows2d(history, "history", B, i32, dev)
+        h_len = _tensor(history_len, "history_len", i32, row, dev)
+        if prompt_len is not None:
+            p_len = _tensor(prompt_len, "prompt_len", i32, row, dev)
+    drafts = d_stride = 0
     if draft_tokens is not None and N > 1:
-        ptr, r.draft_stride = _rows2d(draft_tokens, "draft_tokens", B, dev)
-        n = draft_tokens.shape[1]
-        if n not in (N - 1, N):
+        drafts, d_stride, n = _rows2d(draft_tokens, "draft_tokens", B, i32, dev)
+        if n != N - 1 and n != N:
             raise SSDError("draft_tokens must have N - 1 or N columns")
-        r.draft_tokens = ptr + 4 * (n - (N - 1))
-    r.repetition = _tensor(repetition, "repetition", torch.float32, (B,), dev)
-    r.presence = _tensor(presence, "presence", torch.float32, (B,), dev)
-    r.frequency = _tensor(frequency, "frequency", torch.float32, (B,), dev)
-    if (bias_ids is None) != (bias is None):
+        drafts += 4 * (n - N + 1)
+    if parent is not None:
+        if len(parent) != N:
+            raise SSDError("parent must have N entries")
+        parent = np.asarray(parent, dtype=np.int32).tobytes()
+    rep = 0 if repetition is None else _tensor(repetition, "repetition", f32, row, dev)
+    freq = 0 if frequency is None else _tensor(frequency, "frequency", f32, row, dev)
+    pres = 0 if presence is None else _tensor(presence, "presence", f32, row, dev)
+    n_bias = ids = values = 0
+    if bias_ids is not None and bias is not None:
+        ids, stride, n_bias = _rows2d(bias_ids, "bias_ids", B, i32, dev)
+        if stride != n_bias and B > 1:
+            raise SSDError("bias_ids must be contiguous")
+        values = _tensor(bias, "bias", f32, (B, n_bias), dev)
+    elif bias_ids is not bias:
         raise SSDError("bias_ids and bias go together")
-    if bias_ids is not None:
-        if bias_ids.dim() != 2:
-            raise SSDError("bias_ids: expected [B, n]")
-        r.n_bias = n = bias_ids.shape[1]
-        r.bias_ids = _tensor(bias_ids, "bias_ids", torch.int32, (B, n), dev)
-        r.bias = _tensor(bias, "bias", torch.float32, (B, n), dev)
+    m = m_seq = m_row = 0
     if mask is not None:
         W = (V + 31) // 32
-        if mask.dtype != torch.int32 or mask.device != dev or mask.dim() != 3 or \
-                mask.shape[0] not in (1, B) or mask.shape[1] not in (1, N) or \
-                mask.shape[2] != W or (W > 1 and mask.stride(2) != 1):
+        ms = mask.shape
+        if mask.dtype is not i32 or mask.get_device() != dev or len(ms) != 3 or ms[2] != W or \
+                ms[0] not in (1, B) or ms[1] not in (1, N) or (W > 1 and mask.stride(2) != 1):
             raise SSDError("mask: expected int32 words [B or 1, N or 1, ceil(V / 32)]")
-        r.mask = mask.data_ptr()
-        r.mask_seq_stride = mask.stride(0) if mask.shape[0] > 1 else 0
-        r.mask_row_stride = mask.stride(1) if mask.shape[1] > 1 else 0
-    r.fill = fill
-    st = lib().ssd_process_logits(ctypes.byref(_logits(logits)), ctypes.byref(_logits(z)), B, N, V,
-                                  ctypes.byref(r), count, _dev_ptr(dev_status),
-                                  _use_stream(stream, o.values()))
-    _check(st, "ssd_process_logits")
+        m, strides = mask.data_ptr(), mask.stride()
+        m_seq = strides[0] if ms[0] > 1 else 0
+        m_row = strides[1] if ms[1] > 1 else 0
+    r = _LogitRules(h, h_stride, h_max, n_bias, h_len, p_len, drafts, d_stride, parent, rep, freq,
+                    pres, ids, values, m, m_seq, m_row, fill, 0)
+    st = lib().ssd_process_logits(_rows3d(logits), _rows3d(z), B, N, V, r, count,
+                                  _dev_ptr(dev_status), _use_stream(stream, dev, o.values()))
+    if st:
+        _check(st, "ssd_process_logits")
     return o
 
 
@@ -687,38 +688,34 @@ def page_plan(lens, new, held, tables, free_pages, free_count, page_size, max_ro
     int32 [1].  `out`: the dict of an earlier call, to use its tensors again
     (not while its kv_len, held or free_count are this call's inputs)."""
     torch = _torch()
-    B = lens.shape[0] if lens.dim() == 1 else 0
-    dev, i32 = lens.device, torch.int32
-    T = int(max_rows)
+    i32 = torch.int32
+    dev = lens.get_device()
+    if dev < 0 or lens.dim() != 1:
+        raise SSDError("expected lengths [B] on the GPU")
+    B, T = lens.shape[0], int(max_rows)
+    row, rows, one = (B,), (T,), (1,)
     o = out if out is not None else {}
     if "slots" not in o:
-        o["slots"] = torch.empty(T, dtype=torch.int64, device=dev)
+        o["slots"] = torch.empty(T, dtype=torch.int64, device=lens.device)
         for name, n in (("positions", T), ("owner", T), ("cu", B + 1), ("kv_len", B),
                         ("held", B), ("served", B), ("free_count", 1)):
-            o[name] = torch.empty(n, dtype=i32, device=dev)
-    table_ptr, table_stride = _rows2d(tables, "tables", B, dev)
-    if not lens.is_cuda:
-        raise SSDError("expected CUDA tensors")
+            o[name] = torch.empty(n, dtype=i32, device=lens.device)
+    table, stride, cols = _rows2d(tables, "tables", B, i32, dev)
     st = lib().ssd_page_plan(
-        _tensor(lens, "lens", i32, (B,), dev), _tensor(new, "new", i32, (B,), dev),
-        _tensor(held, "held", i32, (B,), dev), B, table_ptr, table_stride, tables.shape[1],
+        _tensor(lens, "lens", i32, row, dev), _tensor(new, "new", i32, row, dev),
+        _tensor(held, "held", i32, row, dev), B, table, stride, cols,
         _tensor(free_pages, "free_pages", i32, free_pages.shape, dev), free_pages.numel(),
-        _tensor(free_count, "free_count", i32, (1,), dev), int(page_size), T,
-        _tensor(o["slots"], "slots", torch.int64, (T,), dev),
-        _tensor(o["positions"], "positions", i32, (T,), dev),
-        _tensor(o["owner"], "owner", i32, (T,), dev), _tensor(o["cu"], "cu", i32, (B + 1,), dev),
-        _tensor(o["kv_len"], "kv_len", i32, (B,), dev), _tensor(o["held"], "held", i32, (B,), dev),
-        _tensor(o["served"], "served", i32, (B,), dev),
-        _tensor(o["free_count"], "free_count", i32, (1,), dev), _dev_ptr(dev_status),
-        _use_stream(stream, o.values()))
-    _check(st, "ssd_page_plan")
+        _tensor(free_count, "free_count", i32, one, dev), int(page_size), T,
+        _tensor(o["slots"], "slots", torch.int64, rows, dev),
+        _tensor(o["positions"], "positions", i32, rows, dev),
+        _tensor(o["owner"], "owner", i32, rows, dev), _tensor(o["cu"], "cu", i32, (B + 1,), dev),
+        _tensor(o["kv_len"], "kv_len", i32, row, dev), _tensor(o["held"], "held", i32, row, dev),
+        _tensor(o["served"], "served", i32, row, dev),
+        _tensor(o["free_count"], "free_count", i32, one, dev), _dev_ptr(dev_status),
+        _use_stream(stream, dev, o.values()))
+    if st:
+        _check(st, "ssd_page_plan")
     return o
-
-
-def _paged(t):
-    if t.stride(3) != 1:
-        raise SSDError("the head dimension of the cache must be contiguous")
-    return _Paged(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
 
 
 def prefix_attention(q, k_cache, v_cache, prefix_tables, prefix_len, group_off, tables=None,
@@ -736,49 +733,52 @@ def prefix_attention(q, k_cache, v_cache, prefix_tables, prefix_len, group_off, 
     [R, Hq].  `out`: the dict of an earlier call of these shapes, to use its
     tensors and workspace again."""
     torch = _torch()
-    if q.dim() != 3 or k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
-        raise SSDError("expected q [R, Hq, D] and caches [pages, page_size, Hkv, D]")
-    R, Hq, D = q.shape
-    pages, page, Hkv, Dk = k_cache.shape
-    dev = q.device
-    dt = {torch.bfloat16: SSD_BF16, torch.float16: SSD_F16}.get(q.dtype)
-    if dt is None or k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
-        raise SSDError("q and the caches must share bfloat16 or float16")
-    if not q.is_cuda or k_cache.device != dev or v_cache.device != dev:
-        raise SSDError("q and the caches must be on one GPU")
-    if Dk != D or q.stride(2) != 1:
-        raise SSDError("q and the caches must share a contiguous head dimension")
-    o = out if out is not None else {}
-    if "out" not in o:
-        o["out"] = torch.empty((R, Hq, D), dtype=q.dtype, device=dev)
-        if lse:
-            o["lse"] = torch.empty((R, Hq), dtype=torch.float32, device=dev)
-    y = o["out"]
-    if y.shape != q.shape or y.dtype != q.dtype or y.device != dev or y.stride(2) != 1:
-        raise SSDError("out must have q's shape, type and device")
-    G = prefix_len.shape[0]
     i32 = torch.int32
-    a = _Attention(dt, R, Hq, Hkv, D, G, pages, page, q.data_ptr(), q.stride(0), q.stride(1),
-                   _paged(k_cache), _paged(v_cache))
-    a.prefix_tables, a.prefix_table_stride = _rows2d(prefix_tables, "prefix_tables", G, dev)
-    a.prefix_cols = prefix_tables.shape[1]
-    a.prefix_len = _tensor(prefix_len, "prefix_len", i32, (G,), dev)
-    a.group_off = _tensor(group_off, "group_off", i32, (G + 1,), dev)
-    if (tables is None) != (lens is None):
+    qs, ks, dt = q.shape, k_cache.shape, q.dtype
+    if len(qs) != 3 or len(ks) != 4 or v_cache.shape != ks or ks[3] != qs[2]:
+        raise SSDError("expected q [R, Hq, D] and caches [pages, page_size, Hkv, D]")
+    R, Hq, D = qs
+    code = SSD_BF16 if dt is torch.bfloat16 else SSD_F16 if dt is torch.float16 else -1
+    if code < 0 or k_cache.dtype is not dt or v_cache.dtype is not dt:
+        raise SSDError("q and the caches must share bfloat16 or float16")
+    dev = q.get_device()
+    if dev < 0 or k_cache.get_device() != dev or v_cache.get_device() != dev:
+        raise SSDError("q and the caches must be on one GPU")
+    o = out if out is not None else {}
+    y = o.get("out")
+    if y is None:
+        y = o["out"] = torch.empty(qs, dtype=dt, device=q.device)
+        if lse:
+            o["lse"] = torch.empty((R, Hq), dtype=torch.float32, device=q.device)
+    elif y.shape != qs or y.dtype is not dt or y.get_device() != dev:
+        raise SSDError("out must have q's shape, type and device")
+    q_at, k_at, v_at, y_at = q.stride(), k_cache.stride(), v_cache.stride(), y.stride()
+    if q_at[2] != 1 or k_at[3] != 1 or v_at[3] != 1 or y_at[2] != 1:
+        raise SSDError("the head dimension must be contiguous")
+    G = prefix_len.numel()
+    pt, pt_stride, pt_cols = _rows2d(prefix_tables, "prefix_tables", G, i32, dev)
+    t = t_stride = t_cols = n = 0
+    if tables is not None and lens is not None:
+        t, t_stride, t_cols = _rows2d(tables, "tables", R, i32, dev)
+        n = _tensor(lens, "lens", i32, (R,), dev)
+    elif tables is not lens:
         raise SSDError("tables and lens go together")
-    if tables is not None:
-        a.tables, a.table_stride = _rows2d(tables, "tables", R, dev)
-        a.cols = tables.shape[1]
-        a.lens = _tensor(lens, "lens", i32, (R,), dev)
-    a.out, a.out_row_stride, a.out_head_stride = y.data_ptr(), y.stride(0), y.stride(1)
-    a.lse = _tensor(o["lse"], "lse", torch.float32, (R, Hq), dev) if lse else None
-    a.scale = D ** -0.5 if scale is None else scale
+    a = _Attention(code, R, Hq, ks[2], D, G, ks[0], ks[1], q.data_ptr(), q_at[0], q_at[1],
+                   (k_cache.data_ptr(), k_at[0], k_at[1], k_at[2]),
+                   (v_cache.data_ptr(), v_at[0], v_at[1], v_at[2]), pt,
+                   _tensor(prefix_len, "prefix_len", i32, (G,), dev),
+                   _tensor(group_off, "group_off", i32, (G + 1,), dev), t, n, pt_stride, t_stride,
+                   pt_cols, t_cols, y.data_ptr(), y_at[0], y_at[1],
+                   _tensor(o["lse"], "lse", torch.float32, (R, Hq), dev) if lse else 0,
+                   D ** -0.5 if scale is None else scale, 0)
     L = lib()
     ws = workspace if workspace is not None else o.get("workspace")
     if ws is None:
-        need = L.ssd_prefix_attention_workspace_size(ctypes.byref(a))
-        ws = o["workspace"] = _workspace(need, dev)
-    st = L.ssd_prefix_attention(ctypes.byref(a), ws.data_ptr(), ws.numel(), _dev_ptr(dev_status),
-                                _use_stream(stream, (*o.values(), ws)))
-    _check(st, "ssd_prefix_attention")
+        ws = o["workspace"] = _workspace(L.ssd_prefix_attention_workspace_size(a), q.device)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise SSDError("the workspace must be a contiguous tensor on q's GPU")
+    st = L.ssd_prefix_attention(a, ws.data_ptr(), ws.numel() * ws.element_size(),
+                                _dev_ptr(dev_status), _use_stream(stream, dev, (*o.values(), ws)))
+    if st:
+        _check(st, "ssd_prefix_attention")
     return o

@@ -390,9 +390,11 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
 
 template <int DT>
 cudaError_t launch(const LogitParams& p, int64_t grid, size_t smem, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(
-      logits_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  if (smem > 46 * 1024) {  // more than a kernel may have without asking (48 KB with its static part)
+    const cudaError_t e = cudaFuncSetAttribute(
+        logits_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   logits_kernel<DT><<<(unsigned)grid, kThreads, smem, s>>>(p);
   return cudaGetLastError();
 }

@@ -223,8 +223,10 @@ extern "C" ssd_status ssd_page_plan(const int32_t* lens, const int32_t* new_toke
   const size_t smem = (size_t)3 * (B + 1) * sizeof(int);
   const int64_t work = std::max<int64_t>(max_rows / kRowsPerCta, B / kThreads);
   const int grid = (int)std::min<int64_t>(std::max(num_sms(), 1), 1 + work);
-  cudaError_t e = cudaFuncSetAttribute(
-      page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaSuccess;
+  if (smem > 46 * 1024)  // more than a kernel may have without asking
+    e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)smem);
   if (e == cudaSuccess) {
     page_plan_kernel<<<grid, kThreads, smem, static_cast<cudaStream_t>(stream)>>>(p);
     e = cudaGetLastError();

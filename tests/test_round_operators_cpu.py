@@ -27,8 +27,7 @@ def _logits_call(L, B=2, N=3, V=64, stride=64, dtype=0, out_dtype=0, out_ptr=2 *
     for k, v in rules:
         setattr(r, k, v)
     if parent is not None:
-        par = np.asarray(parent, dtype=np.int32)
-        r.parent = par.ctypes.data
+        r.parent = np.asarray(parent, dtype=np.int32).tobytes()
     return L.ssd_process_logits(ctypes.byref(a), ctypes.byref(b), B, N, V, ctypes.byref(r), None,
                                 None, None)
 
