@@ -303,6 +303,21 @@ inline WsLayout ws_layout(int groups, int rpg, int K, int V, int esize, int nch,
   return L;
 }
 
+// Division of numbers below 2^31 by a divisor known to the host: with
+// 2^s >= d, m = ceil(2^(32 + s) / d) - 2^32 gives n / d = (n + (n * m >> 32)) >> s.
+struct Divisor {
+  uint32_t d, m, s;
+  __device__ __forceinline__ int quotient(int n) const {
+    return (int)(((uint64_t)__umulhi((uint32_t)n, m) + (uint32_t)n) >> s);
+  }
+};
+inline Divisor divisor(int d) {
+  Divisor v{(uint32_t)d, 0, 0};
+  while ((1ull << v.s) < (uint64_t)d) ++v.s;
+  v.m = (uint32_t)(((1ull << (32 + v.s)) + d - 1) / (uint64_t)d - (1ull << 32));
+  return v;
+}
+
 // ---- launchers (ssd_stream_*.cu / ssd_cache.cu) ----------------------------------
 template <int DT>
 cudaError_t launch_stream_dt(const VerifyParams& p, int grid, cudaStream_t s);

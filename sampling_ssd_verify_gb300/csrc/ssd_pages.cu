@@ -26,7 +26,8 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxRequests = 8192;  // three sums each in shared memory
+constexpr int kMaxRequests = 8192;  // five numbers each in shared memory
+constexpr int kBatch = 4;           // new tokens per thread at a time
 constexpr int kRowsPerCta = 2048;   // new tokens per CTA before another one is added
 
 struct PageParams {
@@ -39,6 +40,7 @@ struct PageParams {
   int free_cap;
   const int32_t* free_count;
   int page, max_rows;
+  Divisor by_page;
   int64_t* slots;
   int32_t *positions, *owner, *cu, *kv_len, *held_out, *served, *free_out, *status;
 };
@@ -55,8 +57,10 @@ __device__ __forceinline__ Request request(const PageParams& p, int b) {
   q.held = p.held[b];
   const int64_t end = (int64_t)q.len + q.add;
   q.ok = q.len >= 0 && q.add >= 0 && q.held >= 0 && q.held <= p.cols &&
-         end <= min((int64_t)p.cols * p.page, (int64_t)0x7fffffff) && q.len <= (int64_t)q.held * p.page;
-  q.need = q.ok ? (int)((end + p.page - 1) / p.page) : q.held;
+         end <= min((int64_t)p.cols * p.page, (int64_t)0x7fffffff) &&
+         q.len <= (int64_t)q.held * p.page;
+  q.need = q.ok ? p.by_page.quotient((int)end) + (p.by_page.quotient((int)end) * p.page < end)
+                : q.held;
   if (!q.ok) q.add = 0;
   return q;
 }
@@ -81,6 +85,8 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const PageParams p)
   int* s_cu = s_sums;                   // [B + 1] new tokens before request b
   int* s_back = s_cu + p.B + 1;         // [B + 1] pages given back before it
   int* s_ask = s_back + p.B + 1;        // [B + 1] pages asked for before it
+  int* s_len = s_ask + p.B + 1;         // [B] its tokens,
+  int* s_held = s_len + p.B;            // [B] and pages
   __shared__ int64_t s_warp[3][kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n0 = *p.free_count;
@@ -122,6 +128,8 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const PageParams p)
     s_cu[b] = clamp32(run[0]);
     s_back[b] = clamp32(run[1]);
     s_ask[b] = clamp32(run[2]);
+    s_len[b] = q.len;
+    s_held[b] = q.held;
     run[0] += q.add;
     run[1] += max(q.held - q.need, 0);
     run[2] += max(q.need - q.held, 0);
@@ -137,45 +145,58 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const PageParams p)
   const int total = s_cu[p.B], back = s_back[p.B], ask = s_ask[p.B];
   const int64_t top = (int64_t)n + back;
 
-  // entry i of the stack with the returned pages on it, 0 <= i < top
-  auto stack = [&](int64_t i) {
-    if (i < n) return p.free_pages[i];
+  // where entry i of the stack with the returned pages on it is, 0 <= i < top
+  auto stack_at = [&](int64_t i) -> const int32_t* {
+    if (i < n) return p.free_pages + i;
     const int k = (int)(i - n);
-    const int b = find(s_back, p.B, k);
-    return p.tables[b * p.table_stride + request(p, b).need + (k - s_back[b])];
+    const int b = find(s_back, p.B, k);  // it gives back its last pages
+    return p.tables + b * p.table_stride + (s_held[b] - (s_back[b + 1] - k));
   };
   auto is_served = [&](const Request& q, int b) {
     return q.ok && (q.need <= q.held || (int64_t)s_ask[b + 1] <= top);
   };
 
   const int gtid = blockIdx.x * kThreads + tid, nthreads = gridDim.x * kThreads;
-  // ---- rows of the new tokens ----------------------------------------------------
-  for (int t = gtid; t < p.max_rows; t += nthreads) {
-    int64_t slot = -1;
-    int pos = -1, own = -1;
-    if (t < total) {
-      own = find(s_cu, p.B, t);
-      const Request q = request(p, own);
-      pos = q.len + (t - s_cu[own]);
-      if (is_served(q, own)) {
-        const int col = pos / p.page;
-        const int pg = col < q.held ? p.tables[own * p.table_stride + col]
-                                    : stack(top - 1 - (s_ask[own] + (col - q.held)));
-        slot = (int64_t)pg * p.page + (pos - col * p.page);
+  // ---- rows of the new tokens (of consistent requests only) -------------------------
+  for (int t0 = gtid; t0 < p.max_rows; t0 += nthreads * kBatch) {
+    const int32_t* from[kBatch];
+    int pos[kBatch], own[kBatch], off[kBatch], page[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int t = t0 + j * nthreads;
+      from[j] = nullptr;
+      pos[j] = own[j] = -1;
+      off[j] = 0;
+      if (t < p.max_rows && t < total) {
+        const int b = find(s_cu, p.B, t), held = s_held[b];
+        own[j] = b;
+        pos[j] = s_len[b] + (t - s_cu[b]);
+        const int col = p.by_page.quotient(pos[j]);
+        off[j] = pos[j] - col * p.page;
+        if (s_ask[b] == s_ask[b + 1] || (int64_t)s_ask[b + 1] <= top)  // served
+          from[j] = col < held ? p.tables + b * p.table_stride + col
+                               : stack_at(top - 1 - (s_ask[b] + (col - held)));
       }
     }
-    p.slots[t] = slot;
-    if (p.positions) p.positions[t] = pos;
-    if (p.owner) p.owner[t] = own;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) page[j] = from[j] ? *from[j] : 0;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int t = t0 + j * nthreads;
+      if (t >= p.max_rows) break;
+      p.slots[t] = from[j] ? (int64_t)page[j] * p.page + off[j] : -1;
+      if (p.positions) p.positions[t] = pos[j];
+      if (p.owner) p.owner[t] = own[j];
+    }
   }
   // ---- pages taken, pages given back ---------------------------------------------
   for (int64_t i = gtid; i < min((int64_t)ask, top); i += nthreads) {
     const int b = find(s_ask, p.B, (int)i);
     if ((int64_t)s_ask[b + 1] <= top)
-      p.tables[b * p.table_stride + p.held[b] + ((int)i - s_ask[b])] = stack(top - 1 - i);
+      p.tables[b * p.table_stride + s_held[b] + ((int)i - s_ask[b])] = *stack_at(top - 1 - i);
   }
   for (int k = gtid; k < back; k += nthreads)
-    if (n + (int64_t)k < p.free_cap) p.free_pages[n + k] = stack(n + (int64_t)k);
+    if (n + (int64_t)k < p.free_cap) p.free_pages[n + k] = *stack_at(n + (int64_t)k);
   // ---- the requests ----------------------------------------------------------------
   for (int b = gtid; b < p.B; b += nthreads) {
     const Request q = request(p, b);
@@ -218,9 +239,9 @@ extern "C" ssd_status ssd_page_plan(const int32_t* lens, const int32_t* new_toke
   if ((free_cap > 0 && !free_pages) || (max_rows > 0 && !slots)) return SSD_ERR_INVALID_ARG;
   if (B > kMaxRequests) return SSD_ERR_UNSUPPORTED;
   const PageParams p{lens,     new_tokens, held,  B, tables, table_stride, cols,
-                     free_pages, free_cap, free_count, page,    max_rows, slots, positions,
+                     free_pages, free_cap, free_count, page,    max_rows, divisor(page), slots, positions,
                      owner,    cu,         kv_len, held_out,   served, free_out,     dev_status};
-  const size_t smem = (size_t)3 * (B + 1) * sizeof(int);
+  const size_t smem = (size_t)5 * (B + 1) * sizeof(int);
   const int64_t work = std::max<int64_t>(max_rows / kRowsPerCta, B / kThreads);
   const int grid = (int)std::min<int64_t>(std::max(num_sms(), 1), 1 + work);
   cudaError_t e = cudaSuccess;
