@@ -41,7 +41,9 @@ constexpr int kMinSlice = 1024;
 constexpr int kMaxRows = 16;        // rows of a CTA: 8 KB of mask bits
 constexpr int kVecs = 2;            // vectors of a thread and step: 8 KB per CTA
 constexpr int kStages = 2;          // steps of the ring
-constexpr int kBatch = 8;           // history tokens in flight per thread
+constexpr int kBatch = 8;           // history tokens in flight per thread,
+constexpr int kBiasBatch = 2;       // biases
+static_assert(kMaxTreeNodes <= kThreads, "a draft per thread");
 constexpr uint32_t kPromptBit = 0x80000000u;  // counts word: token occurs in the prompt,
 constexpr uint32_t kDraftBit = 0x40000000u;   // among the drafts of some row
 constexpr uint32_t kCountBits = kDraftBit - 1;
@@ -193,21 +195,30 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
 #pragma unroll
   for (int d = 0; d < kStages - 1; ++d) fetch_next(d);
 
-  // ---- the sequence's rules -----------------------------------------------------
-  Rules ru{1.f, 1.f, 0.f, 0.f, r.bias + b * r.n_bias, s_tok, s_parent};
-  int bad = 0;
-  if (r.repetition) {
-    ru.rep = r.repetition[b];
-    if (!(ru.rep > 0.f) || isinf(ru.rep)) { ru.rep = 1.f; bad = SSD_DEV_BAD_PENALTY; }
+  // ---- what the sequence's rules say: all loads first, so that they wait for memory
+  // together (a CTA lives for about 20 us) ------------------------------------------
+  float rep = 1.f, freq = 0.f, pres = 0.f;
+  int len = 0, prompt = 0, tok = 0, h[kBatch], id[kBiasBatch];
+  const int32_t* hist = r.history + b * r.history_stride;
+  const int32_t* ids = r.bias_ids + b * r.n_bias;
+  if (r.repetition) rep = r.repetition[b];
+  if (r.frequency) freq = r.frequency[b];
+  if (r.presence) pres = r.presence[b];
+  if (r.history) {
+    len = r.history_len[b];
+    if (r.prompt_len) prompt = r.prompt_len[b];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {  // before the length is known
+      const int i = tid + j * kThreads;
+      h[j] = i < r.history_max ? hist[i] : 0;
+    }
   }
-  ru.inv = 1.f / ru.rep;
-  if (r.frequency) {
-    ru.freq = r.frequency[b];
-    if (!isfinite(ru.freq)) { ru.freq = 0.f; bad = SSD_DEV_BAD_PENALTY; }
-  }
-  if (r.presence) {
-    ru.pres = r.presence[b];
-    if (!isfinite(ru.pres)) { ru.pres = 0.f; bad = SSD_DEV_BAD_PENALTY; }
+  const bool draft = r.draft_tokens && tid > 0 && tid < p.N;  // N <= kThreads
+  if (draft) tok = r.draft_tokens[b * r.draft_stride + tid - 1];
+#pragma unroll
+  for (int j = 0; j < kBiasBatch; ++j) {
+    const int i = tid + j * kThreads;
+    id[j] = i < r.n_bias ? ids[i] : -1;
   }
 
   // ---- counts of the slice's tokens ---------------------------------------------
@@ -216,65 +227,73 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
   if (r.n_bias)
     for (int i = tid; i < p.slice / 8; i += kThreads)
       reinterpret_cast<uint4*>(bias_at)[i] = make_uint4(0u, 0u, 0u, 0u);
-  if (r.draft_tokens)
-    for (int u = 1 + tid; u < p.N; u += kThreads) {
-      const int t = r.draft_tokens[b * r.draft_stride + u - 1];
-      s_tok[u] = t;
-      s_parent[u] = p.parent[u];
-      if ((unsigned)t >= (unsigned)p.V) bad |= SSD_DEV_BAD_TOKEN;
-    }
+  int bad = 0;
+  if (!(rep > 0.f) || isinf(rep)) { rep = 1.f; bad = SSD_DEV_BAD_PENALTY; }
+  if (!isfinite(freq)) { freq = 0.f; bad = SSD_DEV_BAD_PENALTY; }
+  if (!isfinite(pres)) { pres = 0.f; bad = SSD_DEV_BAD_PENALTY; }
+  const Rules ru{rep, 1.f / rep, freq, pres, r.bias + b * r.n_bias, s_tok, s_parent};
+  if (len < 0 || len > r.history_max) {
+    bad |= SSD_DEV_BAD_LENGTH;
+    len = min(max(len, 0), r.history_max);
+  }
   __syncthreads();
-  if (r.history) {
-    int len = r.history_len[b];
-    int prompt = r.prompt_len ? r.prompt_len[b] : 0;
-    if (len < 0 || len > r.history_max) {
-      bad |= SSD_DEV_BAD_LENGTH;
-      len = min(max(len, 0), r.history_max);
+
+  auto touch = [&](int k) { atomicOr(&touched[k >> 5], 1u << (k & 31)); };
+  for (int i0 = tid; i0 < len;) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + j * kThreads, k = h[j] - v0;
+      if (i >= len) break;
+      if ((unsigned)h[j] >= (unsigned)p.V) {
+        bad |= SSD_DEV_BAD_TOKEN;
+      } else if ((unsigned)k < (unsigned)nv) {
+        if (i < prompt) atomicOr(&count[k], kPromptBit);
+        else atomicAdd(&count[k], 1u);
+        touch(k);
+      }
     }
-    const int32_t* h = r.history + b * r.history_stride;
-    for (int i0 = tid; i0 < len; i0 += kThreads * kBatch) {
-      int t[kBatch];
+    i0 += kThreads * kBatch;
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int i = i0 + j * kThreads;
-        t[j] = i < len ? h[i] : 0;
-      }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int i = i0 + j * kThreads, k = t[j] - v0;
-        if (i >= len) break;
-        if ((unsigned)t[j] >= (unsigned)p.V) {
-          bad |= SSD_DEV_BAD_TOKEN;
-        } else if ((unsigned)k < (unsigned)nv) {
-          if (i < prompt) atomicOr(&count[k], kPromptBit);
-          else atomicAdd(&count[k], 1u);
-          atomicOr(&touched[k >> 5], 1u << (k & 31));
-        }
-      }
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + j * kThreads;
+      h[j] = i < len ? hist[i] : 0;
     }
   }
-  if (r.draft_tokens)
-    for (int u = 1 + tid; u < p.N; u += kThreads) {
-      const int t = s_tok[u], k = t - v0;
-      if ((unsigned)t < (unsigned)p.V && (unsigned)k < (unsigned)nv) {
-        atomicOr(&count[k], kDraftBit);
-        atomicOr(&touched[k >> 5], 1u << (k & 31));
+  if (draft) {
+    const int k = tok - v0;
+    s_tok[tid] = tok;
+    s_parent[tid] = p.parent[tid];
+    if ((unsigned)tok >= (unsigned)p.V) {
+      bad |= SSD_DEV_BAD_TOKEN;
+    } else if ((unsigned)k < (unsigned)nv) {
+      atomicOr(&count[k], kDraftBit);
+      touch(k);
+    }
+  }
+  for (int i0 = tid; i0 < r.n_bias;) {
+#pragma unroll
+    for (int j = 0; j < kBiasBatch; ++j) {
+      const int i = i0 + j * kThreads, k = id[j] - v0;
+      if (i >= r.n_bias) break;
+      if (id[j] >= p.V) {
+        bad |= SSD_DEV_BAD_TOKEN;
+      } else if (id[j] >= 0 && (unsigned)k < (unsigned)nv) {
+        // the latest entry of a token holds: the largest index + 1
+        unsigned short* at = &bias_at[k];
+        unsigned short old = *at;
+        while (old < (unsigned short)(i + 1)) {
+          const unsigned short seen = atomicCAS(at, old, (unsigned short)(i + 1));
+          if (seen == old) break;
+          old = seen;
+        }
+        touch(k);
       }
     }
-  for (int i = tid; i < r.n_bias; i += kThreads) {
-    const int t = r.bias_ids[b * r.n_bias + i], k = t - v0;
-    if (t >= p.V) {
-      bad |= SSD_DEV_BAD_TOKEN;
-    } else if (t >= 0 && (unsigned)k < (unsigned)nv) {
-      // the latest entry of a token holds: the largest index + 1
-      unsigned short* at = &bias_at[k];
-      unsigned short old = *at;
-      while (old < (unsigned short)(i + 1)) {
-        const unsigned short seen = atomicCAS(at, old, (unsigned short)(i + 1));
-        if (seen == old) break;
-        old = seen;
-      }
-      atomicOr(&touched[k >> 5], 1u << (k & 31));
+    i0 += kThreads * kBiasBatch;
+#pragma unroll
+    for (int j = 0; j < kBiasBatch; ++j) {
+      const int i = i0 + j * kThreads;
+      id[j] = i < r.n_bias ? ids[i] : -1;
     }
   }
   if (bad && p.status) atomicOr(p.status, bad);
