@@ -14,12 +14,13 @@
 // has a bit of its own in its count, and the few such tokens walk the path of
 // their row when they are met, so that the rows need no counts of their own.
 //
-// A warp streams its own vectors through its own part of a ring in shared
-// memory, filled by asynchronous copies, four vectors per thread a step.  A
-// bitmap tells which tokens of a vector are touched; the warp lists those of a
-// step and shares them out evenly, a token per lane (one in thirty is touched
-// after 4096 tokens: each lane by itself would take its hits one after the
-// other, with most lanes idle).  No barrier stands between the rows.
+// A warp streams its own vectors, 64 in a row of a step, through its own part of
+// a ring in shared memory, filled by asynchronous copies.  Which of its tokens
+// are touched is the same in every row, so they are listed once; in each row the
+// warp first adjusts those in the ring, one per lane (one token in thirty is
+// touched after 4096), and then streams the vectors through the mask.  What
+// bounds the kernel next to memory is what it issues: 241 instructions per warp
+// and vector when touched tokens were looked for in every vector of every row.
 //
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -41,6 +42,7 @@ constexpr int kMinSlice = 1024;
 constexpr int kMaxRows = 16;        // rows of a CTA: 8 KB of mask bits
 constexpr int kVecs = 2;            // vectors of a thread and step: 8 KB per CTA
 constexpr int kStages = 2;          // steps of the ring
+constexpr int kMaxLists = kMaxSlice / (kVecs * 32 * 4);  // touched tokens, per warp and step
 constexpr int kBatch = 8;           // history tokens in flight per thread,
 constexpr int kBiasBatch = 2;       // biases
 static_assert(kMaxTreeNodes <= kThreads, "a draft per thread");
@@ -114,18 +116,47 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t* map, int k) {
   return __funnelshift_r(map[k >> 5], map[(k >> 5) + 1], k & 31);
 }
 
+// The top bits of four bytes, chosen by `which`, each repeated over its byte.
+__device__ __forceinline__ uint32_t tops(uint32_t x, uint32_t which) {
+  uint32_t y;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(y) : "r"(x), "r"(which));
+  return y;
+}
+
+// A vector with the tokens whose bit is not set replaced.
 template <int DT>
-__global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant__ LogitParams p) {
+__device__ __forceinline__ uint4 masked(uint4 x, uint32_t ok,
+                                        typename Elem<DT>::type fill) {
+  if constexpr (DT == SSD_BF16) {
+    // four bits to the top of four bytes, then each spread over two bytes
+    const uint32_t lo = (ok & 15u) * 0x10204080u & 0x80808080u;
+    const uint32_t hi = (ok >> 4) * 0x10204080u & 0x80808080u;
+    const uint32_t m0 = tops(lo, 0x9988), m1 = tops(lo, 0xbbaa);
+    const uint32_t m2 = tops(hi, 0x9988), m3 = tops(hi, 0xbbaa);
+    const uint32_t f = (uint32_t)fill * 0x10001u;
+    return make_uint4((x.x & m0) | (f & ~m0), (x.y & m1) | (f & ~m1), (x.z & m2) | (f & ~m2),
+                      (x.w & m3) | (f & ~m3));
+  } else {
+    const uint32_t f = __float_as_uint(fill);
+    return make_uint4(ok & 1u ? x.x : f, ok & 2u ? x.y : f, ok & 4u ? x.z : f, ok & 8u ? x.w : f);
+  }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_constant__ LogitParams p) {
   using E = typename Elem<DT>::type;
   constexpr int VE = 16 / (int)sizeof(E);  // tokens of a vector
   constexpr uint32_t kAll = (1u << VE) - 1u;
   extern __shared__ uint4 smem4[];
-  uint4* ring = smem4;                                              // [kStages][kVecs][kThreads]
-  constexpr int kHits = kVecs * 32 * VE;                            // tokens of a warp and step
-  uint16_t* list = reinterpret_cast<uint16_t*>(ring + kStages * kVecs * kThreads) +
-                   (threadIdx.x >> 5) * kHits;
-  uint32_t* count =                                                 // [slice]
-      reinterpret_cast<uint32_t*>(list + (kThreads / 32 - (threadIdx.x >> 5)) * kHits);
+  constexpr int kStep = kVecs * kThreads;                           // vectors of a step
+  uint4* ring = smem4;                                              // [kStages][kStep]
+  // Touched tokens of each warp and step: those whose vector is the warp's in a
+  // row that starts on a vector, or the one after (rows that do not start on one
+  // shift their vectors by less than a vector).
+  constexpr int kList = (kVecs * 32 + 1) * VE;
+  const int lists = (p.slice + kStep * VE - 1) / (kStep * VE) * (kThreads / 32);
+  uint16_t* list = reinterpret_cast<uint16_t*>(ring + kStages * kStep);  // [lists][kList]
+  uint32_t* count = reinterpret_cast<uint32_t*>(list + lists * kList);   // [slice]
   uint32_t* touched = count + p.slice;                              // [slice / 32 + 4]
   const int words = p.slice / 32 + 4;
   uint32_t* bits = touched + words;                                 // [rows][words] if a mask
@@ -133,6 +164,7 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
   __shared__ int s_tok[kMaxTreeNodes];
   __shared__ int16_t s_parent[kMaxTreeNodes];
   __shared__ int s_sum[kThreads / 32];
+  __shared__ int s_listed[kMaxLists];
 
   const int tid = threadIdx.x;
   const int64_t cta = blockIdx.x;
@@ -145,38 +177,45 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
   const ssd_logit_rules& r = p.r;
 
   // ---- the rows' vectors: steps of kVecs * kThreads, alike for the whole CTA ----------
-  constexpr int kStep = kVecs * kThreads;
   struct Place {
     int u, i;               // row, its first vector of the step
     const E* in;            // the slice of the row
+    E* out;
     int head, nvec;         // tokens before its first whole vector, vectors
   };
-  auto row_at = [&](Place& q) {
-    q.in = static_cast<const E*>(p.in) + (b * p.N + q.u) * p.in_stride + v0;
-    const E* out = static_cast<const E*>(p.out) + (b * p.N + q.u) * p.out_stride + v0;
+  auto measure = [&](Place& q) {
     const uint32_t mis = (uint32_t)(uintptr_t)q.in & 15u;
-    const bool vec = mis == ((uint32_t)(uintptr_t)out & 15u);
+    const bool vec = mis == ((uint32_t)(uintptr_t)q.out & 15u);
     q.head = vec ? min(nv, (int)((16u - mis) & 15u) / (int)sizeof(E)) : nv;
     q.nvec = (nv - q.head) / VE;
     q.i = 0;
   };
-  auto settle = [&](Place& q) {  // to the next row that has vectors
-    while (q.u < u1 && q.i >= q.nvec)
-      if (++q.u < u1) row_at(q);
+  auto next_row = [&](Place& q) {
+    q.in += p.in_stride;
+    q.out += p.out_stride;
+    ++q.u;
+    measure(q);
   };
-  Place ahead;
-  ahead.u = u0;
-  row_at(ahead);
+  auto settle = [&](Place& q) {  // to the next row that has vectors
+    while (q.u < u1 && q.i >= q.nvec) next_row(q);
+  };
+  Place first;
+  first.u = u0;
+  first.in = static_cast<const E*>(p.in) + (b * p.N + u0) * p.in_stride + v0;
+  first.out = static_cast<E*>(p.out) + (b * p.N + u0) * p.out_stride + v0;
+  measure(first);
+  Place ahead = first;
   settle(ahead);
   Place at = ahead;
+  const int lane = tid & 31, warp = tid >> 5, mine = warp * kVecs * 32;
+  const uint32_t my_ring = smem_addr(ring + mine + lane);
   auto fetch_next = [&](int stage) {
     if (ahead.u < u1) {
-      const uint4* in = reinterpret_cast<const uint4*>(ahead.in + ahead.head);
+      const uint4* in = reinterpret_cast<const uint4*>(ahead.in + ahead.head) + ahead.i + mine + lane;
 #pragma unroll
-      for (int j = 0; j < kVecs; ++j) {
-        const int i = ahead.i + j * kThreads + tid;
-        if (i < ahead.nvec) fetch(smem_addr(ring + stage * kStep + j * kThreads + tid), in + i);
-      }
+      for (int j = 0; j < kVecs; ++j)
+        if (ahead.i + mine + j * 32 + lane < ahead.nvec)
+          fetch(my_ring + (stage * kStep + j * 32) * 16, in + j * 32);
       ahead.i += kStep;
       settle(ahead);
     }
@@ -302,81 +341,86 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
   fetch_wait<kStages - 1>();  // the mask bits
   __syncthreads();
 
-  const int lane = tid & 31;
+  // ---- the touched tokens of each warp and step ------------------------------------------
+  for (int s = warp; s < lists; s += kThreads / 32) {
+    const int from = s * kVecs * 32 * VE, to = min(from + kList, p.slice);
+    int n = 0;
+    for (int w0 = from; w0 < to; w0 += 32 * 32) {  // a word of the bitmap per lane
+      const int k = w0 + lane * 32;
+      uint32_t m = k < to ? touched[k >> 5] : 0u;
+      if (to - k < 32 && k < to) m &= (1u << (to - k)) - 1u;
+      int before = __popc(m);
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, before, d);
+        if (lane >= d) before += y;
+      }
+      const int all = __shfl_sync(0xffffffffu, before, 31);
+      before += n - __popc(m);
+      for (; m != 0u; m &= m - 1u) list[s * kList + before++] = (uint16_t)(k + __ffs(m) - 1);
+      n += all;
+    }
+    if (lane == 0) s_listed[s] = n;
+  }
+  __syncthreads();
+
+  int row_step = warp;  // the warp's list of this step
   for (int stage = 0; at.u < u1; stage = (stage + 1) % kStages) {
     fetch_next((stage + kStages - 1) % kStages);
     fetch_wait<kStages - 1>();
     __syncwarp();  // the warp's copies are there for all its lanes
-    E* out = static_cast<E*>(p.out) + (b * p.N + at.u) * p.out_stride + v0;
     const uint32_t* allow = bits + (at.u - u0) * words;
-    const int k0 = at.head + at.i * VE;  // the step's first token
-    uint32_t hit[kVecs];
-    int n = 0;
+    uint4* mem = ring + stage * kStep + mine;
+    const int i0 = at.i + mine;         // the warp's first vector
+    const int n = s_listed[row_step];
+    for (int t = lane; t < n; t += 32) {
+      const int k = list[row_step * kList + t], d = k - at.head, i = d / VE;
+      if (d < 0 || (unsigned)(i - i0) >= (unsigned)(kVecs * 32) || i >= at.nvec) continue;
+      if (r.mask && !(allow[k >> 5] >> (k & 31) & 1u)) continue;
+      E* z = reinterpret_cast<E*>(mem + (i - i0)) + d % VE;
+      *z = Elem<DT>::store(adjust(Elem<DT>::load(*z), count[k], r.n_bias ? bias_at[k] : 0u, ru,
+                                  v0 + k, at.u));
+    }
+    __syncwarp();
+    uint4* out = reinterpret_cast<uint4*>(at.out + at.head) + i0 + lane;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-      const int i = at.i + j * kThreads + tid, k = at.head + i * VE;
-      hit[j] = 0u;
+      const int i = i0 + j * 32 + lane;
       if (i < at.nvec) {
-        const uint4 x = ring[stage * kStep + j * kThreads + tid];
-        uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        const uint32_t ok = r.mask ? bits_at(allow, k) & kAll : kAll;
-        hit[j] = bits_at(touched, k) & ok;
-        if (ok != kAll) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if constexpr (DT == SSD_BF16) {
-              const uint32_t m = (ok >> (2 * q) & 1u ? 0xffffu : 0u) |
-                                 (ok >> (2 * q + 1) & 1u ? 0xffff0000u : 0u);
-              w[q] = (w[q] & m) | (((uint32_t)fill * 0x10001u) & ~m);
-            } else {
-              w[q] = ok >> q & 1u ? w[q] : __float_as_uint(fill);
-            }
-          }
+        uint4 x = mem[j * 32 + lane];
+        if (r.mask) {
+          uint32_t ok;
+          if (at.head != 0)
+            ok = bits_at(allow, at.head + i * VE) & kAll;
+          else if constexpr (VE == 8)
+            ok = reinterpret_cast<const uint8_t*>(allow)[i];
+          else
+            ok = reinterpret_cast<const uint8_t*>(allow)[i >> 1] >> (i & 1) * 4 & 15u;
+          if (ok != kAll) x = masked<DT>(x, ok, fill);
         }
-        __stcs(reinterpret_cast<uint4*>(out + k), make_uint4(w[0], w[1], w[2], w[3]));
-        n += __popc(hit[j]);
+        __stcs(out + j * 32, x);
       }
     }
-    // the touched tokens of the warp's vectors, listed and then taken one per lane
-    int before = n;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, before, d);
-      if (lane >= d) before += y;
-    }
-    const int total = __shfl_sync(0xffffffffu, before, 31);
-    before -= n;
-#pragma unroll
-    for (int j = 0; j < kVecs; ++j)
-      for (uint32_t h = hit[j]; h != 0u; h &= h - 1u)
-        list[before++] = (uint16_t)((j * kThreads + tid) * VE + __ffs(h) - 1);
-    __syncwarp();
-    const E* raw = reinterpret_cast<const E*>(ring + stage * kStep);
-    for (int t = lane; t < total; t += 32) {
-      const int e = list[t], k = k0 + e;
-      const float z = adjust(Elem<DT>::load(raw[e]), count[k], r.n_bias ? bias_at[k] : 0u, ru,
-                             v0 + k, at.u);
-      out[k] = Elem<DT>::store(z);
-    }
-    __syncwarp();  // list and ring are read
+    __syncwarp();  // the ring is read
     at.i += kStep;
-    settle(at);
+    row_step += kThreads / 32;
+    if (at.i >= at.nvec) {
+      row_step = warp;
+      settle(at);
+    }
   }
 
   const int last_word = (p.V - 1) >> 5;
   for (int u = u0; u < u1; ++u) {
     // ---- the ends of rows that are not aligned, token by token -------------------------
-    Place q;
-    q.u = u;
-    row_at(q);
-    E* out = static_cast<E*>(p.out) + (b * p.N + u) * p.out_stride + v0;
+    const Place& q = first;
     auto single = [&](int k) {
       E e = q.in[k];
       if (touched[k >> 5] >> (k & 31) & 1u)
         e = Elem<DT>::store(adjust(Elem<DT>::load(e), count[k], r.n_bias ? bias_at[k] : 0u, ru,
                                    v0 + k, u));
       if (r.mask && !(bits[(u - u0) * words + (k >> 5)] >> (k & 31) & 1u)) e = fill;
-      out[k] = e;
+      q.out[k] = e;
     };
     for (int k = tid; k < q.head; k += kThreads) single(k);
     for (int k = q.head + q.nvec * VE + tid; k < nv; k += kThreads) single(k);
@@ -404,6 +448,7 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
       }
       __syncthreads();  // s_sum is read
     }
+    next_row(first);
   }
 }
 
@@ -476,8 +521,10 @@ extern "C" ssd_status ssd_process_logits(const ssd_logits* in, const ssd_logits*
   if (grid > 0x7fffffff) return SSD_ERR_UNSUPPORTED;
   const size_t words = p.slice / 32 + 4;
   const int ve = in->dtype == SSD_BF16 ? 8 : 4;
-  const size_t smem = (size_t)kStages * kVecs * kThreads * 16 + kVecs * kThreads * ve * 2 +
-                      (p.slice + words) * 4 +
+  const size_t lists = (p.slice + kVecs * kThreads * ve - 1) / (kVecs * kThreads * ve) *
+                       (kThreads / 32);
+  const size_t smem = (size_t)kStages * kVecs * kThreads * 16 +
+                      lists * (kVecs * 32 + 1) * ve * 2 + (p.slice + words) * 4 +
                       (r.mask ? p.rows * words * 4 : 0) + (r.n_bias ? p.slice * 2 : 0);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = in->dtype == SSD_BF16 ? launch<SSD_BF16>(p, grid, smem, s)
