@@ -40,9 +40,7 @@ constexpr int kThreads = 256;
 constexpr int kMaxSlice = 4096;     // tokens of a slice: 16 KB of counts, 8 KB of bias entries
 constexpr int kMinSlice = 1024;
 constexpr int kMaxRows = 16;        // rows of a CTA: 8 KB of mask bits
-constexpr int kVecs = 2;            // vectors of a thread and step: 8 KB per CTA
 constexpr int kStages = 2;          // steps of the ring
-constexpr int kMaxLists = kMaxSlice / (kVecs * 32 * 4);  // touched tokens, per warp and step
 constexpr int kBatch = 8;           // history tokens in flight per thread,
 constexpr int kBiasBatch = 2;       // biases
 static_assert(kMaxTreeNodes <= kThreads, "a draft per thread");
@@ -64,13 +62,16 @@ struct LogitParams {
   int16_t parent[kMaxTreeNodes];
 };
 
+// A step is a slice of kMaxSlice tokens: kVecs vectors per thread.
 template <int DT> struct Elem;
 template <> struct Elem<SSD_BF16> {
+  static constexpr int kVecs = 2;
   using type = uint16_t;
   static __device__ float load(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
   static __device__ uint16_t store(float z) { return __bfloat16_as_ushort(__float2bfloat16_rn(z)); }
 };
 template <> struct Elem<SSD_F32> {
+  static constexpr int kVecs = 4;
   using type = float;
   static __device__ float load(float x) { return x; }
   static __device__ float store(float z) { return z; }
@@ -146,15 +147,17 @@ template <int DT>
 __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_constant__ LogitParams p) {
   using E = typename Elem<DT>::type;
   constexpr int VE = 16 / (int)sizeof(E);  // tokens of a vector
+  constexpr int kVecs = Elem<DT>::kVecs;
+  static_assert(kVecs * kThreads * VE == kMaxSlice, "a step per row");
   constexpr uint32_t kAll = (1u << VE) - 1u;
   extern __shared__ uint4 smem4[];
   constexpr int kStep = kVecs * kThreads;                           // vectors of a step
   uint4* ring = smem4;                                              // [kStages][kStep]
-  // Touched tokens of each warp and step: those whose vector is the warp's in a
+  // Touched tokens of each warp: those whose vector is the warp's in a
   // row that starts on a vector, or the one after (rows that do not start on one
   // shift their vectors by less than a vector).
   constexpr int kList = (kVecs * 32 + 1) * VE;
-  const int lists = (p.slice + kStep * VE - 1) / (kStep * VE) * (kThreads / 32);
+  constexpr int lists = kThreads / 32;
   uint16_t* list = reinterpret_cast<uint16_t*>(ring + kStages * kStep);  // [lists][kList]
   uint32_t* count = reinterpret_cast<uint32_t*>(list + lists * kList);   // [slice]
   uint32_t* touched = count + p.slice;                              // [slice / 32 + 4]
@@ -164,7 +167,6 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
   __shared__ int s_tok[kMaxTreeNodes];
   __shared__ int16_t s_parent[kMaxTreeNodes];
   __shared__ int s_sum[kThreads / 32];
-  __shared__ int s_listed[kMaxLists];
 
   const int tid = threadIdx.x;
   const int64_t cta = blockIdx.x;
@@ -178,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
 
   // ---- the rows' vectors: steps of kVecs * kThreads, alike for the whole CTA ----------
   struct Place {
-    int u, i;               // row, its first vector of the step
+    int u;                  // row
     const E* in;            // the slice of the row
     E* out;
     int head, nvec;         // tokens before its first whole vector, vectors
@@ -188,16 +190,17 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
     const bool vec = mis == ((uint32_t)(uintptr_t)q.out & 15u);
     q.head = vec ? min(nv, (int)((16u - mis) & 15u) / (int)sizeof(E)) : nv;
     q.nvec = (nv - q.head) / VE;
-    q.i = 0;
   };
+  // rows that start alike have the same head and vectors
+  const bool alike = ((p.in_stride | p.out_stride) * (int64_t)sizeof(E)) % 16 == 0;
   auto next_row = [&](Place& q) {
     q.in += p.in_stride;
     q.out += p.out_stride;
     ++q.u;
-    measure(q);
+    if (!alike) measure(q);
   };
   auto settle = [&](Place& q) {  // to the next row that has vectors
-    while (q.u < u1 && q.i >= q.nvec) next_row(q);
+    while (q.u < u1 && q.nvec == 0) next_row(q);
   };
   Place first;
   first.u = u0;
@@ -211,12 +214,12 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
   const uint32_t my_ring = smem_addr(ring + mine + lane);
   auto fetch_next = [&](int stage) {
     if (ahead.u < u1) {
-      const uint4* in = reinterpret_cast<const uint4*>(ahead.in + ahead.head) + ahead.i + mine + lane;
+      const uint4* in = reinterpret_cast<const uint4*>(ahead.in + ahead.head) + mine + lane;
 #pragma unroll
       for (int j = 0; j < kVecs; ++j)
-        if (ahead.i + mine + j * 32 + lane < ahead.nvec)
+        if (mine + j * 32 + lane < ahead.nvec)
           fetch(my_ring + (stage * kStep + j * 32) * 16, in + j * 32);
-      ahead.i += kStep;
+      next_row(ahead);
       settle(ahead);
     }
     fetch_commit();
@@ -224,10 +227,10 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
   // the rows' mask bits, then the first vectors: both arrive while the counts are made
   if (r.mask) {
     const int w0 = v0 >> 5, per = min(p.slice / 32 + 1, ((p.V - 1) >> 5) + 1 - w0);
-    const int32_t* m = r.mask + b * r.mask_seq_stride + w0;
-    for (int i = tid; i < (u1 - u0) * per; i += kThreads) {
-      const int u = i / per, w = i - u * per;
-      fetch4(smem_addr(bits + u * words + w), m + (u0 + u) * r.mask_row_stride + w);
+    for (int u = u0 + warp; u < u1; u += kThreads / 32) {
+      const int32_t* m = r.mask + b * r.mask_seq_stride + u * r.mask_row_stride + w0;
+      const uint32_t d = smem_addr(bits + (u - u0) * words);
+      for (int i = lane; i < per; i += 32) fetch4(d + i * 4, m + i);
     }
   }
   fetch_commit();
@@ -341,14 +344,15 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
   fetch_wait<kStages - 1>();  // the mask bits
   __syncthreads();
 
-  // ---- the touched tokens of each warp and step ------------------------------------------
-  for (int s = warp; s < lists; s += kThreads / 32) {
-    const int from = s * kVecs * 32 * VE, to = min(from + kList, p.slice);
-    int n = 0;
+  // ---- the touched tokens of each warp ----------------------------------------------------
+  uint16_t* my_list = list + warp * kList;
+  int n = 0;
+  {
+    const int from = mine * VE, to = min(from + kList, p.slice);
     for (int w0 = from; w0 < to; w0 += 32 * 32) {  // a word of the bitmap per lane
       const int k = w0 + lane * 32;
       uint32_t m = k < to ? touched[k >> 5] : 0u;
-      if (to - k < 32 && k < to) m &= (1u << (to - k)) - 1u;
+      if (k < to && to - k < 32) m &= (1u << (to - k)) - 1u;
       int before = __popc(m);
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -357,35 +361,30 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
       }
       const int all = __shfl_sync(0xffffffffu, before, 31);
       before += n - __popc(m);
-      for (; m != 0u; m &= m - 1u) list[s * kList + before++] = (uint16_t)(k + __ffs(m) - 1);
+      for (; m != 0u; m &= m - 1u) my_list[before++] = (uint16_t)(k + __ffs(m) - 1);
       n += all;
     }
-    if (lane == 0) s_listed[s] = n;
   }
-  __syncthreads();
 
-  int row_step = warp;  // the warp's list of this step
   for (int stage = 0; at.u < u1; stage = (stage + 1) % kStages) {
     fetch_next((stage + kStages - 1) % kStages);
     fetch_wait<kStages - 1>();
     __syncwarp();  // the warp's copies are there for all its lanes
     const uint32_t* allow = bits + (at.u - u0) * words;
     uint4* mem = ring + stage * kStep + mine;
-    const int i0 = at.i + mine;         // the warp's first vector
-    const int n = s_listed[row_step];
     for (int t = lane; t < n; t += 32) {
-      const int k = list[row_step * kList + t], d = k - at.head, i = d / VE;
-      if (d < 0 || (unsigned)(i - i0) >= (unsigned)(kVecs * 32) || i >= at.nvec) continue;
+      const int k = my_list[t], d = k - at.head, i = d / VE;
+      if (d < 0 || (unsigned)(i - mine) >= (unsigned)(kVecs * 32) || i >= at.nvec) continue;
       if (r.mask && !(allow[k >> 5] >> (k & 31) & 1u)) continue;
-      E* z = reinterpret_cast<E*>(mem + (i - i0)) + d % VE;
+      E* z = reinterpret_cast<E*>(mem + (i - mine)) + d % VE;
       *z = Elem<DT>::store(adjust(Elem<DT>::load(*z), count[k], r.n_bias ? bias_at[k] : 0u, ru,
                                   v0 + k, at.u));
     }
     __syncwarp();
-    uint4* out = reinterpret_cast<uint4*>(at.out + at.head) + i0 + lane;
+    uint4* out = reinterpret_cast<uint4*>(at.out + at.head) + mine + lane;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-      const int i = i0 + j * 32 + lane;
+      const int i = mine + j * 32 + lane;
       if (i < at.nvec) {
         uint4 x = mem[j * 32 + lane];
         if (r.mask) {
@@ -402,44 +401,43 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
       }
     }
     __syncwarp();  // the ring is read
-    at.i += kStep;
-    row_step += kThreads / 32;
-    if (at.i >= at.nvec) {
-      row_step = warp;
-      settle(at);
+    next_row(at);
+    settle(at);
+  }
+
+  // ---- the ends of rows that do not start or end on a vector, token by token -------------
+  if (!alike || first.head + first.nvec * VE < nv || first.head > 0) {
+    for (; first.u < u1; next_row(first)) {
+      auto single = [&](int k) {
+        E e = first.in[k];
+        if (touched[k >> 5] >> (k & 31) & 1u)
+          e = Elem<DT>::store(adjust(Elem<DT>::load(e), count[k], r.n_bias ? bias_at[k] : 0u, ru,
+                                     v0 + k, first.u));
+        if (r.mask && !(bits[(first.u - u0) * words + (k >> 5)] >> (k & 31) & 1u)) e = fill;
+        first.out[k] = e;
+      };
+      for (int k = tid; k < first.head; k += kThreads) single(k);
+      for (int k = first.head + first.nvec * VE + tid; k < nv; k += kThreads) single(k);
     }
   }
 
-  const int last_word = (p.V - 1) >> 5;
-  for (int u = u0; u < u1; ++u) {
-    // ---- the ends of rows that are not aligned, token by token -------------------------
-    const Place& q = first;
-    auto single = [&](int k) {
-      E e = q.in[k];
-      if (touched[k >> 5] >> (k & 31) & 1u)
-        e = Elem<DT>::store(adjust(Elem<DT>::load(e), count[k], r.n_bias ? bias_at[k] : 0u, ru,
-                                   v0 + k, u));
-      if (r.mask && !(bits[(u - u0) * words + (k >> 5)] >> (k & 31) & 1u)) e = fill;
-      q.out[k] = e;
-    };
-    for (int k = tid; k < q.head; k += kThreads) single(k);
-    for (int k = q.head + q.nvec * VE + tid; k < nv; k += kThreads) single(k);
-
-    // ---- allowed tokens: each row is counted whole by one of the slices' CTAs --------
-    if (p.allowed && (u - u0) % p.nslice == sl) {
-      int n = 0;
+  // ---- allowed tokens: each row is counted whole by one of the slices' CTAs --------------
+  if (p.allowed) {
+    const int last_word = (p.V - 1) >> 5;
+    for (int u = u0 + sl; u < u1; u += p.nslice) {
+      int n = tid == 0 ? p.V : 0;
       if (r.mask) {
         const int32_t* mask = r.mask + b * r.mask_seq_stride + u * r.mask_row_stride;
+        n = 0;
+#pragma unroll 4
         for (int i = tid; i <= last_word; i += kThreads) {
           uint32_t m = (uint32_t)mask[i];
           if (i == last_word && (p.V & 31)) m &= (1u << (p.V & 31)) - 1u;
           n += __popc(m);
         }
-      } else {
-        n = tid == 0 ? p.V : 0;
       }
       n = __reduce_add_sync(0xffffffffu, n);
-      if ((tid & 31) == 0) s_sum[tid >> 5] = n;
+      if (lane == 0) s_sum[warp] = n;
       __syncthreads();
       if (tid == 0) {
         int t = 0;
@@ -448,7 +446,6 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
       }
       __syncthreads();  // s_sum is read
     }
-    next_row(first);
   }
 }
 
@@ -520,12 +517,11 @@ extern "C" ssd_status ssd_process_logits(const ssd_logits* in, const ssd_logits*
   const int64_t grid = ctas();
   if (grid > 0x7fffffff) return SSD_ERR_UNSUPPORTED;
   const size_t words = p.slice / 32 + 4;
-  const int ve = in->dtype == SSD_BF16 ? 8 : 4;
-  const size_t lists = (p.slice + kVecs * kThreads * ve - 1) / (kVecs * kThreads * ve) *
-                       (kThreads / 32);
-  const size_t smem = (size_t)kStages * kVecs * kThreads * 16 +
-                      lists * (kVecs * 32 + 1) * ve * 2 + (p.slice + words) * 4 +
-                      (r.mask ? p.rows * words * 4 : 0) + (r.n_bias ? p.slice * 2 : 0);
+  const int es = in->dtype == SSD_BF16 ? 2 : 4;
+  const size_t smem = (size_t)kStages * kMaxSlice * es +                     // ring
+                      (kMaxSlice + kThreads / 32 * (16 / es)) * 2 +           // lists
+                      (p.slice + words) * 4 + (r.mask ? p.rows * words * 4 : 0) +
+                      (r.n_bias ? p.slice * 2 : 0);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = in->dtype == SSD_BF16 ? launch<SSD_BF16>(p, grid, smem, s)
                                               : launch<SSD_F32>(p, grid, smem, s);
