@@ -319,25 +319,34 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32)
 }
 
 // ---- the join ------------------------------------------------------------------------
-// One warp per (row, key/value head, up to eight of its query heads): the row's
-// own tokens, or their partials, then the prefix's partials, then the output.
+// One warp per row and up to eight of its query heads: the row's own tokens, or
+// their partials, then the prefix's partials, then the output.  With few query
+// heads to a key/value head a warp takes several key/value heads (eight, four or
+// two), so that its lanes all have a head: their scores come from one product
+// each, of which a lane keeps its own head's, and the sums add up over the
+// key/value heads, with the weights of the others' heads zero.
 //
 // Own tokens are few in the calls that this kernel is made for (a branch's
 // drafts), and such a task is a chain of loads: page, tokens, partials.  It is
 // bound by their latency and by what it issues around them, so the operands of
 // the products come straight from global memory, in an order of the dimensions
 // that needs no exchange between lanes and in which every load of a warp takes
-// whole sectors (the cache of an SM that still runs the kernel before is small).
-// In 16-byte chunks of 8 dimensions: lane (gid, quad) holds chunks quad + 4 i of
-// query head gid and of token gid, whose elements 4 s .. 4 s + 3 are the k of
-// product s of Q K^T; and chunks gid + 8 i of tokens 2 quad and 2 quad + 1, whose
-// element e is column gid of product 8 i + e of the sums: so it receives, of head
-// gid, dimensions 64 i + 16 quad + e and + 8.  Long own caches go through
-// own_kernel, split over many warps.
+// whole sectors.  In 16-byte chunks of 8 dimensions: lane (gid, quad) holds
+// chunks quad + 4 i of query head gid and of token gid, whose elements 4 s .. 4 s
+// + 3 are the k of product s of Q K^T; and chunks gid + 8 i of tokens 2 quad and
+// 2 quad + 1, whose element e is column gid of product 8 i + e of the sums: so it
+// receives, of head gid, dimensions 64 i + 16 quad + e and + 8.  Long own caches
+// go through own_kernel, split over many warps.
 constexpr int kJoinWarps = 8;
 constexpr int kJoinHeads = 8;
 template <int D> constexpr int kJoinCtas = D == 256 ? 1 : 2;  // per SM, by registers
 constexpr int kShortOwn = 64;  // tokens of an own cache up to which the join reads it
+
+// How a row's query heads are dealt to tasks: `pack` key/value heads of 8 / pack
+// lanes each, or, with more than eight query heads, `blocks` tasks for one.
+struct Deal {
+  int pack, blocks, tasks;
+};
 
 // The prefix's partials of a pair: np of them, from `slot` on, at row `i`.
 struct Parts {
@@ -391,7 +400,7 @@ __device__ __forceinline__ uint32_t word(const uint4& x, int i) {
 
 template <typename T, int D, bool SHORT_OWN>
 __global__ void __launch_bounds__(kJoinWarps * 32, kJoinCtas<D>)
-    join_kernel(const __grid_constant__ AttnParams p, int head_blocks) {
+    join_kernel(const __grid_constant__ AttnParams p, Deal deal) {
   constexpr int EL = D / 4;          // dimensions of a lane
   constexpr int NI = D / 64;         // its runs of 16 of the sums
   const int lane = threadIdx.x & 31, gid = lane >> 2, quad = lane & 3;
@@ -422,121 +431,163 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinCtas<D>)
     const int32_t* table = a.tables + (int64_t)r * a.table_stride;
     if (SHORT_OWN && a.lens && threadIdx.x == 0 && len != a.lens[r]) flag(p, SSD_DEV_BAD_LENGTH);
 
-    for (int task = threadIdx.x >> 5; task < a.Hkv * head_blocks; task += blockDim.x >> 5) {
-      const int h = head_blocks == 1 ? task : task / head_blocks;
-      const int in_h = (task - h * head_blocks) * kJoinHeads + gid;  // this lane's query head
-      const bool mine = in_h < p.gqa;
+    for (int task = threadIdx.x >> 5; task < deal.tasks; task += blockDim.x >> 5) {
+      // key/value heads h0 .. of the task, this lane's one and its query head in it
+      const int lanes = kJoinHeads / deal.pack;
+      const int h0 = deal.pack > 1 ? task * deal.pack : task / deal.blocks;
+      const int sub = gid / lanes, h = h0 + sub;
+      const int in_h = deal.pack > 1 ? gid - sub * lanes
+                                     : (task - h0 * deal.blocks) * kJoinHeads + gid;
+      const bool mine = in_h < p.gqa && h < a.Hkv;
       const int head = h * p.gqa + in_h;
+      const int packed = min(deal.pack, a.Hkv - h0);
+      if (SHORT_OWN && gid < next_len && (unsigned)next_first < (unsigned)a.num_pages) {
+        // the next row's tokens on their way to L2: lines of K and V, two lanes each
+        const ssd_paged& c = quad < 2 ? a.k : a.v;
+        const T* x = static_cast<const T*>(c.ptr) + (int64_t)next_first * c.page_stride +
+                     (int64_t)(gid - page_col * a.page_size) * c.token_stride +
+                     (int64_t)h0 * c.head_stride + (quad & 1) * 64;
+        for (int z = 0; z < packed; ++z)
+#pragma unroll
+          for (int d = 0; d < D; d += 128)
+            if ((quad & 1) * 64 + d < D)
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(x + (int64_t)z * c.head_stride + d));
+      }
 
       // where the partials are, on its way while the own tokens are read
       const Parts s = mine ? parts_of(p, row, h, in_h) : Parts{0, 0, 0};
 
-      // sums at dimensions 64 i + 16 quad + e; the first partial is loaded into
-      // them, beside the own tokens
-      float o[NI][16] = {};
+      float o[NI][16] = {};            // sums at dimensions 64 i + 16 quad + e
       float m = -INFINITY, l = 0.f;
-      if (s.np > 0) {
-        const float2 ml = p.pml[(int64_t)s.slot * p.mt + s.i];
-        m = ml.x;
-        l = quad == 0 ? ml.y : 0.f;      // summed over the quad below
-        const float* x = p.po + part_at<D>(s.slot, p.mt, s.i, quad * 16);
+      for (int t0 = 0; SHORT_OWN && t0 < len; t0 += 8) {
+        const int t = t0 + gid, col = p.by_page.quotient(t);
+        int page = -1, in_page = 0;
+        if (t < len) {
+          page = t0 == 0 ? first : table[col];
+          in_page = t - col * a.page_size;
+          if ((unsigned)page >= (unsigned)a.num_pages) {
+            flag(p, SSD_DEV_BAD_PAGE);
+            page = -1;               // reads as zeros
+          }
+        }
+        float s0 = 0.f, s1 = 0.f;    // scores of tokens t0 + 2 quad, + 1
+        {
+          const T* kt = static_cast<const T*>(a.k.ptr) + (int64_t)page * a.k.page_stride +
+                        (int64_t)in_page * a.k.token_stride + (int64_t)h0 * a.k.head_stride +
+                        quad * 8;
+          uint4 q[EL / 8];
+          load_chunks<4>(q, static_cast<const T*>(a.q) + (int64_t)r * a.q_row_stride +
+                                (int64_t)head * a.q_head_stride + quad * 8, mine);
+          for (int z = 0; z < packed; z += 2) {  // two key/value heads at a time
+            uint4 k0[EL / 8], k1[EL / 8];
+            load_chunks<4>(k0, kt + (int64_t)z * a.k.head_stride, page >= 0);
+            load_chunks<4>(k1, kt + (int64_t)(z + 1) * a.k.head_stride,
+                           page >= 0 && z + 1 < packed);
+            float x0 = 0.f, x1 = 0.f, y0 = 0.f, y1 = 0.f;
+#pragma unroll
+            for (int i = 0; i < EL / 4; ++i)
+              mma_k16<T>(x0, x1, word(q[i / 2], i % 2 * 2), word(q[i / 2], i % 2 * 2 + 1),
+                         word(k0[i / 2], i % 2 * 2), word(k0[i / 2], i % 2 * 2 + 1));
+            if (z + 1 < packed) {
+#pragma unroll
+              for (int i = 0; i < EL / 4; ++i)
+                mma_k16<T>(y0, y1, word(q[i / 2], i % 2 * 2), word(q[i / 2], i % 2 * 2 + 1),
+                           word(k1[i / 2], i % 2 * 2), word(k1[i / 2], i % 2 * 2 + 1));
+            }
+            if (sub == z) {
+              s0 = x0;
+              s1 = x1;
+            }
+            if (sub == z + 1) {
+              s0 = y0;
+              s1 = y1;
+            }
+          }
+        }
+        s0 = t0 + quad * 2 < len ? s0 * p.scale_log2 : -INFINITY;
+        s1 = t0 + quad * 2 + 1 < len ? s1 * p.scale_log2 : -INFINITY;
+        float top = fmaxf(s0, s1);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float m1 = fmaxf(m, top), off = m1 == -INFINITY ? 0.f : m1;
+        const float keep = exp2_fast(m - off);
+        m = m1;
+        s0 = exp2_fast(s0 - off);
+        s1 = exp2_fast(s1 - off);
+        l = l * keep + s0 + s1;
+        const uint32_t pw = pack2<T>(s0, s1);
+        const int pg0 = __shfl_sync(0xffffffffu, page, quad * 8);
+        const int pg1 = __shfl_sync(0xffffffffu, page, quad * 8 + 4);
+        const int ip0 = __shfl_sync(0xffffffffu, in_page, quad * 8);
+        const int ip1 = __shfl_sync(0xffffffffu, in_page, quad * 8 + 4);
+        const T* vh = static_cast<const T*>(a.v.ptr) + (int64_t)h0 * a.v.head_stride + gid * 8;
+        const int64_t at0 = (int64_t)pg0 * a.v.page_stride + (int64_t)ip0 * a.v.token_stride;
+        const int64_t at1 = (int64_t)pg1 * a.v.page_stride + (int64_t)ip1 * a.v.token_stride;
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            *reinterpret_cast<float4*>(&o[i][c * 4]) =
-                *reinterpret_cast<const float4*>(x + (i * 16 + c) * 4 * p.mt);
-      }
-      if (SHORT_OWN && len > 0) {
-        uint4 q[EL / 8];
-        load_chunks<4>(q, static_cast<const T*>(a.q) + (int64_t)r * a.q_row_stride +
-                        (int64_t)head * a.q_head_stride + quad * 8, mine);
-        for (int t0 = 0; t0 < len; t0 += 8) {
-          const int t = t0 + gid, col = p.by_page.quotient(t);
-          int page = -1, in_page = 0;
-          if (t < len) {
-            page = t0 == 0 ? first : table[col];
-            in_page = t - col * a.page_size;
-            if ((unsigned)page >= (unsigned)a.num_pages) {
-              flag(p, SSD_DEV_BAD_PAGE);
-              page = -1;               // reads as zeros
-            }
-          }
-          uint4 k[EL / 8], v0[NI], v1[NI];
-          load_chunks<4>(k, static_cast<const T*>(a.k.ptr) + (int64_t)page * a.k.page_stride +
-                          (int64_t)in_page * a.k.token_stride + (int64_t)h * a.k.head_stride + quad * 8,
-                   page >= 0);
-          const T* vh = static_cast<const T*>(a.v.ptr) + (int64_t)h * a.v.head_stride + gid * 8;
-          const int pg0 = __shfl_sync(0xffffffffu, page, quad * 8);
-          const int pg1 = __shfl_sync(0xffffffffu, page, quad * 8 + 4);
-          const int ip0 = __shfl_sync(0xffffffffu, in_page, quad * 8);
-          const int ip1 = __shfl_sync(0xffffffffu, in_page, quad * 8 + 4);
-          load_chunks<8>(v0, vh + (int64_t)pg0 * a.v.page_stride + (int64_t)ip0 * a.v.token_stride,
-                   pg0 >= 0);
-          load_chunks<8>(v1, vh + (int64_t)pg1 * a.v.page_stride + (int64_t)ip1 * a.v.token_stride,
-                   pg1 >= 0);
-          float s0 = 0.f, s1 = 0.f;    // scores of tokens t0 + 2 quad, + 1
-#pragma unroll
-          for (int i = 0; i < EL / 4; ++i)
-            mma_k16<T>(s0, s1, word(q[i / 2], i % 2 * 2), word(q[i / 2], i % 2 * 2 + 1),
-                       word(k[i / 2], i % 2 * 2), word(k[i / 2], i % 2 * 2 + 1));
-          s0 = t0 + quad * 2 < len ? s0 * p.scale_log2 : -INFINITY;
-          s1 = t0 + quad * 2 + 1 < len ? s1 * p.scale_log2 : -INFINITY;
-          float top = fmaxf(s0, s1);
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const float m1 = fmaxf(m, top), off = m1 == -INFINITY ? 0.f : m1;
-          const float keep = exp2_fast(m - off);
-          m = m1;
-          s0 = exp2_fast(s0 - off);
-          s1 = exp2_fast(s1 - off);
-          l = l * keep + s0 + s1;
-          const uint32_t pw = pack2<T>(s0, s1);
+          for (int e = 0; e < 16; ++e) o[i][e] *= keep;
+#pragma unroll 2
+        for (int z = 0; z < packed; ++z) {
+          uint4 v0[NI], v1[NI];
+          load_chunks<8>(v0, vh + at0 + (int64_t)z * a.v.head_stride, pg0 >= 0);
+          load_chunks<8>(v1, vh + at1 + (int64_t)z * a.v.head_stride, pg1 >= 0);
+          const uint32_t w = sub == z ? pw : 0u;
 #pragma unroll
           for (int i = 0; i < NI; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              o[i][e] *= keep;
-              o[i][e + 8] *= keep;
-              mma_k8<T>(o[i][e], o[i][e + 8], pw,
+            for (int e = 0; e < 8; ++e)
+              mma_k8<T>(o[i][e], o[i][e + 8], w,
                         __byte_perm(word(v0[i], e / 2), word(v1[i], e / 2),
                                     e & 1 ? 0x7632 : 0x5410));
-            }
         }
       }
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
       if (!mine) continue;
 
-      // one more stretch: its sums of four dimensions 4 c .. of the lane's at
-      // x + (i * 16 + c) * step
-      auto add = [&](float2 ml, const float* x, int64_t step) {
-        const float m1 = fmaxf(m, ml.x), off = m1 == -INFINITY ? 0.f : m1;
-        const float f = exp2_fast(m - off), g = exp2_fast(ml.x - off);
-        m = m1;
-        l = l * f + ml.y * g;
+      // The partials: first the largest maximum, then the sums, 16 dimensions at a
+      // time, so that no load waits for another stretch's.
+      const int64_t pair = (int64_t)r * a.Hq + head;
+      const int per = SHORT_OWN || len == 0 ? 1 : own_stretch(p, len);
+      const int ns = SHORT_OWN ? 0 : (len + per - 1) / per;  // of the own tokens
+      const float2* ml_p = p.pml + (int64_t)s.slot * p.mt + s.i;
+      const float2* ml_o = p.sml + pair * p.nsplit;
+      float top = m;
+#pragma unroll 4
+      for (int j = 0; j < s.np; ++j) top = fmaxf(top, ml_p[(int64_t)j * p.mt].x);
+#pragma unroll 4
+      for (int j = 0; j < ns; ++j) top = fmaxf(top, ml_o[j].x);
+      const float off = top == -INFINITY ? 0.f : top, keep = exp2_fast(m - off);
+      m = top;
+      l *= keep;
+      for (int j = 0; j < s.np; ++j) {
+        const float2 ml = ml_p[(int64_t)j * p.mt];
+        l = fmaf(ml.y, exp2_fast(ml.x - off), l);
+      }
+      for (int j = 0; j < ns; ++j) l = fmaf(ml_o[j].y, exp2_fast(ml_o[j].x - off), l);
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
+      for (int i = 0; i < NI; ++i) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[i][e] *= keep;
+        auto add = [&](float g, const float* x, int step) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const float4 y = *reinterpret_cast<const float4*>(x + (i * 16 + c) * step);
-            o[i][c * 4] = fmaf(y.x, g, o[i][c * 4] * f);
-            o[i][c * 4 + 1] = fmaf(y.y, g, o[i][c * 4 + 1] * f);
-            o[i][c * 4 + 2] = fmaf(y.z, g, o[i][c * 4 + 2] * f);
-            o[i][c * 4 + 3] = fmaf(y.w, g, o[i][c * 4 + 3] * f);
+            const float4 y = *reinterpret_cast<const float4*>(x + c * step);
+            o[i][c * 4] = fmaf(y.x, g, o[i][c * 4]);
+            o[i][c * 4 + 1] = fmaf(y.y, g, o[i][c * 4 + 1]);
+            o[i][c * 4 + 2] = fmaf(y.z, g, o[i][c * 4 + 2]);
+            o[i][c * 4 + 3] = fmaf(y.w, g, o[i][c * 4 + 3]);
           }
-      };
-      const int64_t pair = (int64_t)r * a.Hq + head;
-      if (!SHORT_OWN && len > 0) {
-        const int ns = (len + own_stretch(p, len) - 1) / own_stretch(p, len);
-        for (int j = 0; j < ns; ++j) {
-          const int64_t at = pair * p.nsplit + j;
-          add(p.sml[at], p.so + at * D + quad * 16, 4);
-        }
+        };
+        const float* po = p.po + part_at<D>(s.slot, p.mt, s.i, quad * 16 + i * 64);
+#pragma unroll 4
+        for (int j = 0; j < s.np; ++j)
+          add(exp2_fast(ml_p[(int64_t)j * p.mt].x - off), po + (int64_t)j * p.mt * D, 4 * p.mt);
+        const float* so = p.so + pair * p.nsplit * D + quad * 16 + i * 64;
+#pragma unroll 4
+        for (int j = 0; j < ns; ++j) add(exp2_fast(ml_o[j].x - off), so + (int64_t)j * D, 4);
       }
-      for (int j = 1; j < s.np; ++j)
-        add(p.pml[(int64_t)(s.slot + j) * p.mt + s.i],
-            p.po + part_at<D>(s.slot + j, p.mt, s.i, quad * 16), 4 * p.mt);
       // no token at all: zeros and -inf
       const float inv = l == 0.f ? 0.f : 1.f / l;
       T* to = static_cast<T*>(a.out) + (int64_t)r * a.out_row_stride +
@@ -611,13 +662,13 @@ bool plan(const ssd_attention& a, AttnParams& p, Layout& L) {
   if (items * (tiles + 1) > 0x7fffffff) return false;
   p.nslots = a.G > 0 ? (int)(items + p.workers) : 0;
   // own tokens: read by the join where they are few; else in stretches of two
-  // tiles or more, four for each resident warp, which evens out their lengths
+  // tiles or more, eight for each resident warp, which evens out their lengths
   const int64_t most = a.lens ? (int64_t)a.cols * a.page_size : 0;
   L.short_own = most <= kShortOwn;
   L.own_blocks = (p.gqa + kBlockRows - 1) / kBlockRows;
   const int64_t own = (int64_t)a.R * a.Hkv * L.own_blocks;
   p.nsplit = (int)std::max<int64_t>(
-      1, std::min<int64_t>((most + 2 * kTileTokens - 1) / (2 * kTileTokens), 4 * warps / own));
+      1, std::min<int64_t>((most + 2 * kTileTokens - 1) / (2 * kTileTokens), 8 * warps / own));
   if (own * p.nsplit / kWarpsPerCta >= 0x7fffffff) return false;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -637,9 +688,9 @@ bool plan(const ssd_attention& a, AttnParams& p, Layout& L) {
 }
 
 // The next kernel of a call, which may start before the one before is done.
-template <typename... A>
-cudaError_t launch_next(void (*kernel)(A...), int grid, int threads, int smem, cudaStream_t s,
-                        bool early_start, const AttnParams& p, int n) {
+template <typename N>
+cudaError_t launch_next(void (*kernel)(AttnParams, N), int grid, int threads, int smem,
+                        cudaStream_t s, bool early_start, const AttnParams& p, N n) {
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
@@ -677,8 +728,16 @@ cudaError_t launch(const AttnParams& p, const Layout& L, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     first = false;
   }
-  const int head_blocks = (p.gqa + kJoinHeads - 1) / kJoinHeads;
-  const int threads = std::min(kJoinWarps, p.a.Hkv * head_blocks) * 32;
+  Deal deal{1, (p.gqa + kJoinHeads - 1) / kJoinHeads, 0};
+  // Few rows: every key/value head has its warp (12 branches of one sequence: 30 us
+  // instead of 39).  When that takes more than a turn: as many heads to a warp as it
+  // has lanes for (32 x 12 branches: 110 us instead of 116; 256 x 24: 312 of 332).
+  const int64_t warps = (int64_t)std::max(num_sms(), 1) * kJoinCtas<D> * kJoinWarps;
+  while (deal.pack * 2 * p.gqa <= kJoinHeads &&
+         (int64_t)p.a.R * p.a.Hkv / deal.pack > warps)
+    deal.pack *= 2;
+  deal.tasks = deal.pack > 1 ? (p.a.Hkv + deal.pack - 1) / deal.pack : p.a.Hkv * deal.blocks;
+  const int threads = std::min(kJoinWarps, deal.tasks) * 32;
   const int resident = std::max(num_sms(), 1) * kJoinCtas<D> * kJoinWarps * 32 / threads;
   const int grid = std::min(p.a.R, resident);
   // Started early, the join finds the shared-memory split of the kernel before on
@@ -686,8 +745,8 @@ cudaError_t launch(const AttnParams& p, const Layout& L, cudaStream_t s) {
   // on its cache), a call of one turn 2 us less.
   const bool early = !first && p.a.R <= resident;
   return L.short_own
-             ? launch_next(join_kernel<T, D, true>, grid, threads, 0, s, early, p, head_blocks)
-             : launch_next(join_kernel<T, D, false>, grid, threads, 0, s, early, p, head_blocks);
+             ? launch_next(join_kernel<T, D, true>, grid, threads, 0, s, early, p, deal)
+             : launch_next(join_kernel<T, D, false>, grid, threads, 0, s, early, p, deal);
 }
 
 template <typename T>
