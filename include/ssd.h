@@ -445,8 +445,9 @@ ssd_status ssd_fanout(int K, int budget, double a, double r, int32_t* F_out);
  * in, out      [B, N, V] logits of one dtype, row (b, u) is row b*N + u; out
  *              is in itself (same pointer and row stride) or does not overlap
  *              it.
- * history      device int32, sequence b's tokens start at b * history_stride
- *              (or NULL: no history).  A token outside [0, V) is passed over
+ * history      device int32, sequence b's tokens start at b * history_stride,
+ *              with room for history_max (those past its length are not used;
+ *              NULL: no history).  A token outside [0, V) is passed over
  *              and sets SSD_DEV_BAD_TOKEN.
  * history_len  device [B] int32 in [0, history_max] (a value outside is
  *              clamped and sets SSD_DEV_BAD_LENGTH).
@@ -530,7 +531,8 @@ ssd_status ssd_process_logits(const ssd_logits* in, const ssd_logits* out, int B
  * Outputs are not inputs: kv_len, held_out and free_out are arrays of their
  * own.
  *
- * lens, new_tokens, held  device [B] int32.      B <= 8192.
+ * lens, new_tokens, held  device [B] int32.  B <= 8192; B * cols and max_rows
+ *             at most 2^30.
  * tables      device int32, request b's row starts at b * table_stride, cols
  *             columns.
  * free_pages  device [free_cap] int32; free_count device int32 in [0,

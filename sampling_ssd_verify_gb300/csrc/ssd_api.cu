@@ -256,7 +256,7 @@ const char* ssd_status_string(int status) {
   }
 }
 
-int ssd_version(void) { return 100; }
+int ssd_version(void) { return 200; }
 
 ssd_status ssd_fanout(int K, int budget, double a, double r, int32_t* F_out) {
   if (K < 0 || K > 4096 || budget < 0 || !(a > 0.0) || !std::isfinite(a) || !(r >= 0.0) ||

@@ -28,6 +28,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxRequests = 8192;  // five numbers each in shared memory
 constexpr int kBatch = 4;           // new tokens per thread at a time
+constexpr int kMaxCount = 1 << 30;
 constexpr int kRowsPerCta = 2048;   // new tokens per CTA before another one is added
 
 struct PageParams {
@@ -237,7 +238,9 @@ extern "C" ssd_status ssd_page_plan(const int32_t* lens, const int32_t* new_toke
   if (B < 1 || cols < 1 || page < 1 || free_cap < 0 || max_rows < 0 || table_stride < cols)
     return SSD_ERR_INVALID_ARG;
   if ((free_cap > 0 && !free_pages) || (max_rows > 0 && !slots)) return SSD_ERR_INVALID_ARG;
-  if (B > kMaxRequests) return SSD_ERR_UNSUPPORTED;
+  // sums of pages and indexes of rows stay below 2^31 with room for a stride
+  if (B > kMaxRequests || (int64_t)B * cols > kMaxCount || max_rows > kMaxCount)
+    return SSD_ERR_UNSUPPORTED;
   const PageParams p{lens,     new_tokens, held,  B, tables, table_stride, cols,
                      free_pages, free_cap, free_count, page,    max_rows, divisor(page), slots, positions,
                      owner,    cu,         kv_len, held_out,   served, free_out,     dev_status};

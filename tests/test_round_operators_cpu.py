@@ -68,6 +68,7 @@ def _plan_call(L, **kw):
     (dict(tables=None), INVALID), (dict(cu=None), INVALID), (dict(slots=None), INVALID),
     (dict(stride=7), INVALID), (dict(cols=0), INVALID), (dict(page=0), INVALID),
     (dict(cap=-1), INVALID), (dict(free=None), INVALID), (dict(rows=-1), INVALID),
+    (dict(cols=1 << 28, stride=1 << 28, B=5), UNSUPPORTED), (dict(rows=(1 << 30) + 1), UNSUPPORTED),
     (dict(free_out=PTR), INVALID), (dict(kv=PTR), INVALID), (dict(held_out=2 * PTR), INVALID),
 ])
 def test_page_plan_refusals(L, kw, status):
