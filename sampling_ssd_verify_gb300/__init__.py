@@ -675,6 +675,21 @@ def process_logits(logits, history=None, history_len=None, prompt_len=None, draf
     return o
 
 
+_PLAN = ("positions", "owner", "cu", "kv_len", "held", "served", "free_count")
+
+
+def _plan_views(torch, B, T, device):
+    """page_plan's outputs: the slots, and the others in one buffer, each on a
+    64-byte boundary."""
+    counts = (T, T, B + 1, B, B, B, 1)
+    base = torch.empty(sum(n + 15 & ~15 for n in counts), dtype=torch.int32, device=device)
+    views, at = {"slots": torch.empty(T, dtype=torch.int64, device=device)}, 0
+    for name, n in zip(_PLAN, counts):
+        views[name] = base[at:at + n]
+        at += n + 15 & ~15
+    return views
+
+
 def page_plan(lens, new, held, tables, free_pages, free_count, page_size, max_rows,
               dev_status=None, stream=None, out=None):
     """ssd_page_plan: the pages of a paged key/value cache after a round, and
@@ -693,26 +708,34 @@ def page_plan(lens, new, held, tables, free_pages, free_count, page_size, max_ro
     if dev < 0 or lens.dim() != 1:
         raise SSDError("expected lengths [B] on the GPU")
     B, T = lens.shape[0], int(max_rows)
-    row, rows, one = (B,), (T,), (1,)
+    if T < 0:
+        raise SSDError("max_rows must not be negative")
+    row, one = (B,), (1,)
     o = out if out is not None else {}
     if "slots" not in o:
-        o["slots"] = torch.empty(T, dtype=torch.int64, device=lens.device)
-        for name, n in (("positions", T), ("owner", T), ("cu", B + 1), ("kv_len", B),
-                        ("held", B), ("served", B), ("free_count", 1)):
-            o[name] = torch.empty(n, dtype=i32, device=lens.device)
+        o.update(_plan_views(torch, B, T, lens.device))
+    # all but the slots are views of one buffer, one after the other
+    base = o["cu"]._base
+    if base is None or base.dtype is not i32 or base.get_device() != dev or \
+            o["cu"].numel() != B + 1:
+        raise SSDError("out: expected the dict of an earlier call with these sizes")
+    first = at = base.data_ptr()
+    ptrs = []
+    for name, n in zip(_PLAN, (T, T, B + 1, B, B, B, 1)):
+        if n and o[name].data_ptr() != at:
+            raise SSDError(f"out: {name} is not that of an earlier call with these sizes")
+        ptrs.append(at)
+        at += (n + 15 & ~15) * 4
+    if at - first > base.numel() * 4:
+        raise SSDError("out: expected the dict of an earlier call with these sizes")
     table, stride, cols = _rows2d(tables, "tables", B, i32, dev)
     st = lib().ssd_page_plan(
         _tensor(lens, "lens", i32, row, dev), _tensor(new, "new", i32, row, dev),
         _tensor(held, "held", i32, row, dev), B, table, stride, cols,
         _tensor(free_pages, "free_pages", i32, free_pages.shape, dev), free_pages.numel(),
         _tensor(free_count, "free_count", i32, one, dev), int(page_size), T,
-        _tensor(o["slots"], "slots", torch.int64, rows, dev),
-        _tensor(o["positions"], "positions", i32, rows, dev),
-        _tensor(o["owner"], "owner", i32, rows, dev), _tensor(o["cu"], "cu", i32, (B + 1,), dev),
-        _tensor(o["kv_len"], "kv_len", i32, row, dev), _tensor(o["held"], "held", i32, row, dev),
-        _tensor(o["served"], "served", i32, row, dev),
-        _tensor(o["free_count"], "free_count", i32, one, dev), _dev_ptr(dev_status),
-        _use_stream(stream, dev, o.values()))
+        _tensor(o["slots"], "slots", torch.int64, (T,), dev), *ptrs, _dev_ptr(dev_status),
+        _use_stream(stream, dev, (base, o["slots"])))
     if st:
         _check(st, "ssd_page_plan")
     return o

@@ -405,19 +405,27 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
     settle(at);
   }
 
-  // ---- the ends of rows that do not start or end on a vector, token by token -------------
+  // ---- the ends of rows that do not start or end on a vector, token by token: up to 2 VE
+  // of a row, all rows side by side; rows whose vectors lie differently in and out have no
+  // vectors, and are taken one after the other ------------------------------------------
   if (!alike || first.head + first.nvec * VE < nv || first.head > 0) {
-    for (; first.u < u1; next_row(first)) {
-      auto single = [&](int k) {
-        E e = first.in[k];
+    const bool whole = first.nvec == 0 && nv >= 2 * VE;
+    const int per = whole ? kThreads : 2 * VE;  // threads of a row
+    for (int u = u0 + tid / per; u < u1; u += kThreads / per) {
+      Place q = first;
+      q.in += (u - u0) * p.in_stride;
+      q.out += (u - u0) * p.out_stride;
+      measure(q);
+      const int skip = q.nvec * VE;  // the tokens between the ends
+      for (int i = tid % per; i < nv - skip; i += per) {
+        const int k = i < q.head ? i : i + skip;
+        E e = q.in[k];
         if (touched[k >> 5] >> (k & 31) & 1u)
           e = Elem<DT>::store(adjust(Elem<DT>::load(e), count[k], r.n_bias ? bias_at[k] : 0u, ru,
-                                     v0 + k, first.u));
-        if (r.mask && !(bits[(first.u - u0) * words + (k >> 5)] >> (k & 31) & 1u)) e = fill;
-        first.out[k] = e;
-      };
-      for (int k = tid; k < first.head; k += kThreads) single(k);
-      for (int k = first.head + first.nvec * VE + tid; k < nv; k += kThreads) single(k);
+                                     v0 + k, u));
+        if (r.mask && !(bits[(u - u0) * words + (k >> 5)] >> (k & 31) & 1u)) e = fill;
+        q.out[k] = e;
+      }
     }
   }
 

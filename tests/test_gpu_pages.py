@@ -170,7 +170,12 @@ def test_refusals():
     i = torch.zeros(4, dtype=torch.int32, device=dev)
     t = torch.zeros((4, 5), dtype=torch.int32, device=dev)
     ok = (i, i, i, t, i, i[:1], 16, 8)
-    ssd.page_plan(*ok)
+    o = ssd.page_plan(*ok)
+    for out in (dict(o, cu=o["cu"].clone()), dict(o, slots=o["slots"].int()),
+                ssd.page_plan(*ok[:-1], 7), ssd.page_plan(i[:3], i[:3], i[:3], t[:3], *ok[4:])):
+        with pytest.raises(ssd.SSDError):
+            ssd.page_plan(*ok, out=out)
+    ssd.page_plan(*ok, out=o)
     for at, x in ((0, i[:3]), (1, i.long()), (2, i.cpu()), (3, t[:3]), (3, t.t()), (3, t.long()),
                   (4, i.float()), (5, i), (6, 0), (7, -1)):
         args = list(ok)
