@@ -313,9 +313,9 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32)
   int64_t task = (int64_t)blockIdx.x * kWarpsPerCta + warp;
   if (task < (int64_t)p.a.R * p.a.Hkv * blocks * p.nsplit)
     own_task<T, D>(p, smem_addr(s_ring) + warp * kRing * step_bytes<D>(), task, blocks);
-  // It needs nothing of the prefixes' kernel; the join that waits for this one
-  // must find that one done too.
-  wait_previous();
+  // It needs nothing of the prefixes' kernel; but the join that waits for this one
+  // must find that one done too, so one CTA stays until it is.
+  if (blockIdx.x == gridDim.x - 1) wait_previous();
 }
 
 // ---- the join ------------------------------------------------------------------------
