@@ -343,10 +343,16 @@ template <int D> constexpr int kJoinCtas = D == 256 ? 1 : 2;  // per SM, by regi
 constexpr int kShortOwn = 64;  // tokens of an own cache up to which the join reads it
 
 // How a row's query heads are dealt to tasks: `pack` key/value heads of 8 / pack
-// lanes each, or, with more than eight query heads, `blocks` tasks for one.
+// lanes each, or, with more than eight query heads, `blocks` tasks for one.  With
+// few tasks, `split` warps (a CTA) share the partials of one: two rows over a
+// prefix of 10000 tokens have a hundred.
 struct Deal {
-  int pack, blocks, tasks;
+  int pack, blocks, tasks, split;
 };
+template <int D>
+constexpr int join_bytes(int split) {  // half the warps' sums, weights and maxima
+  return split / 2 * 32 * (D / 4 + 2) * 4;
+}
 
 // The prefix's partials of a pair: np of them, from `slot` on, at row `i`.
 struct Parts {
@@ -407,7 +413,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinCtas<D>)
   // a row per CTA and turn: its warps meet the same lengths, tables and places,
   // which are looked up one turn ahead
   const ssd_attention& a = p.a;
-  const int step = gridDim.x;
+  extern __shared__ float s_sums[];
+  const int warp = threadIdx.x >> 5, part = deal.split > 1 ? warp : 0;
+  const int step = deal.split > 1 ? a.R : gridDim.x;  // one task and done
   int page_col = p.by_page.quotient(gid);
   if (page_col >= a.cols) page_col = -1;
   auto page_of = [&](int r) {        // of token gid, before the length is known
@@ -418,7 +426,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinCtas<D>)
   auto items_of = [&](int r) {
     return a.G > 0 && r < a.R ? p.row_items[r] : row_items_of(-1, 0, 0);
   };
-  int r = blockIdx.x;
+  int r = deal.split > 1 ? blockIdx.x / deal.tasks : blockIdx.x;
   int next_len = length_of(r), next_first = page_of(r);
   wait_previous();
   int4 next_row = items_of(r);
@@ -431,7 +439,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinCtas<D>)
     const int32_t* table = a.tables + (int64_t)r * a.table_stride;
     if (SHORT_OWN && a.lens && threadIdx.x == 0 && len != a.lens[r]) flag(p, SSD_DEV_BAD_LENGTH);
 
-    for (int task = threadIdx.x >> 5; task < deal.tasks; task += blockDim.x >> 5) {
+    for (int task = deal.split > 1 ? blockIdx.x - r * deal.tasks : warp; task < deal.tasks;
+         task += deal.split > 1 ? deal.tasks : blockDim.x >> 5) {
       // key/value heads h0 .. of the task, this lane's one and its query head in it
       const int lanes = kJoinHeads / deal.pack;
       const int h0 = deal.pack > 1 ? task * deal.pack : task / deal.blocks;
@@ -459,7 +468,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinCtas<D>)
 
       float o[NI][16] = {};            // sums at dimensions 64 i + 16 quad + e
       float m = -INFINITY, l = 0.f;
-      for (int t0 = 0; SHORT_OWN && t0 < len; t0 += 8) {
+      for (int t0 = 0; SHORT_OWN && part == 0 && t0 < len; t0 += 8) {
         const int t = t0 + gid, col = p.by_page.quotient(t);
         int page = -1, in_page = 0;
         if (t < len) {
@@ -544,28 +553,27 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinCtas<D>)
       }
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
-      if (!mine) continue;
 
       // The partials: first the largest maximum, then the sums, 16 dimensions at a
       // time, so that no load waits for another stretch's.
       const int64_t pair = (int64_t)r * a.Hq + head;
       const int per = SHORT_OWN || len == 0 ? 1 : own_stretch(p, len);
-      const int ns = SHORT_OWN ? 0 : (len + per - 1) / per;  // of the own tokens
+      const int ns = SHORT_OWN || !mine ? 0 : (len + per - 1) / per;  // of the own tokens
       const float2* ml_p = p.pml + (int64_t)s.slot * p.mt + s.i;
       const float2* ml_o = p.sml + pair * p.nsplit;
       float top = m;
 #pragma unroll 4
-      for (int j = 0; j < s.np; ++j) top = fmaxf(top, ml_p[(int64_t)j * p.mt].x);
+      for (int j = part; j < s.np; j += deal.split) top = fmaxf(top, ml_p[(int64_t)j * p.mt].x);
 #pragma unroll 4
-      for (int j = 0; j < ns; ++j) top = fmaxf(top, ml_o[j].x);
+      for (int j = part; j < ns; j += deal.split) top = fmaxf(top, ml_o[j].x);
       const float off = top == -INFINITY ? 0.f : top, keep = exp2_fast(m - off);
       m = top;
       l *= keep;
-      for (int j = 0; j < s.np; ++j) {
+      for (int j = part; j < s.np; j += deal.split) {
         const float2 ml = ml_p[(int64_t)j * p.mt];
         l = fmaf(ml.y, exp2_fast(ml.x - off), l);
       }
-      for (int j = 0; j < ns; ++j) l = fmaf(ml_o[j].y, exp2_fast(ml_o[j].x - off), l);
+      for (int j = part; j < ns; j += deal.split) l = fmaf(ml_o[j].y, exp2_fast(ml_o[j].x - off), l);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
 #pragma unroll
@@ -582,12 +590,36 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinCtas<D>)
         };
         const float* po = p.po + part_at<D>(s.slot, p.mt, s.i, quad * 16 + i * 64);
 #pragma unroll 4
-        for (int j = 0; j < s.np; ++j)
+        for (int j = part; j < s.np; j += deal.split)
           add(exp2_fast(ml_p[(int64_t)j * p.mt].x - off), po + (int64_t)j * p.mt * D, 4 * p.mt);
         const float* so = p.so + pair * p.nsplit * D + quad * 16 + i * 64;
 #pragma unroll 4
-        for (int j = 0; j < ns; ++j) add(exp2_fast(ml_o[j].x - off), so + (int64_t)j * D, 4);
+        for (int j = part; j < ns; j += deal.split) add(exp2_fast(ml_o[j].x - off), so + (int64_t)j * D, 4);
       }
+      for (int w = deal.split / 2; w > 0; w /= 2) {  // the warps' sums, by halves
+        float* mem = s_sums + (warp % w) * 32 * (D / 4 + 2) + lane;
+        if (warp >= w && warp < 2 * w) {
+          mem[0] = m;
+          mem[32] = l;
+#pragma unroll
+          for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) mem[(2 + i * 16 + e) * 32] = o[i][e];
+        }
+        __syncthreads();
+        if (warp < w) {
+          const float m1 = fmaxf(m, mem[0]), off1 = m1 == -INFINITY ? 0.f : m1;
+          const float f = exp2_fast(m - off1), g = exp2_fast(mem[0] - off1);
+          m = m1;
+          l = l * f + mem[32] * g;
+#pragma unroll
+          for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[i][e] = o[i][e] * f + mem[(2 + i * 16 + e) * 32] * g;
+        }
+        __syncthreads();
+      }
+      if (!mine || part != 0) continue;
       // no token at all: zeros and -inf
       const float inv = l == 0.f ? 0.f : 1.f / l;
       T* to = static_cast<T*>(a.out) + (int64_t)r * a.out_row_stride +
@@ -706,29 +738,29 @@ cudaError_t launch_next(void (*kernel)(AttnParams, N), int grid, int threads, in
 
 template <typename T, int D>
 cudaError_t launch(const AttnParams& p, const Layout& L, cudaStream_t s) {
-  const int smem = kWarpsPerCta * kRing * step_bytes<D>();
+  const int ring = kWarpsPerCta * kRing * step_bytes<D>();
   cudaError_t e;
   bool first = p.a.G == 0;
   if (p.a.G > 0 && L.tc) {
     e = launch_prefix_tc(p, s);
     if (e != cudaSuccess) return e;
   } else if (p.a.G > 0) {
-    e = cudaFuncSetAttribute(prefix_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(prefix_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
     if (e != cudaSuccess) return e;
-    prefix_kernel<T, D><<<p.workers / kWarpsPerCta, kWarpsPerCta * 32, smem, s>>>(p);
+    prefix_kernel<T, D><<<p.workers / kWarpsPerCta, kWarpsPerCta * 32, ring, s>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   if (!L.short_own) {
-    e = cudaFuncSetAttribute(own_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(own_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
     if (e != cudaSuccess) return e;
     const int64_t tasks = (int64_t)p.a.R * p.a.Hkv * L.own_blocks * p.nsplit;
     e = launch_next(own_kernel<T, D>, (int)((tasks + kWarpsPerCta - 1) / kWarpsPerCta),
-                    kWarpsPerCta * 32, smem, s, !first, p, L.own_blocks);
+                    kWarpsPerCta * 32, ring, s, !first, p, L.own_blocks);
     if (e != cudaSuccess) return e;
     first = false;
   }
-  Deal deal{1, (p.gqa + kJoinHeads - 1) / kJoinHeads, 0};
+  Deal deal{1, (p.gqa + kJoinHeads - 1) / kJoinHeads, 0, 1};
   // Few rows: every key/value head has its warp (12 branches of one sequence: 30 us
   // instead of 39).  When that takes more than a turn: as many heads to a warp as it
   // has lanes for (32 x 12 branches: 110 us instead of 116; 256 x 24: 312 of 332).
@@ -737,16 +769,19 @@ cudaError_t launch(const AttnParams& p, const Layout& L, cudaStream_t s) {
          (int64_t)p.a.R * p.a.Hkv / deal.pack > warps)
     deal.pack *= 2;
   deal.tasks = deal.pack > 1 ? (p.a.Hkv + deal.pack - 1) / deal.pack : p.a.Hkv * deal.blocks;
-  const int threads = std::min(kJoinWarps, deal.tasks) * 32;
-  const int resident = std::max(num_sms(), 1) * kJoinCtas<D> * kJoinWarps * 32 / threads;
-  const int grid = std::min(p.a.R, resident);
+  const int64_t tasks = (int64_t)p.a.R * deal.tasks;
+  while (deal.split < kJoinWarps && tasks * deal.split * 2 <= warps) deal.split *= 2;
+  const int threads = (deal.split > 1 ? deal.split : std::min(kJoinWarps, deal.tasks)) * 32;
+  const int resident = (int)warps * 32 / threads;
+  const int grid = deal.split > 1 ? (int)tasks : std::min(p.a.R, resident);
+  const int smem = join_bytes<D>(deal.split > 1 ? deal.split : 0);
   // Started early, the join finds the shared-memory split of the kernel before on
   // its SM: 256 x 24 branches then take 52 us more (it has many turns, and lives
   // on its cache), a call of one turn 2 us less.
-  const bool early = !first && p.a.R <= resident;
+  const bool early = !first && (deal.split > 1 || p.a.R <= resident);
   return L.short_own
-             ? launch_next(join_kernel<T, D, true>, grid, threads, 0, s, early, p, deal)
-             : launch_next(join_kernel<T, D, false>, grid, threads, 0, s, early, p, deal);
+             ? launch_next(join_kernel<T, D, true>, grid, threads, smem, s, early, p, deal)
+             : launch_next(join_kernel<T, D, false>, grid, threads, smem, s, early, p, deal);
 }
 
 template <typename T>

@@ -169,6 +169,15 @@ def test_long_prefixes(page):
     check(s, call(s), rows=list(range(0, 193, 7)) + [39, 40, 42, 43, 192])
 
 
+@pytest.mark.parametrize("D,page", [(256, 64), (128, 64), (64, 20)])
+@pytest.mark.parametrize("suf", [[3, 0, 9, 100], [1, 2, 0, 3]])
+def test_few_rows_over_long_prefixes(D, page, suf):
+    """A hundred partials for a row: several warps join them."""
+    s = make([2, 1, 1], [9990, 0, 6011], suf, 14, 2, D, page, dtype_of("float16"), seed=D)
+    poison(s)
+    check(s, call(s))
+
+
 @pytest.mark.parametrize("page", [16, 128, 20])
 def test_many_short_groups(page):
     """Every worker has many items, most of them of one tile."""
