@@ -171,9 +171,15 @@ def _check(status: int, what: str):
 
 
 # ---- tensor marshalling ---------------------------------------------------------------
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dev_ptr(t):

@@ -246,7 +246,7 @@ extern "C" ssd_status ssd_page_plan(const int32_t* lens, const int32_t* new_toke
                      owner,    cu,         kv_len, held_out,   served, free_out,     dev_status};
   const size_t smem = (size_t)5 * (B + 1) * sizeof(int);
   const int64_t work = std::max<int64_t>(max_rows / kRowsPerCta, B / kThreads);
-  const int grid = (int)std::min<int64_t>(std::max(num_sms(), 1), 1 + work);
+  const int grid = work == 0 ? 1 : (int)std::min<int64_t>(std::max(num_sms(), 1), 1 + work);
   cudaError_t e = cudaSuccess;
   if (smem > 46 * 1024)  // more than a kernel may have without asking
     e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
