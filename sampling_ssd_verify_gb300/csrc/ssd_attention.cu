@@ -465,6 +465,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinCtas<D>)
 
       // where the partials are, on its way while the own tokens are read
       const Parts s = mine ? parts_of(p, row, h, in_h) : Parts{0, 0, 0};
+      if (SHORT_OWN && s.np > 0) {
+        // the first partial on its way to L2 meanwhile: four heads share its lines
+        const float* x = p.po + part_at<D>(s.slot, p.mt, s.i, quad * 16 + (gid & 3) * 4);
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(x + (int64_t)i * 64 * p.mt));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.pml + (int64_t)s.slot * p.mt + s.i));
+      }
 
       float o[NI][16] = {};            // sums at dimensions 64 i + 16 quad + e
       float m = -INFINITY, l = 0.f;
