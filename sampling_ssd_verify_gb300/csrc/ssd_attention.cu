@@ -262,6 +262,7 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32)
   k.unit = s_start[warp].unit;
   k.item = s_start[warp].item;
   k.w = w;
+  k.hh = 0;
   Stretch s;
   while (next_stretch(p, k, s)) {
     if (s.slot >= p.nslots) break;  // cannot happen: the host sized the slots for every split
@@ -354,16 +355,17 @@ constexpr int join_bytes(int split) {  // half the warps' sums, weights and maxi
   return split / 2 * 32 * (D / 4 + 2) * 4;
 }
 
-// The prefix's partials of a pair: np of them, from `slot` on, at row `i`.
+// The prefix's partials of a pair: np of them, every hg-th from `slot` on, at row `i`.
 struct Parts {
   int np, slot, i;
 };
 __device__ __forceinline__ Parts parts_of(const AttnParams& p, const int4& row, int h, int head) {
   if (row.x < 0) return Parts{0, 0, 0};
   const int i = row.y + head, mb = p.mt == kTcBlock ? i / kTcBlock : i / kBlockRows;
-  const int item = row.x + h * row.z + mb;
+  const int set = h / p.hg, hh = h - set * p.hg;
+  const int item = (row.x + set * row.z + mb) * p.hg + hh;
   const int2 w = p.item_workers[item];
-  return Parts{w.y - w.x + 1, item + w.x, i - mb * p.mt};
+  return Parts{w.y - w.x + 1, item + w.x * p.hg, i - mb * p.mt};
 }
 
 // Eight rows (heads) of the 16 that an instruction has; the others are zeros.
@@ -569,16 +571,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinCtas<D>)
       const int ns = SHORT_OWN || !mine ? 0 : (len + per - 1) / per;  // of the own tokens
       const float2* ml_p = p.pml + (int64_t)s.slot * p.mt + s.i;
       const float2* ml_o = p.sml + pair * p.nsplit;
+      const int64_t next = (int64_t)p.mt * p.hg;  // rows from one partial to the next
       float top = m;
 #pragma unroll 4
-      for (int j = part; j < s.np; j += deal.split) top = fmaxf(top, ml_p[(int64_t)j * p.mt].x);
+      for (int j = part; j < s.np; j += deal.split) top = fmaxf(top, ml_p[j * next].x);
 #pragma unroll 4
       for (int j = part; j < ns; j += deal.split) top = fmaxf(top, ml_o[j].x);
       const float off = top == -INFINITY ? 0.f : top, keep = exp2_fast(m - off);
       m = top;
       l *= keep;
       for (int j = part; j < s.np; j += deal.split) {
-        const float2 ml = ml_p[(int64_t)j * p.mt];
+        const float2 ml = ml_p[j * next];
         l = fmaf(ml.y, exp2_fast(ml.x - off), l);
       }
       for (int j = part; j < ns; j += deal.split) l = fmaf(ml_o[j].y, exp2_fast(ml_o[j].x - off), l);
@@ -599,7 +602,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinCtas<D>)
         const float* po = p.po + part_at<D>(s.slot, p.mt, s.i, quad * 16 + i * 64);
 #pragma unroll 4
         for (int j = part; j < s.np; j += deal.split)
-          add(exp2_fast(ml_p[(int64_t)j * p.mt].x - off), po + (int64_t)j * p.mt * D, 4 * p.mt);
+          add(exp2_fast(ml_p[j * next].x - off), po + j * next * D, 4 * p.mt);
         const float* so = p.so + pair * p.nsplit * D + quad * 16 + i * 64;
 #pragma unroll 4
         for (int j = part; j < ns; j += deal.split) add(exp2_fast(ml_o[j].x - off), so + (int64_t)j * D, 4);
@@ -695,12 +698,18 @@ bool plan(const ssd_attention& a, AttnParams& p, Layout& L) {
   p.mt = L.tc ? kTcBlock : kBlockRows;
   p.tn = L.tc ? kTcTile : kTileTokens;
   const int warps = sms * ctas_per_sm(a.D) * kWarpsPerCta;  // resident at once
-  p.workers = L.tc ? sms : warps;
+  // sets of up to eight heads where a token's heads lie closer than its neighbour
+  p.hg = 1;
+  if (L.tc && a.k.head_stride < a.k.token_stride && a.v.head_stride < a.v.token_stride)
+    for (int n = 2; n <= std::min(8, sms); ++n)
+      if (a.Hkv % n == 0) p.hg = n;
+  p.sets = a.Hkv / p.hg;
+  p.workers = L.tc ? sms / p.hg : warps;
   const int64_t items =
       a.Hkv * ((int64_t)a.R * p.gqa / p.mt + std::min<int64_t>(a.G, a.R));
   const int64_t tiles = ((int64_t)a.prefix_cols * a.page_size + p.tn - 1) / p.tn;
   if (items * (tiles + 1) > 0x7fffffff) return false;
-  p.nslots = a.G > 0 ? (int)(items + p.workers) : 0;
+  p.nslots = a.G > 0 ? (int)(items + (int64_t)p.workers * p.hg) : 0;
   // own tokens: read by the join where they are few; else in stretches of two
   // tiles or more, eight for each resident warp, which evens out their lengths
   const int64_t most = a.lens ? (int64_t)a.cols * a.page_size : 0;

@@ -12,6 +12,10 @@
 // partials are joined afterwards.  The partial of item i by worker w has slot
 // i + w: along the sequence of stretches one of the two steps up each time,
 // so slots are never shared, and need no counter.
+//
+// Where the key/value heads of a token lie side by side, a worker is `hg` CTAs
+// that go through the same stretches, each for its head of a set of hg: they
+// read neighbouring pieces of memory at about the same time.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -65,12 +69,14 @@ struct AttnParams {
   int gqa;                // query heads per key/value head
   // prefixes: items, partials
   int mt, tn;             // rows of a block, tokens of a tile
-  int workers;
+  int hg, sets;           // key/value heads of a set, sets
+  int workers;            // of hg CTAs each
   int nslots;
   float* po;              // [nslots, D / 4, mt, 4] unnormalised sums (part_at)
   float2* pml;            // [nslots, mt] largest score (base 2), weight
   int4* row_items;        // [R] row_items_of
-  int2* item_workers;     // [items] first and last worker of an item with tokens
+  int2* item_workers;     // [items] first and last worker of an item with tokens; items of a
+                          // set are hg in a row
   // own tokens: nsplit stretches per row, each with its partial
   int nsplit;
   float* so;              // [R, Hq, nsplit, D]
@@ -97,7 +103,7 @@ __device__ __forceinline__ void wait_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// What the join needs of a row's group: the number of the group's first item,
+// What the join needs of a row's group: the number of the group's first set of items,
 // or -1 when there is no prefix to join; the row's first pair in the group; the
 // blocks of a key/value head.
 __device__ __forceinline__ int4 row_items_of(int item, int pair, int blocks) {
@@ -163,7 +169,7 @@ __device__ __forceinline__ int find_starts(const AttnParams& p, int w0, Start* s
       if (g < G) {
         q = group_of(p, g);
         torn |= q.torn;
-        mine = torn ? mine : make_int2(p.a.Hkv * q.blocks * q.cost, p.a.Hkv * q.blocks);
+        mine = torn ? mine : make_int2(p.sets * q.blocks * q.cost, p.sets * q.blocks);
         if (pass == 0 && blockIdx.x == 0 && q.bad) flag(p, SSD_DEV_BAD_LENGTH);
       }
       int2 x = mine;
@@ -234,17 +240,17 @@ struct Stretch {
 struct Walk {
   int u, u1;              // tiles still to do
   int g, unit, item;
-  int w;
+  int w, hh;              // worker, head of a set
 };
 __device__ __forceinline__ bool next_stretch(const AttnParams& p, Walk& k, Stretch& s) {
   while (k.u < k.u1) {
     Group q = group_of(p, k.g);
-    int n = p.a.Hkv * q.blocks * q.cost;
+    int n = p.sets * q.blocks * q.cost;
     while (k.u >= k.unit + n) {  // ends: u < u1 <= total
       k.unit += n;
-      k.item += p.a.Hkv * q.blocks;
+      k.item += p.sets * q.blocks;
       q = group_of(p, ++k.g);
-      n = p.a.Hkv * q.blocks * q.cost;
+      n = p.sets * q.blocks * q.cost;
     }
     const int local = (k.u - k.unit) / q.cost;   // item within the group
     const int at = (k.u - k.unit) - local * q.cost;
@@ -252,12 +258,13 @@ __device__ __forceinline__ bool next_stretch(const AttnParams& p, Walk& k, Stret
     k.u += take;
     s.q = q;
     s.g = k.g;
-    s.h = local / q.blocks;
-    s.mb = local - s.h * q.blocks;
+    const int set = local / q.blocks;
+    s.h = set * p.hg + k.hh;
+    s.mb = local - set * q.blocks;
     s.tile0 = max(at - 1, 0);
     s.tile1 = at + take - 1;
-    s.item = k.item + local;
-    s.slot = s.item + k.w;
+    s.item = (k.item + local) * p.hg + k.hh;
+    s.slot = s.item + k.w * p.hg;
     if (s.tile1 > s.tile0) return true;  // not only the unit of the item's start
   }
   return false;

@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh.drained, 1);
     fence_barrier_init();
   }
-  const int w = blockIdx.x;
+  const int w = blockIdx.x / p.hg;
   const int total = find_starts<kThreads, 1>(p, w, &sh.start, sh.warp_sums);
   fence_before();
   __syncthreads();
@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   k.u = first_unit(p, w, total);
   k.u1 = first_unit(p, w + 1, total);
   k.w = w;
+  k.hh = blockIdx.x - w * p.hg;
   if (k.u < k.u1) {
     k.g = sh.start.g;
     k.unit = sh.start.unit;
@@ -621,7 +622,7 @@ cudaError_t launch(const AttnParams& p, const CUtensorMap& km, const CUtensorMap
   const cudaError_t e = cudaFuncSetAttribute(
       prefix_tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  prefix_tc_kernel<T, D><<<p.workers, kThreads, smem, s>>>(p, km, vm);
+  prefix_tc_kernel<T, D><<<p.workers * p.hg, kThreads, smem, s>>>(p, km, vm);
   return cudaGetLastError();
 }
 
