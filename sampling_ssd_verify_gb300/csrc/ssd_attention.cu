@@ -249,14 +249,14 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32)
     prefix_kernel(const __grid_constant__ AttnParams p) {
   extern __shared__ __align__(128) unsigned char s_ring[];
   __shared__ Start s_start[kWarpsPerCta];
-  __shared__ int2 s_warp[kWarpsPerCta];
+  __shared__ int3 s_warp[kWarpsPerCta];
   start_next();
   const int w0 = blockIdx.x * kWarpsPerCta, warp = threadIdx.x >> 5, w = w0 + warp;
-  const int total = find_starts<kWarpsPerCta * 32, kWarpsPerCta>(p, w0, s_start, s_warp);
+  const Split all = find_starts<kWarpsPerCta * 32, kWarpsPerCta>(p, w0, s_start, s_warp);
   const uint32_t ring = smem_addr(s_ring) + warp * kRing * step_bytes<D>();
   Walk k;
-  k.u = first_unit(p, w, total);
-  k.u1 = first_unit(p, w + 1, total);
+  k.u = all.first(w);
+  k.u1 = all.first(w + 1);
   if (k.u >= k.u1) return;
   k.g = s_start[warp].g;
   k.unit = s_start[warp].unit;
@@ -697,6 +697,7 @@ bool plan(const ssd_attention& a, AttnParams& p, Layout& L) {
   L.tc = prefix_tc_fits(a);
   p.mt = L.tc ? kTcBlock : kBlockRows;
   p.tn = L.tc ? kTcTile : kTileTokens;
+  p.in_step = L.tc;
   const int warps = sms * ctas_per_sm(a.D) * kWarpsPerCta;  // resident at once
   // sets of up to eight heads where a token's heads lie closer than its neighbour
   p.hg = 1;

@@ -181,7 +181,7 @@ struct Header {
   uint64_t o_empty;                 // the sums of a stretch have been read
   uint64_t drained;
   Job job[2];                       // by the parity of the stretch
-  int2 warp_sums[kThreads / 32];
+  int3 warp_sums[kThreads / 32];
   Start start;
   uint32_t tmem;
   volatile int err;
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
   }
   const int w = blockIdx.x / p.hg;
-  const int total = find_starts<kThreads, 1>(p, w, &sh.start, sh.warp_sums);
+  const Split all = find_starts<kThreads, 1>(p, w, &sh.start, sh.warp_sums);
   fence_before();
   __syncthreads();
   fence_after();
@@ -240,8 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // the third warpgroup's warps walk the stretches by themselves
   Walk k;
-  k.u = first_unit(p, w, total);
-  k.u1 = first_unit(p, w + 1, total);
+  k.u = all.first(w);
+  k.u1 = all.first(w + 1);
   k.w = w;
   k.hh = blockIdx.x - w * p.hg;
   if (k.u < k.u1) {

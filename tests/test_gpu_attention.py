@@ -178,6 +178,21 @@ def test_few_rows_over_long_prefixes(D, page, suf):
     check(s, call(s))
 
 
+@pytest.mark.parametrize("sizes,pre", [
+    ([33], [4999]),                     # two blocks of a prefix's pairs
+    ([95], [2111]), ([160], [3001]),    # three, five
+    ([250], [4090]), ([310], [1000]),   # eight, ten
+    ([64, 60, 5], [1500, 700, 900]),    # blocks of several prefixes, one of a single block
+    ([130, 8, 8], [6000, 0, 0]),        # groups without tokens beside
+])
+def test_several_blocks_of_a_prefix(sizes, pre):
+    """As many blocks as divide the workers or not: some may be left out."""
+    R = sum(sizes)
+    s = make(sizes, pre, np.arange(R) * 7 % 80, 32, 8, 128, 32, dtype_of("bfloat16"), seed=R)
+    poison(s)
+    check(s, call(s), rows=sorted(set(range(0, R, 5)) | {R - 1}))
+
+
 @pytest.mark.parametrize("page", [16, 128, 20])
 def test_many_short_groups(page):
     """Every worker has many items, most of them of one tile."""
