@@ -290,11 +290,14 @@ __device__ __forceinline__ int own_stretch(const AttnParams& p, int len) {
 template <typename T, int D>
 __device__ __forceinline__ void own_task(const AttnParams& p, uint32_t ring, int64_t task,
                                          int blocks) {
+  // heads side by side: a token's lie next to each other (256 rows with 450 tokens
+  // on 8 heads over a prompt of 16000: 151 us instead of 153; own caches of 900, 279
+  // instead of 283 over 40000; 19 groups of a few rows on 4 heads 24.6 instead of 24.3)
+  const int h = (int)(task % p.a.Hkv);
+  task /= p.a.Hkv;
   const int split = (int)(task % p.nsplit);
   task /= p.nsplit;
-  const int mb = (int)(task % blocks);
-  task /= blocks;
-  const int h = (int)(task % p.a.Hkv), r = (int)(task / p.a.Hkv);
+  const int mb = (int)(task % blocks), r = (int)(task / blocks);
   const int len = own_len(p, r), n = own_stretch(p, len);
   const int t0 = min(len, split * n), t1 = min(len, t0 + n);
   if (h == 0 && mb == 0 && split == 0 && (threadIdx.x & 31) == 0 && len != p.a.lens[r])
