@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32)
     prefix_kernel(const __grid_constant__ AttnParams p) {
   extern __shared__ __align__(128) unsigned char s_ring[];
   __shared__ Start s_start[kWarpsPerCta];
-  __shared__ int3 s_warp[kWarpsPerCta];
+  __shared__ int4 s_warp[kWarpsPerCta];
   start_next();
   const int w0 = blockIdx.x * kWarpsPerCta, warp = threadIdx.x >> 5, w = w0 + warp;
   const Split all = find_starts<kWarpsPerCta * 32, kWarpsPerCta>(p, w0, s_start, s_warp);
@@ -718,6 +718,7 @@ bool plan(const ssd_attention& a, AttnParams& p, Layout& L) {
   // tiles or more, eight for each resident warp, which evens out their lengths
   const int64_t most = a.lens ? (int64_t)a.cols * a.page_size : 0;
   L.short_own = most <= kShortOwn;
+  p.own_apart = L.tc && !L.short_own;
   L.own_blocks = (p.gqa + kBlockRows - 1) / kBlockRows;
   const int64_t own = (int64_t)a.R * a.Hkv * L.own_blocks;
   p.nsplit = (int)std::max<int64_t>(

@@ -78,7 +78,8 @@ struct AttnParams {
   int2* item_workers;     // [items] first and last worker of an item with tokens; items of a
                           // set are hg in a row
   // own tokens: nsplit stretches per row, each with its partial
-  int in_step;            // workers may be left out to keep the others in step
+  int in_step;            // workers may be left out to keep the others in step,
+  int own_apart;          // or for own tokens in a kernel of their own
   int nsplit;
   float* so;              // [R, Hq, nsplit, D]
   float2* sml;            // [R, Hq, nsplit]
@@ -156,8 +157,19 @@ struct Split {
 // without own tokens, 32 heads on 8, of 19 workers (8 CTAs each): 8 blocks over
 // 40000 tokens take 145 us by 16, 202 by 19; over 3000, 32 and 36; 3 blocks over
 // 24000 take 50 us by 18, 59 by 19; but 10 blocks 166 by 10, 117 by 19.
-__device__ __forceinline__ Split split_of(const AttnParams& p, int total, int items, int shared) {
+//
+// A prefix of several blocks leaves the memory idle, which own tokens in a kernel of
+// their own wait for.  With enough of those, half the workers take the prefixes and
+// the other SMs go to the own tokens at once.  `own` counts 16 tokens a unit.  In own
+// tokens x heads x D / 128 to prefix tokens x heads x blocks: at 0.6 it takes 122 us
+// instead of 129, at 0.9 140 instead of 151, at 3.4 115 instead of 121; at 0.45 123
+// instead of 118, and with 16 items, more than the 9 workers left, 206 instead of 197.
+__device__ __forceinline__ Split split_of(const AttnParams& p, int total, int items, int shared,
+                                          int own) {
   Split s{total, min(p.workers, total)};
+  if (p.own_apart && shared >= total - shared && 2 * items <= s.workers &&
+      2ll * own * 16 * p.a.Hkv * p.a.D >= 128ll * total * p.hg * p.tn)
+    s.workers /= 2;
   if (p.in_step && items > 0 && shared >= total - shared) {
     const int idle = s.workers % items;
     if (items <= s.workers && 4 * idle <= s.workers) s.workers -= idle;
@@ -173,15 +185,20 @@ struct Start {
 };
 template <int NT, int NW>
 __device__ __forceinline__ Split find_starts(const AttnParams& p, int w0, Start* s_start,
-                                             int3* s_warp) {
+                                             int4* s_warp) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.a.G;
   // pass 0 forms the total, pass 1 the starts that it determines; up to NT
   // groups, the sums of pass 0 serve for pass 1
-  int torn = 0;
+  int torn = 0, own = 0;
   Split all{0, 0};
+  if (p.own_apart) {
+    const int most = p.a.cols * p.a.page_size;
+    for (int r = tid; r < p.a.R; r += NT) own += min(max(p.a.lens[r], 0), most) >> 4;
+    own = __reduce_add_sync(0xffffffffu, own);
+  }
   for (int pass = 0; pass < 2; ++pass) {
-    int3 base = make_int3(0, 0, 0);
+    int4 base = make_int4(0, 0, 0, 0);
     for (int g0 = 0; g0 < G; g0 += NT) {
       const int g = g0 + tid;
       int2 mine = make_int2(0, 0);
@@ -200,17 +217,18 @@ __device__ __forceinline__ Split find_starts(const AttnParams& p, int w0, Start*
         const int b = __shfl_up_sync(0xffffffffu, x.y, d);
         if (lane >= d) { x.x += a; x.y += b; }
       }
-      if (lane == 31) s_warp[warp] = make_int3(x.x, x.y, shared);
+      if (lane == 31) s_warp[warp] = make_int4(x.x, x.y, shared, own);
       const int any_torn = __syncthreads_or(torn);
-      int3 before = base;
+      int4 before = base;
+      base.w = 0;  // the same for all groups
       for (int w = 0; w < NT / 32; ++w) {
-        const int3 y = s_warp[w];
+        const int4 y = s_warp[w];
         if (w < warp) { before.x += y.x; before.y += y.y; }
-        base = make_int3(base.x + y.x, base.y + y.y, base.z + y.z);
+        base = make_int4(base.x + y.x, base.y + y.y, base.z + y.z, base.w + y.w);
       }
       if (G <= NT) {
         torn = any_torn;
-        all = split_of(p, torn ? 0 : base.x, base.y, base.z);
+        all = split_of(p, torn ? 0 : base.x, base.y, base.z, base.w);
         pass = 1;
       }
       if (pass == 1 && g < G) {
@@ -239,7 +257,7 @@ __device__ __forceinline__ Split find_starts(const AttnParams& p, int w0, Start*
     }
     if (pass == 0) {
       torn = __syncthreads_or(torn);
-      all = split_of(p, torn ? 0 : base.x, base.y, base.z);
+      all = split_of(p, torn ? 0 : base.x, base.y, base.z, base.w);
     }
   }
   // rows of no group

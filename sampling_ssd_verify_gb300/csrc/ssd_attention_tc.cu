@@ -181,7 +181,7 @@ struct Header {
   uint64_t o_empty;                 // the sums of a stretch have been read
   uint64_t drained;
   Job job[2];                       // by the parity of the stretch
-  int3 warp_sums[kThreads / 32];
+  int4 warp_sums[kThreads / 32];
   Start start;
   uint32_t tmem;
   volatile int err;

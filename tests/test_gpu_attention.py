@@ -185,10 +185,12 @@ def test_few_rows_over_long_prefixes(D, page, suf):
     ([64, 60, 5], [1500, 700, 900]),    # blocks of several prefixes, one of a single block
     ([130, 8, 8], [6000, 0, 0]),        # groups without tokens beside
 ])
-def test_several_blocks_of_a_prefix(sizes, pre):
-    """As many blocks as divide the workers or not: some may be left out."""
+@pytest.mark.parametrize("own", [80, 900])
+def test_several_blocks_of_a_prefix(sizes, pre, own):
+    """As many blocks as divide the workers or not: some may be left out, half of
+    them with long own caches."""
     R = sum(sizes)
-    s = make(sizes, pre, np.arange(R) * 7 % 80, 32, 8, 128, 32, dtype_of("bfloat16"), seed=R)
+    s = make(sizes, pre, np.arange(R) * 157 % own, 32, 8, 128, 32, dtype_of("bfloat16"), seed=R)
     poison(s)
     check(s, call(s), rows=sorted(set(range(0, R, 5)) | {R - 1}))
 
