@@ -554,14 +554,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinCtas<D>)
           uint4 v0[NI], v1[NI];
           load_chunks<8>(v0, vh + at0 + (int64_t)z * a.v.head_stride, pg0 >= 0);
           load_chunks<8>(v1, vh + at1 + (int64_t)z * a.v.head_stride, pg1 >= 0);
-          const uint32_t w = sub == z ? pw : 0u;
+          // a lane's sums stay as they are unless the head is its own: a weight of
+          // zero would not do, for zero times an infinity or NaN is NaN
 #pragma unroll
           for (int i = 0; i < NI; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              mma_k8<T>(o[i][e], o[i][e + 8], w,
+            for (int e = 0; e < 8; ++e) {
+              float x = o[i][e], y = o[i][e + 8];
+              mma_k8<T>(x, y, pw,
                         __byte_perm(word(v0[i], e / 2), word(v1[i], e / 2),
                                     e & 1 ? 0x7632 : 0x5410));
+              o[i][e] = sub == z ? x : o[i][e];
+              o[i][e + 8] = sub == z ? y : o[i][e + 8];
+            }
         }
       }
       l += __shfl_xor_sync(0xffffffffu, l, 1);

@@ -266,6 +266,34 @@ def test_rising_scores():
     check(s, call(s), rows=range(0, 20, 4))
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,rows,suf", [
+    (128, 32, 8, 700, 6), (64, 8, 8, 900, 9),   # several key/value heads to a warp
+    (256, 24, 8, 500, 5),
+    (128, 32, 8, 20, 6),                        # a warp each
+    (128, 32, 8, 60, 200), (256, 8, 4, 9, 70),  # a kernel of their own for own tokens
+])
+def test_infinite_values_stay_with_their_head(D, Hq, Hkv, rows, suf):
+    """An infinity or NaN among a head's values reaches the rows and heads that
+    read it, and no others."""
+    torch, dev = torch_dev()
+    sizes = [rows // 2, rows - rows // 2]
+    s = make(sizes, [70, 33], [suf] * rows, Hq, Hkv, D, 16, torch.float16, seed=rows)
+    want = call(s)["out"].clone()
+    M = Hq // Hkv
+    hit = torch.zeros((rows, Hq), dtype=torch.bool, device=dev)
+    v = s["v"]
+    for r, h, x in ((0, 1, float("inf")), (rows - 1, 0, float("nan")),
+                    (rows // 3, Hkv - 1, float("-inf")), (rows // 3 + 1, 2, float("nan"))):
+        v[int(s["t"][r, (suf - 1) // 16]), (suf - 1) % 16, h] = x
+        hit[r, h * M:(h + 1) * M] = True
+    v[int(s["pt"][1, 1]), 3, 3] = float("inf")      # a token of the second prefix
+    hit[sizes[0]:, 3 * M:4 * M] = True
+    got = call(s)["out"]
+    assert bool(torch.isfinite(got[~hit]).all())
+    assert torch.equal(got[~hit], want[~hit])
+    assert not bool(torch.isfinite(got[hit]).any())
+
+
 def test_rows_in_no_group():
     torch, dev = torch_dev()
     s = make([3, 4, 2], [50, 60, 70], [5] * 9, 4, 2, 64, 16, torch.bfloat16)
