@@ -294,6 +294,20 @@ def test_infinite_values_stay_with_their_head(D, Hq, Hkv, rows, suf):
     assert not bool(torch.isfinite(got[hit]).any())
 
 
+@pytest.mark.parametrize("D,page,rows,suf", [(128, 16, 700, 6), (64, 20, 30, 90), (256, 16, 40, 3)])
+def test_queries_that_are_no_numbers_stay_in_their_row(D, page, rows, suf):
+    torch, dev = torch_dev()
+    s = make([rows], [500], [suf] * rows, 16, 4, D, page, torch.bfloat16, seed=rows)
+    s["q"][3, 5] = float("nan")
+    s["q"][rows - 2, 0, 7] = float("inf")
+    keep = torch.ones((rows, 16), dtype=torch.bool, device=dev)
+    keep[3, 5] = keep[rows - 2, 0] = False
+    got = call(s)["out"]
+    assert bool(torch.isfinite(got[keep]).all())
+    assert not bool(torch.isfinite(got[~keep]).any())
+    check(s, call(s), rows=[0, 2, 4, rows // 2, rows - 3, rows - 1])
+
+
 def test_rows_in_no_group():
     torch, dev = torch_dev()
     s = make([3, 4, 2], [50, 60, 70], [5] * 9, 4, 2, 64, 16, torch.bfloat16)
