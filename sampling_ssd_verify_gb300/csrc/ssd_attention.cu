@@ -344,7 +344,11 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32)
 constexpr int kJoinWarps = 8;
 constexpr int kJoinHeads = 8;
 template <int D> constexpr int kJoinCtas = D == 256 ? 1 : 2;  // per SM, by registers
-constexpr int kShortOwn = 64;  // tokens of an own cache up to which the join reads it
+// Own caches that the join reads: of so many tokens, or of one page of so many, which
+// is rarely full.  32 x 12 branches: 109 us instead of 111 with 4 tokens, 115 and 114
+// with 16, 126 and 119 with 30; 256 x 24 with 4 of a page of 64: 301 instead of 420,
+// with 1 to 32 tokens 408 and 441, with 1 to 64 528 and 481.
+constexpr int kShortOwn = 16, kShortPage = 64;
 
 // How a row's query heads are dealt to tasks: `pack` key/value heads of 8 / pack
 // lanes each, or, with more than eight query heads, `blocks` tasks for one.  With
@@ -744,7 +748,7 @@ bool plan(const ssd_attention& a, AttnParams& p, Layout& L) {
   // own tokens: read by the join where they are few; else in stretches of two
   // tiles or more, eight for each resident warp, which evens out their lengths
   const int64_t most = a.lens ? (int64_t)a.cols * a.page_size : 0;
-  L.short_own = most <= kShortOwn;
+  L.short_own = most <= (a.cols == 1 ? kShortPage : kShortOwn);
   p.own_apart = L.tc && !L.short_own;
   L.own_blocks = (p.gqa + kBlockRows - 1) / kBlockRows;
   const int64_t own = (int64_t)a.R * a.Hkv * L.own_blocks;
