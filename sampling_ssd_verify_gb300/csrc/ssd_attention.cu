@@ -746,14 +746,16 @@ bool plan(const ssd_attention& a, AttnParams& p, Layout& L) {
   if (items * (tiles + 1) > 0x7fffffff) return false;
   p.nslots = a.G > 0 ? (int)(items + (int64_t)p.workers * p.hg) : 0;
   // own tokens: read by the join where they are few; else in stretches of two
-  // tiles or more, eight for each resident warp, which evens out their lengths
+  // tiles or more, four for each resident warp, which evens out their lengths.
+  // (256 rows with 450 tokens over a prompt of 16000: 131 us, by eight 137, by two 137;
+  // 100 rows with 3000: 217, 227, 235; 256 with 1500: 309, 292, 332.)
   const int64_t most = a.lens ? (int64_t)a.cols * a.page_size : 0;
   L.short_own = most <= (a.cols == 1 ? kShortPage : kShortOwn);
   p.own_apart = L.tc && !L.short_own;
   L.own_blocks = (p.gqa + kBlockRows - 1) / kBlockRows;
   const int64_t own = (int64_t)a.R * a.Hkv * L.own_blocks;
   p.nsplit = (int)std::max<int64_t>(
-      1, std::min<int64_t>((most + 2 * kTileTokens - 1) / (2 * kTileTokens), 8 * warps / own));
+      1, std::min<int64_t>((most + 2 * kTileTokens - 1) / (2 * kTileTokens), 4 * warps / own));
   if (own * p.nsplit / kWarpsPerCta >= 0x7fffffff) return false;
   size_t at = 0;
   auto take = [&](size_t bytes) {
