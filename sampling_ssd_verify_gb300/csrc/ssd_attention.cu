@@ -5,6 +5,11 @@
 // out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m), with m the running
 // maximum, over any stretch of tokens; two stretches join by weighting each
 // with exp(m_i - max m).
+//
+// The join is bound by the latency of its loads (partials from L2, own tokens from
+// memory), not by bytes: 96 us for 6144 rows with 1 to 8 own tokens, whose queries,
+// own tokens and outputs would be 31 us at the copy rate.  The kernel of long own caches reads
+// them at 5.4 TB/s of the 6.8 of a copy when it has the memory to itself.
 
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -816,9 +821,10 @@ cudaError_t launch(const AttnParams& p, const Layout& L, cudaStream_t s) {
     first = false;
   }
   Deal deal{1, (p.gqa + kJoinHeads - 1) / kJoinHeads, 0, 1};
-  // Few rows: every key/value head has its warp (12 branches of one sequence: 30 us
-  // instead of 39).  When that takes more than a turn: as many heads to a warp as it
-  // has lanes for (32 x 12 branches: 110 us instead of 116; 256 x 24: 312 of 332).
+  // Few rows: every key/value head has its warp (12 branches of one sequence: 23 us
+  // instead of 40), or several that share its partials (23 instead of 31).  When a warp
+  // each takes more than a turn: as many heads to a warp as it has lanes for (32 x 12
+  // branches: 109 us instead of 114; 256 x 24: 305 instead of 350).
   const int64_t warps = (int64_t)std::max(num_sms(), 1) * kJoinCtas<D> * kJoinWarps;
   while (deal.pack * 2 * p.gqa <= kJoinHeads &&
          (int64_t)p.a.R * p.a.Hkv / deal.pack > warps)
@@ -831,8 +837,8 @@ cudaError_t launch(const AttnParams& p, const Layout& L, cudaStream_t s) {
   const int grid = deal.split > 1 ? (int)tasks : std::min(p.a.R, resident);
   const int smem = join_bytes<D>(deal.split > 1 ? deal.split : 0);
   // Started early, the join finds the shared-memory split of the kernel before on
-  // its SM: 256 x 24 branches then take 52 us more (it has many turns, and lives
-  // on its cache), a call of one turn 2 us less.
+  // its SM: 256 x 24 branches then take 23 us more (it has many turns, and lives
+  // on its cache), uneven groups of a few rows, one turn, 1 us less.
   const bool early = !first && (deal.split > 1 || p.a.R <= resident);
   return L.short_own
              ? launch_next(join_kernel<T, D, true>, grid, threads, smem, s, early, p, deal)

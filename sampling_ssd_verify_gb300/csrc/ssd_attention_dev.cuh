@@ -162,8 +162,8 @@ struct Split {
 // their own wait for.  With enough of those, half the workers take the prefixes and
 // the other SMs go to the own tokens at once.  `own` counts 16 tokens a unit.  In own
 // tokens x heads x D / 128 to prefix tokens x heads x blocks: at 0.6 it takes 122 us
-// instead of 129, at 0.9 140 instead of 151, at 3.4 115 instead of 121; at 0.45 123
-// instead of 118, and with 16 items, more than the 9 workers left, 206 instead of 197.
+// instead of 128, at 0.9 130 instead of 153, at 3.4 116 instead of 124; at 0.45 122
+// instead of 115, and with 16 items, more than the 9 workers left, 218 instead of 209.
 __device__ __forceinline__ Split split_of(const AttnParams& p, int total, int items, int shared,
                                           int own) {
   Split s{total, min(p.workers, total)};
