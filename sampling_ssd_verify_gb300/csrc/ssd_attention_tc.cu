@@ -40,6 +40,7 @@ namespace {
 constexpr int kBlock = kTcBlock;  // pairs of a block (M)
 constexpr int kTile = kTcTile;    // tokens of a tile
 constexpr int kSoftmax = 256;     // threads of the two warpgroups
+constexpr int kHeader = 3 << 10;  // bytes of shared memory before the rings
 constexpr int kThreads = kSoftmax + 128;  // a third warpgroup: copies and products
 constexpr int kCopyK = 8, kCopyV = 9, kMmaWarp = 10, kQueryWarp = 11;
 // Registers per thread: launched with 168 (12 warps), of which the third
@@ -52,7 +53,7 @@ template <int D> struct Shape {
   static constexpr int kPanels = D / 64;
   static constexpr int kSlot = kPanels * kPanel;    // K or V of a tile
   static constexpr int kSlots = D == 64 ? 6 : 3;    // K and V: 192 KB, one CTA per SM
-  static constexpr int kSmem = 3072 + (2 * kSlots + 1) * kSlot;  // header, rings, queries
+  static constexpr int kSmem = kHeader + (2 * kSlots + 1) * kSlot;  // header, rings, queries
 };
 
 // tensor memory columns: scores (and weights) of the two streams, their sums
@@ -193,7 +194,7 @@ struct Header {
 };
 // With the rings it fills the 227 KB of an SM: it ends where they start, on a
 // 1024-byte boundary.
-static_assert(sizeof(Header) <= 3072, "header");
+static_assert(sizeof(Header) <= kHeader, "header");
 
 // Whether a wait of the CTA ran out (to every lane of a warp alike): no new
 // work is begun then.
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) unsigned char s_raw[];
   Header& sh = *reinterpret_cast<Header*>(s_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t kring = smem_addr(s_raw) + 3072;
+  const uint32_t kring = smem_addr(s_raw) + kHeader;
   const uint32_t vring = kring + S::kSlots * S::kSlot;
   const uint32_t qs = vring + S::kSlots * S::kSlot;
 
