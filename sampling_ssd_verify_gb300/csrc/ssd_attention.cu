@@ -729,6 +729,7 @@ int ctas_per_sm(int D) { return D == 256 ? 1 : D == 128 ? 2 : 4; }  // by shared
 bool plan(const ssd_attention& a, AttnParams& p, Layout& L) {
   const int sms = std::max(num_sms(), 1);
   p.a = a;
+  if (!a.tables) p.a.cols = 0;  // no own tokens whatever cols says: the join looks pages up by it
   p.gqa = a.Hq / a.Hkv;
   p.by_page = divisor(a.page_size);
   p.by_gqa = divisor(p.gqa);
