@@ -196,11 +196,20 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on_current(dev):
+    """The library launches on the current GPU: tensors of another are refused."""
+    now = _torch()._C._cuda_getDevice()
+    if dev != now:
+        raise SSDError(f"the tensors are on cuda:{dev}, the current GPU is cuda:{now}: make the "
+                       f"call within torch.cuda.device({dev})")
+
+
 def _logits(t, nrows_inner=None):
     """Describe a [..., R, V] tensor whose rows are evenly spaced."""
     torch = _torch()
     if not t.is_cuda:
         raise SSDError("logits must be on the GPU")
+    _on_current(t.get_device())
     if t.dtype == torch.bfloat16:
         dt = SSD_BF16
     elif t.dtype == torch.float32:
@@ -513,6 +522,8 @@ def cache_bytes(n_keys: int) -> int:
 def cache_build(row, k, t, branch, table=None, dev_status=None, stream=None):
     torch = _torch()
     n = row.numel()
+    if row.is_cuda:
+        _on_current(row.get_device())
     if table is None:
         table = torch.empty(cache_bytes(n), dtype=torch.uint8, device=row.device)
     st = lib().ssd_cache_build(_dev_ptr(table), table.numel(), _dev_ptr(_i32(row)),
@@ -525,6 +536,8 @@ def cache_build(row, k, t, branch, table=None, dev_status=None, stream=None):
 def cache_build_guesses(guesses, table=None, dev_status=None, stream=None):
     torch = _torch()
     B, Kq, Fmax = guesses.shape
+    if guesses.is_cuda:
+        _on_current(guesses.get_device())
     if table is None:
         table = torch.empty(cache_bytes(B * Kq * Fmax), dtype=torch.uint8, device=guesses.device)
     st = lib().ssd_cache_build_guesses(_dev_ptr(table), table.numel(), _dev_ptr(_i32(guesses)),
@@ -536,6 +549,8 @@ def cache_build_guesses(guesses, table=None, dev_status=None, stream=None):
 def cache_lookup(table, accept_len, bonus, out=None, stream=None):
     torch = _torch()
     B = accept_len.numel()
+    if accept_len.is_cuda:
+        _on_current(accept_len.get_device())
     o = out if out is not None else {
         "branch": torch.empty(B, dtype=torch.int32, device=accept_len.device),
         "all_hit": torch.empty(1, dtype=torch.int32, device=accept_len.device)}
@@ -620,6 +635,7 @@ def process_logits(logits, history=None, history_len=None, prompt_len=None, draf
     dev = logits.get_device()
     if len(shape) != 3 or dev < 0 or logits.dtype not in (torch.bfloat16, f32):
         raise SSDError("expected bfloat16 or float32 logits [B, N, V] on the GPU")
+    _on_current(dev)
     B, N, V = shape
     o = out if out is not None else {}
     z = o.get("logits")
@@ -713,6 +729,7 @@ def page_plan(lens, new, held, tables, free_pages, free_count, page_size, max_ro
     dev = lens.get_device()
     if dev < 0 or lens.dim() != 1:
         raise SSDError("expected lengths [B] on the GPU")
+    _on_current(dev)
     B, T = lens.shape[0], int(max_rows)
     if T < 0:
         raise SSDError("max_rows must not be negative")
@@ -773,6 +790,7 @@ def prefix_attention(q, k_cache, v_cache, prefix_tables, prefix_len, group_off, 
     dev = q.get_device()
     if dev < 0 or k_cache.get_device() != dev or v_cache.get_device() != dev:
         raise SSDError("q and the caches must be on one GPU")
+    _on_current(dev)
     o = out if out is not None else {}
     y = o.get("out")
     if y is None:

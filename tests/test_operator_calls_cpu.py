@@ -1,0 +1,35 @@
+"""Calls of process_logits, page_plan and prefix_attention whose outcome is settled before
+anything is enqueued: no device is touched."""
+
+import pytest
+
+import sampling_ssd_verify_gb300 as ssd
+
+
+def test_tensors_of_a_gpu_that_is_not_current_are_refused(monkeypatch):
+    """A launch goes to the current GPU, whatever the tensors' is."""
+    import torch
+
+    class Elsewhere(torch.Tensor):
+        is_cuda = True
+
+        def get_device(self):
+            return 1
+
+    def there(*shape, dtype=torch.int32):
+        return torch.zeros(shape, dtype=dtype).as_subclass(Elsewhere)
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    i = there(2)
+    c = there(3, 16, 2, 64, dtype=torch.bfloat16)
+    z = there(2, 3, 32, dtype=torch.float32)
+    for call in (lambda: ssd.process_logits(z),
+                 lambda: ssd.page_plan(i, i, i, there(2, 4), i, there(1), 16, 4),
+                 lambda: ssd.prefix_attention(there(2, 4, 64, dtype=torch.bfloat16), c, c,
+                                              there(1, 2), there(1), i),
+                 lambda: ssd._logits(z),           # verification and sampling
+                 lambda: ssd.cache_build(i, i, i, i, table=i),
+                 lambda: ssd.cache_build_guesses(there(2, 3, 2), table=i),
+                 lambda: ssd.cache_lookup(i, i, i)):
+        with pytest.raises(ssd.SSDError, match="cuda:1.*cuda:0"):
+            call()
