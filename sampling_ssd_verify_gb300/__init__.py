@@ -712,6 +712,26 @@ def _plan_views(torch, B, T, device):
     return views
 
 
+def _plan_pointers(o, B, T, i32, dev):
+    """Addresses of page_plan's outputs but the slots: views of one buffer, one
+    after the other.  That they are is told by the buffer's memory (a view made
+    in inference mode knows no base)."""
+    cu = o["cu"]
+    if cu.dtype is not i32 or cu.get_device() != dev or cu.numel() != B + 1:
+        raise SSDError("out: expected the dict of an earlier call with these sizes")
+    memory = cu.untyped_storage()
+    first = at = memory.data_ptr()
+    ptrs = []
+    for name, n in zip(_PLAN, (T, T, B + 1, B, B, B, 1)):
+        if n and o[name].data_ptr() != at:
+            raise SSDError(f"out: {name} is not that of an earlier call with these sizes")
+        ptrs.append(at)
+        at += (n + 15 & ~15) * 4
+    if at - first > memory.nbytes():
+        raise SSDError("out: expected the dict of an earlier call with these sizes")
+    return ptrs
+
+
 def page_plan(lens, new, held, tables, free_pages, free_count, page_size, max_rows,
               dev_status=None, stream=None, out=None):
     """ssd_page_plan: the pages of a paged key/value cache after a round, and
@@ -737,20 +757,7 @@ def page_plan(lens, new, held, tables, free_pages, free_count, page_size, max_ro
     o = out if out is not None else {}
     if "slots" not in o:
         o.update(_plan_views(torch, B, T, lens.device))
-    # all but the slots are views of one buffer, one after the other
-    base = o["cu"]._base
-    if base is None or base.dtype is not i32 or base.get_device() != dev or \
-            o["cu"].numel() != B + 1:
-        raise SSDError("out: expected the dict of an earlier call with these sizes")
-    first = at = base.data_ptr()
-    ptrs = []
-    for name, n in zip(_PLAN, (T, T, B + 1, B, B, B, 1)):
-        if n and o[name].data_ptr() != at:
-            raise SSDError(f"out: {name} is not that of an earlier call with these sizes")
-        ptrs.append(at)
-        at += (n + 15 & ~15) * 4
-    if at - first > base.numel() * 4:
-        raise SSDError("out: expected the dict of an earlier call with these sizes")
+    ptrs = _plan_pointers(o, B, T, i32, dev)
     table, stride, cols = _rows2d(tables, "tables", B, i32, dev)
     st = lib().ssd_page_plan(
         _tensor(lens, "lens", i32, row, dev), _tensor(new, "new", i32, row, dev),
@@ -758,7 +765,7 @@ def page_plan(lens, new, held, tables, free_pages, free_count, page_size, max_ro
         _tensor(free_pages, "free_pages", i32, free_pages.shape, dev), free_pages.numel(),
         _tensor(free_count, "free_count", i32, one, dev), int(page_size), T,
         _tensor(o["slots"], "slots", torch.int64, (T,), dev), *ptrs, _dev_ptr(dev_status),
-        _use_stream(stream, dev, (base, o["slots"])))
+        _use_stream(stream, dev, (o["cu"], o["slots"])))
     if st:
         _check(st, "ssd_page_plan")
     return o

@@ -43,3 +43,20 @@ def test_no_own_tables_whatever_their_columns():
                                     torch.cuda.current_stream().cuda_stream)
         assert st == 0
         assert torch.equal(out, want["out"]) and torch.equal(lse, want["lse"])
+
+
+@pytest.mark.parametrize("room", [0, 60])
+def test_inference_mode(room):
+    """A serving program's mode, in which views have no base: outputs new and used again."""
+    torch, dev = torch_dev()
+    rng = np.random.default_rng(2)
+    state = list(pages.random_state(rng, 9, 16, 90, 5, 40, 60))
+    state[-1] = room
+    with torch.inference_mode():
+        pages.run(*state)                 # three calls, two of them with out=
+        z, d, parent = logits.make(2, 3, 500, 9, torch.float32, seed=1)
+        o = logits.run_case(z, d, parent)
+        logits.run_case(z, d, parent, out=o)
+        s = attention.make([2, 3], [40, 7], [3] * 5, 4, 2, 64, 16, torch.bfloat16)
+        o = attention.call(s)
+        attention.check(s, attention.call(s, out=o))

@@ -33,3 +33,20 @@ def test_tensors_of_a_gpu_that_is_not_current_are_refused(monkeypatch):
                  lambda: ssd.cache_lookup(i, i, i)):
         with pytest.raises(ssd.SSDError, match="cuda:1.*cuda:0"):
             call()
+
+
+@pytest.mark.parametrize("T", [0, 1, 40])
+def test_outputs_of_a_plan_are_known_again_in_inference_mode(T):
+    """Views made in inference mode know no base."""
+    import torch
+
+    for mode in (torch.inference_mode, torch.no_grad):
+        with mode():
+            o = ssd._plan_views(torch, 9, T, torch.device("cpu"))
+            at = ssd._plan_pointers(o, 9, T, torch.int32, -1)
+            assert [p for p, k in zip(at, ssd._PLAN) if o[k].numel()] == \
+                [o[k].data_ptr() for k in ssd._PLAN if o[k].numel()]
+            for B, rows, out in ((8, T, o), (9, T + 17, o), (9, T, dict(o, cu=o["cu"].clone())),
+                                 (9, T, dict(o, held=o["served"]))):
+                with pytest.raises(ssd.SSDError):
+                    ssd._plan_pointers(out, B, rows, torch.int32, -1)
