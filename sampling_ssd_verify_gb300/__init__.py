@@ -698,6 +698,7 @@ def process_logits(logits, history=None, history_len=None, prompt_len=None, draf
 
 
 _PLAN = ("positions", "owner", "cu", "kv_len", "held", "served", "free_count")
+_PLAN_NAMES = {"slots", *_PLAN}
 
 
 def _plan_views(torch, B, T, device):
@@ -716,6 +717,8 @@ def _plan_pointers(o, B, T, i32, dev):
     """Addresses of page_plan's outputs but the slots: views of one buffer, one
     after the other.  That they are is told by the buffer's memory (a view made
     in inference mode knows no base)."""
+    if not o.keys() >= _PLAN_NAMES:
+        raise SSDError("out: expected all outputs of an earlier call")
     cu = o["cu"]
     if cu.dtype is not i32 or cu.get_device() != dev or cu.numel() != B + 1:
         raise SSDError("out: expected the dict of an earlier call with these sizes")
@@ -755,7 +758,7 @@ def page_plan(lens, new, held, tables, free_pages, free_count, page_size, max_ro
         raise SSDError("max_rows must not be negative")
     row, one = (B,), (1,)
     o = out if out is not None else {}
-    if "slots" not in o:
+    if _PLAN_NAMES.isdisjoint(o):
         o.update(_plan_views(torch, B, T, lens.device))
     ptrs = _plan_pointers(o, B, T, i32, dev)
     table, stride, cols = _rows2d(tables, "tables", B, i32, dev)

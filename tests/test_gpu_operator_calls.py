@@ -60,3 +60,17 @@ def test_inference_mode(room):
         s = attention.make([2, 3], [40, 7], [3] * 5, 4, 2, 64, 16, torch.bfloat16)
         o = attention.call(s)
         attention.check(s, attention.call(s, out=o))
+
+
+def test_plan_outputs_that_are_not_an_earlier_calls():
+    torch, dev = torch_dev()
+    i = torch.zeros(4, dtype=torch.int32, device=dev)
+    args = (i, i, i, torch.zeros((4, 5), dtype=torch.int32, device=dev), i, i[:1], 16, 8)
+    o = ssd.page_plan(*args)
+    for out in ({"slots": o["slots"]}, {k: v for k, v in o.items() if k != "served"},
+                dict(o, cu=o["cu"].long()), dict(o, cu=o["cu"].cpu()),
+                {k: v.clone() for k, v in o.items()}):
+        with pytest.raises(ssd.SSDError):
+            ssd.page_plan(*args, out=out)
+    with torch.inference_mode():
+        ssd.page_plan(*args, out=o)       # made outside, used inside

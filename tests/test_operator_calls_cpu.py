@@ -50,3 +50,12 @@ def test_outputs_of_a_plan_are_known_again_in_inference_mode(T):
                                  (9, T, dict(o, held=o["served"]))):
                 with pytest.raises(ssd.SSDError):
                     ssd._plan_pointers(out, B, rows, torch.int32, -1)
+
+
+def test_outputs_of_a_plan_come_whole():
+    import torch
+
+    o = ssd._plan_views(torch, 4, 8, torch.device("cpu"))
+    for name in o:
+        with pytest.raises(ssd.SSDError):
+            ssd._plan_pointers({k: v for k, v in o.items() if k != name}, 4, 8, torch.int32, -1)
