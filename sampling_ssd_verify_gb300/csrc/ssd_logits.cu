@@ -459,11 +459,25 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
   }
 }
 
+// Bytes of shared memory of a call.
 template <int DT>
-cudaError_t launch(const LogitParams& p, int64_t grid, size_t smem, cudaStream_t s) {
+constexpr size_t smem_bytes(int slice, int rows, bool mask, bool bias) {
+  constexpr size_t es = sizeof(typename Elem<DT>::type);
+  const size_t words = slice / 32 + 4;
+  return (size_t)kStages * kMaxSlice * es +                  // ring
+         (kMaxSlice + kThreads / 32 * (16 / es)) * 2 +       // lists
+         (slice + words) * 4 + (mask ? rows * words * 4 : 0) + (bias ? (size_t)slice * 2 : 0);
+}
+
+template <int DT>
+cudaError_t launch(const LogitParams& p, int64_t grid, cudaStream_t s) {
+  const size_t smem = smem_bytes<DT>(p.slice, p.rows, p.r.mask != nullptr, p.r.n_bias > 0);
   if (smem > 46 * 1024) {  // more than a kernel may have without asking (48 KB with its static part)
+    // the most that any call needs: the limit is the function's, and a call of another
+    // thread may come between this and the launch
     const cudaError_t e = cudaFuncSetAttribute(
-        logits_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        logits_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        (int)smem_bytes<DT>(kMaxSlice, kMaxRows, true, true));
     if (e != cudaSuccess) return e;
   }
   logits_kernel<DT><<<(unsigned)grid, kThreads, smem, s>>>(p);
@@ -526,15 +540,9 @@ extern "C" ssd_status ssd_process_logits(const ssd_logits* in, const ssd_logits*
   while (ctas() < want && p.slice > kMinSlice) p.slice /= 2;
   const int64_t grid = ctas();
   if (grid > 0x7fffffff) return SSD_ERR_UNSUPPORTED;
-  const size_t words = p.slice / 32 + 4;
-  const int es = in->dtype == SSD_BF16 ? 2 : 4;
-  const size_t smem = (size_t)kStages * kMaxSlice * es +                     // ring
-                      (kMaxSlice + kThreads / 32 * (16 / es)) * 2 +           // lists
-                      (p.slice + words) * 4 + (r.mask ? p.rows * words * 4 : 0) +
-                      (r.n_bias ? p.slice * 2 : 0);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = in->dtype == SSD_BF16 ? launch<SSD_BF16>(p, grid, smem, s)
-                                              : launch<SSD_F32>(p, grid, smem, s);
+  const cudaError_t e = in->dtype == SSD_BF16 ? launch<SSD_BF16>(p, grid, s)
+                                              : launch<SSD_F32>(p, grid, s);
   if (e == cudaSuccess) return SSD_OK;
   cudaGetLastError();
   return SSD_ERR_CUDA;

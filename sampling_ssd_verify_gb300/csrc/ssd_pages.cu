@@ -28,6 +28,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxRequests = 8192;  // five numbers each in shared memory
+constexpr int smem_bytes(int B) { return 5 * (B + 1) * (int)sizeof(int); }
 constexpr int kBatch = 4;           // new tokens per thread at a time
 constexpr int kMaxCount = 1 << 30;
 constexpr int kRowsPerCta = 2048;   // new tokens per CTA before another one is added
@@ -245,13 +246,14 @@ extern "C" ssd_status ssd_page_plan(const int32_t* lens, const int32_t* new_toke
   const PageParams p{lens,     new_tokens, held,  B, tables, table_stride, cols,
                      free_pages, free_cap, free_count, page,    max_rows, divisor(page), slots, positions,
                      owner,    cu,         kv_len, held_out,   served, free_out,     dev_status};
-  const size_t smem = (size_t)5 * (B + 1) * sizeof(int);
+  const int smem = smem_bytes(B);
   const int64_t work = std::max<int64_t>(max_rows / kRowsPerCta, B / kThreads);
   const int grid = work == 0 ? 1 : (int)std::min<int64_t>(std::max(num_sms(), 1), 1 + work);
   cudaError_t e = cudaSuccess;
-  if (smem > 46 * 1024)  // more than a kernel may have without asking
+  if (smem > 46 * 1024)  // more than a kernel may have without asking; the most that any call
+    // needs, since the limit is the function's and another thread's call may come between
     e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem);
+                             smem_bytes(kMaxRequests));
   if (e == cudaSuccess) {
     page_plan_kernel<<<grid, kThreads, smem, static_cast<cudaStream_t>(stream)>>>(p);
     e = cudaGetLastError();

@@ -74,3 +74,83 @@ def test_plan_outputs_that_are_not_an_earlier_calls():
             ssd.page_plan(*args, out=out)
     with torch.inference_mode():
         ssd.page_plan(*args, out=o)       # made outside, used inside
+
+
+def _hammer(monkeypatch, calls, workers=3, times=3000):
+    """Repeats the library calls that `calls` make, each from several threads at once and on
+    a stream of its own, with nothing of Python between; returns their status codes."""
+    torch, dev = torch_dev()
+    L = ssd.lib()
+    made = []
+
+    class Record:
+        def __getattr__(self, name):
+            def call(*args):
+                made.append((getattr(L, name), args))
+                return made[-1][0](*args)
+            return call
+
+    with monkeypatch.context() as m:
+        m.setattr(ssd, "_lib", Record())
+        for call in calls:
+            for _ in range(workers):
+                with torch.cuda.stream(torch.cuda.Stream()):
+                    call()
+    torch.cuda.synchronize()
+    seen, start = set(), threading.Barrier(len(made))
+
+    def work(fn, args):
+        start.wait()
+        for _ in range(times):
+            seen.add(fn(*args))
+
+    threads = [threading.Thread(target=work, args=x) for x in made]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return seen
+
+
+@pytest.mark.parametrize("dt,sizes", [("float32", (9, 5)), ("bfloat16", (16, 9))])
+def test_logits_of_two_sizes_in_several_threads(monkeypatch, dt, sizes):
+    """Calls that ask for more shared memory beside calls that ask for less."""
+    torch, dev = torch_dev()
+    calls, kept = [], []
+    for N in sizes:
+        z, d, parent = logits.make(310, N, 4099, 9, getattr(torch, dt), seed=N, mask_rows=(1, 1))
+        f = lambda a: torch.from_numpy(a).to(dev)  # noqa: E731
+        args = (z, i32(d["hist"]), i32(d["hlen"]), i32(d["plen"]))
+        kw = dict(draft_tokens=i32(d["drafts"]), parent=parent, repetition=f(d["rep"]),
+                  bias_ids=i32(d["ids"]), bias=f(d["bias"]), mask=f(logits.pack(d["mask"])))
+        want = ssd.process_logits(*args, **kw)["logits"]
+
+        def call(args=args, kw=kw, want=want):
+            kept.append((ssd.process_logits(*args, **kw)["logits"], want))
+
+        calls.append(call)
+    torch.cuda.synchronize()
+    assert _hammer(monkeypatch, calls) == {0}
+    for got, want in kept:
+        assert torch.equal(got, want)
+
+
+def test_plans_of_two_sizes_in_several_threads(monkeypatch):
+    torch, dev = torch_dev()
+    calls, kept = [], []
+    for B in (8000, 2500):
+        i = i32(np.full(B, 3))
+        args = (i, i, i32(np.ones(B)), i32(np.arange(2 * B).reshape(B, 2)), i32(np.zeros(4)),
+                i32([0]), 16, 3 * B)
+        want = ssd.page_plan(*args)
+
+        def call(args=args, want=want):
+            kept.append((ssd.page_plan(*args), want))
+
+        calls.append(call)
+    torch.cuda.synchronize()
+    assert _hammer(monkeypatch, calls) == {0}
+    for got, want in kept:
+        for k in want:
+            assert torch.equal(got[k], want[k]), k
