@@ -576,11 +576,12 @@ ssd_status ssd_page_plan(const int32_t* lens, const int32_t* new_tokens, const i
  *             for q, any order of the first three dimensions.  Bytes of a
  *             page past the last token are not used, whatever they hold.
  * prefix_tables, tables  device int32 page ids, rows of prefix_cols / cols
- *             columns.  An id outside [0, num_pages) of a token that is read
- *             sets SSD_DEV_BAD_PAGE; the token reads as zeros.
+ *             columns (of none: NULL too).  An id outside [0, num_pages) of a
+ *             token that is read sets SSD_DEV_BAD_PAGE; the token reads as
+ *             zeros.
  * prefix_len  device [G] int32 in [0, prefix_cols * page_size]; lens device
  *             [R] int32 in [0, cols * page_size] (NULL tables and lens: no
- *             own tokens).  Values outside are clamped and set
+ *             own tokens, whatever cols).  Values outside are clamped and set
  *             SSD_DEV_BAD_LENGTH.
  * group_off   device [G + 1] int32, not falling, within [0, R]; otherwise
  *             SSD_DEV_BAD_LENGTH is set and the rows concerned are undefined.

@@ -710,9 +710,10 @@ ssd_status check(const ssd_attention* a) {
       a->num_pages < 1 || a->page_size < 1 || !std::isfinite(a->scale))
     return SSD_ERR_INVALID_ARG;
   if (a->D != 64 && a->D != 128 && a->D != 256) return SSD_ERR_UNSUPPORTED;
-  if (a->prefix_cols < 0 || a->cols < 0 || (a->tables == nullptr) != (a->lens == nullptr))
-    return SSD_ERR_INVALID_ARG;
-  if (a->G > 0 && (!a->prefix_tables || !a->prefix_len || !a->group_off ||
+  if (a->prefix_cols < 0 || a->cols < 0) return SSD_ERR_INVALID_ARG;
+  // tables of no columns may have no address
+  if (a->tables ? !a->lens : a->lens && a->cols > 0) return SSD_ERR_INVALID_ARG;
+  if (a->G > 0 && ((!a->prefix_tables && a->prefix_cols > 0) || !a->prefix_len || !a->group_off ||
                    a->prefix_table_stride < a->prefix_cols))
     return SSD_ERR_INVALID_ARG;
   if (a->tables && a->table_stride < a->cols) return SSD_ERR_INVALID_ARG;

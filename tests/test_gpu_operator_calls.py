@@ -154,3 +154,23 @@ def test_plans_of_two_sizes_in_several_threads(monkeypatch):
     for got, want in kept:
         for k in want:
             assert torch.equal(got[k], want[k]), k
+
+
+@pytest.mark.parametrize("page", [16, 20])
+def test_tables_without_columns(page):
+    """No prefix in the whole batch, no own page, neither."""
+    torch, dev = torch_dev()
+    none = torch.empty((2, 0), dtype=torch.int32, device=dev)
+    s = attention.make([2, 1], [0, 0], [3, 0, 40], 4, 2, 64, page, torch.bfloat16)
+    attention.check(s, attention.call(dict(s, pt=none)))
+    attention.check(s, attention.call(dict(s, pt=none, t=s["t"][:, :40 // page + 1].contiguous())))
+    rows = torch.empty((3, 0), dtype=torch.int32, device=dev)
+    s = attention.make([2, 1], [50, 200], [0, 0, 0], 4, 2, 64, page, torch.bfloat16)
+    attention.check(s, attention.call(dict(s, t=rows)))
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    o = attention.call(dict(s, t=rows, pt=none, l=i32([0, 0, 0]), pl=i32([0, 0])),
+                       dev_status=status)
+    assert bool((o["out"] == 0).all()) and bool((o["lse"] == -float("inf")).all())
+    assert int(status.item()) == 0
+    attention.call(dict(s, t=rows, l=i32([0, 2, 0])), dev_status=status)
+    assert int(status.item()) == ssd.DEV_BAD_LENGTH

@@ -1,9 +1,12 @@
 """Calls of process_logits, page_plan and prefix_attention whose outcome is settled before
 anything is enqueued: no device is touched."""
 
+import ctypes
+
 import pytest
 
 import sampling_ssd_verify_gb300 as ssd
+from tests.test_round_operators_cpu import INVALID, WORKSPACE, _attention
 
 
 def test_tensors_of_a_gpu_that_is_not_current_are_refused(monkeypatch):
@@ -59,3 +62,18 @@ def test_outputs_of_a_plan_come_whole():
     for name in o:
         with pytest.raises(ssd.SSDError):
             ssd._plan_pointers({k: v for k, v in o.items() if k != name}, 4, 8, torch.int32, -1)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(prefix_tables=None, prefix_cols=0), WORKSPACE), (dict(tables=None, cols=0), WORKSPACE),
+    (dict(tables=None, lens=None), WORKSPACE),
+    (dict(prefix_tables=None), INVALID), (dict(tables=None), INVALID),
+    (dict(lens=None, cols=0), INVALID),
+])
+def test_tables_without_columns_have_no_address(kw, status):
+    """A tensor of no elements has a null address."""
+    ssd.build()
+    L = ssd.lib()
+    a = _attention(**kw)
+    assert L.ssd_prefix_attention(ctypes.byref(a), None, 0, None, None) == status
+    assert (L.ssd_prefix_attention_workspace_size(ctypes.byref(a)) > 0) == (status == WORKSPACE)
