@@ -787,7 +787,8 @@ def prefix_attention(q, k_cache, v_cache, prefix_tables, prefix_len, group_off, 
     pages tables[r, :] (int32 [R, W']).  scale: 1 / sqrt(D) when None.
     Returns a dict: ``out`` [R, Hq, D] and, unless lse=False, ``lse`` float32
     [R, Hq].  `out`: the dict of an earlier call of these shapes, to use its
-    tensors and workspace again."""
+    tensors and workspace again, or one with some of them; what is absent is
+    added."""
     torch = _torch()
     i32 = torch.int32
     qs, ks, dt = q.shape, k_cache.shape, q.dtype
@@ -805,10 +806,10 @@ def prefix_attention(q, k_cache, v_cache, prefix_tables, prefix_len, group_off, 
     y = o.get("out")
     if y is None:
         y = o["out"] = torch.empty(qs, dtype=dt, device=q.device)
-        if lse:
-            o["lse"] = torch.empty((R, Hq), dtype=torch.float32, device=q.device)
     elif y.shape != qs or y.dtype is not dt or y.get_device() != dev:
         raise SSDError("out must have q's shape, type and device")
+    if lse and o.get("lse") is None:
+        o["lse"] = torch.empty((R, Hq), dtype=torch.float32, device=q.device)
     q_at, k_at, v_at, y_at = q.stride(), k_cache.stride(), v_cache.stride(), y.stride()
     if q_at[2] != 1 or k_at[3] != 1 or v_at[3] != 1 or y_at[2] != 1:
         raise SSDError("the head dimension must be contiguous")

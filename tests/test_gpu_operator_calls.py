@@ -174,3 +174,19 @@ def test_tables_without_columns(page):
     assert int(status.item()) == 0
     attention.call(dict(s, t=rows, l=i32([0, 2, 0])), dev_status=status)
     assert int(status.item()) == ssd.DEV_BAD_LENGTH
+
+
+def _attn(**kw):
+    torch, dev = torch_dev()
+    return attention.make([2, 1], [40, 7], [3, 0, 9], 4, 2, 64, 16, torch.bfloat16, **kw)
+
+
+def test_out_without_lse():
+    torch, dev = torch_dev()
+    s = _attn()
+    y = torch.empty_like(s["q"])
+    o = attention.call(s, out={"out": y})
+    assert o["out"] is y
+    attention.check(s, o)
+    first = attention.call(s, lse=False)
+    attention.check(s, attention.call(s, out=first))
