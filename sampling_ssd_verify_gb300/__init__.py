@@ -613,6 +613,11 @@ def _use_stream(stream, dev, tensors):
     return stream.cuda_stream
 
 
+def _results(o, name, wanted):
+    """The call's results: `o`, but for an earlier call's that this one was not asked for."""
+    return o if wanted or name not in o else {k: v for k, v in o.items() if k != name}
+
+
 def process_logits(logits, history=None, history_len=None, prompt_len=None, draft_tokens=None,
                    parent=None, repetition=None, presence=None, frequency=None, bias_ids=None,
                    bias=None, mask=None, fill=MASKED_LOGIT, allowed=False, dev_status=None,
@@ -694,7 +699,7 @@ def process_logits(logits, history=None, history_len=None, prompt_len=None, draf
                                   _dev_ptr(dev_status), _use_stream(stream, dev, o.values()))
     if st:
         _check(st, "ssd_process_logits")
-    return o
+    return _results(o, "allowed", allowed)
 
 
 _PLAN = ("positions", "owner", "cu", "kv_len", "held", "served", "free_count")
@@ -839,4 +844,4 @@ def prefix_attention(q, k_cache, v_cache, prefix_tables, prefix_len, group_off, 
                                 _dev_ptr(dev_status), _use_stream(stream, dev, (*o.values(), ws)))
     if st:
         _check(st, "ssd_prefix_attention")
-    return o
+    return _results(o, "lse", lse)

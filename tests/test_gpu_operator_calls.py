@@ -190,3 +190,17 @@ def test_out_without_lse():
     attention.check(s, o)
     first = attention.call(s, lse=False)
     attention.check(s, attention.call(s, out=first))
+
+
+def test_results_that_were_not_asked_for_are_not_returned():
+    """The caller's dict keeps its tensors; the one returned has this call's results alone."""
+    torch, dev = torch_dev()
+    s = _attn()
+    kept = attention.call(s)
+    o = attention.call(s, lse=False, out=kept)
+    assert "lse" not in o and "lse" in kept and o["out"] is kept["out"]
+    assert o["workspace"] is kept["workspace"]
+    z = torch.zeros((2, 3, 64), device=dev)
+    kept = ssd.process_logits(z, allowed=True)
+    o = ssd.process_logits(z, out=kept)
+    assert "allowed" not in o and "allowed" in kept and o["logits"] is kept["logits"]
