@@ -52,6 +52,7 @@ DEV_BAD_PAGE = 0x400
 MASKED_LOGIT = -1048576.0  # what a token outside the grammar gets: -2^20
 
 SSD_BF16, SSD_F32, SSD_F16 = 0, 1, 2
+_ERR_WORKSPACE = 5
 _lib = None
 
 
@@ -793,7 +794,8 @@ def prefix_attention(q, k_cache, v_cache, prefix_tables, prefix_len, group_off, 
     Returns a dict: ``out`` [R, Hq, D] and, unless lse=False, ``lse`` float32
     [R, Hq].  `out`: the dict of an earlier call of these shapes, to use its
     tensors and workspace again, or one with some of them; what is absent is
-    added."""
+    added, and a workspace that is too small (more groups, wider tables) replaced:
+    a captured graph needs a dict of its own."""
     torch = _torch()
     i32 = torch.int32
     qs, ks, dt = q.shape, k_cache.shape, q.dtype
@@ -840,8 +842,14 @@ def prefix_attention(q, k_cache, v_cache, prefix_tables, prefix_len, group_off, 
         ws = o["workspace"] = _workspace(L.ssd_prefix_attention_workspace_size(a), q.device)
     elif ws.get_device() != dev or not ws.is_contiguous():
         raise SSDError("the workspace must be a contiguous tensor on q's GPU")
+    handle = _use_stream(stream, dev, (*o.values(), ws))
     st = L.ssd_prefix_attention(a, ws.data_ptr(), ws.numel() * ws.element_size(),
-                                _dev_ptr(dev_status), _use_stream(stream, dev, (*o.values(), ws)))
+                                _dev_ptr(dev_status), handle)
+    if st == _ERR_WORKSPACE and workspace is None:
+        # the rows are as before, but not the groups or tables; nothing has been launched
+        ws = o["workspace"] = _workspace(L.ssd_prefix_attention_workspace_size(a), q.device)
+        handle = _use_stream(stream, dev, (ws,))
+        st = L.ssd_prefix_attention(a, ws.data_ptr(), ws.numel(), _dev_ptr(dev_status), handle)
     if st:
         _check(st, "ssd_prefix_attention")
     return _results(o, "lse", lse)

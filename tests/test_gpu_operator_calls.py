@@ -204,3 +204,18 @@ def test_results_that_were_not_asked_for_are_not_returned():
     kept = ssd.process_logits(z, allowed=True)
     o = ssd.process_logits(z, out=kept)
     assert "allowed" not in o and "allowed" in kept and o["logits"] is kept["logits"]
+
+
+def test_workspace_of_an_earlier_call_grows():
+    """The same rows over more groups, more columns, longer own caches."""
+    torch, dev = torch_dev()
+    small = attention.make([64], [20], [1] * 64, 8, 2, 128, 16, torch.bfloat16)
+    o = attention.call(small)
+    few = o["workspace"].numel()
+    for sizes, pre, suf in (([1] * 64, [200] * 64, [5] * 64), ([64], [900], [2000] + [3] * 63)):
+        s = attention.make(sizes, pre, suf, 8, 2, 128, 16, torch.bfloat16)
+        attention.check(s, attention.call(s, out=o), rows=range(0, 64, 5))
+    assert o["workspace"].numel() > few
+    attention.check(small, attention.call(small, out=o), rows=range(0, 64, 9))
+    with pytest.raises(ssd.SSDError):     # the caller's own is not replaced
+        attention.call(s, workspace=torch.empty(few, dtype=torch.uint8, device=dev))
