@@ -536,8 +536,10 @@ ssd_status ssd_process_logits(const ssd_logits* in, const ssd_logits* out, int B
  * tables      device int32, request b's row starts at b * table_stride, cols
  *             columns.
  * free_pages  device [free_cap] int32; free_count device int32 in [0,
- *             free_cap] (clamped otherwise, SSD_DEV_BAD_LENGTH).  Pages that
- *             do not fit the array are lost, and set SSD_DEV_BAD_LENGTH.
+ *             free_cap] (clamped otherwise, SSD_DEV_BAD_LENGTH).  Pages given
+ *             back may pass the array's end where the same call takes them
+ *             again; those that do not fit it after step 2 are lost, and set
+ *             SSD_DEV_BAD_LENGTH.
  * slots       device [max_rows] int64 out; positions, owner [max_rows] int32
  *             out (each may be NULL).  Rows past the last token are -1; tokens
  *             past max_rows have no row, and set SSD_DEV_BAD_LENGTH.

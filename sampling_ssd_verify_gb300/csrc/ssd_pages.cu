@@ -201,6 +201,11 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const PageParams p)
   for (int k = gtid; k < back; k += nthreads)
     if (n + (int64_t)k < p.free_cap) p.free_pages[n + k] = *stack_at(n + (int64_t)k);
   // ---- the requests ----------------------------------------------------------------
+  // the stack once `taken` pages are off it: what lies past the array then is lost
+  auto leave = [&](int taken) {
+    *p.free_out = (int)min(top - taken, (int64_t)p.free_cap);
+    if (top - taken > p.free_cap) bad |= SSD_DEV_BAD_LENGTH;
+  };
   for (int b = gtid; b < p.B; b += nthreads) {
     const Request q = request(p, b);
     const bool ok = is_served(q, b);
@@ -210,13 +215,12 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(const PageParams p)
     p.served[b] = ok;
     if (q.ok && !ok) bad |= SSD_DEV_NO_PAGES;
     // the pages left after the last request that got what it asked for
-    if (s_ask[b] < s_ask[b + 1] && s_ask[b] <= top && s_ask[b + 1] > top)
-      *p.free_out = (int)min(top - s_ask[b], (int64_t)p.free_cap);
+    if (s_ask[b] < s_ask[b + 1] && s_ask[b] <= top && s_ask[b + 1] > top) leave(s_ask[b]);
   }
   if (gtid == 0) {
     p.cu[p.B] = total;
-    if (ask <= top) *p.free_out = (int)min(top - ask, (int64_t)p.free_cap);
-    if (n != n0 || top > p.free_cap || total > p.max_rows) bad |= SSD_DEV_BAD_LENGTH;
+    if (ask <= top) leave(ask);
+    if (n != n0 || total > p.max_rows) bad |= SSD_DEV_BAD_LENGTH;
   }
   if (bad && p.status) atomicOr(p.status, bad);
 }

@@ -219,3 +219,26 @@ def test_workspace_of_an_earlier_call_grows():
     attention.check(small, attention.call(small, out=o), rows=range(0, 64, 9))
     with pytest.raises(ssd.SSDError):     # the caller's own is not replaced
         attention.call(s, workspace=torch.empty(few, dtype=torch.uint8, device=dev))
+
+
+@pytest.mark.parametrize("ask,flag,left", [
+    (3, 0, 3),                       # what does not fit the array is taken again
+    (1, ssd.DEV_BAD_LENGTH, 4),      # one page of five does not fit
+    (9, ssd.DEV_NO_PAGES | ssd.DEV_BAD_LENGTH, 4),  # all six stay: two do not fit
+])
+def test_surplus_pages_are_flagged_where_they_are_lost(ask, flag, left):
+    torch, dev = torch_dev()
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    tables = np.full((2, 10), -1)
+    tables[0, :4], tables[1, 0] = [10, 11, 12, 13], 14
+    t, free = i32(tables), i32([20, 21, 22, -1])
+    # request 0 keeps one page of four, request 1 wants `ask` more
+    o = ssd.page_plan(i32([16, 16]), i32([0, 16 * ask]), i32([4, 1]), t, free, i32([3]), 16, 200,
+                      dev_status=status)
+    assert int(status.item()) == flag
+    assert int(o["free_count"].item()) == left
+    stack = [20, 21, 22, 11, 12, 13]
+    took = stack[::-1][:ask] if ask <= 6 else []
+    assert t[1, 1:1 + len(took)].tolist() == took
+    assert free.tolist()[:left] == stack[:left]
+    assert o["held"].tolist() == [1, 1 + len(took)]
