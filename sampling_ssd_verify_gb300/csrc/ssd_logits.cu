@@ -81,7 +81,7 @@ template <> struct Elem<SSD_F32> {
 
 // What a rule needs of its sequence.
 struct Rules {
-  float rep, inv, freq, pres;  // inv = 1 / rep: one more rounding than a division, 20 instructions less
+  float rep, freq, pres;
   const float* bias;
   const int* tok;           // draft token of each node
   const int16_t* parent;
@@ -93,7 +93,8 @@ __device__ __forceinline__ float adjust(float z, uint32_t word, uint32_t bias_en
   uint32_t c = word & kCountBits;
   if (word & kDraftBit)
     for (int w = u; w > 0; w = ru.parent[w]) c += ru.tok[w] == v;
-  if (c != 0u || (word & kPromptBit)) z *= z > 0.f ? ru.inv : ru.rep;
+  // a division: 1 / rep would be infinite for the smallest rep, and one rounding more
+  if (c != 0u || (word & kPromptBit)) z = z > 0.f ? z / ru.rep : z * ru.rep;
   if (c != 0u) z = z - ru.freq * (float)c - ru.pres;
   if (bias_entry != 0u) z += ru.bias[bias_entry - 1];
   return z;
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
   if (!(rep > 0.f) || isinf(rep)) { rep = 1.f; bad = SSD_DEV_BAD_PENALTY; }
   if (!isfinite(freq)) { freq = 0.f; bad = SSD_DEV_BAD_PENALTY; }
   if (!isfinite(pres)) { pres = 0.f; bad = SSD_DEV_BAD_PENALTY; }
-  const Rules ru{rep, 1.f / rep, freq, pres, r.bias + b * r.n_bias, s_tok, s_parent};
+  const Rules ru{rep, freq, pres, r.bias + b * r.n_bias, s_tok, s_parent};
   if (len < 0 || len > r.history_max) {
     bad |= SSD_DEV_BAD_LENGTH;
     len = min(max(len, 0), r.history_max);

@@ -242,3 +242,27 @@ def test_surplus_pages_are_flagged_where_they_are_lost(ask, flag, left):
     assert t[1, 1:1 + len(took)].tolist() == took
     assert free.tolist()[:left] == stack[:left]
     assert o["held"].tolist() == [1, 1 + len(took)]
+
+
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+def test_repetition_is_a_quotient(dt):
+    """z / r and z * r, each rounded to float32 once and then to the type: equal to the
+    last bit, down to the smallest and up to the largest r."""
+    torch, dev = torch_dev()
+    r = torch.tensor([1.1, 1.3, 0.7, 7.0, 1e-39, 2.0 ** -149, 2.0 ** -127, 3e-38, 1e38, 3.4e38, 2.0 ** 126],
+                     dtype=torch.float32)
+    B, V = len(r), 3000
+    gen = torch.Generator().manual_seed(4)
+    z = torch.randn((B, 1, V), generator=gen) * 4
+    z[:, :, ::7] *= 1e-38
+    z[:, :, 1::7] *= 1e30
+    z[:, :, 2] = 0.0
+    z = z.to(getattr(torch, dt))
+    history = torch.arange(0, V, 2, dtype=torch.int32).repeat(B, 1)
+    f = z.float()
+    want = f.clone()
+    rr = r[:, None, None]
+    want[..., ::2] = torch.where(f > 0, f / rr, f * rr)[..., ::2]
+    got = ssd.process_logits(z.to(dev), history.to(dev), i32(np.full(B, V // 2)),
+                             repetition=r.to(dev))["logits"]
+    assert torch.equal(got.cpu(), want.to(z.dtype))
