@@ -573,7 +573,9 @@ ssd_status ssd_page_plan(const int32_t* lens, const int32_t* new_tokens, const i
  *
  * q, out      [R, Hq, D] of dtype (SSD_BF16 or SSD_F16); D elements are
  *             contiguous, strides are in elements and multiples of 8, bases
- *             16-byte aligned.  D: 64, 128 or 256.  Hkv divides Hq.
+ *             16-byte aligned.  D: 64, 128 or 256.  Hkv divides Hq.  out is q
+ *             itself (same pointer and strides) or does not overlap it, nor k
+ *             and v.
  * k, v        [num_pages, page_size, Hkv, D] of dtype, strides and bases as
  *             for q, any order of the first three dimensions.  Bytes of a
  *             page past the last token are not used, whatever they hold.

@@ -828,7 +828,9 @@ cudaError_t launch(const AttnParams& p, const Layout& L, cudaStream_t s) {
   // each takes more than a turn: as many heads to a warp as it has lanes for (32 x 12
   // branches: 109 us instead of 114; 256 x 24: 305 instead of 350).
   const int64_t warps = (int64_t)std::max(num_sms(), 1) * kJoinCtas<D> * kJoinWarps;
-  while (deal.pack * 2 * p.gqa <= kJoinHeads &&
+  // In place a warp takes one: several are taken again where an output is NaN, and
+  // would find outputs for their queries.
+  while (p.a.out != p.a.q && deal.pack * 2 * p.gqa <= kJoinHeads &&
          (int64_t)p.a.R * p.a.Hkv / deal.pack > warps)
     deal.pack *= 2;
   deal.tasks = deal.pack > 1 ? (p.a.Hkv + deal.pack - 1) / deal.pack : p.a.Hkv * deal.blocks;
@@ -878,6 +880,9 @@ ssd_status ssd_prefix_attention(const ssd_attention* a, void* workspace, size_t 
       !strides_ok(a->out, {a->out_row_stride, a->out_head_stride}) ||
       !strides_ok(a->k.ptr, {a->k.page_stride, a->k.token_stride, a->k.head_stride}) ||
       !strides_ok(a->v.ptr, {a->v.page_stride, a->v.token_stride, a->v.head_stride}))
+    return SSD_ERR_INVALID_ARG;
+  if (a->out == a->q &&
+      (a->out_row_stride != a->q_row_stride || a->out_head_stride != a->q_head_stride))
     return SSD_ERR_INVALID_ARG;
   AttnParams p{};
   Layout L;

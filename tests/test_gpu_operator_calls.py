@@ -266,3 +266,21 @@ def test_repetition_is_a_quotient(dt):
     got = ssd.process_logits(z.to(dev), history.to(dev), i32(np.full(B, V // 2)),
                              repetition=r.to(dev))["logits"]
     assert torch.equal(got.cpu(), want.to(z.dtype))
+
+
+@pytest.mark.parametrize("Hkv,M,R,D", [(8, 1, 1300, 128), (8, 2, 700, 64), (8, 4, 330, 128),
+                                       (5, 3, 520, 256), (4, 4, 9, 128)])
+@pytest.mark.parametrize("suf", [6, 40])
+def test_attention_in_place(Hkv, M, R, D, suf):
+    """Outputs over the queries, with values that are no numbers among the own tokens."""
+    torch, dev = torch_dev()
+    s = attention.make([R], [70], [suf] * R, Hkv * M, Hkv, D, 16, torch.bfloat16, seed=R)
+    if suf <= 16:
+        s["t"] = s["t"][:, :1].contiguous()   # the join reads them
+    s["v"][int(s["t"][R // 2, 0]), 3, 1] = float("nan")
+    want = attention.call(s)
+    q = s["q"].clone()
+    o = attention.call(dict(s, q=q), out={"out": q, "lse": torch.empty_like(want["lse"])})
+    assert o["out"] is q
+    assert torch.equal(q.view(torch.int16), want["out"].view(torch.int16))
+    assert torch.equal(o["lse"], want["lse"])

@@ -77,3 +77,12 @@ def test_tables_without_columns_have_no_address(kw, status):
     a = _attention(**kw)
     assert L.ssd_prefix_attention(ctypes.byref(a), None, 0, None, None) == status
     assert (L.ssd_prefix_attention_workspace_size(ctypes.byref(a)) > 0) == (status == WORKSPACE)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(), WORKSPACE), (dict(out_row_stride=2048), INVALID), (dict(out_head_stride=136), INVALID),
+])
+def test_attention_in_place_keeps_the_strides(kw, status):
+    ssd.build()
+    a = _attention(out=_attention().q, **kw)
+    assert ssd.lib().ssd_prefix_attention(ctypes.byref(a), None, 0, None, None) == status
