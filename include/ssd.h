@@ -528,8 +528,8 @@ ssd_status ssd_process_logits(const ssd_logits* in, const ssd_logits* out, int B
  * are negative, held > cols, lens + new > cols * page, or held pages do not
  * hold lens tokens; it keeps its pages and has no rows.
  *
- * Outputs are not inputs: kv_len, held_out and free_out are arrays of their
- * own.
+ * Outputs are not inputs, but arrays of their own (SSD_ERR_INVALID_ARG where
+ * an output has an input's address).
  *
  * lens, new_tokens, held  device [B] int32.  B <= 8192; B * cols and max_rows
  *             at most 2^30.

@@ -752,7 +752,7 @@ def page_plan(lens, new, held, tables, free_pages, free_count, page_size, max_ro
     Returns a dict of device tensors: slots int64, positions and owner int32
     [max_rows]; cu int32 [B + 1]; kv_len, held, served int32 [B]; free_count
     int32 [1].  `out`: the dict of an earlier call, to use its tensors again
-    (not while its kv_len, held or free_count are this call's inputs)."""
+    (not while one of them is this call's input)."""
     torch = _torch()
     i32 = torch.int32
     dev = lens.get_device()

@@ -239,7 +239,7 @@ extern "C" ssd_status ssd_page_plan(const int32_t* lens, const int32_t* new_toke
                                     int32_t* held_out, int32_t* served, int32_t* free_out,
                                     int32_t* dev_status, void* stream) {
   if (!lens || !new_tokens || !held || !tables || !free_count || !cu || !kv_len || !held_out ||
-      !served || !free_out || free_out == free_count || kv_len == lens || held_out == held)
+      !served || !free_out)
     return SSD_ERR_INVALID_ARG;
   if (B < 1 || cols < 1 || page < 1 || free_cap < 0 || max_rows < 0 || table_stride < cols)
     return SSD_ERR_INVALID_ARG;
@@ -247,6 +247,13 @@ extern "C" ssd_status ssd_page_plan(const int32_t* lens, const int32_t* new_toke
   // sums of pages and indexes of rows stay below 2^31 with room for a stride
   if (B > kMaxRequests || (int64_t)B * cols > kMaxCount || max_rows > kMaxCount)
     return SSD_ERR_UNSUPPORTED;
+  // lengths and pages are read again while outputs are written
+  for (const void* out : {(const void*)slots, (const void*)positions, (const void*)owner,
+                          (const void*)cu, (const void*)kv_len, (const void*)held_out,
+                          (const void*)served, (const void*)free_out})
+    for (const int32_t* in : {lens, new_tokens, held, (const int32_t*)tables,
+                              (const int32_t*)free_pages, free_count})
+      if (out && out == in) return SSD_ERR_INVALID_ARG;
   const PageParams p{lens,     new_tokens, held,  B, tables, table_stride, cols,
                      free_pages, free_cap, free_count, page,    max_rows, divisor(page), slots, positions,
                      owner,    cu,         kv_len, held_out,   served, free_out,     dev_status};

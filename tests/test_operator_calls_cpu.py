@@ -6,7 +6,7 @@ import ctypes
 import pytest
 
 import sampling_ssd_verify_gb300 as ssd
-from tests.test_round_operators_cpu import INVALID, WORKSPACE, _attention
+from tests.test_round_operators_cpu import INVALID, PTR, WORKSPACE, _attention
 
 
 def test_tensors_of_a_gpu_that_is_not_current_are_refused(monkeypatch):
@@ -86,3 +86,17 @@ def test_attention_in_place_keeps_the_strides(kw, status):
     ssd.build()
     a = _attention(out=_attention().q, **kw)
     assert ssd.lib().ssd_prefix_attention(ctypes.byref(a), None, 0, None, None) == status
+
+
+@pytest.mark.parametrize("out", ["slots", "pos", "own", "cu", "kv", "held_out", "served", "free_out"])
+@pytest.mark.parametrize("of", ["lens", "new", "held", "tables", "free", "count"])
+def test_outputs_of_a_plan_are_not_its_inputs(out, of):
+    """The kernel reads its inputs again after the first outputs are written."""
+    ssd.build()
+    a = dict(lens=1, new=2, held=3, B=4, tables=4, stride=8, cols=8, free=5, cap=4, count=6,
+             page=16, rows=10, slots=7, pos=8, own=9, cu=10, kv=11, held_out=12, served=13,
+             free_out=14)
+    a = {k: v if k in ("B", "stride", "cols", "cap", "page", "rows") else v * PTR
+         for k, v in a.items()}
+    a[out] = a[of]
+    assert ssd.lib().ssd_page_plan(*a.values(), None, None) == INVALID
