@@ -614,9 +614,9 @@ def _use_stream(stream, dev, tensors):
     return stream.cuda_stream
 
 
-def _results(o, name, wanted):
+def _without(o, name):
     """The call's results: `o`, but for an earlier call's that this one was not asked for."""
-    return o if wanted or name not in o else {k: v for k, v in o.items() if k != name}
+    return {k: v for k, v in o.items() if k != name}
 
 
 def process_logits(logits, history=None, history_len=None, prompt_len=None, draft_tokens=None,
@@ -700,7 +700,7 @@ def process_logits(logits, history=None, history_len=None, prompt_len=None, draf
                                   _dev_ptr(dev_status), _use_stream(stream, dev, o.values()))
     if st:
         _check(st, "ssd_process_logits")
-    return _results(o, "allowed", allowed)
+    return o if allowed or "allowed" not in o else _without(o, "allowed")
 
 
 _PLAN = ("positions", "owner", "cu", "kv_len", "held", "served", "free_count")
@@ -723,16 +723,16 @@ def _plan_pointers(o, B, T, i32, dev):
     """Addresses of page_plan's outputs but the slots: views of one buffer, one
     after the other.  That they are is told by the buffer's memory (a view made
     in inference mode knows no base)."""
-    if not o.keys() >= _PLAN_NAMES:
+    cu = o.get("cu")
+    if cu is None or "slots" not in o:
         raise SSDError("out: expected all outputs of an earlier call")
-    cu = o["cu"]
     if cu.dtype is not i32 or cu.get_device() != dev or cu.numel() != B + 1:
         raise SSDError("out: expected the dict of an earlier call with these sizes")
     memory = cu.untyped_storage()
     first = at = memory.data_ptr()
     ptrs = []
     for name, n in zip(_PLAN, (T, T, B + 1, B, B, B, 1)):
-        if n and o[name].data_ptr() != at:
+        if name not in o or n and o[name].data_ptr() != at:
             raise SSDError(f"out: {name} is not that of an earlier call with these sizes")
         ptrs.append(at)
         at += (n + 15 & ~15) * 4
@@ -764,7 +764,7 @@ def page_plan(lens, new, held, tables, free_pages, free_count, page_size, max_ro
         raise SSDError("max_rows must not be negative")
     row, one = (B,), (1,)
     o = out if out is not None else {}
-    if _PLAN_NAMES.isdisjoint(o):
+    if "cu" not in o and _PLAN_NAMES.isdisjoint(o):
         o.update(_plan_views(torch, B, T, lens.device))
     ptrs = _plan_pointers(o, B, T, i32, dev)
     table, stride, cols = _rows2d(tables, "tables", B, i32, dev)
@@ -852,4 +852,4 @@ def prefix_attention(q, k_cache, v_cache, prefix_tables, prefix_len, group_off, 
         st = L.ssd_prefix_attention(a, ws.data_ptr(), ws.numel(), _dev_ptr(dev_status), handle)
     if st:
         _check(st, "ssd_prefix_attention")
-    return _results(o, "lse", lse)
+    return o if lse or "lse" not in o else _without(o, "lse")
