@@ -586,7 +586,8 @@ ssd_status ssd_page_plan(const int32_t* lens, const int32_t* new_tokens, const i
  * prefix_len  device [G] int32 in [0, prefix_cols * page_size]; lens device
  *             [R] int32 in [0, cols * page_size] (NULL tables and lens: no
  *             own tokens, whatever cols).  Values outside are clamped and set
- *             SSD_DEV_BAD_LENGTH.
+ *             SSD_DEV_BAD_LENGTH.  Tables of 2^31 - 2^20 tokens or more, and as
+ *             many (row, head) pairs, are SSD_ERR_UNSUPPORTED.
  * group_off   device [G + 1] int32, not falling, within [0, R]; otherwise
  *             SSD_DEV_BAD_LENGTH is set and the rows concerned are undefined.
  * lse         device [R, Hq] float out (or NULL).

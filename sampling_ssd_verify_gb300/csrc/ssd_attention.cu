@@ -703,6 +703,10 @@ bool strides_ok(const void* ptr, std::initializer_list<int64_t> strides) {
   return true;
 }
 
+// Tokens and (row, head) pairs are counted in 32 bits, in tiles, blocks and stretches that
+// may end after the last one.
+constexpr int64_t kMaxCount = 0x7fffffff - (1 << 20);
+
 ssd_status check(const ssd_attention* a) {
   if (!a || (a->dtype != SSD_BF16 && a->dtype != SSD_F16) || a->pad_ != 0)
     return SSD_ERR_INVALID_ARG;
@@ -717,8 +721,8 @@ ssd_status check(const ssd_attention* a) {
                    a->prefix_table_stride < a->prefix_cols))
     return SSD_ERR_INVALID_ARG;
   if (a->tables && a->table_stride < a->cols) return SSD_ERR_INVALID_ARG;
-  if ((int64_t)a->prefix_cols * a->page_size > 0x7fffffff ||
-      (int64_t)a->cols * a->page_size > 0x7fffffff || (int64_t)a->R * a->Hq > 0x7fffffff)
+  if ((int64_t)a->prefix_cols * a->page_size > kMaxCount ||
+      (int64_t)a->cols * a->page_size > kMaxCount || (int64_t)a->R * a->Hq > kMaxCount)
     return SSD_ERR_UNSUPPORTED;
   return SSD_OK;
 }

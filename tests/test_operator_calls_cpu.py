@@ -6,7 +6,7 @@ import ctypes
 import pytest
 
 import sampling_ssd_verify_gb300 as ssd
-from tests.test_round_operators_cpu import INVALID, PTR, WORKSPACE, _attention
+from tests.test_round_operators_cpu import INVALID, PTR, UNSUPPORTED, WORKSPACE, _attention
 
 
 def test_tensors_of_a_gpu_that_is_not_current_are_refused(monkeypatch):
@@ -100,3 +100,15 @@ def test_outputs_of_a_plan_are_not_its_inputs(out, of):
          for k, v in a.items()}
     a[out] = a[of]
     assert ssd.lib().ssd_page_plan(*a.values(), None, None) == INVALID
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(prefix_cols=1, page_size=2 ** 31 - 1), UNSUPPORTED),
+    (dict(cols=1, prefix_cols=0, page_size=2 ** 31 - 2 ** 20), UNSUPPORTED),
+    (dict(cols=1, prefix_cols=1, page_size=2 ** 31 - 2 ** 20 - 8), WORKSPACE),
+])
+def test_lengths_leave_room_for_a_step_below_32_bits(kw, status):
+    """Tokens are counted in steps and stretches past the last one."""
+    ssd.build()
+    a = _attention(R=1, G=1, **kw)
+    assert ssd.lib().ssd_prefix_attention(ctypes.byref(a), None, 0, None, None) == status
