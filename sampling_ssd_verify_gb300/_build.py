@@ -50,9 +50,11 @@ def build(force: bool = False, verbose: bool = False, checks: bool = False) -> s
     """Compile and link libssd.so if it is missing or older than its sources.
 
     checks=True builds libssd_checks.so instead: every global, shared and
-    workspace access of the kernels is bounds-checked (-DSSD_CHECKS); a failed
-    check is recorded in the last 256 bytes of the workspace and the access is
-    skipped.  It is a debugging aid, not the product path."""
+    workspace access of the verification, sampling and tree kernels is
+    bounds-checked (-DSSD_CHECKS); a failed check is recorded in the last 256
+    bytes of the workspace and the access is skipped.  The kernels around a
+    round (ssd_logits.cu, ssd_pages.cu, ssd_attention*.cu) have no checks.  It
+    is a debugging aid, not the product path."""
     lib_path = CHECKS_LIB_PATH if checks else LIB_PATH
     out_dir = OUT_DIR + ("_checks" if checks else "")
     if not force and up_to_date(lib_path):

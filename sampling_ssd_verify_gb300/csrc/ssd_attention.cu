@@ -8,8 +8,9 @@
 //
 // The join is bound by the latency of its loads (partials from L2, own tokens from
 // memory), not by bytes: 96 us for 6144 rows with 1 to 8 own tokens, whose queries,
-// own tokens and outputs would be 31 us at the copy rate.  The kernel of long own caches reads
-// them at 5.4 TB/s of the 6.8 of a copy when it has the memory to itself.
+// own tokens and outputs would be 31 us at the copy rate.  The kernel of long own caches with
+// the join reads them at 5.7 TB/s (256 rows of 0 to 3000 tokens) to 6.7 (64 of 8000) of the
+// 6.8 of a copy when it has the memory to itself.
 
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -214,6 +215,8 @@ __device__ __forceinline__ void warp_stretch(const AttnParams& p, uint32_t ring,
         }
       l[r] = l[r] * keep[r] + sum;
     }
+    // weights in the type of the values, as the product takes them: half a step of each,
+    // which an output averages over its tokens; their sum l is of the unrounded ones
     const uint32_t pf[4] = {pack2<T>(sc[0][0], sc[0][1]), pack2<T>(sc[0][2], sc[0][3]),
                             pack2<T>(sc[1][0], sc[1][1]), pack2<T>(sc[1][2], sc[1][3])};
     const int tok = (lane & 7) + (((lane >> 3) & 1) << 3);
@@ -295,9 +298,9 @@ __device__ __forceinline__ int own_stretch(const AttnParams& p, int len) {
 template <typename T, int D>
 __device__ __forceinline__ void own_task(const AttnParams& p, uint32_t ring, int64_t task,
                                          int blocks) {
-  // heads side by side: a token's lie next to each other (256 rows with 450 tokens
-  // on 8 heads over a prompt of 16000: 151 us instead of 153; own caches of 900, 279
-  // instead of 283 over 40000; 19 groups of a few rows on 4 heads 24.6 instead of 24.3)
+  // heads side by side: a token's lie next to each other (256 rows with 0 to 900 tokens
+  // on 8 heads over a prompt of 16000: 128.0 us instead of 128.7; own caches of 0 to 1800
+  // over 40000 and 19 groups of a few rows on 4 heads: the same)
   const int h = (int)(task % p.a.Hkv);
   task /= p.a.Hkv;
   const int split = (int)(task % p.nsplit);
@@ -350,9 +353,12 @@ constexpr int kJoinWarps = 8;
 constexpr int kJoinHeads = 8;
 template <int D> constexpr int kJoinCtas = D == 256 ? 1 : 2;  // per SM, by registers
 // Own caches that the join reads: of so many tokens, or of one page of so many, which
-// is rarely full.  32 x 12 branches: 109 us instead of 111 with 4 tokens, 115 and 114
-// with 16, 126 and 119 with 30; 256 x 24 with 4 of a page of 64: 301 instead of 420,
-// with 1 to 32 tokens 408 and 441, with 1 to 64 528 and 481.
+// is rarely full.  The host knows the tables' width, not the lengths.  Read by the join
+// and by own_kernel: 32 x 12 branches with up to 4 tokens 106 and 109 us, up to 16 111 and
+// 110, up to 30 118 and 112; 256 x 24 with up to 4 of a page of 64 291 and 415, up to 8
+// 299 and 417, up to 32 406 and 437, up to 64 522 and 478; up to 16 of a page of 16 337
+// and 423.  So a few tokens in wider tables, which go through own_kernel, take up to 124
+// us more than they would in the join.
 constexpr int kShortOwn = 16, kShortPage = 64;
 
 // How a row's query heads are dealt to tasks: `pack` key/value heads of 8 / pack
@@ -561,7 +567,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinCtas<D>)
         s0 = exp2_fast(s0 - off);
         s1 = exp2_fast(s1 - off);
         l = l * keep + s0 + s1;
-        const uint32_t pw = pack2<T>(s0, s1);
+        const uint32_t pw = pack2<T>(s0, s1);  // rounded to the type of the values, for the product
         const int pg0 = __shfl_sync(0xffffffffu, page, quad * 8);
         const int pg1 = __shfl_sync(0xffffffffu, page, quad * 8 + 4);
         const int ip0 = __shfl_sync(0xffffffffu, in_page, quad * 8);
@@ -758,8 +764,8 @@ bool plan(const ssd_attention& a, AttnParams& p, Layout& L) {
   p.nslots = a.G > 0 ? (int)(items + (int64_t)p.workers * p.hg) : 0;
   // own tokens: read by the join where they are few; else in stretches of two
   // tiles or more, four for each resident warp, which evens out their lengths.
-  // (256 rows with 450 tokens over a prompt of 16000: 131 us, by eight 137, by two 137;
-  // 100 rows with 3000: 217, 227, 235; 256 with 1500: 309, 292, 332.)
+  // (256 rows with 0 to 900 tokens over a prompt of 16000: 128 us, by eight 135, by two
+  // 135; 100 rows with 0 to 6000: 233, 233, 248; 256 with 0 to 3000: 312, 292, 338.)
   const int64_t most = a.lens ? (int64_t)a.cols * a.page_size : 0;
   L.short_own = most <= (a.cols == 1 ? kShortPage : kShortOwn);
   p.own_apart = L.tc && !L.short_own;
@@ -827,10 +833,10 @@ cudaError_t launch(const AttnParams& p, const Layout& L, cudaStream_t s) {
     first = false;
   }
   Deal deal{1, (p.gqa + kJoinHeads - 1) / kJoinHeads, 0, 1};
-  // Few rows: every key/value head has its warp (12 branches of one sequence: 23 us
-  // instead of 40), or several that share its partials (23 instead of 31).  When a warp
-  // each takes more than a turn: as many heads to a warp as it has lanes for (32 x 12
-  // branches: 109 us instead of 114; 256 x 24: 305 instead of 350).
+  // Few rows: every key/value head has its warp (12 branches of one sequence: 28 us, two
+  // heads to a warp 38), or several that share its partials (20).  When a warp each takes
+  // more than a turn: as many heads to a warp as it has lanes for (32 x 12 branches: 106
+  // us instead of 108; 256 x 24: 300 instead of 344).  Times of the kernels alone.
   const int64_t warps = (int64_t)std::max(num_sms(), 1) * kJoinCtas<D> * kJoinWarps;
   // In place a warp takes one: several are taken again where an output is NaN, and
   // would find outputs for their queries.
@@ -845,8 +851,9 @@ cudaError_t launch(const AttnParams& p, const Layout& L, cudaStream_t s) {
   const int grid = deal.split > 1 ? (int)tasks : std::min(p.a.R, resident);
   const int smem = join_bytes<D>(deal.split > 1 ? deal.split : 0);
   // Started early, the join finds the shared-memory split of the kernel before on
-  // its SM: 256 x 24 branches then take 23 us more (it has many turns, and lives
-  // on its cache), uneven groups of a few rows, one turn, 1 us less.
+  // its SM: 256 x 24 branches then take 26 us more (it has many turns, and lives
+  // on its cache).  With one turn it makes little difference: uneven groups of a few rows
+  // 26.8 us instead of 27.1 called one by one, 24.2 instead of 23.5 in a graph.
   const bool early = !first && (deal.split > 1 || p.a.R <= resident);
   return L.short_own
              ? launch_next(join_kernel<T, D, true>, grid, threads, smem, s, early, p, deal)

@@ -43,6 +43,8 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// 2^x to about 2^-22 of the value, results below 2^-126 as zero: far below the half step
+// (2^-8 or 2^-11) of the 16-bit weights that are made of it.
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -155,15 +157,17 @@ struct Split {
 // then begins with a worker of its own; that pays where no more than a quarter of
 // them is left idle and most units are of prefixes with several blocks.  Measured
 // without own tokens, 32 heads on 8, of 19 workers (8 CTAs each): 8 blocks over
-// 40000 tokens take 145 us by 16, 202 by 19; over 3000, 32 and 36; 3 blocks over
-// 24000 take 50 us by 18, 59 by 19; but 10 blocks 166 by 10, 117 by 19.
+// 40000 tokens take 144 us by 16, 201 by 19; over 16000, 68 and 69; over 3000, 29 and 33;
+// 3 blocks over 24000 take 47 us by 18, 57 by 19; but 10 blocks 170 by 10, 116 by 19.
 //
 // A prefix of several blocks leaves the memory idle, which own tokens in a kernel of
 // their own wait for.  With enough of those, half the workers take the prefixes and
-// the other SMs go to the own tokens at once.  `own` counts 16 tokens a unit.  In own
-// tokens x heads x D / 128 to prefix tokens x heads x blocks: at 0.6 it takes 122 us
-// instead of 128, at 0.9 130 instead of 153, at 3.4 116 instead of 124; at 0.45 122
-// instead of 115, and with 16 items, more than the 9 workers left, 218 instead of 209.
+// the other SMs go to the own tokens at once.  `own` counts 16 tokens a unit.  The rule
+// goes by own tokens x heads x D / 128 to prefix tokens x heads x blocks, half or more.
+// Half and all of the workers, 256 rows over a prompt of 16000: at 0.2 119 and 91 us, 0.45
+// 120 and 112, 0.6 120 and 124, 0.9 128 and 150, 3.4 348 and 363.  Where the lines cross
+// differs by 0.3 either way: 64 rows over 16000 at 0.25 47 and 52, 256 rows over 40000 at
+// 0.6 264 and 260.  With 16 items, more than the 9 workers left, 183 and 174.
 __device__ __forceinline__ Split split_of(const AttnParams& p, int total, int items, int shared,
                                           int own) {
   Split s{total, min(p.workers, total)};

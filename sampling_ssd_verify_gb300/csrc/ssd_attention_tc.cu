@@ -16,8 +16,12 @@
 //     products of one run during the exponentials of the other;
 //   - two warpgroups compute the exponentials, one per stream, a row of scores
 //     per thread.  Each keeps its own maximum and weight; P replaces S in
-//     tensor memory and is the A operand from there.  The sums are rescaled
-//     only when the maximum rose by more than 2^8.
+//     tensor memory and is the A operand from there, in the type of V as the
+//     product takes it: each weight is off by at most half a step, which an
+//     output averages over its tokens (against 64 bits 0.0022 of the outputs'
+//     norm instead of the 0.0017 of their own rounding, in bf16); its sum is of
+//     the unrounded weights.  Any offset gives the same quotient, so the sums
+//     are rescaled only when the maximum rose by more than 2^8.
 // At the end of a stretch the two streams' sums are joined, each warpgroup
 // half of the columns, and written as one partial.
 //

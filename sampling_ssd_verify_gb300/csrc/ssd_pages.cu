@@ -11,8 +11,8 @@
 // taken lie at columns >= held, those read below it; stack entries written
 // lie at >= *free_count, those read below it.  Bound by the latency of the
 // launch, the loads of the lengths and the scan; bytes count from about a
-// hundred thousand new tokens on (16 bytes each): 4.1 us for 32 requests, 5.9 for 256,
-// 10.6 for 1000 with half a million new tokens.
+// hundred thousand new tokens on (16 bytes each): 4.1 us for 32 requests, 6.0 for 256,
+// 10.5 for 1000 with half a million new tokens.
 
 #include <cuda_runtime.h>
 #include <stdint.h>
