@@ -728,7 +728,8 @@ ssd_status check(const ssd_attention* a) {
     return SSD_ERR_INVALID_ARG;
   if (a->tables && a->table_stride < a->cols) return SSD_ERR_INVALID_ARG;
   if ((int64_t)a->prefix_cols * a->page_size > kMaxCount ||
-      (int64_t)a->cols * a->page_size > kMaxCount || (int64_t)a->R * a->Hq > kMaxCount)
+      (a->tables && (int64_t)a->cols * a->page_size > kMaxCount) ||
+      (int64_t)a->R * a->Hq > kMaxCount)
     return SSD_ERR_UNSUPPORTED;
   return SSD_OK;
 }

@@ -67,6 +67,7 @@ def test_outputs_of_a_plan_come_whole():
 @pytest.mark.parametrize("kw,status", [
     (dict(prefix_tables=None, prefix_cols=0), WORKSPACE), (dict(tables=None, cols=0), WORKSPACE),
     (dict(tables=None, lens=None), WORKSPACE),
+    (dict(tables=None, lens=None, cols=2 ** 31 - 1), WORKSPACE),
     (dict(prefix_tables=None), INVALID), (dict(tables=None), INVALID),
     (dict(lens=None, cols=0), INVALID),
 ])
