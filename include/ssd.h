@@ -627,6 +627,184 @@ size_t ssd_prefix_attention_workspace_size(const ssd_attention* a);
 ssd_status ssd_prefix_attention(const ssd_attention* a, void* workspace, size_t workspace_bytes,
                                 int32_t* dev_status, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * ssd_tree_attention -- attention of drafted tokens over a paged cache and
+ * over one another, before they are verified: the target's pass over a tree
+ * (or chain) of drafts, one layer.  [SD-7.3] §7.3.9 item 3 (树形草稿), as in
+ * ssd_tree_verify; a chain gives the pass that ssd_verify's logits come from,
+ * and N = 1 plain decoding.
+ *
+ * Node u of sequence b (node 0: its last token, as in ssd_tree_verify) attends
+ * to the first lens[b] tokens of pages tables[b, :] and to the nodes on its
+ * path, from node 0 to u itself.  With s_j = scale * q . k_j over all of them,
+ * per query head, query head i reading key/value head i / (Hq/Hkv):
+ *   lse = log sum_j exp(s_j);   out = sum_j exp(s_j - lse) v_j.
+ * The nodes' keys and values are not in the cache: the accepted ones are put
+ * there by ssd_append_path.  What a node off the path holds, infinities and
+ * NaN included, has no effect.  Where every score is -inf: out = 0, lse = -inf.
+ *
+ * q, out      [B, N, Hq, D] of dtype (SSD_BF16 or SSD_F16); D elements are
+ *             contiguous, strides are in elements, multiples of 8 and not
+ *             negative, bases 16-byte aligned.  D: 64, 128 or 256.  Hkv
+ *             divides Hq.  out is q itself (same pointer and strides) or does
+ *             not overlap it, nor any key or value.
+ * k, v        [B, N, Hkv, D] of dtype, the nodes': page_stride is a
+ *             sequence's, token_stride a node's.
+ * k_cache, v_cache  [num_pages, page_size, Hkv, D] of dtype, any order of the
+ *             first three dimensions.  Bytes of a page past the last token
+ *             are not used, whatever they hold.
+ * tables      device int32 page ids, rows of cols columns (of none: NULL
+ *             too).  An id outside [0, num_pages) of a token that is read
+ *             sets SSD_DEV_BAD_PAGE; the token reads as zeros.
+ * lens        device [B] int32 in [0, cols * page_size]; values outside are
+ *             clamped and set SSD_DEV_BAD_LENGTH.  Tables of 2^31 - 2^20
+ *             tokens or more, as many (node, head) pairs of the batch, and
+ *             work beyond 32-bit counts are SSD_ERR_UNSUPPORTED.
+ * parent      HOST [N] int32 as in ssd_tree_verify, or NULL for a chain.
+ * lse         device [B, N, Hq] float out (or NULL).
+ * workspace   256-byte aligned, >= ssd_tree_attention_workspace_size of the
+ *             same descriptor.
+ * N <= 256.  Scores, their maxima and sums and the outputs' sums are held in
+ * float32; the weights exp(s_j - max) are rounded to dtype for the matrix
+ * product.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t dtype; /* ssd_dtype */
+  int32_t B, N, Hq, Hkv, D;
+  int32_t num_pages, page_size;
+  const void* q;
+  int64_t q_seq_stride, q_node_stride, q_head_stride;
+  ssd_paged k, v, k_cache, v_cache;
+  const int32_t* tables;
+  const int32_t* lens;
+  int64_t table_stride;
+  const int32_t* parent; /* host */
+  void* out;
+  int64_t out_seq_stride, out_node_stride, out_head_stride;
+  float* lse;
+  int32_t cols;
+  float scale;
+} ssd_tree_attn;
+size_t ssd_tree_attention_workspace_size(const ssd_tree_attn* a);
+ssd_status ssd_tree_attention(const ssd_tree_attn* a, void* workspace, size_t workspace_bytes,
+                              int32_t* dev_status, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ssd_append_path -- the keys and values of accepted nodes, of all layers, go
+ * into the cache: the slots that ssd_page_plan gave a sequence's new tokens
+ * take the nodes of its accepted path, in order.
+ *
+ * For every row t with slots[t] >= 0, of sequence b = owner[t], i = t - cu[b]:
+ *   node = i == 0 ? 0 : path[b, i - 1]   (without path, a chain: i);
+ *   cache[l, slots[t] / page_size, slots[t] % page_size] = nodes[l, b, node]
+ * for every layer l, for k and for v.  Other bytes of the caches stay.
+ *
+ * nodes       k, v: [L, B, N, H] rows of row_bytes bytes (a head's), strides in
+ *             bytes (page_stride: a sequence's); k_cache, v_cache: [L,
+ *             num_pages, page_size, H] rows.  row_bytes, strides and bases are
+ *             multiples of 16, strides not negative; the caches overlap
+ *             neither one another nor the nodes.  v and v_cache may both be
+ *             NULL.
+ * slots       device [rows] int64, owner [rows] and cu [B + 1] device int32, as
+ *             ssd_page_plan writes them.  Slots at or past num_pages *
+ *             page_size are passed over and set SSD_DEV_BAD_PAGE; no two rows
+ *             have one slot.
+ * path        device int32, sequence b's row of path_cols starts at b *
+ *             path_stride: accepted nodes as ssd_tree_verify writes them.  A row
+ *             whose owner, place or node is out of range is passed over and
+ *             sets SSD_DEV_BAD_LENGTH.
+ * One launch, no workspace.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  void* ptr;
+  int64_t layer_stride, page_stride, token_stride, head_stride;
+} ssd_layers;
+typedef struct {
+  int32_t L, B, N, H;
+  int32_t row_bytes;
+  int32_t num_pages, page_size;
+  int32_t rows, path_cols;
+  int32_t pad_; /* must be 0 */
+  ssd_layers k, v, k_cache, v_cache;
+  const int64_t* slots;
+  const int32_t* owner;
+  const int32_t* cu;
+  const int32_t* path;
+  int64_t path_stride;
+} ssd_append;
+ssd_status ssd_append_path(const ssd_append* a, int32_t* dev_status, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * ssd_fork_rows -- rows of the block tables are continued, forked and freed:
+ * samples of one prompt, beams, branches that become sequences, requests that
+ * end.  Pages may be held by several rows: shares[p] counts the rows that hold
+ * page p beside the first, so a page that ssd_page_plan gives out has 0.
+ *
+ * Row b of the new tables continues row s = src[b] of the old ones (-1: it is
+ * empty).
+ *   1. An old row that no b continues gives back its pages tables[s, 0 ..
+ *      held): shares[p] falls by one each time; a page whose last holder
+ *      gives it back is pushed on the stack free_pages[0 .. *free_count), in
+ *      the order of s and of columns.
+ *   2. The lowest b of an old row takes over its table, all held pages.
+ *   3. Every other b, in order, shares its full pages (lens[s] / page of them,
+ *      shares[p] rises by one) and, where lens[s] % page tokens are left,
+ *      takes a page from the stack's top, into which these tokens of all
+ *      layers are copied.  When the stack is empty, it and every later one
+ *      that needs a page are left empty: served[b] = 0 (SSD_DEV_NO_PAGES).
+ * A page that holds tokens at or past lens[s] is not to be shared: 3 never
+ * does.
+ * The inputs are left as they are but for entries of free_pages at or past
+ * *free_count and the copied tokens, so a call repeated on the same inputs
+ * gives the same results; the next call passes the outputs.
+ * An old row whose lens or held is negative, held > cols, or lens > held *
+ * page sets SSD_DEV_BAD_LENGTH: it keeps no pages for others (rows that
+ * continue it are empty and not served) and gives none back.  src outside
+ * [-1, S): as that.
+ *
+ * S, B        rows before and after, at most 8192 each; S * cols and B * cols
+ *             at most 2^30.  src device [B] int32; lens, held device [S] int32.
+ * tables      device int32, row s starts at s * table_stride, cols columns.  A
+ *             page id outside [0, num_pages) is passed over where it is given
+ *             back or shared, and sets SSD_DEV_BAD_PAGE, as does a page given
+ *             back more often than it is held.
+ * shares      device [num_pages] int32, not negative.
+ * free_pages  device [free_cap] int32; free_count device int32 in [0,
+ *             free_cap] (clamped otherwise, SSD_DEV_BAD_LENGTH).  Pages past
+ *             its end: as in ssd_page_plan.
+ * tables_out  device [B, cols] int32 out, -1 past a row's pages; lens_out,
+ *             held_out, served device [B] int32 out; shares_out device
+ *             [num_pages] int32 out; free_out device int32 out.  Outputs are not
+ *             inputs (SSD_ERR_INVALID_ARG where one has an input's address).
+ * k_cache, v_cache  as in ssd_append_path, L layers of H rows of row_bytes.  L
+ *             = 0: nothing is copied (ptr NULL).
+ * workspace   256-byte aligned, >= ssd_fork_rows_workspace_size.
+ * Two launches.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t S, B, cols, page_size, num_pages, free_cap;
+  int32_t L, H, row_bytes;
+  int32_t pad_; /* must be 0 */
+  const int32_t* src;
+  const int32_t* lens;
+  const int32_t* held;
+  const int32_t* tables;
+  int64_t table_stride;
+  const int32_t* shares;
+  int32_t* free_pages;
+  const int32_t* free_count;
+  ssd_layers k_cache, v_cache;
+  int32_t* tables_out;
+  int32_t* lens_out;
+  int32_t* held_out;
+  int32_t* served;
+  int32_t* shares_out;
+  int32_t* free_out;
+} ssd_fork;
+size_t ssd_fork_rows_workspace_size(const ssd_fork* f);
+ssd_status ssd_fork_rows(const ssd_fork* f, void* workspace, size_t workspace_bytes,
+                         int32_t* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

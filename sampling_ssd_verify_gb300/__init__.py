@@ -10,8 +10,11 @@ Entry points (same names as the C ABI):
   verify, topf_bonus, saguaro_sample, cache_build, cache_build_guesses,
   cache_lookup, fanout, plus verify_host (host tensors in, host results out,
   copies included); around a round: process_logits (penalties, biases and
-  grammar masks), page_plan (pages, slots and positions of a paged cache) and
-  prefix_attention (attention of rows that share prefixes).
+  grammar masks), page_plan (pages, slots and positions of a paged cache),
+  prefix_attention (attention of rows that share prefixes), tree_attention
+  (of drafts, as a tree or chain, over the cache and one another), append_path
+  (accepted drafts' keys and values into the cache) and fork_rows (rows of the
+  block tables continued, forked and freed).
 
 Sources (page title, section):
   [SSD-note] "论文阅读：Speculative Speculative Decoding — 消除推测解码的最后一个顺序瓶颈"
@@ -31,7 +34,8 @@ __all__ = [
     "SSDError", "build", "lib", "verify", "verify_round", "verify_host", "topf_bonus",
     "saguaro_sample", "tree_verify",
     "cache_bytes", "cache_build", "cache_build_guesses", "cache_lookup", "fanout",
-    "process_logits", "page_plan", "prefix_attention", "MASKED_LOGIT",
+    "process_logits", "page_plan", "prefix_attention", "tree_attention", "append_path",
+    "fork_rows", "MASKED_LOGIT",
     "DEV_BAD_TOKEN", "DEV_ZERO_RESIDUAL", "DEV_TIMEOUT", "DEV_TABLE_FULL", "DEV_DUPLICATE_KEY",
     "DEV_BAD_TEMPERATURE", "DEV_BAD_FANOUT", "DEV_BAD_PENALTY", "DEV_BAD_LENGTH",
     "DEV_NO_PAGES", "DEV_BAD_PAGE",
@@ -98,6 +102,50 @@ class _Attention(ctypes.Structure):
                 ("lse", ctypes.c_void_p), ("scale", ctypes.c_float), ("pad_", ctypes.c_int32)]
 
 
+class _TreeAttn(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("B", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("q", ctypes.c_void_p), ("q_seq_stride", ctypes.c_int64),
+                ("q_node_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("k", _Paged), ("v", _Paged), ("k_cache", _Paged), ("v_cache", _Paged),
+                ("tables", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("parent", ctypes.c_char_p),
+                ("out", ctypes.c_void_p), ("out_seq_stride", ctypes.c_int64),
+                ("out_node_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("lse", ctypes.c_void_p), ("cols", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class _Layers(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("layer_stride", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class _Append(ctypes.Structure):
+    _fields_ = [("L", ctypes.c_int32), ("B", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("row_bytes", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("rows", ctypes.c_int32), ("path_cols", ctypes.c_int32), ("pad_", ctypes.c_int32),
+                ("k", _Layers), ("v", _Layers), ("k_cache", _Layers), ("v_cache", _Layers),
+                ("slots", ctypes.c_void_p), ("owner", ctypes.c_void_p), ("cu", ctypes.c_void_p),
+                ("path", ctypes.c_void_p), ("path_stride", ctypes.c_int64)]
+
+
+class _Fork(ctypes.Structure):
+    _fields_ = [("S", ctypes.c_int32), ("B", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("free_cap", ctypes.c_int32), ("L", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("row_bytes", ctypes.c_int32), ("pad_", ctypes.c_int32),
+                ("src", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("held", ctypes.c_void_p),
+                ("tables", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("shares", ctypes.c_void_p), ("free_pages", ctypes.c_void_p),
+                ("free_count", ctypes.c_void_p), ("k_cache", _Layers), ("v_cache", _Layers),
+                ("tables_out", ctypes.c_void_p), ("lens_out", ctypes.c_void_p),
+                ("held_out", ctypes.c_void_p), ("served", ctypes.c_void_p),
+                ("shares_out", ctypes.c_void_p), ("free_out", ctypes.c_void_p)]
+
+
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
@@ -137,6 +185,11 @@ _SIGS = {
                       [_vp] * 10, _i),
     "ssd_prefix_attention_workspace_size": ([ctypes.POINTER(_Attention)], _sz),
     "ssd_prefix_attention": ([ctypes.POINTER(_Attention), _vp, _sz, _vp, _vp], _i),
+    "ssd_tree_attention_workspace_size": ([ctypes.POINTER(_TreeAttn)], _sz),
+    "ssd_tree_attention": ([ctypes.POINTER(_TreeAttn), _vp, _sz, _vp, _vp], _i),
+    "ssd_append_path": ([ctypes.POINTER(_Append), _vp, _vp], _i),
+    "ssd_fork_rows_workspace_size": ([ctypes.POINTER(_Fork)], _sz),
+    "ssd_fork_rows": ([ctypes.POINTER(_Fork), _vp, _sz, _vp, _vp], _i),
 }
 
 
@@ -853,3 +906,201 @@ def prefix_attention(q, k_cache, v_cache, prefix_tables, prefix_len, group_off, 
     if st:
         _check(st, "ssd_prefix_attention")
     return o if lse or "lse" not in o else _without(o, "lse")
+
+
+def _launch(name, a, o, workspace, dev, device, dev_status, stream, lent=()):
+    """Call ssd_<name> with a workspace of the dict's, which is made, or replaced when it is
+    too small; `lent`: tensors of the call's own, beside the dict's."""
+    L = lib()
+    size, fn = getattr(L, f"ssd_{name}_workspace_size"), getattr(L, f"ssd_{name}")
+    ws = workspace if workspace is not None else o.get("workspace")
+    if ws is None:
+        ws = o["workspace"] = _workspace(size(a), device)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise SSDError(f"the workspace must be a contiguous tensor on cuda:{dev}")
+    status = _dev_ptr(dev_status)
+    handle = _use_stream(stream, dev, (*o.values(), ws, *lent))
+    st = fn(a, ws.data_ptr(), ws.numel() * ws.element_size(), status, handle)
+    if st == _ERR_WORKSPACE and workspace is None:  # nothing has been launched
+        ws = o["workspace"] = _workspace(size(a), device)
+        handle = _use_stream(stream, dev, (ws,))
+        st = fn(a, ws.data_ptr(), ws.numel(), status, handle)
+    if st:
+        _check(st, f"ssd_{name}")
+
+
+def tree_attention(q, k, v, k_cache, v_cache, tables, lens, parent=None, scale=None, lse=True,
+                   workspace=None, dev_status=None, stream=None, out=None):
+    """ssd_tree_attention: drafted nodes of a sequence over its cache and one another.
+
+    q [B, N, Hq, D] and the nodes' k, v [B, N, Hkv, D] (bf16 or fp16, any strides with a
+    contiguous head dimension, so pieces of one projection too); caches [pages, page_size, Hkv,
+    D] of that type; tables int32 [B, W], lens int32 [B]: tokens in the cache, without the nodes.
+    parent: N ints as in tree_verify (a chain when None): node u attends to the cache and to the
+    nodes on its path, itself included.  N = 1: one token per sequence.  scale: 1 / sqrt(D) when
+    None.
+    Returns a dict: ``out`` [B, N, Hq, D] and, unless lse=False, ``lse`` float32 [B, N, Hq].
+    `out`: as in prefix_attention; a captured graph needs a dict of its own."""
+    torch = _torch()
+    i32 = torch.int32
+    qs, ks, cs, dt = q.shape, k.shape, k_cache.shape, q.dtype
+    if len(qs) != 4 or len(ks) != 4 or len(cs) != 4 or v.shape != ks or v_cache.shape != cs or \
+            ks[:2] != qs[:2] or ks[3] != qs[3] or cs[2:] != ks[2:]:
+        raise SSDError("expected q [B, N, Hq, D], k and v [B, N, Hkv, D] and caches [pages, "
+                       "page_size, Hkv, D]")
+    B, N, Hq, D = qs
+    code = SSD_BF16 if dt is torch.bfloat16 else SSD_F16 if dt is torch.float16 else -1
+    dev = q.get_device()
+    for t in (k, v, k_cache, v_cache):
+        if t.dtype is not dt:
+            code = -1
+        if t.get_device() != dev:
+            raise SSDError("q, the nodes and the caches must be on one GPU")
+    if code < 0:
+        raise SSDError("q, the nodes and the caches must share bfloat16 or float16")
+    if dev < 0:
+        raise SSDError("q, the nodes and the caches must be on one GPU")
+    _on_current(dev)
+    o = out if out is not None else {}
+    y = o.get("out")
+    if y is None:
+        y = o["out"] = torch.empty(qs, dtype=dt, device=q.device)
+    elif y.shape != qs or y.dtype is not dt or y.get_device() != dev:
+        raise SSDError("out must have q's shape, type and device")
+    at = 0
+    if lse:
+        if o.get("lse") is None:
+            o["lse"] = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device)
+        at = _tensor(o["lse"], "lse", torch.float32, (B, N, Hq), dev)
+    views = []
+    for t in (q, y, k, v, k_cache, v_cache):
+        s = t.stride()
+        if s[3] != 1:
+            raise SSDError("the head dimension must be contiguous")
+        views.append((t.data_ptr(), s[0], s[1], s[2]))
+    if parent is not None:
+        if len(parent) != N:
+            raise SSDError("parent must have N entries")
+        parent = np.asarray(parent, dtype=np.int32).tobytes()
+    table, stride, cols = _rows2d(tables, "tables", B, i32, dev)
+    a = _TreeAttn(code, B, N, Hq, ks[2], D, cs[0], cs[1], *views[0], *views[2:], table,
+                  _tensor(lens, "lens", i32, (B,), dev), stride, parent, *views[1], at, cols,
+                  D ** -0.5 if scale is None else scale)
+    _launch("tree_attention", a, o, workspace, dev, q.device, dev_status, stream)
+    return o if lse or "lse" not in o else _without(o, "lse")
+
+
+def _layers(t, name, dev):
+    """ssd_layers and shape of a tensor [L, X, Y, H, D], or [X, Y, H, D] of one layer."""
+    s, shape = t.stride(), t.shape
+    if len(shape) == 4:
+        s, shape = (0, *s), (1, *shape)
+    if len(shape) != 5 or t.get_device() != dev:
+        raise SSDError(f"{name}: expected a tensor of 4 dimensions, or 5 with the layers, on "
+                       f"cuda:{dev}")
+    es = t.element_size()
+    if s[4] != 1 or shape[4] * es % 16 != 0:
+        raise SSDError(f"{name}: a head must be contiguous, and a multiple of 16 bytes")
+    return _Layers(t.data_ptr(), s[0] * es, s[1] * es, s[2] * es, s[3] * es), tuple(shape)
+
+
+_NO_LAYERS = _Layers()
+
+
+def append_path(k, v, k_cache, v_cache, slots, owner, cu, path=None, dev_status=None,
+                stream=None):
+    """ssd_append_path: accepted nodes' keys and values into the caches of all layers.
+
+    k, v [L, B, N, H, D] and caches [L, pages, page_size, H, D], or without the first dimension
+    for one layer; any one type, any strides with contiguous heads of a multiple of 16 bytes;
+    v and v_cache may both be None.  slots int64 [T], owner int32 [T] and cu int32 [B + 1] are
+    page_plan's for the accepted tokens: row t of sequence b = owner[t] takes the node at place
+    t - cu[b] of its path: node 0, then path[b, 0], path[b, 1], .. (int32 [B, n], tree_verify's;
+    None: a chain).  Rows with a negative slot are passed over.  The caches are written in place
+    and do not overlap the nodes.  Returns None."""
+    torch = _torch()
+    i32 = torch.int32
+    dev = k_cache.get_device()
+    if dev < 0:
+        raise SSDError("expected caches on the GPU")
+    _on_current(dev)
+    if (v is None) != (v_cache is None):
+        raise SSDError("v and v_cache go together")
+    kl, ks = _layers(k, "k", dev)
+    cl, cs = _layers(k_cache, "k_cache", dev)
+    if ks[0] != cs[0] or ks[3:] != cs[3:] or k.dtype is not k_cache.dtype:
+        raise SSDError("nodes and caches must share the layers, heads and type")
+    vl = wl = _NO_LAYERS
+    if v is not None:
+        if v.shape != k.shape or v_cache.shape != k_cache.shape or v.dtype is not k.dtype or \
+                v_cache.dtype is not k.dtype:
+            raise SSDError("v and v_cache must have the shapes and type of k and k_cache")
+        (vl, _), (wl, _) = _layers(v, "v", dev), _layers(v_cache, "v_cache", dev)
+    L, B, N, H, D = ks
+    if slots.dim() != 1:
+        raise SSDError("expected slots [T]")
+    T = slots.shape[0]
+    p = p_stride = p_cols = 0
+    if path is not None:
+        p, p_stride, p_cols = _rows2d(path, "path", B, i32, dev)
+    a = _Append(L, B, N, H, D * k.element_size(), cs[1], cs[2], T, p_cols, 0, kl, vl, cl, wl,
+                _tensor(slots, "slots", torch.int64, (T,), dev),
+                _tensor(owner, "owner", i32, (T,), dev), _tensor(cu, "cu", i32, (B + 1,), dev), p,
+                p_stride)
+    st = lib().ssd_append_path(a, _dev_ptr(dev_status), _use_stream(stream, dev, ()))
+    if st:
+        _check(st, "ssd_append_path")
+
+
+def fork_rows(src, lens, held, tables, shares, free_pages, free_count, page_size, k_cache=None,
+              v_cache=None, workspace=None, dev_status=None, stream=None, out=None):
+    """ssd_fork_rows: rows of the block tables continued, forked and freed.
+
+    src int32 [B]: the old row that each new one continues (-1: none); lens, held int32 [S] and
+    tables int32 [S, W] of the old rows; shares int32 [pages]: rows that hold a page beside the
+    first; the stack free_pages int32 [n] with free_count int32 [1] (entries past it are
+    written).  Old rows that nobody continues give their pages back; the first row that
+    continues one keeps its pages, the others share the full ones and get a copy of the tokens
+    of the last in a page from the stack.  k_cache, v_cache [L, pages, page_size, H, D] (or of
+    one layer) hold those tokens (None: nothing is copied; v_cache alone may be None too).
+    Returns a dict of device tensors: tables [B, W], lens, held, served [B], shares [pages],
+    free_count [1], all int32.  `out`: the dict of an earlier call of these sizes, to use its
+    tensors and workspace again (not while one of them is this call's input)."""
+    torch = _torch()
+    i32 = torch.int32
+    dev = src.get_device()
+    if dev < 0 or src.dim() != 1 or lens.dim() != 1 or shares.dim() != 1:
+        raise SSDError("expected src [B], lens [S] and shares [pages] on the GPU")
+    _on_current(dev)
+    B, S, pages = src.shape[0], lens.shape[0], shares.shape[0]
+    table, stride, cols = _rows2d(tables, "tables", S, i32, dev)
+    kl = vl = _NO_LAYERS
+    L = H = row = 0
+    if k_cache is not None:
+        kl, ks = _layers(k_cache, "k_cache", dev)
+        L, H, row = ks[0], ks[3], ks[4] * k_cache.element_size()
+        if ks[1] != pages or ks[2] != page_size:
+            raise SSDError("the caches must have one page for each entry of shares, of page_size "
+                           "tokens")
+        if v_cache is not None:
+            if v_cache.shape != k_cache.shape or v_cache.dtype is not k_cache.dtype:
+                raise SSDError("the caches must have one shape and type")
+            vl, _ = _layers(v_cache, "v_cache", dev)
+    elif v_cache is not None:
+        raise SSDError("v_cache goes with k_cache")
+    o = out if out is not None else {}
+    at = []
+    for name, shape in (("tables", (B, cols)), ("lens", (B,)), ("held", (B,)), ("served", (B,)),
+                        ("shares", (pages,)), ("free_count", (1,))):
+        t = o.get(name)
+        if t is None:
+            t = o[name] = torch.empty(shape, dtype=i32, device=src.device)
+        at.append(_tensor(t, name, i32, shape, dev))
+    a = _Fork(S, B, cols, int(page_size), pages, free_pages.numel(), L, H, row, 0,
+              _tensor(src, "src", i32, (B,), dev), _tensor(lens, "lens", i32, (S,), dev),
+              _tensor(held, "held", i32, (S,), dev), table, stride,
+              _tensor(shares, "shares", i32, (pages,), dev),
+              _tensor(free_pages, "free_pages", i32, free_pages.shape, dev),
+              _tensor(free_count, "free_count", i32, (1,), dev), kl, vl, *at)
+    _launch("fork_rows", a, o, workspace, dev, src.device, dev_status, stream)
+    return o

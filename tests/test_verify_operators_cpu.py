@@ -1,0 +1,185 @@
+"""Refusals of tree_attention, append_path and fork_rows: every argument error returns its status
+before anything is enqueued (no device is touched), and the Python layer refuses tensors of the
+wrong place, type or shape."""
+
+import ctypes
+
+import numpy as np
+import pytest
+
+import sampling_ssd_verify_gb300 as ssd
+
+INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 5
+PTR = 0x10000
+
+
+@pytest.fixture(scope="module")
+def L():
+    ssd.build()
+    return ssd.lib()
+
+
+def _tree(**kw):
+    a = ssd._TreeAttn(dtype=0, B=2, N=3, Hq=4, Hkv=2, D=64, num_pages=9, page_size=16, q=PTR,
+                      q_seq_stride=768, q_node_stride=256, q_head_stride=64,
+                      k=(2 * PTR, 384, 128, 64), v=(3 * PTR, 384, 128, 64),
+                      k_cache=(4 * PTR, 2048, 128, 64), v_cache=(5 * PTR, 2048, 128, 64),
+                      tables=6 * PTR, lens=7 * PTR, table_stride=4, parent=None, out=8 * PTR,
+                      out_seq_stride=768, out_node_stride=256, out_head_stride=64, lse=None,
+                      cols=4, scale=0.125)
+    for k, v in kw.items():
+        if k == "parent":
+            v = np.asarray(v, dtype=np.int32).tobytes()
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(), WORKSPACE), (dict(dtype=1), INVALID), (dict(dtype=7), INVALID), (dict(B=0), INVALID),
+    (dict(N=0), INVALID), (dict(N=257), UNSUPPORTED), (dict(N=256), WORKSPACE),
+    (dict(Hq=3), INVALID), (dict(Hq=0), INVALID), (dict(Hkv=0), INVALID),
+    (dict(D=80), UNSUPPORTED), (dict(D=0), UNSUPPORTED), (dict(num_pages=0), INVALID),
+    (dict(page_size=0), INVALID), (dict(q=None), INVALID), (dict(q=PTR + 8), INVALID),
+    (dict(q_seq_stride=764), INVALID), (dict(q_node_stride=-256), INVALID),
+    (dict(q_head_stride=65), INVALID), (dict(out=None), INVALID), (dict(out_head_stride=4), INVALID),
+    (dict(k=(0, 384, 128, 64)), INVALID), (dict(v=(3 * PTR + 2, 384, 128, 64)), INVALID),
+    (dict(k=(2 * PTR, 380, 128, 64)), INVALID), (dict(k_cache=(4 * PTR, 2048, 100, 64)), INVALID),
+    (dict(v_cache=(0, 2048, 128, 64)), INVALID), (dict(v_cache=(PTR, -2048, 128, 64)), INVALID),
+    (dict(tables=None), INVALID), (dict(lens=None), INVALID), (dict(table_stride=3), INVALID),
+    (dict(tables=None, cols=0), WORKSPACE), (dict(cols=-1), INVALID),
+    (dict(scale=float("inf")), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(scale=-1.0), WORKSPACE), (dict(scale=0.0), WORKSPACE),
+    (dict(parent=[-1, 0, 0]), WORKSPACE), (dict(parent=[0, 0, 0]), INVALID),
+    (dict(parent=[-1, 1, 0]), INVALID), (dict(parent=[-1, 0, -1]), INVALID),
+    (dict(parent=[-2, 0, 0]), INVALID),
+    (dict(cols=1, page_size=2 ** 31 - 2 ** 20), UNSUPPORTED),
+    (dict(B=2 ** 30), UNSUPPORTED), (dict(Hq=2 ** 30, Hkv=2 ** 29), UNSUPPORTED),
+    (dict(out=PTR), WORKSPACE), (dict(out=PTR, out_node_stride=512), INVALID),
+    (dict(out=PTR, out_seq_stride=1536), INVALID), (dict(out=PTR, out_head_stride=128), INVALID),
+])
+def test_tree_attention_refusals(L, kw, status):
+    a = _tree(**kw)
+    assert L.ssd_tree_attention(ctypes.byref(a), None, 0, None, None) == status
+    if status == WORKSPACE:
+        n = L.ssd_tree_attention_workspace_size(ctypes.byref(a))
+        assert n > 0 and n % 256 == 0
+        assert L.ssd_tree_attention(ctypes.byref(a), PTR + 128, n, None, None) == WORKSPACE
+        assert L.ssd_tree_attention(ctypes.byref(a), PTR, n - 1, None, None) == WORKSPACE
+    assert L.ssd_tree_attention(None, None, 0, None, None) == INVALID
+    assert L.ssd_tree_attention_workspace_size(None) == 0
+
+
+def _append(**kw):
+    row = (1 << 20, 4096, 256, 128)
+    a = ssd._Append(L=2, B=3, N=4, H=2, row_bytes=128, num_pages=9, page_size=16, rows=0,
+                    path_cols=3, pad_=0, k=(PTR, *row), v=(2 * PTR, *row), k_cache=(3 * PTR, *row),
+                    v_cache=(4 * PTR, *row), slots=PTR, owner=PTR, cu=PTR, path=PTR, path_stride=3)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+ROW = (1 << 20, 4096, 256, 128)
+APPEND = [
+    (dict(), 0), (dict(L=0), INVALID), (dict(B=0), INVALID), (dict(N=0), INVALID),
+    (dict(H=0), INVALID), (dict(row_bytes=0), INVALID), (dict(row_bytes=24), INVALID),
+    (dict(num_pages=0), INVALID), (dict(page_size=0), INVALID), (dict(rows=-1), INVALID),
+    (dict(path_cols=-1), INVALID), (dict(pad_=1), INVALID), (dict(cu=None), INVALID),
+    (dict(rows=4, slots=None), INVALID), (dict(rows=4, owner=None), INVALID),
+    (dict(path_stride=2), INVALID), (dict(path=None, path_stride=0), 0),
+    (dict(k=(0, *ROW)), INVALID), (dict(k=(PTR + 8, *ROW)), INVALID),
+    (dict(v=(0, *ROW)), INVALID), (dict(v_cache=(0, *ROW)), INVALID),
+    (dict(v=(0, *ROW), v_cache=(0, *ROW)), 0), (dict(k_cache=(3 * PTR, -16, 4096, 256, 128)), INVALID),
+    (dict(k_cache=(3 * PTR, 1 << 20, 4096, 250, 128)), INVALID),
+    (dict(k_cache=(PTR, *ROW)), INVALID), (dict(k_cache=(2 * PTR, *ROW)), INVALID),
+    (dict(v_cache=(3 * PTR, *ROW)), INVALID), (dict(v_cache=(PTR, *ROW)), INVALID),
+    (dict(v_cache=(2 * PTR, *ROW)), INVALID),
+    (dict(row_bytes=1 << 24, H=2), UNSUPPORTED), (dict(rows=2 ** 31 - 1), UNSUPPORTED),
+]
+
+
+@pytest.mark.parametrize("kw,status", APPEND)
+def test_append_path_refusals(L, kw, status):
+    a = _append(**kw)                  # no rows: nothing is launched
+    assert L.ssd_append_path(ctypes.byref(a), None, None) == status
+    assert L.ssd_append_path(None, None, None) == INVALID
+
+
+def _fork(**kw):
+    a = ssd._Fork(S=3, B=4, cols=5, page_size=16, num_pages=9, free_cap=8, L=2, H=2, row_bytes=128,
+                  pad_=0, src=PTR, lens=2 * PTR, held=3 * PTR, tables=4 * PTR, table_stride=5,
+                  shares=5 * PTR, free_pages=6 * PTR, free_count=7 * PTR, k_cache=(8 * PTR, *ROW),
+                  v_cache=(9 * PTR, *ROW), tables_out=10 * PTR, lens_out=11 * PTR,
+                  held_out=12 * PTR, served=13 * PTR, shares_out=14 * PTR, free_out=15 * PTR)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(), WORKSPACE), (dict(S=0), INVALID), (dict(B=0), INVALID), (dict(cols=0), INVALID),
+    (dict(page_size=0), INVALID), (dict(num_pages=0), INVALID), (dict(free_cap=-1), INVALID),
+    (dict(L=-1), INVALID), (dict(H=0), INVALID), (dict(row_bytes=20), INVALID),
+    (dict(pad_=1), INVALID), (dict(S=8193), UNSUPPORTED), (dict(B=8193), UNSUPPORTED),
+    (dict(S=8192, cols=2 ** 18, table_stride=2 ** 18), UNSUPPORTED), (dict(row_bytes=1 << 25), UNSUPPORTED),
+    (dict(num_pages=2 ** 30 + 1), UNSUPPORTED),
+    (dict(src=None), INVALID), (dict(lens=None), INVALID), (dict(held=None), INVALID),
+    (dict(tables=None), INVALID), (dict(shares=None), INVALID), (dict(free_pages=None), INVALID),
+    (dict(free_pages=None, free_cap=0), WORKSPACE), (dict(free_count=None), INVALID),
+    (dict(table_stride=4), INVALID), (dict(tables_out=None), INVALID), (dict(lens_out=None), INVALID),
+    (dict(held_out=None), INVALID), (dict(served=None), INVALID), (dict(shares_out=None), INVALID),
+    (dict(free_out=None), INVALID), (dict(k_cache=(0, *ROW)), INVALID),
+    (dict(k_cache=(0, *ROW), v_cache=(0, *ROW)), INVALID),
+    (dict(L=0, k_cache=(0, 0, 0, 0, 0), v_cache=(0, 0, 0, 0, 0)), WORKSPACE),
+    (dict(v_cache=(0, *ROW)), WORKSPACE), (dict(v_cache=(8 * PTR, *ROW)), INVALID),
+    (dict(v_cache=(9 * PTR, 8, 4096, 256, 128)), INVALID),
+    *[({out: i * PTR}, INVALID) for out in ("tables_out", "lens_out", "held_out", "served",
+                                            "shares_out", "free_out") for i in range(1, 8)],
+])
+def test_fork_rows_refusals(L, kw, status):
+    f = _fork(**kw)
+    assert L.ssd_fork_rows(ctypes.byref(f), None, 0, None, None) == status
+    if status == WORKSPACE:
+        n = L.ssd_fork_rows_workspace_size(ctypes.byref(f))
+        assert n > 0 and n % 256 == 0
+        assert L.ssd_fork_rows(ctypes.byref(f), PTR + 128, n, None, None) == WORKSPACE
+        assert L.ssd_fork_rows(ctypes.byref(f), PTR, n - 1, None, None) == WORKSPACE
+    assert L.ssd_fork_rows(None, None, 0, None, None) == INVALID
+    assert L.ssd_fork_rows_workspace_size(None) == 0
+
+
+def test_python_layer_wants_gpu_tensors():
+    import torch
+
+    c = torch.zeros((9, 16, 2, 64), dtype=torch.bfloat16)
+    x = torch.zeros((2, 3, 4, 64), dtype=torch.bfloat16)
+    i = torch.zeros(2, dtype=torch.int32)
+    t = torch.zeros((2, 4), dtype=torch.int32)
+    for call in (lambda: ssd.tree_attention(x, x[:, :, :2], x[:, :, 2:], c, c, t, i),
+                 lambda: ssd.append_path(x[:, :, :2], x[:, :, 2:], c, c, i.long(), i, i),
+                 lambda: ssd.fork_rows(i, i, i, t, i, i, i[:1], 16)):
+        with pytest.raises(ssd.SSDError):
+            call()
+
+
+def test_tensors_of_a_gpu_that_is_not_current_are_refused(monkeypatch):
+    import torch
+
+    class Elsewhere(torch.Tensor):
+        is_cuda = True
+
+        def get_device(self):
+            return 1
+
+    def there(*shape, dtype=torch.int32):
+        return torch.zeros(shape, dtype=dtype).as_subclass(Elsewhere)
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    c = there(9, 16, 2, 64, dtype=torch.bfloat16)
+    q, k = there(2, 3, 4, 64, dtype=torch.bfloat16), there(2, 3, 2, 64, dtype=torch.bfloat16)
+    i, t = there(2), there(2, 4)
+    for call in (lambda: ssd.tree_attention(q, k, k, c, c, t, i),
+                 lambda: ssd.append_path(k, k, c, c, i, i, i),
+                 lambda: ssd.fork_rows(i, i, i, t, i, i, there(1), 16)):
+        with pytest.raises(ssd.SSDError, match="cuda:1.*cuda:0"):
+            call()
