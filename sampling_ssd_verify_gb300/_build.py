@@ -21,7 +21,8 @@ LIB_PATH = os.path.join(PKG, "libssd.so")
 CHECKS_LIB_PATH = os.path.join(PKG, "libssd_checks.so")
 SOURCES = ["ssd_stream_bf16.cu", "ssd_stream_f32.cu", "ssd_cache.cu", "ssd_api.cu",
            "ssd_noalloc.cu", "ssd_tree.cu", "ssd_logits.cu", "ssd_pages.cu",
-           "ssd_attention.cu", "ssd_attention_tc.cu", "ssd_rows.cu", "ssd_tree_attention.cu"]
+           "ssd_attention.cu", "ssd_attention_tc.cu", "ssd_rows.cu", "ssd_tree_attention.cu",
+           "ssd_tree_attention_bf16.cu", "ssd_tree_attention_f16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -54,7 +55,7 @@ def build(force: bool = False, verbose: bool = False, checks: bool = False) -> s
     bounds-checked (-DSSD_CHECKS); a failed check is recorded in the last 256
     bytes of the workspace and the access is skipped.  The kernels around a
     round (ssd_logits.cu, ssd_pages.cu, ssd_attention*.cu, ssd_rows.cu,
-    ssd_tree_attention.cu) have no checks.  It
+    ssd_tree_attention*) have no checks.  It
     is a debugging aid, not the product path."""
     lib_path = CHECKS_LIB_PATH if checks else LIB_PATH
     out_dir = OUT_DIR + ("_checks" if checks else "")

@@ -1,8 +1,6 @@
 // ssd_tree_attention.cu -- attention of drafted nodes over a paged cache and over
-// the nodes on their paths (ssd_tree_attention).
-//
-// out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m) with m the running maximum: one
-// warp per (sequence, node, query head), one token at a time.
+// the nodes on their paths (ssd_tree_attention): the entry point, the division of the
+// work and the workspace.
 
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -10,102 +8,11 @@
 #include <algorithm>
 #include <cmath>
 
-#include "ssd_attention_dev.cuh"
+#include "ssd_tc_dev.cuh"
+#include "ssd_tree_attention.cuh"
 
 namespace ssd {
 namespace {
-
-constexpr int kWarps = 8;
-constexpr int kMaxNodes = 256;
-
-struct TreeAttnParams {
-  ssd_tree_attn a;
-  Divisor by_page;
-  float scale_log2;
-  int gqa;
-  int64_t rows;
-  int32_t* status;
-  int16_t parent[kMaxNodes];
-};
-
-__device__ __forceinline__ float2 unpack2(uint32_t x, __nv_bfloat16) {
-  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x));
-}
-__device__ __forceinline__ float2 unpack2(uint32_t x, __half) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&x));
-}
-
-template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32)
-    tree_kernel(const __grid_constant__ TreeAttnParams p) {
-  constexpr int E = D / 64;          // pairs of elements of a lane
-  const ssd_tree_attn& a = p.a;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (row >= p.rows) return;
-  const int head = (int)(row % a.Hq), u = (int)(row / a.Hq % a.N), b = (int)(row / a.Hq / a.N);
-  const int h = head / p.gqa;
-  const int64_t most = (int64_t)a.cols * a.page_size;
-  const int given = a.lens[b], len = given < 0 ? 0 : given > most ? (int)most : given;
-  if (len != given && lane == 0 && p.status) atomicOr(p.status, SSD_DEV_BAD_LENGTH);
-  float2 q[E], o[E];
-  const T* from = static_cast<const T*>(a.q) + b * a.q_seq_stride + u * a.q_node_stride +
-                  head * a.q_head_stride + lane * 2;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = unpack2(*reinterpret_cast<const uint32_t*>(from + e * 64), T());
-    o[e] = make_float2(0.f, 0.f);
-  }
-  float m = -INFINITY, l = 0.f;
-  auto token = [&](const T* k, const T* v) {
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float2 x = k ? unpack2(*reinterpret_cast<const uint32_t*>(k + lane * 2 + e * 64), T())
-                         : make_float2(0.f, 0.f);
-      s = fmaf(q[e].x, x.x, fmaf(q[e].y, x.y, s));
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    s *= p.scale_log2;
-    const float m1 = fmaxf(m, s), off = m1 == -INFINITY ? 0.f : m1;
-    const float keep = exp2f(m - off), w = exp2f(s - off);
-    m = m1;
-    l = l * keep + w;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float2 x = v ? unpack2(*reinterpret_cast<const uint32_t*>(v + lane * 2 + e * 64), T())
-                         : make_float2(0.f, 0.f);
-      o[e].x = fmaf(w, x.x, o[e].x * keep);
-      o[e].y = fmaf(w, x.y, o[e].y * keep);
-    }
-  };
-  for (int t = 0; t < len; ++t) {
-    const int col = p.by_page.quotient(t), in_page = t - col * a.page_size;
-    const int page = a.tables[b * a.table_stride + col];
-    if ((unsigned)page >= (unsigned)a.num_pages) {
-      if (lane == 0 && p.status) atomicOr(p.status, SSD_DEV_BAD_PAGE);
-      token(nullptr, nullptr);
-      continue;
-    }
-    token(static_cast<const T*>(a.k_cache.ptr) + page * a.k_cache.page_stride +
-              in_page * a.k_cache.token_stride + h * a.k_cache.head_stride,
-          static_cast<const T*>(a.v_cache.ptr) + page * a.v_cache.page_stride +
-              in_page * a.v_cache.token_stride + h * a.v_cache.head_stride);
-  }
-  for (int n = u; n >= 0; n = p.parent[n])
-    token(static_cast<const T*>(a.k.ptr) + b * a.k.page_stride + n * a.k.token_stride +
-              h * a.k.head_stride,
-          static_cast<const T*>(a.v.ptr) + b * a.v.page_stride + n * a.v.token_stride +
-              h * a.v.head_stride);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  T* to = static_cast<T*>(a.out) + b * a.out_seq_stride + u * a.out_node_stride +
-          head * a.out_head_stride + lane * 2;
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    *reinterpret_cast<uint32_t*>(to + e * 64) = pack2<T>(o[e].x * inv, o[e].y * inv);
-  if (lane == 0 && a.lse) a.lse[row] = (m + log2f(l)) * 0.6931471805599453f;
-}
 
 // ---- set-up ---------------------------------------------------------------------------
 bool view_ok(const void* ptr, std::initializer_list<int64_t> strides) {
@@ -129,7 +36,7 @@ ssd_status check(const ssd_tree_attn* a) {
   // tables of no columns may have no address
   if ((!a->tables && a->cols > 0) || !a->lens || a->table_stride < a->cols)
     return SSD_ERR_INVALID_ARG;
-  if ((a->D != 64 && a->D != 128 && a->D != 256) || a->N > kMaxNodes) return SSD_ERR_UNSUPPORTED;
+  if ((a->D != 64 && a->D != 128 && a->D != 256) || a->N > kTreeNodes) return SSD_ERR_UNSUPPORTED;
   if (a->parent)
     for (int u = 0; u < a->N; ++u)
       if (a->parent[u] >= u || a->parent[u] < (u > 0 ? 0 : -1)) return SSD_ERR_INVALID_ARG;
@@ -138,15 +45,64 @@ ssd_status check(const ssd_tree_attn* a) {
   return SSD_OK;
 }
 
-template <typename T>
-cudaError_t launch(const TreeAttnParams& p, cudaStream_t s) {
-  const unsigned grid = (unsigned)((p.rows + kWarps - 1) / kWarps);
-  switch (p.a.D) {
-    case 64: tree_kernel<T, 64><<<grid, kWarps * 32, 0, s>>>(p); break;
-    case 128: tree_kernel<T, 128><<<grid, kWarps * 32, 0, s>>>(p); break;
-    default: tree_kernel<T, 256><<<grid, kWarps * 32, 0, s>>>(p); break;
+struct Layout {
+  size_t po, pml, begun, last, total;
+};
+
+// The division of the work and the workspace of a call; false when its work is beyond
+// 32-bit counts.
+bool plan(const ssd_tree_attn& a, TreeAttnParams& p, Layout& L) {
+  const int sms = std::max(num_sms(), 1), tile = tree_tile(a.D);
+  p.a = a;
+  p.a.parent = nullptr;                // of the host
+  p.gqa = a.Hq / a.Hkv;
+  p.by_page = divisor(a.page_size);
+  p.by_gqa = divisor(p.gqa);
+  p.pairs = a.N * p.gqa;
+  const int rows = 128 * tree_blocks(a.D, p.pairs);
+  p.blocks = (p.pairs + rows - 1) / rows;
+  p.join_groups = (std::min(p.pairs, rows) + 7) / 8;
+  // -q for a negative scale, 0 for none: the maximum is taken before the scale
+  p.scale_log2 = (float)(std::fabs((double)a.scale) * 1.4426950408889634);
+  p.q_and = ~0u;
+  p.q_xor = 0u;
+  if (p.scale_log2 == 0.f) {
+    p.scale_log2 = 1.f;
+    p.q_and = 0u;
+  } else if (a.scale < 0.f) {
+    p.q_xor = 0x80008000u;
   }
-  return cudaGetLastError();
+  p.q_plain = a.scale > 0.f && p.q_and != 0u;
+  // sets of up to eight heads where a token's heads lie closer than its neighbour
+  p.hg = 1;
+  if (a.k_cache.head_stride < a.k_cache.token_stride &&
+      a.v_cache.head_stride < a.v_cache.token_stride)
+    for (int n = 2; n <= std::min(8, sms); ++n)
+      if (a.Hkv % n == 0) p.hg = n;
+  p.sets = a.Hkv / p.hg;
+  p.workers = sms / p.hg;
+  const int64_t items = (int64_t)a.B * p.sets * p.blocks;
+  const int64_t tiles = ((int64_t)a.cols * a.page_size + tile - 1) / tile + (a.N + tile - 1) / tile;
+  if (items * p.hg > 0x7fffffff || items > 0x7fffffff / (tiles + 1)) return false;
+  // boxes have to tile a page and a tile alike, and lie on the copy's grid
+  p.boxes = a.page_size % 8 == 0 && (tile % a.page_size == 0 || a.page_size % tile == 0) &&
+            box_strides(a.k_cache, a.Hkv, a.page_size, a.num_pages) &&
+            box_strides(a.v_cache, a.Hkv, a.page_size, a.num_pages) &&
+            box_strides(a.k, a.Hkv, a.N, a.B) && box_strides(a.v, a.Hkv, a.N, a.B);
+  p.node_rows = std::min(tile, (a.N + 7) / 8 * 8);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align256(bytes);
+    return here;
+  };
+  const size_t ctas = (size_t)p.workers * p.hg;
+  L.po = take(2 * ctas * rows * a.D * 4);
+  L.pml = take(2 * ctas * rows * 8);
+  L.begun = take(ctas * 4);
+  L.last = take((size_t)items * p.hg * 4);
+  L.total = at;
+  return true;
 }
 
 }  // namespace
@@ -157,7 +113,9 @@ using namespace ssd;
 extern "C" {
 
 size_t ssd_tree_attention_workspace_size(const ssd_tree_attn* a) {
-  return check(a) == SSD_OK ? 256 : 0;
+  TreeAttnParams p{};
+  Layout L;
+  return check(a) == SSD_OK && plan(*a, p, L) ? L.total : 0;
 }
 
 ssd_status ssd_tree_attention(const ssd_tree_attn* a, void* workspace, size_t workspace_bytes,
@@ -172,19 +130,25 @@ ssd_status ssd_tree_attention(const ssd_tree_attn* a, void* workspace, size_t wo
       (a->out_seq_stride != a->q_seq_stride || a->out_node_stride != a->q_node_stride ||
        a->out_head_stride != a->q_head_stride))
     return SSD_ERR_INVALID_ARG;
-  if (!workspace || (uintptr_t)workspace % 256 != 0 || workspace_bytes < 256)
-    return SSD_ERR_WORKSPACE;
   TreeAttnParams p{};
-  p.a = *a;
-  p.gqa = a->Hq / a->Hkv;
-  p.by_page = divisor(a->page_size);
-  p.scale_log2 = (float)((double)a->scale * 1.4426950408889634);
-  p.rows = (int64_t)a->B * a->N * a->Hq;
+  Layout L;
+  if (!plan(*a, p, L)) return SSD_ERR_UNSUPPORTED;
+  if (!workspace || (uintptr_t)workspace % 256 != 0 || workspace_bytes < L.total)
+    return SSD_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  p.po = reinterpret_cast<float*>(ws + L.po);
+  p.pml = reinterpret_cast<float2*>(ws + L.pml);
+  p.begun = reinterpret_cast<int*>(ws + L.begun);
+  p.last = reinterpret_cast<int*>(ws + L.last);
   p.status = dev_status;
-  for (int u = 0; u < a->N; ++u) p.parent[u] = (int16_t)(a->parent ? a->parent[u] : u - 1);
-  const cudaError_t e = a->dtype == SSD_BF16
-                            ? launch<__nv_bfloat16>(p, static_cast<cudaStream_t>(stream))
-                            : launch<__half>(p, static_cast<cudaStream_t>(stream));
+  p.chain = 1;
+  for (int u = 1; u < a->N; ++u) {
+    const int par = a->parent ? a->parent[u] : u - 1;
+    p.parent[u] = (uint8_t)par;
+    p.chain &= par == u - 1;
+  }
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = a->dtype == SSD_BF16 ? launch_tree_bf16(p, s) : launch_tree_f16(p, s);
   if (e == cudaSuccess) return SSD_OK;
   cudaGetLastError();
   return SSD_ERR_CUDA;

@@ -1,0 +1,917 @@
+// ssd_tree_attention_kernel.cuh -- attention of drafted nodes over a paged cache and
+// the nodes on their paths, on the 5th-generation tensor cores.
+//
+// A block is 128 (node, head) pairs of one sequence and key/value head, a tile kTile
+// tokens: of the cache, and after those of the sequence's nodes, where each pair's
+// weights of nodes off its path are zero.  S = Q K^T, P = exp2(S * scale - m), O += P V,
+// out = O / sum P.  An item is a sequence's key/value head and one or two blocks, and
+// costs a unit for its start and end and one for each tile; the units of all items, in
+// order, are divided evenly among the workers, so every worker has the same share
+// however the lengths differ.  An item that one worker does alone is written
+// out by it; of the others every stretch leaves a partial (unnormalised sums, their
+// largest score and weight), which the join puts together.  A worker has two such
+// stretches at most, one that goes on with an item and one that begins one, so
+// partials have places by the CTA.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "ssd_attention_dev.cuh"
+#include "ssd_tc_dev.cuh"
+#include "ssd_tree_attention.cuh"
+
+namespace ssd {
+namespace {
+
+constexpr int kRows = 128;                // pairs of a block (M)
+constexpr int kSoftmax = 256;             // threads of the two warpgroups
+constexpr int kHeaderBytes = 3 << 10;     // of shared memory before the rings
+constexpr int kTreeThreads = kSoftmax + 128;  // a third warpgroup: copies and products
+constexpr int kCopyK = 8, kCopyV = 9, kMmaWarp = 10, kQueryWarp = 11;
+// Registers per thread: launched with 168 (12 warps), of which the third warpgroup
+// gives up 80 and the others take 40 each: 8 * 208 + 4 * 88 = 12 * 168.
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+constexpr float kRise = 8.f;              // scores may pass the kept maximum by this (base 2)
+
+// BLOCKS: of an item.  The rings and the queries take 224 KB, one CTA per SM.
+template <int D, int BLOCKS> struct TreeShape {
+  static constexpr int kTile = tree_tile(D);
+  static constexpr int kPanels = D / 64;
+  static constexpr int kPanel = kTile * 128;          // kTile rows x 64 elements, swizzled
+  static constexpr int kSlot = kPanels * kPanel;      // K or V of a tile
+  static constexpr int kQueryPanel = kRows * 128;
+  static constexpr int kQueries = kPanels * kQueryPanel;  // of a block
+  static constexpr int kSlotsK = D == 64 ? 6 : 3;
+  static constexpr int kSlotsV = D == 64 ? 6 : D == 128 && BLOCKS == 1 ? 3 : 2;
+  static constexpr int kSmem = kHeaderBytes + (kSlotsK + kSlotsV) * kSlot + BLOCKS * kQueries;
+  static_assert(kSmem <= 227 << 10, "shared memory");
+  // How the two warpgroups of exponentials share the work:
+  //   tiles   the even and the odd tiles of a block, each with sums of its own;
+  //   blocks  a block each, of every tile;
+  //   one     the first does all: the sums (256 columns) have room for one stream.
+  static constexpr bool kByBlocks = BLOCKS == 2;
+  static constexpr bool kOne = D == 256;
+  static constexpr bool kByTiles = !kByBlocks && !kOne;
+};
+
+// tensor memory columns: scores (and weights) of two streams or tiles, their sums
+constexpr int kColS = 0, kColO = 256, kColStep = 128;
+
+// What the product and exponential warps know of a stretch.
+struct TreeJob {
+  int tiles;        // 0: no more
+  int cached;       // of them, of the cache (may be negative or more than tiles)
+  int tokens;       // of the cache from the first tile on
+  int seq, head, pair0, pairs;  // sequence, key/value head, the item's pairs
+  int slot;         // of the partial; -1: the item is done here
+};
+
+struct TreeHeader {
+  float2 ml[2][kRows];              // the streams' maxima and weights, handed over at the end
+  uint64_t k_full[6], k_empty[6];   // ring slots
+  uint64_t v_full[6], v_empty[6];
+  uint64_t q_full, q_empty;         // a stretch's job and queries; its scores are all done
+  uint64_t job_read;                // its job is known to the exponentials' threads
+  uint64_t s_full[2];               // scores of a tile are there
+  uint64_t p_full[2];               // its weights are
+  uint64_t o_done[2];               // its part of the sums is (by stream, block or parity)
+  uint64_t ml_full;                 // both streams' maxima and weights are in place
+  uint64_t o_empty;                 // the sums of a stretch have been read
+  uint64_t drained;
+  TreeJob job[2];                   // by the parity of the stretch
+  int2 warp_sums[kTreeThreads / 32];
+  TreeStart start;
+  uint32_t tmem;
+  volatile int err;
+  volatile int odd[2];              // 1 + the last stretch with values that are no numbers
+  uint8_t parent[kTreeNodes];
+};
+static_assert(sizeof(TreeHeader) <= kHeaderBytes, "header");
+
+// Whether a wait of the CTA ran out (to every lane of a warp alike): no new
+// work is begun then.
+__device__ __forceinline__ bool gave_up(const TreeHeader& sh) {
+  return __any_sync(0xffffffffu, sh.err) != 0;
+}
+
+// Whether one of two 16-bit numbers is infinite or NaN: which, as masks.
+template <typename T>
+__device__ __forceinline__ uint32_t odd_mask(uint32_t x) {
+  constexpr uint32_t e = __is_same(T, __half) ? 0x7c00u : 0x7f80u;
+  return ((x & e) == e ? 0xffffu : 0u) | ((x & e << 16) == e << 16 ? 0xffff0000u : 0u);
+}
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+
+template <typename T, int D, int BLOCKS>
+__global__ void __launch_bounds__(kTreeThreads, 1)
+    tree_tc_kernel(const __grid_constant__ TreeAttnParams p, const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap,
+                   const __grid_constant__ CUtensorMap knodes,
+                   const __grid_constant__ CUtensorMap vnodes) {
+  using S = TreeShape<D, BLOCKS>;
+  constexpr int kTile = S::kTile;
+  extern __shared__ __align__(1024) unsigned char s_raw[];
+  TreeHeader& sh = *reinterpret_cast<TreeHeader*>(s_raw);
+  const ssd_tree_attn& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t kring = smem_addr(s_raw) + kHeaderBytes;
+  const uint32_t vring = kring + S::kSlotsK * S::kSlot;
+  const uint32_t qs = vring + S::kSlotsV * S::kSlot;
+
+  start_next();
+  if (warp == kMmaWarp) tmem_alloc(&sh.tmem);
+  if (tid == 0) {
+    sh.err = 0;
+    sh.odd[0] = sh.odd[1] = 0;
+    // a tile by boxes: one arrival and its bytes; by copies of the lanes: theirs
+    const int copies = p.boxes ? 1 : 32;
+    for (int i = 0; i < S::kSlotsK; ++i) {
+      mbar_init(&sh.k_full[i], copies);
+      mbar_init(&sh.k_empty[i], 1);
+    }
+    for (int i = 0; i < S::kSlotsV; ++i) {
+      mbar_init(&sh.v_full[i], copies);
+      mbar_init(&sh.v_empty[i], 1);
+    }
+    mbar_init(&sh.q_full, 32);
+    mbar_init(&sh.q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], kRows);
+      mbar_init(&sh.o_done[i], 1);
+    }
+    mbar_init(&sh.job_read, kSoftmax);
+    mbar_init(&sh.ml_full, kSoftmax);
+    mbar_init(&sh.o_empty, kSoftmax);
+    mbar_init(&sh.drained, 1);
+    fence_barrier_init();
+  }
+  if (tid < a.N) sh.parent[tid] = p.parent[tid];
+  const int w = blockIdx.x / p.hg;
+  const TreeSplit all = tree_starts<kTreeThreads>(p, w, &sh.start, sh.warp_sums);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  // the third warpgroup's warps walk the stretches by themselves
+  TreeWalk k;
+  k.u = all.first(w);
+  k.u1 = all.first(w + 1);
+  k.w = w;
+  k.hh = blockIdx.x - w * p.hg;
+  if (k.u < k.u1) {
+    k.b = sh.start.b;
+    k.unit = sh.start.unit;
+  }
+  TreeStretch s;
+
+  if (warp >= kSoftmax / 32) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == kCopyK || warp == kCopyV) {
+      // ---- copies: a warp for K and one for V ---------------------------------------------
+      const bool v = warp == kCopyV;
+      uint64_t* full = v ? sh.v_full : sh.k_full;
+      uint64_t* empty = v ? sh.v_empty : sh.k_empty;
+      const uint32_t slots = v ? vring : kring;
+      const int nslots = v ? S::kSlotsV : S::kSlotsK;
+      const int P = a.page_size;
+      uint32_t slot = 0, use = 0;                // of the next tile: its slot, turns of the ring
+      auto next_slot = [&] {
+        if (++slot == (uint32_t)nslots) {
+          slot = 0;
+          ++use;
+        }
+      };
+      if (p.boxes) {
+        // a lane per page of a tile: a box of its tokens and 64 dimensions
+        const int rows = min(P, kTile);          // tokens of a box
+        const int boxes = kTile / rows;          // boxes of a whole tile, at most 16
+        // Tokens that one block reads are not read again: they leave L2 first.
+        uint64_t once, again;
+        asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+        asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(again));
+        const uint64_t policy = p.blocks == 1 ? once : again;
+        while (next_stretch(p, k, s)) {
+          const int32_t* table = a.tables + (int64_t)s.b * a.table_stride;
+          auto page_at = [&](int tile) {  // not looked at here: the load stays in flight
+            const int t = tile * kTile + lane * rows;
+            return lane < boxes && tile < s.tile1 && t < s.q.len ? table[p.by_page.quotient(t)]
+                                                                 : 0;
+          };
+          // pages are looked up two tiles ahead of their copies
+          int page = page_at(s.tile0), next = page_at(s.tile0 + 1);
+          for (int tile = s.tile0; tile < s.tile1; ++tile) {
+            if (gave_up(sh)) {
+              k.u = k.u1;
+              break;
+            }
+            const int after = page_at(tile + 2);
+            if (use > 0) mbar_wait(&empty[slot], (use - 1) & 1, &sh.err, p.status);
+            const uint32_t dst = slots + slot * S::kSlot;
+            if (tile < s.q.cached) {
+              if ((unsigned)page >= (unsigned)a.num_pages) {
+                flag_bits(p, SSD_DEV_BAD_PAGE);
+                page = a.num_pages;              // past the end: the box is zeros
+              }
+              const int here = min(kTile, s.q.len - tile * kTile);
+              const int n = (here + rows - 1) / rows;  // boxes with tokens
+              const int in_page = boxes == 1 ? tile * kTile % P : 0;
+              if (lane == 0)
+                mbar_arrive_expect_tx(&full[slot], (uint32_t)(n * rows * 128 * S::kPanels));
+              __syncwarp();
+              if (lane < n) {
+#pragma unroll
+                for (int d = 0; d < S::kPanels; ++d)
+                  tma_box(dst + lane * rows * 128 + d * S::kPanel, v ? &vmap : &kmap, d * 64, s.h,
+                          in_page, page, &full[slot], policy);
+              }
+            } else {
+              if (lane == 0)
+                mbar_arrive_expect_tx(&full[slot], (uint32_t)(p.node_rows * 128 * S::kPanels));
+              __syncwarp();
+              if (lane < S::kPanels)
+                tma_box(dst + lane * S::kPanel, v ? &vnodes : &knodes, lane * 64, s.h,
+                        (tile - s.q.cached) * kTile, s.b, &full[slot], again);
+            }
+            next_slot();
+            page = next;
+            next = after;
+          }
+        }
+        if (sh.err) {  // let the copies in flight land before the memory is given up
+          for (int i = 0; i < nslots; ++i) {
+            const uint32_t turns = use + ((uint32_t)i < slot ? 1 : 0);
+            int none = 0;
+            if (turns > 0) mbar_wait(&full[i], (turns - 1) & 1, &none, nullptr);
+          }
+        }
+      } else {
+        // any pages and strides: 16 bytes a lane at a time, the tokens' places dealt to the lanes
+        constexpr int kLanes = D / 8;            // lanes of a token
+        constexpr int kGroups = kTile / 32;
+        const ssd_paged& cache = v ? a.v_cache : a.k_cache;
+        const ssd_paged& nodes = v ? a.v : a.k;
+        uint32_t told = 0, told_slot = 0, issued = 0;  // tiles whose arrival is told, begun
+        auto tell = [&] {
+          fence_async();
+          mbar_arrive(&full[told_slot]);
+          if (++told_slot == (uint32_t)nslots) told_slot = 0;
+          ++told;
+        };
+        auto flush = [&] {
+          copies_wait<0>();
+          while (told != issued) tell();
+        };
+        while (next_stretch(p, k, s)) {
+          const int32_t* table = a.tables + (int64_t)s.b * a.table_stride;
+          int page[kGroups];
+          auto pages_of = [&](int tile) {
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+              const int t = tile * kTile + g * 32 + lane;
+              page[g] = tile < s.q.cached && t < s.q.len ? table[p.by_page.quotient(t)] : 0;
+            }
+          };
+          pages_of(s.tile0);
+          for (int tile = s.tile0; tile < s.tile1; ++tile) {
+            if (gave_up(sh)) {
+              k.u = k.u1;
+              break;
+            }
+            const bool old = tile < s.q.cached;
+            const int first = (old ? tile : tile - s.q.cached) * kTile;
+            const int here = min(kTile, (old ? s.q.len : a.N) - first);
+            int64_t at[kGroups];                 // of the tokens; negative: zeros
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+              const int r = g * 32 + lane, t = first + r;
+              at[g] = -1;
+              if (r < here) {
+                if (!old) {
+                  at[g] = s.b * nodes.page_stride + t * nodes.token_stride;
+                } else if ((unsigned)page[g] < (unsigned)a.num_pages) {
+                  at[g] = page[g] * cache.page_stride +
+                          (t - p.by_page.quotient(t) * P) * cache.token_stride;
+                } else {
+                  flag_bits(p, SSD_DEV_BAD_PAGE);
+                }
+              }
+            }
+            pages_of(tile + 1);
+            const T* from = static_cast<const T*>(old ? cache.ptr : nodes.ptr) +
+                            s.h * (old ? cache.head_stride : nodes.head_stride) + lane % kLanes * 8;
+            if (use > 0 && !__all_sync(0xffffffffu, mbar_try_wait(&empty[slot], (use - 1) & 1))) {
+              flush();                           // what is waited for may need it
+              mbar_wait(&empty[slot], (use - 1) & 1, &sh.err, p.status);
+            }
+            __syncwarp();
+            const int ch = lane % kLanes;
+            const uint32_t dst = slots + slot * S::kSlot + (ch / 8) * S::kPanel;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+              if (g * 32 >= here) break;
+#pragma unroll 8
+              for (int i = 0; i < kLanes; ++i) {
+                const int r = i * (32 / kLanes) + lane / kLanes;  // of the group
+                const int64_t x = __shfl_sync(0xffffffffu, at[g], r);
+                const int row = g * 32 + r;
+                if (row < here)
+                  copy16(dst + row * 128 + (((ch & 7) ^ (row & 7)) << 4), from + (x < 0 ? 0 : x),
+                         x >= 0);
+              }
+            }
+            copies_commit();
+            ++issued;
+            next_slot();
+            if (issued - told == 2) {            // the one before has had its time
+              copies_wait<1>();
+              tell();
+            }
+          }
+        }
+        flush();
+      }
+    } else if (warp == kQueryWarp) {
+      // ---- queries: a stretch's, as soon as the scores of the one before are done ------
+      uint32_t i = 0;
+      if (lane == 0) p.begun[blockIdx.x] = -1;
+      while (next_stretch(p, k, s)) {
+        const int pair0 = s.mb * BLOCKS * kRows, pairs = min(BLOCKS * kRows, p.pairs - pair0);
+        auto query = [&](const TreeStretch& z, int row) {
+          const int pair = z.mb * BLOCKS * kRows + row, node = p.by_gqa.quotient(pair);
+          return static_cast<const T*>(a.q) + z.b * a.q_seq_stride + node * a.q_node_stride +
+                 (int64_t)(z.h * p.gqa + pair - node * p.gqa) * a.q_head_stride;
+        };
+        if (i > 0) mbar_wait(&sh.q_empty, (i - 1) & 1, &sh.err, p.status);
+        constexpr int kLanes = D / 8;            // lanes of a row, 16 bytes each
+        // rows past the last pair hold whatever was there: a row's scores are its own
+#pragma unroll 4
+        for (int r0 = 0; r0 < pairs; r0 += 32 / kLanes) {
+          const int row = r0 + lane / kLanes, ch = lane % kLanes;
+          if (row < pairs) {
+            const uint32_t dst = qs + (row / kRows) * S::kQueries + (ch / 8) * S::kQueryPanel +
+                                 (row % kRows) * 128 + (((ch & 7) ^ (row & 7)) << 4);
+            const T* from = query(s, row) + ch * 8;
+            if (p.q_plain) {
+              copy16(dst, from, true);
+            } else {                             // a scale that is not positive: -q, or 0
+              const uint4 x = *reinterpret_cast<const uint4*>(from);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst),
+                           "r"((x.x & p.q_and) ^ p.q_xor), "r"((x.y & p.q_and) ^ p.q_xor),
+                           "r"((x.z & p.q_and) ^ p.q_xor), "r"((x.w & p.q_and) ^ p.q_xor)
+                           : "memory");
+            }
+          }
+        }
+        // a thread that waits for the last job must not find two newer ones: a
+        // barrier tells only the parity of its phase
+        if (i > 0) mbar_wait(&sh.job_read, (i - 1) & 1, &sh.err, p.status);
+        if (lane == 0)
+          sh.job[i & 1] = TreeJob{s.tile1 - s.tile0, s.q.cached - s.tile0,
+                                  s.q.len - s.tile0 * kTile, s.b, s.h, pair0, pairs, s.slot};
+        copies_commit();
+        copies_wait<0>();
+        fence_async();
+        mbar_arrive(&sh.q_full);  // 32 arrivals: lane 0's follows the job
+        ++i;
+        if (lane == 0 && s.slot >= 0) {
+          // the join goes by the worker that began the item, and by its last one
+          if (s.tile0 == 0) p.begun[blockIdx.x] = s.item;
+          if (s.tile1 == s.q.tiles) p.last[s.item] = w;
+        }
+        // the next ones into L2 meanwhile
+        TreeWalk k1 = k;
+        TreeStretch s1;
+        if (next_stretch(p, k1, s1)) {
+          const int n = min(BLOCKS * kRows, p.pairs - s1.mb * BLOCKS * kRows);
+          for (int row = lane; row < n; row += 32)
+#pragma unroll
+            for (int d = 0; d < D; d += 64)
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(query(s1, row) + d));
+        }
+      }
+      if (i > 0) {
+        mbar_wait(&sh.q_empty, (i - 1) & 1, &sh.err, p.status);
+        mbar_wait(&sh.job_read, (i - 1) & 1, &sh.err, p.status);
+      }
+      if (lane == 0) sh.job[i & 1].tiles = 0;
+      __syncwarp();
+      mbar_arrive(&sh.q_full);
+    } else {
+      // ---- products: the warp runs in step, one elected thread issues ------------------
+      constexpr uint32_t score = product<T>(kTile, false), sum = product<T>(D, true);
+      uint32_t ks = 0, k_use = 0, vs = 0, v_use = 0;  // ring slots and turns
+      uint32_t c = 0, c1 = 0;                    // tiles so far; of the second block
+      auto scores = [&](int block, uint32_t col) {
+        const uint64_t q_op = operand(qs + block * S::kQueries, 16);
+        const uint64_t k_op = operand(kring + ks * S::kSlot, 16);
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e)
+          mma_ss(tmem + kColS + col * kColStep,
+                 q_op + (((e / 4) * S::kQueryPanel + (e % 4) * 32) >> 4),
+                 k_op + (((e / 4) * S::kPanel + (e % 4) * 32) >> 4), score, e > 0);
+      };
+      auto sums = [&](uint32_t weights, uint32_t col, bool add) {
+        const uint64_t v_op = operand(vring + vs * S::kSlot, S::kPanel);
+#pragma unroll
+        for (int e = 0; e < kTile / 16; ++e)
+          mma_ts(tmem + kColO + col * kColStep, tmem + kColS + weights * kColStep + e * 8,
+                 v_op + ((e * 16 * 128) >> 4), sum, add || e > 0);
+      };
+      auto turn = [](uint32_t& slot, uint32_t& use, int n) {
+        if (++slot == (uint32_t)n) {
+          slot = 0;
+          ++use;
+        }
+      };
+      for (uint32_t i = 0;; ++i) {
+        mbar_wait(&sh.q_full, i & 1, &sh.err, p.status);
+        const int n = gave_up(sh) ? 0 : sh.job[i & 1].tiles;
+        if (n == 0) break;
+        const bool two = S::kByBlocks && sh.job[i & 1].pairs > kRows;
+        fence_after();
+        for (int j = 0; j <= n; ++j) {
+          if constexpr (S::kByBlocks) {
+            // a block's weights, then its next scores in their place
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (x == 1 && !two) break;
+              const uint32_t t = (x == 0 ? c : c1) + j;
+              const bool end = x == 1 || !two;
+              if (j > 0) {
+                if (x == 0 && j == 1 && i > 0)
+                  mbar_wait(&sh.o_empty, (i - 1) & 1, &sh.err, p.status);
+                mbar_wait(&sh.p_full[x], (t - 1) & 1, &sh.err, p.status);
+                if (x == 0) mbar_wait(&sh.v_full[vs], v_use & 1, &sh.err, p.status);
+                fence_after();
+                if (elected()) {
+                  sums(x, x, j > 1);
+                  commit(&sh.o_done[x]);
+                  if (end) commit(&sh.v_empty[vs]);
+                }
+                __syncwarp();
+                if (end) turn(vs, v_use, S::kSlotsV);
+              }
+              if (j < n) {
+                if (x == 0) mbar_wait(&sh.k_full[ks], k_use & 1, &sh.err, p.status);
+                fence_after();
+                if (elected()) {
+                  scores(x, x);
+                  commit(&sh.s_full[x]);
+                  if (end) commit(&sh.k_empty[ks]);
+                  if (end && j == n - 1) commit(&sh.q_empty);
+                }
+                __syncwarp();
+                if (end) turn(ks, k_use, S::kSlotsK);
+              }
+            }
+          } else {
+            if (j < n) {
+              const uint32_t t = c + j;
+              mbar_wait(&sh.k_full[ks], k_use & 1, &sh.err, p.status);
+              fence_after();
+              if (elected()) {
+                scores(0, t & 1);
+                commit(&sh.s_full[t & 1]);
+                commit(&sh.k_empty[ks]);
+                if (j == n - 1) commit(&sh.q_empty);
+              }
+              __syncwarp();
+              turn(ks, k_use, S::kSlotsK);
+            }
+            if (j > 0) {
+              const uint32_t t = c + j - 1, b = t & 1, o = S::kOne ? 0 : b;
+              if (j == 1 && i > 0) mbar_wait(&sh.o_empty, (i - 1) & 1, &sh.err, p.status);
+              mbar_wait(&sh.p_full[b], t >> 1 & 1, &sh.err, p.status);
+              mbar_wait(&sh.v_full[vs], v_use & 1, &sh.err, p.status);
+              fence_after();
+              if (elected()) {
+                sums(b, o, j > (S::kOne ? 1 : 2));
+                commit(&sh.v_empty[vs]);
+                commit(&sh.o_done[b]);
+              }
+              __syncwarp();
+              turn(vs, v_use, S::kSlotsV);
+            }
+          }
+        }
+        c += n;
+        if (two) c1 += n;
+      }
+      if (elected()) commit(&sh.drained);
+      __syncwarp();
+      int none = 0;
+      mbar_wait(&sh.drained, 0, &none, p.status);
+    }
+  } else {
+    // ---- exponentials: warpgroup b, a pair per thread ---------------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const uint32_t b = warp >> 2, m = tid & (kRows - 1);
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
+    const uint32_t acc = S::kOne ? 0 : b;        // its sums
+    const uint32_t to = tmem + lanes + kColO + acc * kColStep;
+    uint32_t c = 0;                              // tiles before the stretch (its block's)
+    uint32_t sees[kTreeNodes / 32];              // nodes on its node's path
+    int seen = -1;                               // its node
+    // V of tile j of the stretch: the ring's slot and turn at the first tile
+    uint32_t v_slot = 0, v_use = 0;
+    for (uint32_t i = 0;; ++i) {
+      mbar_wait(&sh.q_full, i & 1, &sh.err, p.status);
+      const TreeJob job = sh.job[i & 1];
+      const int n = gave_up(sh) ? 0 : job.tiles;
+      mbar_arrive(&sh.job_read);
+      if (n == 0) break;
+      // its tiles: j0, j0 + step, ..
+      const int step = S::kByTiles ? 2 : 1;
+      const int j0 = S::kByTiles ? (int)((b ^ c) & 1) : S::kOne ? (b == 0 ? 0 : n)
+                                 : (b == 0 || job.pairs > kRows ? 0 : n);
+      const int row = (S::kByBlocks ? (int)b * kRows : 0) + (int)m;  // of the item's pairs
+      const bool mine = row < job.pairs;
+      const bool busy = __any_sync(0xffffffffu, mine);
+      if (job.cached < n) {                      // nodes come
+        const int u = p.by_gqa.quotient(job.pair0 + min(row, job.pairs - 1));
+        if (u != seen) {
+          seen = u;
+#pragma unroll
+          for (int x = 0; x < kTreeNodes / 32; ++x)
+            sees[x] = !p.chain ? 0u : u >= x * 32 + 31 ? ~0u : u < x * 32 ? 0u
+                                                                      : (2u << (u & 31)) - 1;
+          if (!p.chain) {
+            for (int v = u;; v = sh.parent[v]) {
+#pragma unroll
+              for (int x = 0; x < kTreeNodes / 32; ++x)
+                if (v >> 5 == x) sees[x] |= 1u << (v & 31);
+              if (v == 0) break;
+            }
+          }
+        }
+      }
+
+      float top = -INFINITY, l = 0.f;
+      for (int j = j0; j < n; j += step) {
+        const uint32_t t = c + j;
+        // where its scores are, and the parity of their turn
+        const uint32_t buf = S::kByBlocks ? b : t & 1;
+        const uint32_t turn = (S::kByBlocks ? t : t >> 1) & 1;
+        const uint32_t ts = tmem + lanes + kColS + buf * kColStep;
+        mbar_wait(&sh.s_full[buf], turn, &sh.err, p.status);
+        __syncwarp();
+        fence_after();
+        const bool nodes = j >= job.cached;
+        const int at = nodes ? (j - job.cached) * kTile : j * kTile;
+        const int here = min(kTile, (nodes ? a.N : job.tokens) - at);
+        if (busy) {
+          uint32_t x[kTile / 32][32];
+#pragma unroll
+          for (int q = 0; q < kTile / 32; ++q) tmem_ld32(x[q], ts + q * 32);
+          tmem_wait_ld();
+          if (nodes || here < kTile) {
+#pragma unroll
+            for (int q = 0; q < kTile / 32; ++q) {
+              uint32_t ok = here >= q * 32 + 32 ? ~0u : here <= q * 32 ? 0u : (1u << (here & 31)) - 1;
+              if (nodes) {
+#pragma unroll
+                for (int y = 0; y < kTreeNodes / kTile; ++y)
+                  if (at == y * kTile) ok &= sees[y * (kTile / 32) + q];
+              }
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(ok & 1u << e)) x[q][e] = 0xff800000u;  // -inf
+            }
+          }
+          float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < kTile / 32; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              t0 = fmaxf(t0, __uint_as_float(x[q][e]));
+              t1 = fmaxf(t1, __uint_as_float(x[q][e + 1]));
+            }
+          const float now = fmaxf(t0, t1) * p.scale_log2;
+          // the kept maximum moves when a score passes it by 2^kRise
+          const bool move = now > top + kRise;
+          const float old = top;
+          if (move) top = now;
+          const float off = top == -INFINITY ? 0.f : top;
+          if (j > j0 && __any_sync(0xffffffffu, move)) {
+            const float f = move ? exp2_fast(old - off) : 1.f;
+            l *= f;
+            const uint32_t done = S::kOne ? (t - 1) & 1 : b;  // of the tile before
+            const uint32_t turns = S::kByTiles ? (t >> 1) - 1 : S::kOne ? (t - 1) >> 1 : t - 1;
+            mbar_wait(&sh.o_done[done], turns & 1, &sh.err, p.status);
+            fence_after();
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t y[32];
+              tmem_ld32(y, to + q * 32);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+              tmem_st32(to + q * 32, y);
+            }
+          }
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int q = 0; q < kTile / 32; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float y = exp2_fast(fmaf(__uint_as_float(x[q][e]), p.scale_log2, -off));
+              sum[e & 3] += y;
+              x[q][e] = __float_as_uint(y);
+            }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          // weights in the type of V, as the product takes them: each is off by at most
+          // half a step, which an output averages over its tokens; their sum l is of
+          // the unrounded ones
+#pragma unroll
+          for (int q = 0; q < kTile / 64; ++q) {
+            uint32_t y[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              y[e] = pack2<T>(__uint_as_float(x[2 * q + e / 16][2 * (e % 16)]),
+                              __uint_as_float(x[2 * q + e / 16][2 * (e % 16) + 1]));
+            tmem_st32(ts + q * 32, y);
+          }
+          tmem_wait_st();
+        }
+        if ((nodes || here < kTile) && (!S::kByBlocks || b == 0)) {
+          // Zero weights must not meet what is no number (0 * NaN): rows of V past the
+          // last token are whatever the page or the slot held, and a node's values may be
+          // off the path of others.  Those that are no numbers are put aside, and
+          // added at the end to the nodes below theirs.
+          uint32_t slot = v_slot + (uint32_t)j, use = v_use;
+          use += slot / S::kSlotsV;
+          slot %= S::kSlotsV;
+          mbar_wait(&sh.v_full[slot], use & 1, &sh.err, p.status);
+          const uint32_t vs = vring + slot * S::kSlot;
+          for (int e = here * 8 + (int)m; e < kTile * 8; e += kRows)
+#pragma unroll
+            for (int d = 0; d < S::kPanels; ++d)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vs + d * S::kPanel +
+                                                                           e * 16),
+                           "r"(0)
+                           : "memory");
+          if (nodes) {
+            for (int e = (int)m; e < here * 8; e += kRows)
+#pragma unroll
+              for (int d = 0; d < S::kPanels; ++d) {
+                const uint32_t where = vs + d * S::kPanel + e * 16;
+                uint32_t y[4], bad = 0;
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                             : "r"(where)
+                             : "memory");
+#pragma unroll
+                for (int z = 0; z < 4; ++z) bad |= odd_mask<T>(y[z]);
+                if (bad) {
+                  sh.odd[i & 1] = (int)i + 1;
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(where),
+                               "r"(y[0] & ~odd_mask<T>(y[0])), "r"(y[1] & ~odd_mask<T>(y[1])),
+                               "r"(y[2] & ~odd_mask<T>(y[2])), "r"(y[3] & ~odd_mask<T>(y[3]))
+                               : "memory");
+                }
+              }
+          }
+          fence_async();
+        }
+        fence_before();
+        mbar_arrive(&sh.p_full[buf]);
+      }
+
+      // ---- the stretch's sums: both streams', half of the columns each, or the block's ----
+      const bool mine_has = S::kOne || j0 < n, other_has = S::kByTiles && (j0 ^ 1) < n;
+      if (S::kOne) {
+        // the first warpgroup's last weights are in place before the second waits
+        if (i > 0) mbar_wait(&sh.o_empty, (i - 1) & 1, &sh.err, p.status);
+        if (b == 0) sh.ml[0][m] = make_float2(top, l);
+        mbar_arrive(&sh.ml_full);
+        mbar_wait(&sh.ml_full, i & 1, &sh.err, p.status);
+        mbar_wait(&sh.o_done[(c + n - 1) & 1], (c + n - 1) >> 1 & 1, &sh.err, p.status);
+      } else {
+        if (j0 < n) {
+          const uint32_t last = S::kByTiles ? (c + j0 + ((n - 1 - j0) & ~1)) >> 1 : c + n - 1;
+          mbar_wait(&sh.o_done[b], last & 1, &sh.err, p.status);
+        }
+        if (i > 0) mbar_wait(&sh.o_empty, (i - 1) & 1, &sh.err, p.status);  // ml has been read
+        sh.ml[b][m] = make_float2(top, l);
+        fence_before();
+        mbar_arrive(&sh.ml_full);
+        mbar_wait(&sh.ml_full, i & 1, &sh.err, p.status);
+      }
+      __syncwarp();
+      fence_after();
+      const bool odd = sh.odd[i & 1] == (int)i + 1;
+      float mx, sum, f0, f1 = 0.f;
+      if constexpr (S::kByTiles) {
+        const float2 m0 = sh.ml[b][m], m1 = sh.ml[b ^ 1][m];
+        mx = fmaxf(m0.x, m1.x);
+        const float off = mx == -INFINITY ? 0.f : mx;
+        f0 = exp2_fast(m0.x - off);
+        f1 = exp2_fast(m1.x - off);
+        sum = m0.y * f0 + m1.y * f1;
+      } else {
+        const float2 m0 = sh.ml[S::kOne ? 0 : b][m];
+        mx = m0.x;
+        sum = m0.y;
+        f0 = 1.f;
+      }
+      const int pair = job.pair0 + row, node = p.by_gqa.quotient(pair);
+      const int head = job.head * p.gqa + pair - node * p.gqa;
+      const bool whole = job.slot < 0;
+      if (mine && (S::kByBlocks || b == 0)) {
+        if (!whole)
+          p.pml[(int64_t)job.slot * (BLOCKS * kRows) + row] = make_float2(mx, sum);
+        else if (a.lse)
+          a.lse[((int64_t)job.seq * a.N + node) * a.Hq + head] =
+              (mx + log2f(sum)) * 0.6931471805599453f;
+      }
+      // no token with a score: zeros and -inf
+      const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+      constexpr int kCols = S::kByBlocks ? D : D / 2;  // of this warpgroup
+      const uint32_t first = S::kByBlocks ? 0 : b * kCols;
+      const uint32_t other = tmem + lanes + kColO + (b ^ 1) * kColStep;
+      if (busy && mine_has | other_has) {
+#pragma unroll 1
+        for (int q = 0; q < kCols; q += 32) {
+          const int col = (int)first + q;
+          uint32_t y[32];
+          if (mine_has) tmem_ld32(y, to + col);
+          if constexpr (S::kByTiles) {
+            uint32_t z[32];
+            if (other_has) tmem_ld32(z, other + col);
+            tmem_wait_ld();
+            // the sums of a stream without tiles are whatever the columns held
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              y[e] = __float_as_uint((mine_has ? __uint_as_float(y[e]) * f0 : 0.f) +
+                                     (other_has ? __uint_as_float(z[e]) * f1 : 0.f));
+          } else {
+            tmem_wait_ld();
+          }
+          if (odd && mine) {
+            // values that are no numbers, of the nodes on the path whose tiles were here
+            for (int v = max(0, -job.cached) * kTile; v < min(a.N, (n - job.cached) * kTile); ++v) {
+              uint32_t word = 0;
+#pragma unroll
+              for (int x = 0; x < kTreeNodes / 32; ++x)
+                if (v >> 5 == x) word = sees[x];
+              if (!(word >> (v & 31) & 1)) continue;
+              const T* value = static_cast<const T*>(a.v.ptr) + job.seq * a.v.page_stride +
+                               v * a.v.token_stride + job.head * a.v.head_stride + col;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float z = to_float(value[e]);
+                if (!(fabsf(z) < INFINITY)) y[e] = __float_as_uint(__uint_as_float(y[e]) + z);
+              }
+            }
+          }
+          if (!mine) continue;
+          if (whole) {
+            T* out = static_cast<T*>(a.out) + job.seq * a.out_seq_stride +
+                     node * a.out_node_stride + head * a.out_head_stride + col;
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint32_t z[4];
+#pragma unroll
+              for (int g = 0; g < 4; ++g)
+                z[g] = pack2<T>(__uint_as_float(y[e + 2 * g]) * inv,
+                                __uint_as_float(y[e + 2 * g + 1]) * inv);
+              *reinterpret_cast<uint4*>(out + e) = make_uint4(z[0], z[1], z[2], z[3]);
+            }
+          } else {
+            float* out = p.po + part_at<D>(job.slot, BLOCKS * kRows, row, col);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(out + e * (BLOCKS * kRows)) =
+                  make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+          }
+        }
+      }
+      fence_before();
+      mbar_arrive(&sh.o_empty);
+      if (!S::kByBlocks || b == 0 || job.pairs > kRows) c += n;
+      v_slot += (uint32_t)n;
+      v_use += v_slot / S::kSlotsV;
+      v_slot %= S::kSlotsV;
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    fence_after();
+    tmem_free(tmem);
+  }
+}
+
+// ---- the join -------------------------------------------------------------------------------
+// A CTA per worker's CTA that began an item that others went on with, and eight of the
+// item's pairs; a warp per 32 dimensions, whose lanes read a line of four dimensions of the
+// eight pairs at a time.
+template <typename T, int D, int BLOCKS>
+__global__ void __launch_bounds__(D) tree_join_kernel(const __grid_constant__ TreeAttnParams p) {
+  constexpr int kPairs = BLOCKS * kRows;
+  const ssd_tree_attn& a = p.a;
+  const int cta = blockIdx.x / p.join_groups, group = blockIdx.x - cta * p.join_groups;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  wait_previous();
+  const int item = p.begun[cta];
+  if (item < 0) return;
+  const int w0 = cta / p.hg, hh = cta - w0 * p.hg;
+  const int np = p.last[item] - w0 + 1;
+  const int i = group * 8 + (lane & 7);
+  int rest = item / p.hg;
+  const int mb = rest % p.blocks;
+  rest /= p.blocks;
+  const int h = rest % p.sets * p.hg + hh, seq = rest / p.sets;
+  const int pair = mb * kPairs + i;
+  const bool mine = i < kPairs && pair < p.pairs;
+  const int at = mine ? i : 0;
+  // the partial of the worker that began it, then those of workers that went on
+  auto slot_of = [&](int j) { return 2 * (cta + j * p.hg) + (j == 0); };
+  float top = -INFINITY;
+#pragma unroll 4
+  for (int j = 0; j < np; ++j) top = fmaxf(top, p.pml[(int64_t)slot_of(j) * kPairs + at].x);
+  const float off = top == -INFINITY ? 0.f : top;
+  const int d = warp * 32 + (lane >> 3) * 4;
+  float l = 0.f;
+  float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 4
+  for (int j = 0; j < np; ++j) {
+    const int slot = slot_of(j);
+    const float2 ml = p.pml[(int64_t)slot * kPairs + at];
+    const float f = exp2_fast(ml.x - off);
+    l = fmaf(ml.y, f, l);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float4 x =
+          *reinterpret_cast<const float4*>(p.po + part_at<D>(slot, kPairs, at, d + e * 16));
+      o[e].x = fmaf(x.x, f, o[e].x);
+      o[e].y = fmaf(x.y, f, o[e].y);
+      o[e].z = fmaf(x.z, f, o[e].z);
+      o[e].w = fmaf(x.w, f, o[e].w);
+    }
+  }
+  if (!mine) return;
+  const int node = p.by_gqa.quotient(pair), head = h * p.gqa + pair - node * p.gqa;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  T* out = static_cast<T*>(a.out) + seq * a.out_seq_stride + node * a.out_node_stride +
+           head * a.out_head_stride + d;
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    *reinterpret_cast<uint2*>(out + e * 16) =
+        make_uint2(pack2<T>(o[e].x * inv, o[e].y * inv), pack2<T>(o[e].z * inv, o[e].w * inv));
+  if (d == 0 && a.lse)
+    a.lse[((int64_t)seq * a.N + node) * a.Hq + head] = (top + log2f(l)) * 0.6931471805599453f;
+}
+
+template <typename T, int D, int BLOCKS>
+cudaError_t launch_tree(const TreeAttnParams& p, cudaStream_t s) {
+  constexpr int smem = TreeShape<D, BLOCKS>::kSmem;
+  const auto kernel = tree_tc_kernel<T, D, BLOCKS>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  CUtensorMap km{}, vm{}, kn{}, vn{};
+  const ssd_tree_attn& a = p.a;
+  if (p.boxes) {
+    const int rows = std::min(a.page_size, tree_tile(D));
+    if (!box_map(&km, a.dtype, a.k_cache, D, a.Hkv, a.page_size, a.num_pages, rows) ||
+        !box_map(&vm, a.dtype, a.v_cache, D, a.Hkv, a.page_size, a.num_pages, rows) ||
+        !box_map(&kn, a.dtype, a.k, D, a.Hkv, a.N, a.B, p.node_rows) ||
+        !box_map(&vn, a.dtype, a.v, D, a.Hkv, a.N, a.B, p.node_rows))
+      return cudaErrorInvalidValue;
+  }
+  kernel<<<p.workers * p.hg, kTreeThreads, smem, s>>>(p, km, vm, kn, vn);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)(p.workers * p.hg * p.join_groups));
+  c.blockDim = dim3(D);
+  c.stream = s;
+  c.attrs = &early;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, tree_join_kernel<T, D, BLOCKS>, p);
+}
+
+template <typename T>
+cudaError_t launch_tree_type(const TreeAttnParams& p, cudaStream_t s) {
+  const bool two = tree_blocks(p.a.D, p.pairs) == 2;
+  switch (p.a.D) {
+    case 64: return two ? launch_tree<T, 64, 2>(p, s) : launch_tree<T, 64, 1>(p, s);
+    case 128: return two ? launch_tree<T, 128, 2>(p, s) : launch_tree<T, 128, 1>(p, s);
+    default: return launch_tree<T, 256, 1>(p, s);
+  }
+}
+
+}  // namespace
+}  // namespace ssd
