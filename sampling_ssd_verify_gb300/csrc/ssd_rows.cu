@@ -10,7 +10,7 @@
 #include <cuda_runtime.h>
 #include <limits.h>
 #include <stdint.h>
-
+#include <stdlib.h>
 #include <algorithm>
 
 #include "ssd_attention_dev.cuh"
@@ -30,11 +30,13 @@ struct Geometry {
   Divisor by_token, by_head;
 };
 
-__device__ __forceinline__ const char* plane_of(const ssd_layers& k, const ssd_layers& v,
-                                                const Geometry& g, int j, const ssd_layers** at) {
-  const ssd_layers& x = g.pair && (j & 1) ? v : k;
-  *at = &x;
-  return static_cast<const char*>(x.ptr) + (int64_t)(g.pair ? j >> 1 : j) * x.layer_stride;
+// Keys or values of plane j, and their first byte.
+__device__ __forceinline__ const ssd_layers& side_of(const ssd_layers& k, const ssd_layers& v,
+                                                     const Geometry& g, int j) {
+  return g.pair && (j & 1) ? v : k;
+}
+__device__ __forceinline__ char* plane_of(const ssd_layers& x, const Geometry& g, int j) {
+  return static_cast<char*>(x.ptr) + (int64_t)(g.pair ? j >> 1 : j) * x.layer_stride;
 }
 // Chunk c of a token: its place in the token's bytes.
 __device__ __forceinline__ int64_t chunk_at(const ssd_layers& x, const Geometry& g, int c) {
@@ -47,12 +49,13 @@ __device__ __forceinline__ int64_t chunk_at(const ssd_layers& x, const Geometry&
 struct AppendParams {
   ssd_append a;
   Geometry g;
-  Divisor by_page, by_group;
-  int groups, per;         // groups of planes of a row, planes of a group
+  Divisor by_group;
+  int groups;              // of planes of a row: a warp each
   int64_t warps;
   int32_t* status;
 };
 
+template <int PLANES, int FLIGHT>    // of a warp; 16-byte loads of a lane and plane in flight
 __global__ void __launch_bounds__(kWarps * 32)
     append_kernel(const __grid_constant__ AppendParams p) {
   const ssd_append& a = p.a;
@@ -61,8 +64,8 @@ __global__ void __launch_bounds__(kWarps * 32)
   if (w >= p.warps) return;
   const int t = p.by_group.quotient((int)w), group = (int)w - t * p.groups;
   const int64_t slot = a.slots[t];
-  if (slot < 0) return;
   const int b = a.owner[t];
+  if (slot < 0) return;
   int bad = 0, node = 0;
   if (slot >= (int64_t)a.num_pages * a.page_size) bad |= SSD_DEV_BAD_PAGE;
   if ((unsigned)b >= (unsigned)a.B) {
@@ -77,45 +80,67 @@ __global__ void __launch_bounds__(kWarps * 32)
     if (group == 0 && lane == 0 && p.status) atomicOr(p.status, bad);
     return;
   }
-  const int64_t page = slot / a.page_size, in_page = slot - page * a.page_size;
-  const int j0 = group * p.per, j1 = min(j0 + p.per, p.g.planes);
-  for (int c0 = lane; c0 < p.g.chunks; c0 += 32 * kFlight) {
-    for (int j = j0; j < j1; ++j) {
-      const ssd_layers *from, *to;
-      const char* x = plane_of(a.k, a.v, p.g, j, &from) + b * from->page_stride +
-                      node * from->token_stride;
-      char* y = const_cast<char*>(plane_of(a.k_cache, a.v_cache, p.g, j, &to)) +
-                page * to->page_stride + in_page * to->token_stride;
-      uint4 z[kFlight];
+  const int page = (int)(slot / a.page_size), in_page = (int)(slot - (int64_t)page * a.page_size);
+  const char* from[PLANES];
+  char* to[PLANES];
 #pragma unroll
-      for (int i = 0; i < kFlight; ++i)
-        if (c0 + i * 32 < p.g.chunks)
-          z[i] = __ldcs(reinterpret_cast<const uint4*>(x + chunk_at(*from, p.g, c0 + i * 32)));
-#pragma unroll
-      for (int i = 0; i < kFlight; ++i)
-        if (c0 + i * 32 < p.g.chunks)
-          *reinterpret_cast<uint4*>(y + chunk_at(*to, p.g, c0 + i * 32)) = z[i];
-    }
+  for (int x = 0; x < PLANES; ++x) {
+    const int j = min(group * PLANES + x, p.g.planes - 1);
+    const ssd_layers& k = side_of(a.k, a.v, p.g, j);
+    const ssd_layers& c = side_of(a.k_cache, a.v_cache, p.g, j);
+    from[x] = plane_of(k, p.g, j) + b * k.page_stride + node * k.token_stride;
+    to[x] = plane_of(c, p.g, j) + page * c.page_stride + in_page * c.token_stride;
   }
+  for (int c0 = lane; c0 < p.g.chunks; c0 += 32 * FLIGHT) {
+    uint4 z[PLANES][FLIGHT];
+#pragma unroll
+    for (int x = 0; x < PLANES; ++x)
+#pragma unroll
+      for (int i = 0; i < FLIGHT; ++i)
+        if (c0 + i * 32 < p.g.chunks)
+          z[x][i] = __ldcs(reinterpret_cast<const uint4*>(
+              from[x] + chunk_at(x & 1 && p.g.pair ? a.v : a.k, p.g, c0 + i * 32)));
+#pragma unroll
+    for (int x = 0; x < PLANES; ++x)
+      if (x == 0 || group * PLANES + x < p.g.planes)
+#pragma unroll
+        for (int i = 0; i < FLIGHT; ++i)
+          if (c0 + i * 32 < p.g.chunks)
+            *reinterpret_cast<uint4*>(
+                to[x] + chunk_at(x & 1 && p.g.pair ? a.v_cache : a.k_cache, p.g, c0 + i * 32)) =
+                z[x][i];
+  }
+}
+
+template <int PLANES, int FLIGHT>
+cudaError_t launch_append(AppendParams& p, cudaStream_t s) {
+  p.groups = (p.g.planes + PLANES - 1) / PLANES;
+  p.by_group = divisor(p.groups);
+  p.warps = (int64_t)p.a.rows * p.groups;
+  append_kernel<PLANES, FLIGHT>
+      <<<(unsigned)((p.warps + kWarps - 1) / kWarps), kWarps * 32, 0, s>>>(p);
+  return cudaGetLastError();
 }
 
 // ---- rows of the tables ----------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanCtas = 8;        // of its cluster, at most
 constexpr int kMaxRows = 8192;
 constexpr int kMaxCount = 1 << 30;
 constexpr int kNoHeir = INT_MAX;    // an old row that ends
+constexpr int kBatch = 4;           // pieces of ending rows that a warp has in flight
 constexpr int kTableCols = 256;     // columns of a table row that a warp writes
 constexpr int kGroupBytes = 8192;   // of a last page that a warp copies, about
+__host__ __device__ constexpr int plan_ints(int S, int B) { return 4 * S + 3 * B + 2; }
 
 struct ForkParams {
   ssd_fork f;
   Geometry g;
   Divisor by_page;
-  int clusters;            // CTAs of the plan's cluster
+  int ctas;                // of the plan's cluster
   int group, groups;       // tokens of a warp's copy, such groups of a page
   int* last;               // [num_pages] the last place that gives the page back
-  int* back;               // [S] pages that an old row gives back for good
-  int* freed;              // [num_pages] those pages, in order
   int4* rows;              // [B] what becomes of the new rows
   int4* copies;            // [B] old page, new page, tokens
   int* ncopies;
@@ -123,7 +148,7 @@ struct ForkParams {
 };
 
 // Exclusive sums over n numbers, consecutive ones per thread, by the whole CTA:
-// s_sum[i] for i <= n.
+// s_sum[i] for i <= n.  Ends with a barrier.
 template <typename F>
 __device__ __forceinline__ void running_sums(int* s_sum, int n, int* s_warp, F value) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -139,142 +164,213 @@ __device__ __forceinline__ void running_sums(int* s_sum, int n, int* s_warp, F v
   }
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  int run = x - sum;
-  for (int w = 0; w < warp; ++w) run += s_warp[w];
+  int run = x - sum + __reduce_add_sync(0xffffffffu, lane < warp ? s_warp[lane] : 0);
   for (int i = i0; i < i1; ++i) {
+    const int v = value(i);
     s_sum[i] = run;
-    run += value(i);
+    run += v;
   }
-  if (i1 == n && (i0 < n || tid == 0)) s_sum[n] = run;  // n > 0: its last thread
+  if (i1 == n && i0 < n) s_sum[n] = run;  // the thread of the last
   __syncthreads();
 }
 
-// One cluster: heirs, pages given back, pages taken.  Every CTA finds the heirs
-// and the sums again in its own shared memory; what goes through memory (the
-// counts of shares, the pages given back) is ordered by the cluster's barriers
-// and read from L2.
+// One cluster, or one CTA.  Every CTA finds the heirs, the pages taken and the
+// places of the pages given back again in its own shared memory; only the counts
+// of shares and the last places go through memory.  The tables' rows that end, in
+// order, are cut into pieces of 32 columns and these divided among the warps, so
+// that the pages given back for good have their order by warps and lanes.  It is a
+// chain of loads and barriers, not of bytes: what can be is loaded side by side, and
+// a page goes from the row that gives it back to the row that takes it without a
+// look at the stack.
 __global__ void __launch_bounds__(kPlanThreads, 1)
     fork_plan_kernel(const __grid_constant__ ForkParams p) {
   extern __shared__ int s_mem[];
   const ssd_fork& f = p.f;
   int* s_heir = s_mem;               // [S] lowest new row of an old one, -1: inconsistent
-  int* s_back = s_heir + f.S;        // [S + 1] pages given back before an old row
-  int* s_nth = s_back + f.S + 1;     // [B + 1] pages taken before a new row
-  __shared__ int s_warp[kPlanThreads / 32];
+  int* s_len = s_heir + f.S;         // [S] an old row's tokens
+  int* s_held = s_len + f.S;         // [S] its pages
+  int* s_piece = s_held + f.S;       // [S + 1] pieces of ending rows before it
+  int* s_src = s_piece + f.S + 1;    // [B]
+  int* s_nth = s_src + f.B;          // [B + 1] pages taken before a new row
+  int* s_taker = s_nth + f.B + 1;    // [B] the new row that takes the i-th page
+  __shared__ int s_warp[kPlanWarps], s_count[kPlanWarps], s_total[kPlanCtas];
   const int tid = threadIdx.x, lane = tid & 31;
-  const int rank = (int)cluster_rank();
-  const int threads = p.clusters * kPlanThreads, gtid = rank * kPlanThreads + tid;
+  const int rank = p.ctas > 1 ? (int)cluster_rank() : 0;
+  const int threads = p.ctas * kPlanThreads, gtid = rank * kPlanThreads + tid;
   const int warps = threads / 32, warp = gtid / 32;
   int bad = 0;
   start_next();
+  auto barrier = [&] {
+    if (p.ctas > 1) cluster_barrier();
+    else __syncthreads();
+  };
 
   // ---- heirs; shares so far ----------------------------------------------------------
+  const int n0 = *f.free_count, n = min(max(n0, 0), f.free_cap);
   for (int s = tid; s < f.S; s += kPlanThreads) {
     const int len = f.lens[s], held = f.held[s];
     const bool ok = len >= 0 && held >= 0 && held <= f.cols && len <= (int64_t)held * f.page_size;
     s_heir[s] = ok ? kNoHeir : -1;
+    s_len[s] = len;
+    s_held[s] = held;
     if (!ok) bad |= SSD_DEV_BAD_LENGTH;
+  }
+  for (int b = tid; b < f.B; b += kPlanThreads) {
+    int s = f.src[b];
+    if (s < -1 || s >= f.S) {
+      bad |= SSD_DEV_BAD_LENGTH;
+      s = -2;
+    }
+    s_src[b] = s;
   }
   __syncthreads();
   for (int b = tid; b < f.B; b += kPlanThreads) {
-    const int s = f.src[b];
-    if (s < -1 || s >= f.S) bad |= SSD_DEV_BAD_LENGTH;
-    else if (s >= 0 && s_heir[s] >= 0) atomicMin(&s_heir[s], b);
+    const int s = s_src[b];
+    if (s >= 0 && s_heir[s] >= 0) atomicMin(&s_heir[s], b);
   }
+#pragma unroll 4
   for (int i = gtid; i < f.num_pages; i += threads) f.shares_out[i] = max(f.shares[i], 0);
   __syncthreads();
-  // Old rows by warps; visit(row, place, page, count so far) of those that end by the lanes
-  // of its warp, 32 columns at a time (no page: -1), which gives a new count; then
-  // after(row, count).
-  auto ending = [&](auto visit, auto after) {
-    for (int s = warp; s < f.S; s += warps) {
-      const int held = s_heir[s] == kNoHeir ? f.held[s] : 0;
-      int count = 0;
-      for (int c0 = 0; c0 < held; c0 += 32) {
-        const int c = c0 + lane;
-        int page = c < held ? f.tables[s * f.table_stride + c] : -1;
-        if (c < held && (unsigned)page >= (unsigned)f.num_pages) {
-          bad |= SSD_DEV_BAD_PAGE;
-          page = -1;
-        }
-        count = visit(s, s * f.cols + c, page, count);
-      }
-      after(s, count);
-    }
-  };
-  auto nothing = [](int, int) {};
-  ending([&](int, int, int page, int) {
-    if (page >= 0) p.last[page] = -1;
-    return 0;
-  }, nothing);
-  cluster_barrier();
-  ending([&](int, int place, int page, int) {
-    if (page >= 0) {
-      atomicSub(f.shares_out + page, 1);
-      atomicMax(p.last + page, place);
-    }
-    return 0;
-  }, nothing);
-  cluster_barrier();
-  // ---- pages whose last holder ends ----------------------------------------------------
-  auto is_freed = [&](int place, int page) {
-    return page >= 0 && __ldcg(f.shares_out + page) < 0 && __ldcg(p.last + page) == place;
-  };
-  ending([&](int, int place, int page, int count) {
-    return count + __popc(__ballot_sync(0xffffffffu, is_freed(place, page)));
-  }, [&](int s, int count) {
-    if (lane == 0) p.back[s] = count;
-  });
-  cluster_barrier();
-  const int n0 = *f.free_count, n = min(max(n0, 0), f.free_cap);
-  running_sums(s_back, f.S, s_warp, [&](int s) { return __ldcg(p.back + s); });
+  running_sums(s_piece, f.S, s_warp,
+               [&](int s) { return s_heir[s] == kNoHeir ? (s_held[s] + 31) >> 5 : 0; });
   auto takes = [&](int b) {          // a page for the last tokens
-    const int s = f.src[b];
-    if (s < 0 || s >= f.S || s_heir[s] < 0 || s_heir[s] == b) return 0;
-    const int len = f.lens[s];
-    return (int)(p.by_page.quotient(len) * f.page_size < len);
+    const int s = s_src[b];
+    if (s < 0 || s_heir[s] < 0 || s_heir[s] == b) return 0;
+    return (int)(p.by_page.quotient(s_len[s]) * f.page_size < s_len[s]);
   };
   running_sums(s_nth, f.B, s_warp, takes);
-  const int64_t top = (int64_t)n + s_back[f.S];
-  ending([&](int s, int place, int page, int count) {
-    const bool freed = is_freed(place, page);
-    const unsigned all = __ballot_sync(0xffffffffu, freed);
-    if (freed) {
-      const int k = s_back[s] + count + __popc(all & ((1u << lane) - 1));
-      p.freed[k] = page;
-      if (n + (int64_t)k < f.free_cap) f.free_pages[n + k] = page;
-      if (__ldcg(f.shares_out + page) < -1) bad |= SSD_DEV_BAD_PAGE;
-      f.shares_out[page] = 0;
-    }
-    return count + __popc(all);
-  }, nothing);
-  cluster_barrier();
-  // ---- the new rows ----------------------------------------------------------------------
   const int asked = s_nth[f.B];
+  for (int b = tid; b < f.B; b += kPlanThreads)
+    if (s_nth[b] < s_nth[b + 1]) s_taker[s_nth[b]] = b;  // read after the next barriers
+
+  // ---- pages given back --------------------------------------------------------------------
+  const int pieces = s_piece[f.S];
+  const int per = (pieces + warps - 1) / warps;
+  const int q0 = min(pieces, warp * per), q1 = min(pieces, q0 + per);
+  const bool once = per <= kBatch;   // a warp's pages stay in its registers
+  int page[kBatch], place[kBatch];   // -1: none
+  auto load = [&](int q) {           // pieces q .. q + kBatch - 1
+    int s = 0;
+    if (q < q1) {                    // the row of the first: s_piece[s] <= q < s_piece[s + 1]
+      int hi = f.S;
+      while (hi - s > 1) {
+        const int mid = (s + hi) >> 1;
+        if (s_piece[mid] <= q) s = mid;
+        else hi = mid;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      place[i] = page[i] = -1;
+      if (q + i < q1) {
+        while (s_piece[s + 1] <= q + i) ++s;  // ends: q + i < s_piece[S]
+        const int c = (q + i - s_piece[s]) * 32 + lane;
+        if (c < s_held[s]) {
+          place[i] = s * f.cols + c;
+          page[i] = f.tables[(int64_t)s * f.table_stride + c];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (place[i] >= 0 && (unsigned)page[i] >= (unsigned)f.num_pages) {
+        bad |= SSD_DEV_BAD_PAGE;
+        page[i] = -1;
+      }
+  };
+  auto each = [&](bool first, auto visit) {  // visit(page, place), -1 where there is none
+    for (int q = q0; q < q1; q += kBatch) {
+      if (first || !once) load(q);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) visit(page[i], place[i]);
+    }
+  };
+  each(true, [&](int pg, int) {
+    if (pg >= 0) p.last[pg] = -1;
+  });
+  barrier();
+  each(false, [&](int pg, int at) {
+    if (pg >= 0) {
+      atomicSub(f.shares_out + pg, 1);
+      atomicMax(p.last + pg, at);
+    }
+  });
+  barrier();
+  // those whose last holder ends, by the last place that gives them back
+  int freed = 0;                     // of this warp
+  each(false, [&](int pg, int at) {
+    const bool yes = pg >= 0 && __ldcg(f.shares_out + pg) < 0 && __ldcg(p.last + pg) == at;
+    freed += __popc(__ballot_sync(0xffffffffu, yes));
+  });
+  if (lane == 0) s_count[tid >> 5] = freed;
+  __syncthreads();
+  const int before_warp =
+      __reduce_add_sync(0xffffffffu, lane < (tid >> 5) ? s_count[lane] : 0);
+  if (p.ctas > 1) {
+    const int total = __reduce_add_sync(0xffffffffu, s_count[lane]);
+    if (tid < p.ctas) st_cluster_u32(cluster_addr(&s_total[rank], tid), (uint32_t)total);
+  } else if (tid < 32) {
+    const int total = __reduce_add_sync(0xffffffffu, s_count[lane]);
+    if (tid == 0) s_total[0] = total;
+  }
+  barrier();
+  int before = before_warp, back = 0;
+  for (int r = 0; r < p.ctas; ++r) {
+    if (r < rank) before += s_total[r];
+    back += s_total[r];
+  }
+  const int64_t top = (int64_t)n + back;
+  if (q0 < q1) {
+    each(false, [&](int pg, int at) {
+      const int left = pg >= 0 ? __ldcg(f.shares_out + pg) : 0;
+      const bool yes = left < 0 && __ldcg(p.last + pg) == at;
+      const unsigned all = __ballot_sync(0xffffffffu, yes);
+      if (yes) {
+        const int i = before + __popc(all & ((1u << lane) - 1));
+        if (n + (int64_t)i < f.free_cap) f.free_pages[n + i] = pg;
+        if (left < -1) bad |= SSD_DEV_BAD_PAGE;
+        f.shares_out[pg] = 0;
+        const int taken = back - 1 - i;    // the stack's top goes first
+        if (taken < asked) {
+          p.rows[s_taker[taken]].w = pg;
+          p.copies[taken].y = pg;
+        }
+      }
+      before += __popc(all);
+    });
+  }
+  // ---- the new rows ----------------------------------------------------------------------
   for (int b = gtid; b < f.B; b += threads) {
-    const int s = f.src[b];
+    const int s = s_src[b];
     int4 row = make_int4(-1, 0, 0, -1);  // 2 * old row + heir; pages; those from its table; a page
     int len = 0, ok = s == -1;
-    if (s >= 0 && s < f.S && s_heir[s] >= 0) {
-      const int full = p.by_page.quotient(f.lens[s]);
-      const bool heir = s_heir[s] == b, take = takes(b) != 0;
-      if (!take || s_nth[b] < top) {
+    bool given = false;
+    if (s >= 0 && s_heir[s] >= 0) {
+      const int full = p.by_page.quotient(s_len[s]), nth = s_nth[b];
+      const bool heir = s_heir[s] == b, take = nth < s_nth[b + 1];
+      if (!take || nth < top) {
         ok = 1;
-        len = f.lens[s];
+        len = s_len[s];
         row.x = 2 * s + heir;
-        row.z = heir ? f.held[s] : full;
+        row.z = heir ? s_held[s] : full;
         row.y = row.z + take;
         if (take) {
-          const int64_t i = top - 1 - s_nth[b];
-          row.w = i < n ? f.free_pages[i] : __ldcg(p.freed + (i - n));
-          p.copies[s_nth[b]] = make_int4(f.tables[s * f.table_stride + full], row.w,
-                                         len - full * f.page_size, 0);
+          given = nth < back;              // its page is put down where it is given back
+          if (!given) row.w = f.free_pages[top - 1 - nth];
+          int* copy = reinterpret_cast<int*>(p.copies + nth);
+          copy[0] = f.tables[(int64_t)s * f.table_stride + full];
+          if (!given) copy[1] = row.w;
+          copy[2] = len - full * f.page_size;
         }
       } else {
         bad |= SSD_DEV_NO_PAGES;
       }
     }
-    p.rows[b] = row;
+    int* to = reinterpret_cast<int*>(p.rows + b);
+    to[0] = row.x;
+    to[1] = row.y;
+    to[2] = row.z;
+    if (!given) to[3] = row.w;
     f.lens_out[b] = len;
     f.held_out[b] = row.y;
     f.served[b] = ok;
@@ -308,11 +404,10 @@ __global__ void __launch_bounds__(kWarps * 32)
       bad |= SSD_DEV_BAD_PAGE;
       continue;
     }
-    const ssd_layers* at;
-    char* x = const_cast<char*>(plane_of(f.k_cache, f.v_cache, p.g, j, &at)) +
-              t0 * at->token_stride;
-    const char* from = x + c.x * at->page_stride;
-    char* to = x + c.y * at->page_stride;
+    const ssd_layers& at = side_of(f.k_cache, f.v_cache, p.g, j);
+    char* x = plane_of(at, p.g, j) + t0 * at.token_stride;
+    const char* from = x + c.x * at.page_stride;
+    char* to = x + c.y * at.page_stride;
     const int total = n * p.g.chunks;
     for (int i0 = lane; i0 < total; i0 += 32 * kFlight) {
       uint4 z[kFlight];
@@ -321,7 +416,7 @@ __global__ void __launch_bounds__(kWarps * 32)
       for (int i = 0; i < kFlight; ++i)
         if (i0 + i * 32 < total) {
           const int e = i0 + i * 32, t = p.g.by_token.quotient(e);
-          where[i] = t * at->token_stride + chunk_at(*at, p.g, e - t * p.g.chunks);
+          where[i] = t * at.token_stride + chunk_at(at, p.g, e - t * p.g.chunks);
           z[i] = *reinterpret_cast<const uint4*>(from + where[i]);
         }
 #pragma unroll
@@ -391,7 +486,7 @@ ssd_status check(const ssd_fork* f) {
   return SSD_OK;
 }
 struct ForkLayout {
-  size_t last, back, freed, rows, copies, ncopies, total;
+  size_t last, rows, copies, ncopies, total;
 };
 ForkLayout layout(const ssd_fork& f) {
   ForkLayout L;
@@ -402,8 +497,6 @@ ForkLayout layout(const ssd_fork& f) {
     return here;
   };
   L.last = take((size_t)f.num_pages * 4);
-  L.back = take((size_t)f.S * 4);
-  L.freed = take((size_t)f.num_pages * 4);
   L.rows = take((size_t)f.B * 16);
   L.copies = take((size_t)f.B * 16);
   L.ncopies = take(4);
@@ -443,16 +536,21 @@ ssd_status ssd_append_path(const ssd_append* a, int32_t* dev_status, void* strea
   AppendParams p{};
   p.a = *a;
   p.g = geometry(a->L, a->H, a->row_bytes, pair, {&a->k, &a->v, &a->k_cache, &a->v_cache});
-  p.per = 1;
-  p.groups = p.g.planes;
-  p.by_group = divisor(p.groups);
-  p.warps = (int64_t)a->rows * p.groups;
   p.status = dev_status;
-  if (p.warps > 0x7fffffff - 64) return SSD_ERR_UNSUPPORTED;
-  if (p.warps == 0) return SSD_OK;
-  append_kernel<<<(unsigned)((p.warps + kWarps - 1) / kWarps), kWarps * 32, 0,
-                  static_cast<cudaStream_t>(stream)>>>(p);
-  return status_of(cudaGetLastError());
+  if ((int64_t)a->rows * p.g.planes > 0x7fffffff - 64) return SSD_ERR_UNSUPPORTED;
+  if (a->rows == 0) return SSD_OK;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  static const int v = getenv("APPEND") ? atoi(getenv("APPEND")) : 0;
+  switch (v) {
+    case 0: return status_of(launch_append<1, 4>(p, s));
+    case 1: return status_of(launch_append<2, 4>(p, s));
+    case 2: return status_of(launch_append<2, 2>(p, s));
+    case 3: return status_of(launch_append<4, 2>(p, s));
+    case 4: return status_of(launch_append<4, 4>(p, s));
+    case 5: return status_of(launch_append<1, 2>(p, s));
+    case 6: return status_of(launch_append<4, 1>(p, s));
+    default: return status_of(launch_append<8, 1>(p, s));
+  }
 }
 
 size_t ssd_fork_rows_workspace_size(const ssd_fork* f) {
@@ -485,8 +583,6 @@ ssd_status ssd_fork_rows(const ssd_fork* f, void* workspace, size_t workspace_by
   p.f = *f;
   p.by_page = divisor(f->page_size);
   p.last = reinterpret_cast<int*>(ws + L.last);
-  p.back = reinterpret_cast<int*>(ws + L.back);
-  p.freed = reinterpret_cast<int*>(ws + L.freed);
   p.rows = reinterpret_cast<int4*>(ws + L.rows);
   p.copies = reinterpret_cast<int4*>(ws + L.copies);
   p.ncopies = reinterpret_cast<int*>(ws + L.ncopies);
@@ -498,20 +594,21 @@ ssd_status ssd_fork_rows(const ssd_fork* f, void* workspace, size_t workspace_by
     p.groups = (f->page_size + p.group - 1) / p.group;
   }
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // 8 CTAs share the tables' rows and the counts of shares when there are many
-  p.clusters = (int64_t)f->S * f->cols + f->num_pages > 8192 ? 8 : 1;
-  const int smem = (2 * f->S + f->B + 2) * (int)sizeof(int);
+  // several CTAs share the tables' rows and the counts of shares when there are many
+  static const int lim = getenv("FORKLIM") ? atoi(getenv("FORKLIM")) : 8192;
+  p.ctas = (int64_t)f->S * f->cols + f->num_pages > lim ? kPlanCtas : 1;
+  const int smem = plan_ints(f->S, f->B) * (int)sizeof(int);
   cudaError_t e = cudaSuccess;
   if (smem > 46 * 1024)  // the most that any call needs: the limit is the function's
     e = cudaFuncSetAttribute(fork_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (3 * kMaxRows + 2) * (int)sizeof(int));
+                             plan_ints(kMaxRows, kMaxRows) * (int)sizeof(int));
   if (e != cudaSuccess) return status_of(e);
   cudaLaunchAttribute attr{};
   cudaLaunchConfig_t c{};
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)p.clusters;
+  attr.val.clusterDim.x = (unsigned)p.ctas;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  c.gridDim = dim3((unsigned)p.clusters);
+  c.gridDim = dim3((unsigned)p.ctas);
   c.blockDim = dim3(kPlanThreads);
   c.dynamicSmemBytes = (size_t)smem;
   c.stream = s;

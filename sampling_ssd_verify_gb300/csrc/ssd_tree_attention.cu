@@ -46,7 +46,7 @@ ssd_status check(const ssd_tree_attn* a) {
 }
 
 struct Layout {
-  size_t po, pml, begun, last, total;
+  size_t po, pml, begun, total;
 };
 
 // The division of the work and the workspace of a call; false when its work is beyond
@@ -99,8 +99,7 @@ bool plan(const ssd_tree_attn& a, TreeAttnParams& p, Layout& L) {
   const size_t ctas = (size_t)p.workers * p.hg;
   L.po = take(2 * ctas * rows * a.D * 4);
   L.pml = take(2 * ctas * rows * 8);
-  L.begun = take(ctas * 4);
-  L.last = take((size_t)items * p.hg * 4);
+  L.begun = take(ctas * 8);
   L.total = at;
   return true;
 }
@@ -138,8 +137,7 @@ ssd_status ssd_tree_attention(const ssd_tree_attn* a, void* workspace, size_t wo
   char* ws = static_cast<char*>(workspace);
   p.po = reinterpret_cast<float*>(ws + L.po);
   p.pml = reinterpret_cast<float2*>(ws + L.pml);
-  p.begun = reinterpret_cast<int*>(ws + L.begun);
-  p.last = reinterpret_cast<int*>(ws + L.last);
+  p.begun = reinterpret_cast<int2*>(ws + L.begun);
   p.status = dev_status;
   p.chain = 1;
   for (int u = 1; u < a->N; ++u) {

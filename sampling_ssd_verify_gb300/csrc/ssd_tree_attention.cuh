@@ -29,8 +29,7 @@ struct TreeAttnParams {
   int join_groups;         // groups of eight pairs of an item
   float* po;               // [2 * CTAs, D / 4, pairs of an item, 4] sums (part_at)
   float2* pml;             // [2 * CTAs, pairs of an item] largest score (base 2), weight
-  int* begun;              // [CTAs] item that it began and did not end, or -1
-  int* last;               // [items] last worker of an item that several have
+  int2* begun;             // [CTAs] item that it began and did not end, or -1, and its partials
   int32_t* status;
   uint8_t parent[kTreeNodes];  // of node u > 0; 0 for node 0
 };
@@ -70,6 +69,12 @@ struct TreeSplit {
   int total, workers;
   __device__ __forceinline__ int first(int w) const {  // unit of worker w
     return w >= workers ? total : (int)((long long)w * total / workers);
+  }
+  __device__ __forceinline__ int worker(int unit) const {  // whose share a unit is in
+    int w = (int)((long long)unit * workers / total);
+    while (first(w + 1) <= unit) ++w;            // a step or none
+    while (first(w) > unit) --w;
+    return w;
   }
 };
 struct TreeStart {
@@ -128,6 +133,7 @@ struct TreeStretch {
   int b, h, mb;            // the item,
   int item, slot;          // its number; the partial's, or -1 when it is done whole
   int tile0, tile1;
+  int end;                 // the item's first unit no more
 };
 struct TreeWalk {
   int u, u1;               // units still to do
@@ -156,6 +162,7 @@ __device__ __forceinline__ bool next_stretch(const TreeAttnParams& p, TreeWalk& 
     s.mb = local - set * p.blocks;
     s.tile0 = max(at - 1, 0);
     s.tile1 = at + take - 1;
+    s.end = k.unit + (local + 1) * cost;
     s.item = (k.b * items + local) * p.hg + k.hh;
     s.slot = s.tile0 == 0 && s.tile1 == q.tiles
                  ? -1 : 2 * (k.w * p.hg + k.hh) + (s.tile0 == 0);

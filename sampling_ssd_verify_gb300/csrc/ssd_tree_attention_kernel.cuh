@@ -108,6 +108,26 @@ __device__ __forceinline__ uint32_t odd_mask(uint32_t x) {
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 
+// Leaves in ok (a bit per node, from node `at` on) those on node u's path.
+template <int TILE>
+__device__ __forceinline__ void on_path(uint32_t (&ok)[TILE / 32], const uint8_t* parent,
+                                        bool chain, int u, int at) {
+  uint32_t path[TILE / 32];
+#pragma unroll
+  for (int q = 0; q < TILE / 32; ++q) {
+    const int left = u + 1 - at - q * 32;
+    path[q] = !chain || left <= 0 ? 0u : left >= 32 ? ~0u : (1u << left) - 1;
+  }
+  for (int v = u; !chain && v >= at; v = parent[v]) {
+#pragma unroll
+    for (int q = 0; q < TILE / 32; ++q)
+      if ((v - at) >> 5 == q) path[q] |= 1u << (v & 31);
+    if (v == 0) break;
+  }
+#pragma unroll
+  for (int q = 0; q < TILE / 32; ++q) ok[q] &= path[q];
+}
+
 template <typename T, int D, int BLOCKS>
 __global__ void __launch_bounds__(kTreeThreads, 1)
     tree_tc_kernel(const __grid_constant__ TreeAttnParams p, const __grid_constant__ CUtensorMap kmap,
@@ -126,6 +146,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
   start_next();
   if (warp == kMmaWarp) tmem_alloc(&sh.tmem);
+  if (p.boxes && warp == kQueryWarp && lane < 4)
+    prefetch_map(lane == 0 ? &kmap : lane == 1 ? &vmap : lane == 2 ? &knodes : &vnodes);
   if (tid == 0) {
     sh.err = 0;
     sh.odd[0] = sh.odd[1] = 0;
@@ -341,7 +363,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     } else if (warp == kQueryWarp) {
       // ---- queries: a stretch's, as soon as the scores of the one before are done ------
       uint32_t i = 0;
-      if (lane == 0) p.begun[blockIdx.x] = -1;
+      if (lane == 0) p.begun[blockIdx.x] = make_int2(-1, 0);
       while (next_stretch(p, k, s)) {
         const int pair0 = s.mb * BLOCKS * kRows, pairs = min(BLOCKS * kRows, p.pairs - pair0);
         auto query = [&](const TreeStretch& z, int row) {
@@ -381,11 +403,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         fence_async();
         mbar_arrive(&sh.q_full);  // 32 arrivals: lane 0's follows the job
         ++i;
-        if (lane == 0 && s.slot >= 0) {
-          // the join goes by the worker that began the item, and by its last one
-          if (s.tile0 == 0) p.begun[blockIdx.x] = s.item;
-          if (s.tile1 == s.q.tiles) p.last[s.item] = w;
-        }
+        // the join goes by the worker that began the item, up to that of its last unit
+        if (lane == 0 && s.slot >= 0 && s.tile0 == 0)
+          p.begun[blockIdx.x] = make_int2(s.item, all.worker(s.end - 1) - w + 1);
         // the next ones into L2 meanwhile
         TreeWalk k1 = k;
         TreeStretch s1;
@@ -473,7 +493,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               }
             }
           } else {
-            if (j < n) {
+            auto next_scores = [&] {
               const uint32_t t = c + j;
               mbar_wait(&sh.k_full[ks], k_use & 1, &sh.err, p.status);
               fence_after();
@@ -485,7 +505,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               }
               __syncwarp();
               turn(ks, k_use, S::kSlotsK);
-            }
+            };
+            // the scores of a tile go before the sums of the one before, but where they
+            // have to wait for its keys
+            const bool late = j > 0 && j < n &&
+                              !__any_sync(0xffffffffu, mbar_try_wait(&sh.k_full[ks], k_use & 1));
+            if (j < n && !late) next_scores();
             if (j > 0) {
               const uint32_t t = c + j - 1, b = t & 1, o = S::kOne ? 0 : b;
               if (j == 1 && i > 0) mbar_wait(&sh.o_empty, (i - 1) & 1, &sh.err, p.status);
@@ -500,6 +525,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               __syncwarp();
               turn(vs, v_use, S::kSlotsV);
             }
+            if (late) next_scores();
           }
         }
         c += n;
@@ -518,83 +544,73 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const uint32_t acc = S::kOne ? 0 : b;        // its sums
     const uint32_t to = tmem + lanes + kColO + acc * kColStep;
     uint32_t c = 0;                              // tiles before the stretch (its block's)
-    uint32_t sees[kTreeNodes / 32];              // nodes on its node's path
-    int seen = -1;                               // its node
-    // V of tile j of the stretch: the ring's slot and turn at the first tile
-    uint32_t v_slot = 0, v_use = 0;
+    uint32_t all_tiles = 0;                      // before the stretch, of any block
     for (uint32_t i = 0;; ++i) {
       mbar_wait(&sh.q_full, i & 1, &sh.err, p.status);
-      const TreeJob job = sh.job[i & 1];
-      const int n = gave_up(sh) ? 0 : job.tiles;
+      // of the job only what the tiles need is kept in registers; it stays until the next
+      // one's is read
+      const TreeJob& job = sh.job[i & 1];
+      const int n = gave_up(sh) ? 0 : job.tiles, cached = job.cached, tokens = job.tokens;
+      const int row = (S::kByBlocks ? (int)b * kRows : 0) + (int)m;  // of the item's pairs
+      const bool mine = row < job.pairs;
+      const bool busy = __any_sync(0xffffffffu, mine);
+      const bool second = job.pairs > kRows;     // two blocks
+      const int mine_node = p.by_gqa.quotient(job.pair0 + min(row, job.pairs - 1));
       mbar_arrive(&sh.job_read);
       if (n == 0) break;
       // its tiles: j0, j0 + step, ..
       const int step = S::kByTiles ? 2 : 1;
       const int j0 = S::kByTiles ? (int)((b ^ c) & 1) : S::kOne ? (b == 0 ? 0 : n)
-                                 : (b == 0 || job.pairs > kRows ? 0 : n);
-      const int row = (S::kByBlocks ? (int)b * kRows : 0) + (int)m;  // of the item's pairs
-      const bool mine = row < job.pairs;
-      const bool busy = __any_sync(0xffffffffu, mine);
-      if (job.cached < n) {                      // nodes come
-        const int u = p.by_gqa.quotient(job.pair0 + min(row, job.pairs - 1));
-        if (u != seen) {
-          seen = u;
-#pragma unroll
-          for (int x = 0; x < kTreeNodes / 32; ++x)
-            sees[x] = !p.chain ? 0u : u >= x * 32 + 31 ? ~0u : u < x * 32 ? 0u
-                                                                      : (2u << (u & 31)) - 1;
-          if (!p.chain) {
-            for (int v = u;; v = sh.parent[v]) {
-#pragma unroll
-              for (int x = 0; x < kTreeNodes / 32; ++x)
-                if (v >> 5 == x) sees[x] |= 1u << (v & 31);
-              if (v == 0) break;
-            }
-          }
-        }
-      }
-
+                                 : (b == 0 || second ? 0 : n);
       float top = -INFINITY, l = 0.f;
       for (int j = j0; j < n; j += step) {
         const uint32_t t = c + j;
         // where its scores are, and the parity of their turn
-        const uint32_t buf = S::kByBlocks ? b : t & 1;
+        const uint32_t buf = S::kOne ? t & 1 : b;
         const uint32_t turn = (S::kByBlocks ? t : t >> 1) & 1;
         const uint32_t ts = tmem + lanes + kColS + buf * kColStep;
+        const bool nodes = j >= cached;
+        const int at = nodes ? (j - cached) * kTile : j * kTile;
+        const int here = min(kTile, (nodes ? a.N : tokens) - at);
+        const bool some = nodes || here < kTile; // not all of the tile's tokens count
+        uint32_t ok[kTile / 32];                 // those that do, for this pair
+        if (some && busy) {
+#pragma unroll
+          for (int q = 0; q < kTile / 32; ++q) {
+            const int left = here - q * 32;
+            ok[q] = left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1;
+          }
+          if (nodes) on_path<kTile>(ok, sh.parent, p.chain, mine_node, at);
+        }
         mbar_wait(&sh.s_full[buf], turn, &sh.err, p.status);
         __syncwarp();
         fence_after();
-        const bool nodes = j >= job.cached;
-        const int at = nodes ? (j - job.cached) * kTile : j * kTile;
-        const int here = min(kTile, (nodes ? a.N : job.tokens) - at);
         if (busy) {
           uint32_t x[kTile / 32][32];
 #pragma unroll
           for (int q = 0; q < kTile / 32; ++q) tmem_ld32(x[q], ts + q * 32);
           tmem_wait_ld();
-          if (nodes || here < kTile) {
+          if (some) {
 #pragma unroll
-            for (int q = 0; q < kTile / 32; ++q) {
-              uint32_t ok = here >= q * 32 + 32 ? ~0u : here <= q * 32 ? 0u : (1u << (here & 31)) - 1;
-              if (nodes) {
-#pragma unroll
-                for (int y = 0; y < kTreeNodes / kTile; ++y)
-                  if (at == y * kTile) ok &= sees[y * (kTile / 32) + q];
-              }
+            for (int q = 0; q < kTile / 32; ++q)
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (!(ok & 1u << e)) x[q][e] = 0xff800000u;  // -inf
-            }
+                if (!(ok[q] & 1u << e)) x[q][e] = 0xff800000u;  // -inf
           }
-          float t0 = -INFINITY, t1 = -INFINITY;
+          float high[8];
 #pragma unroll
-          for (int q = 0; q < kTile / 32; ++q)
+          for (int e = 0; e < 8; ++e) high[e] = __uint_as_float(x[0][e]);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              t0 = fmaxf(t0, __uint_as_float(x[q][e]));
-              t1 = fmaxf(t1, __uint_as_float(x[q][e + 1]));
-            }
-          const float now = fmaxf(t0, t1) * p.scale_log2;
+          for (int e = 8; e < kTile; e += 16)
+#pragma unroll
+            for (int z = 0; z < 8 && e + 8 < kTile; ++z)
+              high[z] = max3(high[z], __uint_as_float(x[(e + z) / 32][(e + z) % 32]),
+                             __uint_as_float(x[(e + 8 + z) / 32][(e + 8 + z) % 32]));
+#pragma unroll
+          for (int z = 0; z < 8; ++z)
+            high[z] = fmaxf(high[z], __uint_as_float(x[kTile / 32 - 1][24 + z]));
+          const float now = max3(max3(high[0], high[1], high[2]), max3(high[3], high[4], high[5]),
+                                 fmaxf(high[6], high[7])) * p.scale_log2;
           // the kept maximum moves when a score passes it by 2^kRise
           const bool move = now > top + kRise;
           const float old = top;
@@ -608,48 +624,43 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             mbar_wait(&sh.o_done[done], turns & 1, &sh.err, p.status);
             fence_after();
 #pragma unroll 1
-            for (int q = 0; q < D / 32; ++q) {
-              uint32_t y[32];
-              tmem_ld32(y, to + q * 32);
+            for (int q = 0; q < D; q += 8) {     // few registers: the scores have 128
+              uint32_t y[8];
+              tmem_ld8(y, to + q);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
-              tmem_st32(to + q * 32, y);
+              for (int e = 0; e < 8; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+              tmem_st8(to + q, y);
             }
           }
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int q = 0; q < kTile / 32; ++q)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float y = exp2_fast(fmaf(__uint_as_float(x[q][e]), p.scale_log2, -off));
-              sum[e & 3] += y;
-              x[q][e] = __float_as_uint(y);
-            }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          const float2 by = make_float2(p.scale_log2, p.scale_log2), less = make_float2(-off, -off);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           // weights in the type of V, as the product takes them: each is off by at most
           // half a step, which an output averages over its tokens; their sum l is of
           // the unrounded ones
 #pragma unroll
-          for (int q = 0; q < kTile / 64; ++q) {
-            uint32_t y[32];
+          for (int q = 0; q < kTile / 32; ++q) {
+            uint32_t z[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              y[e] = pack2<T>(__uint_as_float(x[2 * q + e / 16][2 * (e % 16)]),
-                              __uint_as_float(x[2 * q + e / 16][2 * (e % 16) + 1]));
-            tmem_st32(ts + q * 32, y);
+            for (int e = 0; e < 32; e += 2) {
+              float2 y = fma2(make_float2(__uint_as_float(x[q][e]), __uint_as_float(x[q][e + 1])),
+                              by, less);
+              y = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+              sum[e >> 1 & 1] = add2(sum[e >> 1 & 1], y);
+              z[e / 2] = pack2<T>(y.x, y.y);
+            }
+            tmem_st16(ts + q * 16, z);
           }
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           tmem_wait_st();
         }
-        if ((nodes || here < kTile) && (!S::kByBlocks || b == 0)) {
+        if (some && (!S::kByBlocks || b == 0)) {
           // Zero weights must not meet what is no number (0 * NaN): rows of V past the
           // last token are whatever the page or the slot held, and a node's values may be
           // off the path of others.  Those that are no numbers are put aside, and
           // added at the end to the nodes below theirs.
-          uint32_t slot = v_slot + (uint32_t)j, use = v_use;
-          use += slot / S::kSlotsV;
-          slot %= S::kSlotsV;
-          mbar_wait(&sh.v_full[slot], use & 1, &sh.err, p.status);
+          const uint32_t nth = all_tiles + (uint32_t)j, slot = nth % S::kSlotsV;
+          mbar_wait(&sh.v_full[slot], nth / S::kSlotsV & 1, &sh.err, p.status);
           const uint32_t vs = vring + slot * S::kSlot;
           for (int e = here * 8 + (int)m; e < kTile * 8; e += kRows)
 #pragma unroll
@@ -722,7 +733,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         sum = m0.y;
         f0 = 1.f;
       }
-      const int pair = job.pair0 + row, node = p.by_gqa.quotient(pair);
+      const int pair = job.pair0 + row, node = mine_node;
       const int head = job.head * p.gqa + pair - node * p.gqa;
       const bool whole = job.slot < 0;
       if (mine && (S::kByBlocks || b == 0)) {
@@ -757,19 +768,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           }
           if (odd && mine) {
             // values that are no numbers, of the nodes on the path whose tiles were here
-            for (int v = max(0, -job.cached) * kTile; v < min(a.N, (n - job.cached) * kTile); ++v) {
-              uint32_t word = 0;
-#pragma unroll
-              for (int x = 0; x < kTreeNodes / 32; ++x)
-                if (v >> 5 == x) word = sees[x];
-              if (!(word >> (v & 31) & 1)) continue;
+            const int v0 = max(0, -cached) * kTile, v1 = (n - cached) * kTile;
+            for (int v = node;; v = sh.parent[v]) {
+              if (v < v0) break;
               const T* value = static_cast<const T*>(a.v.ptr) + job.seq * a.v.page_stride +
                                v * a.v.token_stride + job.head * a.v.head_stride + col;
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
                 const float z = to_float(value[e]);
-                if (!(fabsf(z) < INFINITY)) y[e] = __float_as_uint(__uint_as_float(y[e]) + z);
+                if (v < v1 && !(fabsf(z) < INFINITY))
+                  y[e] = __float_as_uint(__uint_as_float(y[e]) + z);
               }
+              if (v == 0) break;
             }
           }
           if (!mine) continue;
@@ -796,10 +806,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       }
       fence_before();
       mbar_arrive(&sh.o_empty);
-      if (!S::kByBlocks || b == 0 || job.pairs > kRows) c += n;
-      v_slot += (uint32_t)n;
-      v_use += v_slot / S::kSlotsV;
-      v_slot %= S::kSlotsV;
+      if (!S::kByBlocks || b == 0 || second) c += n;
+      all_tiles += (uint32_t)n;
     }
   }
   fence_before();
@@ -822,10 +830,9 @@ __global__ void __launch_bounds__(D) tree_join_kernel(const __grid_constant__ Tr
   const int cta = blockIdx.x / p.join_groups, group = blockIdx.x - cta * p.join_groups;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   wait_previous();
-  const int item = p.begun[cta];
+  const int2 begun = p.begun[cta];
+  const int item = begun.x, np = begun.y, hh = cta % p.hg;
   if (item < 0) return;
-  const int w0 = cta / p.hg, hh = cta - w0 * p.hg;
-  const int np = p.last[item] - w0 + 1;
   const int i = group * 8 + (lane & 7);
   int rest = item / p.hg;
   const int mb = rest % p.blocks;
@@ -836,27 +843,44 @@ __global__ void __launch_bounds__(D) tree_join_kernel(const __grid_constant__ Tr
   const int at = mine ? i : 0;
   // the partial of the worker that began it, then those of workers that went on
   auto slot_of = [&](int j) { return 2 * (cta + j * p.hg) + (j == 0); };
-  float top = -INFINITY;
-#pragma unroll 4
-  for (int j = 0; j < np; ++j) top = fmaxf(top, p.pml[(int64_t)slot_of(j) * kPairs + at].x);
-  const float off = top == -INFINITY ? 0.f : top;
+  // the loads of four partials are in flight together
+  constexpr int kBatch = 4;
   const int d = warp * 32 + (lane >> 3) * 4;
-  float l = 0.f;
+  float top = -INFINITY, l = 0.f;
   float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-#pragma unroll 4
-  for (int j = 0; j < np; ++j) {
-    const int slot = slot_of(j);
-    const float2 ml = p.pml[(int64_t)slot * kPairs + at];
-    const float f = exp2_fast(ml.x - off);
-    l = fmaf(ml.y, f, l);
+  for (int j0 = 0; j0 < np; j0 += kBatch) {
+    float2 ml[kBatch];
+    float4 x[kBatch][2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float4 x =
-          *reinterpret_cast<const float4*>(p.po + part_at<D>(slot, kPairs, at, d + e * 16));
-      o[e].x = fmaf(x.x, f, o[e].x);
-      o[e].y = fmaf(x.y, f, o[e].y);
-      o[e].z = fmaf(x.z, f, o[e].z);
-      o[e].w = fmaf(x.w, f, o[e].w);
+    for (int j = 0; j < kBatch; ++j) {
+      const int slot = slot_of(min(j0 + j, np - 1));
+      ml[j] = p.pml[(int64_t)slot * kPairs + at];
+      if (j0 + j >= np) ml[j] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        x[j][e] = *reinterpret_cast<const float4*>(p.po + part_at<D>(slot, kPairs, at, d + e * 16));
+    }
+    float now = top;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) now = fmaxf(now, ml[j].x);
+    const float off = now == -INFINITY ? 0.f : now, keep = exp2_fast(top - off);
+    top = now;
+    l *= keep;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      o[e] = make_float4(o[e].x * keep, o[e].y * keep, o[e].z * keep, o[e].w * keep);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (j0 + j >= np) break;
+      const float f = exp2_fast(ml[j].x - off);
+      l = fmaf(ml[j].y, f, l);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        o[e].x = fmaf(x[j][e].x, f, o[e].x);
+        o[e].y = fmaf(x[j][e].y, f, o[e].y);
+        o[e].z = fmaf(x[j][e].z, f, o[e].z);
+        o[e].w = fmaf(x[j][e].w, f, o[e].w);
+      }
     }
   }
   if (!mine) return;
