@@ -185,10 +185,10 @@ inline Encode encoder() {
   return fn;
 }
 
-// Map of [X, Y, H, D] rows of 16-bit elements for boxes of `rows` rows of one head by
-// 64 elements, 128-byte swizzle; outside of it boxes read zeros.
+// Map of [X, Y, H, D] rows of 16-bit elements for boxes of `rows` rows of some heads (one)
+// by 64 elements, 128-byte swizzle; outside of it boxes read zeros.
 inline bool box_map(CUtensorMap* map, int dtype, const ssd_paged& c, int D, int H, int Y, int X,
-                    int rows) {
+                    int rows, int heads = 1) {
   const Encode encode = encoder();
   if (!encode) return false;
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)Y, (cuuint64_t)X};
@@ -196,7 +196,7 @@ inline bool box_map(CUtensorMap* map, int dtype, const ssd_paged& c, int D, int 
   auto bytes = [](int64_t stride, int64_t n) { return (cuuint64_t)(n > 1 ? stride * 2 : 16); };
   const cuuint64_t strides[3] = {bytes(c.head_stride, H), bytes(c.token_stride, Y),
                                  bytes(c.page_stride, X)};
-  const cuuint32_t box[4] = {64, 1, (cuuint32_t)rows, 1};
+  const cuuint32_t box[4] = {64, (cuuint32_t)heads, (cuuint32_t)rows, 1};
   const cuuint32_t steps[4] = {1, 1, 1, 1};
   return encode(map,
                 dtype == SSD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16

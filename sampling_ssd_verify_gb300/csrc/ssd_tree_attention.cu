@@ -90,6 +90,11 @@ bool plan(const ssd_tree_attn& a, TreeAttnParams& p, Layout& L) {
             box_strides(a.v_cache, a.Hkv, a.page_size, a.num_pages) &&
             box_strides(a.k, a.Hkv, a.N, a.B) && box_strides(a.v, a.Hkv, a.N, a.B);
   p.node_rows = std::min(tile, (a.N + 7) / 8 * 8);
+  // a block's queries are whole nodes, or all there are
+  const ssd_paged q{a.q, a.q_seq_stride, a.q_node_stride, a.q_head_stride};
+  p.q_nodes = p.q_plain && p.gqa <= 128 && (p.pairs <= 128 || 128 % p.gqa == 0) &&
+                      box_strides(q, a.Hq, a.N, a.B)
+                  ? std::min(a.N, 128 / p.gqa) : 0;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;

@@ -25,6 +25,7 @@ struct TreeAttnParams {
   int workers;             // of hg CTAs each
   int boxes;               // tiles come by TMA
   int node_rows;           // rows of a box of nodes
+  int q_nodes;             // nodes of a box of queries (0: copied row by row)
   int chain;               // the tree is one
   int join_groups;         // groups of eight pairs of an item
   float* po;               // [2 * CTAs, D / 4, pairs of an item, 4] sums (part_at)

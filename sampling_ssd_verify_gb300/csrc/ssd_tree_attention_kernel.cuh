@@ -133,7 +133,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     tree_tc_kernel(const __grid_constant__ TreeAttnParams p, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ CUtensorMap knodes,
-                   const __grid_constant__ CUtensorMap vnodes) {
+                   const __grid_constant__ CUtensorMap vnodes,
+                   const __grid_constant__ CUtensorMap qmap) {
   using S = TreeShape<D, BLOCKS>;
   constexpr int kTile = S::kTile;
   extern __shared__ __align__(1024) unsigned char s_raw[];
@@ -148,6 +149,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   if (warp == kMmaWarp) tmem_alloc(&sh.tmem);
   if (p.boxes && warp == kQueryWarp && lane < 4)
     prefetch_map(lane == 0 ? &kmap : lane == 1 ? &vmap : lane == 2 ? &knodes : &vnodes);
+  if (p.q_nodes > 0 && warp == kQueryWarp && lane == 4) prefetch_map(&qmap);
   if (tid == 0) {
     sh.err = 0;
     sh.odd[0] = sh.odd[1] = 0;
@@ -363,6 +365,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     } else if (warp == kQueryWarp) {
       // ---- queries: a stretch's, as soon as the scores of the one before are done ------
       uint32_t i = 0;
+      uint64_t q_policy;
+      asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(q_policy));
       if (lane == 0) p.begun[blockIdx.x] = make_int2(-1, 0);
       while (next_stretch(p, k, s)) {
         const int pair0 = s.mb * BLOCKS * kRows, pairs = min(BLOCKS * kRows, p.pairs - pair0);
@@ -372,23 +376,26 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                  (int64_t)(z.h * p.gqa + pair - node * p.gqa) * a.q_head_stride;
         };
         if (i > 0) mbar_wait(&sh.q_empty, (i - 1) & 1, &sh.err, p.status);
-        constexpr int kLanes = D / 8;            // lanes of a row, 16 bytes each
         // rows past the last pair hold whatever was there: a row's scores are its own
-#pragma unroll 4
-        for (int r0 = 0; r0 < pairs; r0 += 32 / kLanes) {
-          const int row = r0 + lane / kLanes, ch = lane % kLanes;
-          if (row < pairs) {
-            const uint32_t dst = qs + (row / kRows) * S::kQueries + (ch / 8) * S::kQueryPanel +
-                                 (row % kRows) * 128 + (((ch & 7) ^ (row & 7)) << 4);
-            const T* from = query(s, row) + ch * 8;
-            if (p.q_plain) {
-              copy16(dst, from, true);
-            } else {                             // a scale that is not positive: -q, or 0
-              const uint4 x = *reinterpret_cast<const uint4*>(from);
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst),
-                           "r"((x.x & p.q_and) ^ p.q_xor), "r"((x.y & p.q_and) ^ p.q_xor),
-                           "r"((x.z & p.q_and) ^ p.q_xor), "r"((x.w & p.q_and) ^ p.q_xor)
-                           : "memory");
+        if (p.q_nodes == 0) {
+          constexpr int kLanes = D / 8;          // lanes of a row, 16 bytes each
+          const int ch = lane % kLanes;
+#pragma unroll 8
+          for (int r0 = 0; r0 < pairs; r0 += 32 / kLanes) {
+            const int row = r0 + lane / kLanes;
+            if (row < pairs) {
+              const uint32_t dst = qs + (row / kRows) * S::kQueries + (ch / 8) * S::kQueryPanel +
+                                   (row % kRows) * 128 + (((ch & 7) ^ (row & 7)) << 4);
+              const T* from = query(s, row) + ch * 8;
+              if (p.q_plain) {
+                copy16(dst, from, true);
+              } else {                           // a scale that is not positive: -q, or 0
+                const uint4 x = *reinterpret_cast<const uint4*>(from);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst),
+                             "r"((x.x & p.q_and) ^ p.q_xor), "r"((x.y & p.q_and) ^ p.q_xor),
+                             "r"((x.z & p.q_and) ^ p.q_xor), "r"((x.w & p.q_and) ^ p.q_xor)
+                             : "memory");
+              }
             }
           }
         }
@@ -398,10 +405,25 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (lane == 0)
           sh.job[i & 1] = TreeJob{s.tile1 - s.tile0, s.q.cached - s.tile0,
                                   s.q.len - s.tile0 * kTile, s.b, s.h, pair0, pairs, s.slot};
-        copies_commit();
-        copies_wait<0>();
-        fence_async();
-        mbar_arrive(&sh.q_full);  // 32 arrivals: lane 0's follows the job
+        // 32 arrivals: lane 0's follows the job
+        if (p.q_nodes > 0) {
+          // boxes of a block's nodes, their heads side by side, and 64 dimensions
+          const int boxes = (pairs > kRows ? 2 : 1) * S::kPanels;
+          if (lane == 0)
+            mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(boxes * p.q_nodes * p.gqa * 128));
+          __syncwarp();
+          if (lane < boxes) {
+            const int block = lane / S::kPanels, d = lane % S::kPanels;
+            tma_box(qs + block * S::kQueries + d * S::kQueryPanel, &qmap, d * 64, s.h * p.gqa,
+                    (s.mb * BLOCKS + block) * p.q_nodes, s.b, &sh.q_full, q_policy);
+          }
+          if (lane > 0) mbar_arrive(&sh.q_full);
+        } else {
+          copies_commit();
+          copies_wait<0>();
+          fence_async();
+          mbar_arrive(&sh.q_full);
+        }
         ++i;
         // the join goes by the worker that began the item, up to that of its last unit
         if (lane == 0 && s.slot >= 0 && s.tile0 == 0)
@@ -420,6 +442,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (i > 0) {
         mbar_wait(&sh.q_empty, (i - 1) & 1, &sh.err, p.status);
         mbar_wait(&sh.job_read, (i - 1) & 1, &sh.err, p.status);
+      }
+      if (p.q_nodes > 0 && i > 0 && sh.err) {  // let the last copies land
+        int none = 0;
+        mbar_wait(&sh.q_full, (i - 1) & 1, &none, nullptr);
       }
       if (lane == 0) sh.job[i & 1].tiles = 0;
       __syncwarp();
@@ -902,7 +928,7 @@ cudaError_t launch_tree(const TreeAttnParams& p, cudaStream_t s) {
   const auto kernel = tree_tc_kernel<T, D, BLOCKS>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  CUtensorMap km{}, vm{}, kn{}, vn{};
+  CUtensorMap km{}, vm{}, kn{}, vn{}, qm{};
   const ssd_tree_attn& a = p.a;
   if (p.boxes) {
     const int rows = std::min(a.page_size, tree_tile(D));
@@ -912,7 +938,11 @@ cudaError_t launch_tree(const TreeAttnParams& p, cudaStream_t s) {
         !box_map(&vn, a.dtype, a.v, D, a.Hkv, a.N, a.B, p.node_rows))
       return cudaErrorInvalidValue;
   }
-  kernel<<<p.workers * p.hg, kTreeThreads, smem, s>>>(p, km, vm, kn, vn);
+  if (p.q_nodes > 0 &&
+      !box_map(&qm, a.dtype, {a.q, a.q_seq_stride, a.q_node_stride, a.q_head_stride}, D, a.Hq, a.N,
+               a.B, p.q_nodes, p.gqa))
+    return cudaErrorInvalidValue;
+  kernel<<<p.workers * p.hg, kTreeThreads, smem, s>>>(p, km, vm, kn, vn, qm);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute early{};
