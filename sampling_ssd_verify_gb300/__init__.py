@@ -25,6 +25,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -102,50 +103,6 @@ class _Attention(ctypes.Structure):
                 ("lse", ctypes.c_void_p), ("scale", ctypes.c_float), ("pad_", ctypes.c_int32)]
 
 
-class _TreeAttn(ctypes.Structure):
-    _fields_ = [("dtype", ctypes.c_int32), ("B", ctypes.c_int32), ("N", ctypes.c_int32),
-                ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32),
-                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
-                ("q", ctypes.c_void_p), ("q_seq_stride", ctypes.c_int64),
-                ("q_node_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
-                ("k", _Paged), ("v", _Paged), ("k_cache", _Paged), ("v_cache", _Paged),
-                ("tables", ctypes.c_void_p), ("lens", ctypes.c_void_p),
-                ("table_stride", ctypes.c_int64), ("parent", ctypes.c_char_p),
-                ("out", ctypes.c_void_p), ("out_seq_stride", ctypes.c_int64),
-                ("out_node_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
-                ("lse", ctypes.c_void_p), ("cols", ctypes.c_int32), ("scale", ctypes.c_float)]
-
-
-class _Layers(ctypes.Structure):
-    _fields_ = [("ptr", ctypes.c_void_p), ("layer_stride", ctypes.c_int64),
-                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
-                ("head_stride", ctypes.c_int64)]
-
-
-class _Append(ctypes.Structure):
-    _fields_ = [("L", ctypes.c_int32), ("B", ctypes.c_int32), ("N", ctypes.c_int32),
-                ("H", ctypes.c_int32), ("row_bytes", ctypes.c_int32),
-                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
-                ("rows", ctypes.c_int32), ("path_cols", ctypes.c_int32), ("pad_", ctypes.c_int32),
-                ("k", _Layers), ("v", _Layers), ("k_cache", _Layers), ("v_cache", _Layers),
-                ("slots", ctypes.c_void_p), ("owner", ctypes.c_void_p), ("cu", ctypes.c_void_p),
-                ("path", ctypes.c_void_p), ("path_stride", ctypes.c_int64)]
-
-
-class _Fork(ctypes.Structure):
-    _fields_ = [("S", ctypes.c_int32), ("B", ctypes.c_int32), ("cols", ctypes.c_int32),
-                ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
-                ("free_cap", ctypes.c_int32), ("L", ctypes.c_int32), ("H", ctypes.c_int32),
-                ("row_bytes", ctypes.c_int32), ("pad_", ctypes.c_int32),
-                ("src", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("held", ctypes.c_void_p),
-                ("tables", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
-                ("shares", ctypes.c_void_p), ("free_pages", ctypes.c_void_p),
-                ("free_count", ctypes.c_void_p), ("k_cache", _Layers), ("v_cache", _Layers),
-                ("tables_out", ctypes.c_void_p), ("lens_out", ctypes.c_void_p),
-                ("held_out", ctypes.c_void_p), ("served", ctypes.c_void_p),
-                ("shares_out", ctypes.c_void_p), ("free_out", ctypes.c_void_p)]
-
-
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
@@ -185,11 +142,11 @@ _SIGS = {
                       [_vp] * 10, _i),
     "ssd_prefix_attention_workspace_size": ([ctypes.POINTER(_Attention)], _sz),
     "ssd_prefix_attention": ([ctypes.POINTER(_Attention), _vp, _sz, _vp, _vp], _i),
-    "ssd_tree_attention_workspace_size": ([ctypes.POINTER(_TreeAttn)], _sz),
-    "ssd_tree_attention": ([ctypes.POINTER(_TreeAttn), _vp, _sz, _vp, _vp], _i),
-    "ssd_append_path": ([ctypes.POINTER(_Append), _vp, _vp], _i),
-    "ssd_fork_rows_workspace_size": ([ctypes.POINTER(_Fork)], _sz),
-    "ssd_fork_rows": ([ctypes.POINTER(_Fork), _vp, _sz, _vp, _vp], _i),
+    "ssd_tree_attention_workspace_size": ([_vp], _sz),
+    "ssd_tree_attention": ([_vp, _vp, _sz, _vp, _vp], _i),
+    "ssd_append_path": ([_vp, _vp, _vp], _i),
+    "ssd_fork_rows_workspace_size": ([_vp], _sz),
+    "ssd_fork_rows": ([_vp, _vp, _sz, _vp, _vp], _i),
 }
 
 
@@ -908,25 +865,46 @@ def prefix_attention(q, k_cache, v_cache, prefix_tables, prefix_len, group_off, 
     return o if lse or "lse" not in o else _without(o, "lse")
 
 
-def _launch(name, a, o, workspace, dev, device, dev_status, stream, lent=()):
-    """Call ssd_<name> with a workspace of the dict's, which is made, or replaced when it is
-    too small; `lent`: tensors of the call's own, beside the dict's."""
-    L = lib()
-    size, fn = getattr(L, f"ssd_{name}_workspace_size"), getattr(L, f"ssd_{name}")
+# The descriptors of the calls below are packed as the C structs lie in memory (ctypes takes
+# several times as long to fill one): ssd_tree_attn, ssd_append, ssd_fork.
+_PACK_TREE = struct.Struct("@8i" + "Q3q" + "Q3q" * 4 + "QQqQ" + "Q3q" + "Qif").pack
+_PACK_APPEND = struct.Struct("@10i" + "Q4q" * 4 + "4Qq").pack
+_PACK_FORK = struct.Struct("@10i" + "4Qq3Q" + "Q4q" * 2 + "6Q").pack
+_parents = {}  # trees by their bytes: the library reads them by address
+
+
+def _parent_address(parent, N):
+    if len(parent) != N:
+        raise SSDError("parent must have N entries")
+    key = np.asarray(parent, dtype=np.int32).tobytes()
+    kept = _parents.get(key)
+    if kept is None:
+        if len(_parents) >= 256:
+            _parents.clear()
+        kept = _parents[key] = ctypes.create_string_buffer(key, max(len(key), 1))
+    return ctypes.addressof(kept), kept
+
+
+def _launch(fn, size, name, a, o, workspace, dev, device, dev_status, stream):
+    """Call `fn` with a workspace of the dict's, which is made, or replaced when it is too
+    small; `size` gives its bytes."""
     ws = workspace if workspace is not None else o.get("workspace")
     if ws is None:
         ws = o["workspace"] = _workspace(size(a), device)
     elif ws.get_device() != dev or not ws.is_contiguous():
         raise SSDError(f"the workspace must be a contiguous tensor on cuda:{dev}")
-    status = _dev_ptr(dev_status)
-    handle = _use_stream(stream, dev, (*o.values(), ws, *lent))
+    status = None if dev_status is None else _dev_ptr(dev_status)
+    if stream is None:
+        handle = _torch_module._C._cuda_getCurrentRawStream(dev)
+    else:
+        handle = _use_stream(stream, dev, (*o.values(), ws))
     st = fn(a, ws.data_ptr(), ws.numel() * ws.element_size(), status, handle)
     if st == _ERR_WORKSPACE and workspace is None:  # nothing has been launched
         ws = o["workspace"] = _workspace(size(a), device)
         handle = _use_stream(stream, dev, (ws,))
         st = fn(a, ws.data_ptr(), ws.numel(), status, handle)
     if st:
-        _check(st, f"ssd_{name}")
+        _check(st, name)
 
 
 def tree_attention(q, k, v, k_cache, v_cache, tables, lens, parent=None, scale=None, lse=True,
@@ -951,14 +929,11 @@ def tree_attention(q, k, v, k_cache, v_cache, tables, lens, parent=None, scale=N
     B, N, Hq, D = qs
     code = SSD_BF16 if dt is torch.bfloat16 else SSD_F16 if dt is torch.float16 else -1
     dev = q.get_device()
-    for t in (k, v, k_cache, v_cache):
-        if t.dtype is not dt:
-            code = -1
-        if t.get_device() != dev:
-            raise SSDError("q, the nodes and the caches must be on one GPU")
-    if code < 0:
+    if code < 0 or k.dtype is not dt or v.dtype is not dt or k_cache.dtype is not dt or \
+            v_cache.dtype is not dt:
         raise SSDError("q, the nodes and the caches must share bfloat16 or float16")
-    if dev < 0:
+    if dev < 0 or k.get_device() != dev or v.get_device() != dev or \
+            k_cache.get_device() != dev or v_cache.get_device() != dev:
         raise SSDError("q, the nodes and the caches must be on one GPU")
     _on_current(dev)
     o = out if out is not None else {}
@@ -972,39 +947,41 @@ def tree_attention(q, k, v, k_cache, v_cache, tables, lens, parent=None, scale=N
         if o.get("lse") is None:
             o["lse"] = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device)
         at = _tensor(o["lse"], "lse", torch.float32, (B, N, Hq), dev)
-    views = []
-    for t in (q, y, k, v, k_cache, v_cache):
-        s = t.stride()
-        if s[3] != 1:
-            raise SSDError("the head dimension must be contiguous")
-        views.append((t.data_ptr(), s[0], s[1], s[2]))
-    if parent is not None:
-        if len(parent) != N:
-            raise SSDError("parent must have N entries")
-        parent = np.asarray(parent, dtype=np.int32).tobytes()
+    qa, ya, ka, va, kc, vc = (q.stride(), y.stride(), k.stride(), v.stride(), k_cache.stride(),
+                              v_cache.stride())
+    if qa[3] != 1 or ya[3] != 1 or ka[3] != 1 or va[3] != 1 or kc[3] != 1 or vc[3] != 1:
+        raise SSDError("the head dimension must be contiguous")
+    tree, kept = (0, None) if parent is None else _parent_address(parent, N)
     table, stride, cols = _rows2d(tables, "tables", B, i32, dev)
-    a = _TreeAttn(code, B, N, Hq, ks[2], D, cs[0], cs[1], *views[0], *views[2:], table,
-                  _tensor(lens, "lens", i32, (B,), dev), stride, parent, *views[1], at, cols,
-                  D ** -0.5 if scale is None else scale)
-    _launch("tree_attention", a, o, workspace, dev, q.device, dev_status, stream)
+    a = _PACK_TREE(code, B, N, Hq, ks[2], D, cs[0], cs[1], q.data_ptr(), qa[0], qa[1], qa[2],
+                   k.data_ptr(), ka[0], ka[1], ka[2], v.data_ptr(), va[0], va[1], va[2],
+                   k_cache.data_ptr(), kc[0], kc[1], kc[2], v_cache.data_ptr(), vc[0], vc[1],
+                   vc[2], table, _tensor(lens, "lens", i32, (B,), dev), stride, tree,
+                   y.data_ptr(), ya[0], ya[1], ya[2], at, cols,
+                   D ** -0.5 if scale is None else scale)
+    L = lib()
+    _launch(L.ssd_tree_attention, L.ssd_tree_attention_workspace_size, "ssd_tree_attention", a, o,
+            workspace, dev, q.device, dev_status, stream)
     return o if lse or "lse" not in o else _without(o, "lse")
 
 
 def _layers(t, name, dev):
-    """ssd_layers and shape of a tensor [L, X, Y, H, D], or [X, Y, H, D] of one layer."""
+    """The shape [L, X, Y, H, D] of a tensor, and ssd_layers of it (its address, strides in
+    bytes); [X, Y, H, D] is one layer."""
     s, shape = t.stride(), t.shape
-    if len(shape) == 4:
-        s, shape = (0, *s), (1, *shape)
-    if len(shape) != 5 or t.get_device() != dev:
+    n = len(shape)
+    if (n != 5 and n != 4) or t.get_device() != dev:
         raise SSDError(f"{name}: expected a tensor of 4 dimensions, or 5 with the layers, on "
                        f"cuda:{dev}")
     es = t.element_size()
-    if s[4] != 1 or shape[4] * es % 16 != 0:
+    if s[-1] != 1 or shape[-1] * es % 16 != 0:
         raise SSDError(f"{name}: a head must be contiguous, and a multiple of 16 bytes")
-    return _Layers(t.data_ptr(), s[0] * es, s[1] * es, s[2] * es, s[3] * es), tuple(shape)
+    if n == 5:
+        return tuple(shape), (t.data_ptr(), s[0] * es, s[1] * es, s[2] * es, s[3] * es)
+    return (1, *shape), (t.data_ptr(), 0, s[0] * es, s[1] * es, s[2] * es)
 
 
-_NO_LAYERS = _Layers()
+_NO_LAYERS = (0, 0, 0, 0, 0)
 
 
 def append_path(k, v, k_cache, v_cache, slots, owner, cu, path=None, dev_status=None,
@@ -1020,36 +997,69 @@ def append_path(k, v, k_cache, v_cache, slots, owner, cu, path=None, dev_status=
     and do not overlap the nodes.  Returns None."""
     torch = _torch()
     i32 = torch.int32
-    dev = k_cache.get_device()
+    dev, dt = k_cache.get_device(), k_cache.dtype
     if dev < 0:
         raise SSDError("expected caches on the GPU")
     _on_current(dev)
-    if (v is None) != (v_cache is None):
-        raise SSDError("v and v_cache go together")
-    kl, ks = _layers(k, "k", dev)
-    cl, cs = _layers(k_cache, "k_cache", dev)
-    if ks[0] != cs[0] or ks[3:] != cs[3:] or k.dtype is not k_cache.dtype:
+    ks, kl = _layers(k, "k", dev)
+    cs, cl = _layers(k_cache, "k_cache", dev)
+    L, B, N, H, D = ks
+    if L != cs[0] or H != cs[3] or D != cs[4] or k.dtype is not dt:
         raise SSDError("nodes and caches must share the layers, heads and type")
     vl = wl = _NO_LAYERS
-    if v is not None:
-        if v.shape != k.shape or v_cache.shape != k_cache.shape or v.dtype is not k.dtype or \
-                v_cache.dtype is not k.dtype:
+    if v is not None and v_cache is not None:
+        vs, vl = _layers(v, "v", dev)
+        ws, wl = _layers(v_cache, "v_cache", dev)
+        if vs != ks or ws != cs or v.dtype is not dt or v_cache.dtype is not dt:
             raise SSDError("v and v_cache must have the shapes and type of k and k_cache")
-        (vl, _), (wl, _) = _layers(v, "v", dev), _layers(v_cache, "v_cache", dev)
-    L, B, N, H, D = ks
+    elif v is not v_cache:
+        raise SSDError("v and v_cache go together")
     if slots.dim() != 1:
         raise SSDError("expected slots [T]")
-    T = slots.shape[0]
+    row = slots.shape
     p = p_stride = p_cols = 0
     if path is not None:
         p, p_stride, p_cols = _rows2d(path, "path", B, i32, dev)
-    a = _Append(L, B, N, H, D * k.element_size(), cs[1], cs[2], T, p_cols, 0, kl, vl, cl, wl,
-                _tensor(slots, "slots", torch.int64, (T,), dev),
-                _tensor(owner, "owner", i32, (T,), dev), _tensor(cu, "cu", i32, (B + 1,), dev), p,
-                p_stride)
-    st = lib().ssd_append_path(a, _dev_ptr(dev_status), _use_stream(stream, dev, ()))
+    a = _PACK_APPEND(L, B, N, H, D * k.element_size(), cs[1], cs[2], row[0], p_cols, 0, *kl, *vl,
+                     *cl, *wl, _tensor(slots, "slots", torch.int64, row, dev),
+                     _tensor(owner, "owner", i32, row, dev), _tensor(cu, "cu", i32, (B + 1,), dev),
+                     p, p_stride)
+    st = lib().ssd_append_path(a, None if dev_status is None else _dev_ptr(dev_status),
+                               _use_stream(stream, dev, ()))
     if st:
         _check(st, "ssd_append_path")
+
+
+_FORK = ("tables", "lens", "held", "served", "shares", "free_count")
+
+
+def _fork_views(torch, counts, cols, device):
+    """fork_rows' outputs: in one buffer, each on a 64-byte boundary."""
+    base = torch.empty(sum(n + 15 & ~15 for n in counts), dtype=torch.int32, device=device)
+    views, at = {}, 0
+    for name, n in zip(_FORK, counts):
+        views[name] = base[at:at + n]
+        at += n + 15 & ~15
+    views["tables"] = views["tables"].view(-1, cols)
+    return views
+
+
+def _fork_pointers(o, counts, i32, dev):
+    """Addresses of fork_rows' outputs: views of one buffer, one after the other."""
+    t = o.get("tables")
+    if t is None or t.dtype is not i32 or t.get_device() != dev or t.numel() != counts[0]:
+        raise SSDError("out: expected the dict of an earlier call with these sizes")
+    memory = t.untyped_storage()
+    first = at = memory.data_ptr()
+    ptrs = []
+    for name, n in zip(_FORK, counts):
+        if name not in o or o[name].data_ptr() != at:
+            raise SSDError(f"out: {name} is not that of an earlier call with these sizes")
+        ptrs.append(at)
+        at += (n + 15 & ~15) * 4
+    if at - first > memory.nbytes():
+        raise SSDError("out: expected the dict of an earlier call with these sizes")
+    return ptrs
 
 
 def fork_rows(src, lens, held, tables, shares, free_pages, free_count, page_size, k_cache=None,
@@ -1069,38 +1079,43 @@ def fork_rows(src, lens, held, tables, shares, free_pages, free_count, page_size
     torch = _torch()
     i32 = torch.int32
     dev = src.get_device()
-    if dev < 0 or src.dim() != 1 or lens.dim() != 1 or shares.dim() != 1:
-        raise SSDError("expected src [B], lens [S] and shares [pages] on the GPU")
+    if dev < 0 or src.dim() != 1 or lens.dim() != 1 or shares.dim() != 1 or free_pages.dim() != 1:
+        raise SSDError("expected src [B], lens [S], shares [pages] and free_pages [n] on the GPU")
     _on_current(dev)
-    B, S, pages = src.shape[0], lens.shape[0], shares.shape[0]
+    row, old, pool, stack = src.shape, lens.shape, shares.shape, free_pages.shape
+    B, S, pages = row[0], old[0], pool[0]
     table, stride, cols = _rows2d(tables, "tables", S, i32, dev)
     kl = vl = _NO_LAYERS
-    L = H = row = 0
+    L = H = size = 0
     if k_cache is not None:
-        kl, ks = _layers(k_cache, "k_cache", dev)
-        L, H, row = ks[0], ks[3], ks[4] * k_cache.element_size()
+        ks, kl = _layers(k_cache, "k_cache", dev)
+        L, H, size = ks[0], ks[3], ks[4] * k_cache.element_size()
         if ks[1] != pages or ks[2] != page_size:
             raise SSDError("the caches must have one page for each entry of shares, of page_size "
                            "tokens")
         if v_cache is not None:
-            if v_cache.shape != k_cache.shape or v_cache.dtype is not k_cache.dtype:
+            vs, vl = _layers(v_cache, "v_cache", dev)
+            if vs != ks or v_cache.dtype is not k_cache.dtype:
                 raise SSDError("the caches must have one shape and type")
-            vl, _ = _layers(v_cache, "v_cache", dev)
     elif v_cache is not None:
         raise SSDError("v_cache goes with k_cache")
     o = out if out is not None else {}
-    at = []
-    for name, shape in (("tables", (B, cols)), ("lens", (B,)), ("held", (B,)), ("served", (B,)),
-                        ("shares", (pages,)), ("free_count", (1,))):
-        t = o.get(name)
-        if t is None:
-            t = o[name] = torch.empty(shape, dtype=i32, device=src.device)
-        at.append(_tensor(t, name, i32, shape, dev))
-    a = _Fork(S, B, cols, int(page_size), pages, free_pages.numel(), L, H, row, 0,
-              _tensor(src, "src", i32, (B,), dev), _tensor(lens, "lens", i32, (S,), dev),
-              _tensor(held, "held", i32, (S,), dev), table, stride,
-              _tensor(shares, "shares", i32, (pages,), dev),
-              _tensor(free_pages, "free_pages", i32, free_pages.shape, dev),
-              _tensor(free_count, "free_count", i32, (1,), dev), kl, vl, *at)
-    _launch("fork_rows", a, o, workspace, dev, src.device, dev_status, stream)
+    counts = (B * cols, B, B, B, pages, 1)
+    if "tables" not in o and _FORK_NAMES.isdisjoint(o):
+        if cols < 1:
+            raise SSDError("the tables must have columns")
+        o.update(_fork_views(torch, counts, cols, src.device))
+    ptrs = _fork_pointers(o, counts, i32, dev)
+    a = _PACK_FORK(S, B, cols, int(page_size), pages, stack[0], L, H, size, 0,
+                   _tensor(src, "src", i32, row, dev), _tensor(lens, "lens", i32, old, dev),
+                   _tensor(held, "held", i32, old, dev), table, stride,
+                   _tensor(shares, "shares", i32, pool, dev),
+                   _tensor(free_pages, "free_pages", i32, stack, dev),
+                   _tensor(free_count, "free_count", i32, (1,), dev), *kl, *vl, *ptrs)
+    f = lib()
+    _launch(f.ssd_fork_rows, f.ssd_fork_rows_workspace_size, "ssd_fork_rows", a, o, workspace, dev,
+            src.device, dev_status, stream)
     return o
+
+
+_FORK_NAMES = set(_FORK)

@@ -10,7 +10,7 @@
 #include <cuda_runtime.h>
 #include <limits.h>
 #include <stdint.h>
-#include <stdlib.h>
+
 #include <algorithm>
 
 #include "ssd_attention_dev.cuh"
@@ -206,6 +206,13 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
   };
 
   // ---- heirs; shares so far ----------------------------------------------------------
+  constexpr int kEarly = 4;
+  int early[kEarly];                 // shares, on their way while the rows are looked at
+#pragma unroll
+  for (int j = 0; j < kEarly; ++j) {
+    const int i = gtid + j * threads;
+    early[j] = i < f.num_pages ? f.shares[i] : 0;
+  }
   const int n0 = *f.free_count, n = min(max(n0, 0), f.free_cap);
   for (int s = tid; s < f.S; s += kPlanThreads) {
     const int len = f.lens[s], held = f.held[s];
@@ -228,8 +235,13 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     const int s = s_src[b];
     if (s >= 0 && s_heir[s] >= 0) atomicMin(&s_heir[s], b);
   }
+  for (int j = 0; j < kEarly; ++j) {
+    const int i = gtid + j * threads;
+    if (i < f.num_pages) f.shares_out[i] = max(early[j], 0);
+  }
 #pragma unroll 4
-  for (int i = gtid; i < f.num_pages; i += threads) f.shares_out[i] = max(f.shares[i], 0);
+  for (int i = gtid + kEarly * threads; i < f.num_pages; i += threads)
+    f.shares_out[i] = max(f.shares[i], 0);
   __syncthreads();
   running_sums(s_piece, f.S, s_warp,
                [&](int s) { return s_heir[s] == kNoHeir ? (s_held[s] + 31) >> 5 : 0; });
@@ -242,6 +254,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
   const int asked = s_nth[f.B];
   for (int b = tid; b < f.B; b += kPlanThreads)
     if (s_nth[b] < s_nth[b + 1]) s_taker[s_nth[b]] = b;  // read after the next barriers
+  // the page with the last tokens of the row that this thread's first new one forks
+  auto last_page = [&](int b) {
+    const int s = s_src[b];
+    return f.tables[(int64_t)s * f.table_stride + p.by_page.quotient(s_len[s])];
+  };
+  const int early_page = gtid < f.B && s_nth[gtid] < s_nth[gtid + 1] ? last_page(gtid) : 0;
 
   // ---- pages given back --------------------------------------------------------------------
   const int pieces = s_piece[f.S];
@@ -249,6 +267,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
   const int q0 = min(pieces, warp * per), q1 = min(pieces, q0 + per);
   const bool once = per <= kBatch;   // a warp's pages stay in its registers
   int page[kBatch], place[kBatch];   // -1: none
+  int left[kBatch];                  // holders beside the first, if it goes; 0
   auto load = [&](int q) {           // pieces q .. q + kBatch - 1
     int s = 0;
     if (q < q1) {                    // the row of the first: s_piece[s] <= q < s_piece[s + 1]
@@ -278,30 +297,39 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
         page[i] = -1;
       }
   };
-  auto each = [&](bool first, auto visit) {  // visit(page, place), -1 where there is none
+  auto each = [&](bool first, auto visit) {  // visit(i) of the batch
     for (int q = q0; q < q1; q += kBatch) {
       if (first || !once) load(q);
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) visit(page[i], place[i]);
+      for (int i = 0; i < kBatch; ++i) visit(i);
     }
   };
-  each(true, [&](int pg, int) {
-    if (pg >= 0) p.last[pg] = -1;
+  // Whether a page goes: its last holder ends, and this is the last place that gives it back.
+  auto look = [&](int i) {
+    const bool there = page[i] >= 0;
+    const int x = there ? __ldcg(f.shares_out + page[i]) : 0;
+    const int at = there ? __ldcg(p.last + page[i]) : 0;
+    left[i] = x < 0 && at == place[i] ? x : 0;
+  };
+  each(true, [&](int i) {
+    if (page[i] >= 0) p.last[page[i]] = -1;
   });
   barrier();
-  each(false, [&](int pg, int at) {
-    if (pg >= 0) {
-      atomicSub(f.shares_out + pg, 1);
-      atomicMax(p.last + pg, at);
+  each(false, [&](int i) {
+    if (page[i] >= 0) {
+      atomicSub(f.shares_out + page[i], 1);
+      atomicMax(p.last + page[i], place[i]);
     }
   });
   barrier();
-  // those whose last holder ends, by the last place that gives them back
   int freed = 0;                     // of this warp
-  each(false, [&](int pg, int at) {
-    const bool yes = pg >= 0 && __ldcg(f.shares_out + pg) < 0 && __ldcg(p.last + pg) == at;
-    freed += __popc(__ballot_sync(0xffffffffu, yes));
-  });
+  for (int q = q0; q < q1; q += kBatch) {
+    if (!once) load(q);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) look(i);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) freed += __popc(__ballot_sync(0xffffffffu, left[i] < 0));
+  }
   if (lane == 0) s_count[tid >> 5] = freed;
   __syncthreads();
   const int before_warp =
@@ -320,25 +348,22 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     back += s_total[r];
   }
   const int64_t top = (int64_t)n + back;
-  if (q0 < q1) {
-    each(false, [&](int pg, int at) {
-      const int left = pg >= 0 ? __ldcg(f.shares_out + pg) : 0;
-      const bool yes = left < 0 && __ldcg(p.last + pg) == at;
-      const unsigned all = __ballot_sync(0xffffffffu, yes);
-      if (yes) {
-        const int i = before + __popc(all & ((1u << lane) - 1));
-        if (n + (int64_t)i < f.free_cap) f.free_pages[n + i] = pg;
-        if (left < -1) bad |= SSD_DEV_BAD_PAGE;
-        f.shares_out[pg] = 0;
-        const int taken = back - 1 - i;    // the stack's top goes first
-        if (taken < asked) {
-          p.rows[s_taker[taken]].w = pg;
-          p.copies[taken].y = pg;
-        }
+  each(false, [&](int i) {
+    if (!once) look(i);
+    const unsigned all = __ballot_sync(0xffffffffu, left[i] < 0);
+    if (left[i] < 0) {
+      const int nth = before + __popc(all & ((1u << lane) - 1));
+      if (n + (int64_t)nth < f.free_cap) f.free_pages[n + nth] = page[i];
+      if (left[i] < -1) bad |= SSD_DEV_BAD_PAGE;
+      f.shares_out[page[i]] = 0;
+      const int taken = back - 1 - nth;  // the stack's top goes first
+      if (taken < asked) {
+        p.rows[s_taker[taken]].w = page[i];
+        p.copies[taken].y = page[i];
       }
-      before += __popc(all);
-    });
-  }
+    }
+    before += __popc(all);
+  });
   // ---- the new rows ----------------------------------------------------------------------
   for (int b = gtid; b < f.B; b += threads) {
     const int s = s_src[b];
@@ -358,7 +383,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
           given = nth < back;              // its page is put down where it is given back
           if (!given) row.w = f.free_pages[top - 1 - nth];
           int* copy = reinterpret_cast<int*>(p.copies + nth);
-          copy[0] = f.tables[(int64_t)s * f.table_stride + full];
+          copy[0] = b == gtid ? early_page : last_page(b);
           if (!given) copy[1] = row.w;
           copy[2] = len - full * f.page_size;
         }
@@ -540,17 +565,13 @@ ssd_status ssd_append_path(const ssd_append* a, int32_t* dev_status, void* strea
   if ((int64_t)a->rows * p.g.planes > 0x7fffffff - 64) return SSD_ERR_UNSUPPORTED;
   if (a->rows == 0) return SSD_OK;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  static const int v = getenv("APPEND") ? atoi(getenv("APPEND")) : 0;
-  switch (v) {
-    case 0: return status_of(launch_append<1, 4>(p, s));
-    case 1: return status_of(launch_append<2, 4>(p, s));
-    case 2: return status_of(launch_append<2, 2>(p, s));
-    case 3: return status_of(launch_append<4, 2>(p, s));
-    case 4: return status_of(launch_append<4, 4>(p, s));
-    case 5: return status_of(launch_append<1, 2>(p, s));
-    case 6: return status_of(launch_append<4, 1>(p, s));
-    default: return status_of(launch_append<8, 1>(p, s));
-  }
+  // With more tokens and planes than the GPU has warps a warp takes two planes, and its
+  // loads of places serve both: 64 x 4 rows of 2 KB in 32 layers 5.7 us instead of 6.5, 256 x
+  // 4 of 1.25 KB in 12 layers 5.3 instead of 5.6 (4 loads in flight of each, which short
+  // rows leave idle, 6.2); 5 rows in 32 layers 2.9 instead of 2.3.  (From L2.)
+  if ((int64_t)a->rows * p.g.planes <= (int64_t)64 * std::max(num_sms(), 1))
+    return status_of(launch_append<1, 4>(p, s));
+  return status_of(p.g.chunks >= 128 ? launch_append<2, 4>(p, s) : launch_append<2, 2>(p, s));
 }
 
 size_t ssd_fork_rows_workspace_size(const ssd_fork* f) {
@@ -594,9 +615,10 @@ ssd_status ssd_fork_rows(const ssd_fork* f, void* workspace, size_t workspace_by
     p.groups = (f->page_size + p.group - 1) / p.group;
   }
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // several CTAs share the tables' rows and the counts of shares when there are many
-  static const int lim = getenv("FORKLIM") ? atoi(getenv("FORKLIM")) : 8192;
-  p.ctas = (int64_t)f->S * f->cols + f->num_pages > lim ? kPlanCtas : 1;
+  // Several CTAs share the tables' rows and the counts of shares when there are many: 64 rows
+  // of 77 pages 15.0 us with 8 instead of 17.0 with one, 512 of 143 23.9 instead of 74.7; one
+  // row of 97 10.9 instead of 10.1.
+  p.ctas = (int64_t)f->S * f->cols + f->num_pages > 4096 ? kPlanCtas : 1;
   const int smem = plan_ints(f->S, f->B) * (int)sizeof(int);
   cudaError_t e = cudaSuccess;
   if (smem > 46 * 1024)  // the most that any call needs: the limit is the function's

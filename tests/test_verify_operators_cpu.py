@@ -9,6 +9,50 @@ import pytest
 
 import sampling_ssd_verify_gb300 as ssd
 
+class _TreeAttn(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("B", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("q", ctypes.c_void_p), ("q_seq_stride", ctypes.c_int64),
+                ("q_node_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("k", ssd._Paged), ("v", ssd._Paged), ("k_cache", ssd._Paged), ("v_cache", ssd._Paged),
+                ("tables", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("parent", ctypes.c_char_p),
+                ("out", ctypes.c_void_p), ("out_seq_stride", ctypes.c_int64),
+                ("out_node_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("lse", ctypes.c_void_p), ("cols", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class _Layers(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("layer_stride", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class _Append(ctypes.Structure):
+    _fields_ = [("L", ctypes.c_int32), ("B", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("row_bytes", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("rows", ctypes.c_int32), ("path_cols", ctypes.c_int32), ("pad_", ctypes.c_int32),
+                ("k", _Layers), ("v", _Layers), ("k_cache", _Layers), ("v_cache", _Layers),
+                ("slots", ctypes.c_void_p), ("owner", ctypes.c_void_p), ("cu", ctypes.c_void_p),
+                ("path", ctypes.c_void_p), ("path_stride", ctypes.c_int64)]
+
+
+class _Fork(ctypes.Structure):
+    _fields_ = [("S", ctypes.c_int32), ("B", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("free_cap", ctypes.c_int32), ("L", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("row_bytes", ctypes.c_int32), ("pad_", ctypes.c_int32),
+                ("src", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("held", ctypes.c_void_p),
+                ("tables", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("shares", ctypes.c_void_p), ("free_pages", ctypes.c_void_p),
+                ("free_count", ctypes.c_void_p), ("k_cache", _Layers), ("v_cache", _Layers),
+                ("tables_out", ctypes.c_void_p), ("lens_out", ctypes.c_void_p),
+                ("held_out", ctypes.c_void_p), ("served", ctypes.c_void_p),
+                ("shares_out", ctypes.c_void_p), ("free_out", ctypes.c_void_p)]
+
+
 INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 5
 PTR = 0x10000
 
@@ -20,7 +64,7 @@ def L():
 
 
 def _tree(**kw):
-    a = ssd._TreeAttn(dtype=0, B=2, N=3, Hq=4, Hkv=2, D=64, num_pages=9, page_size=16, q=PTR,
+    a = _TreeAttn(dtype=0, B=2, N=3, Hq=4, Hkv=2, D=64, num_pages=9, page_size=16, q=PTR,
                       q_seq_stride=768, q_node_stride=256, q_head_stride=64,
                       k=(2 * PTR, 384, 128, 64), v=(3 * PTR, 384, 128, 64),
                       k_cache=(4 * PTR, 2048, 128, 64), v_cache=(5 * PTR, 2048, 128, 64),
@@ -71,7 +115,7 @@ def test_tree_attention_refusals(L, kw, status):
 
 def _append(**kw):
     row = (1 << 20, 4096, 256, 128)
-    a = ssd._Append(L=2, B=3, N=4, H=2, row_bytes=128, num_pages=9, page_size=16, rows=0,
+    a = _Append(L=2, B=3, N=4, H=2, row_bytes=128, num_pages=9, page_size=16, rows=0,
                     path_cols=3, pad_=0, k=(PTR, *row), v=(2 * PTR, *row), k_cache=(3 * PTR, *row),
                     v_cache=(4 * PTR, *row), slots=PTR, owner=PTR, cu=PTR, path=PTR, path_stride=3)
     for k, v in kw.items():
@@ -106,7 +150,7 @@ def test_append_path_refusals(L, kw, status):
 
 
 def _fork(**kw):
-    a = ssd._Fork(S=3, B=4, cols=5, page_size=16, num_pages=9, free_cap=8, L=2, H=2, row_bytes=128,
+    a = _Fork(S=3, B=4, cols=5, page_size=16, num_pages=9, free_cap=8, L=2, H=2, row_bytes=128,
                   pad_=0, src=PTR, lens=2 * PTR, held=3 * PTR, tables=4 * PTR, table_stride=5,
                   shares=5 * PTR, free_pages=6 * PTR, free_count=7 * PTR, k_cache=(8 * PTR, *ROW),
                   v_cache=(9 * PTR, *ROW), tables_out=10 * PTR, lens_out=11 * PTR,
@@ -183,3 +227,49 @@ def test_tensors_of_a_gpu_that_is_not_current_are_refused(monkeypatch):
                  lambda: ssd.fork_rows(i, i, i, t, i, i, there(1), 16)):
         with pytest.raises(ssd.SSDError, match="cuda:1.*cuda:0"):
             call()
+
+
+def test_packed_descriptors_are_the_structs():
+    """What the binding packs has the size of the structs, field after field."""
+    for pack, kind, floats in ((ssd._PACK_TREE, _TreeAttn, 1), (ssd._PACK_APPEND, _Append, 0),
+                               (ssd._PACK_FORK, _Fork, 0)):
+        leaves = []
+
+        def walk(prefix, t):
+            for name, f in t._fields_:
+                if issubclass(f, ctypes.Structure):
+                    walk(prefix + [name], f)
+                else:
+                    leaves.append(prefix + [name])
+
+        walk([], kind)
+        values = [i + 1 for i in range(len(leaves))]
+        b = pack(*values)
+        assert len(b) == ctypes.sizeof(kind)
+        if kind is _TreeAttn:            # a pointer to bytes reads them
+            kind = type("T", (ctypes.Structure,), {"_fields_": [
+                (n, ctypes.c_void_p if f is ctypes.c_char_p else f) for n, f in kind._fields_]})
+        x = kind.from_buffer_copy(b)
+        for want, at in zip(values, leaves):
+            y = x
+            for name in at:
+                y = getattr(y, name)
+            assert y == want, at
+
+
+def test_outputs_of_a_fork_are_known_again_and_come_whole():
+    import torch
+
+    counts = (4 * 7, 4, 4, 4, 33, 1)
+    for mode in (torch.inference_mode, torch.no_grad):
+        with mode():
+            o = ssd._fork_views(torch, counts, 7, torch.device("cpu"))
+            assert ssd._fork_pointers(o, counts, torch.int32, -1) == [o[k].data_ptr() for k in ssd._FORK]
+            for name in ssd._FORK:
+                for bad in ({k: v for k, v in o.items() if k != name},
+                            dict(o, **{name: o[name].clone()})):
+                    with pytest.raises(ssd.SSDError):
+                        ssd._fork_pointers(bad, counts, torch.int32, -1)
+            for other in ((4 * 7, 4, 4, 4, 49, 1), (5 * 7, 5, 5, 5, 33, 1), (4 * 7, 20, 4, 4, 33, 1)):
+                with pytest.raises(ssd.SSDError):
+                    ssd._fork_pointers(o, other, torch.int32, -1)
