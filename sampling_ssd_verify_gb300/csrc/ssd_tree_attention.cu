@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <numeric>
 
 #include "ssd_tc_dev.cuh"
 #include "ssd_tree_attention.cuh"
@@ -73,22 +74,32 @@ bool plan(const ssd_tree_attn& a, TreeAttnParams& p, Layout& L) {
     p.q_xor = 0x80008000u;
   }
   p.q_plain = a.scale > 0.f && p.q_and != 0u;
-  // sets of up to eight heads where a token's heads lie closer than its neighbour
-  p.hg = 1;
+  // A worker's CTAs go through the same stretches side by side, up to eight of them: for the
+  // items of a head, which read the same tiles, and for the heads of a set where a token's
+  // heads lie closer than its neighbour.
+  const int most = std::min(8, sms);
+  p.bg = p.hg = 1;
+  for (int n = 2; n <= most; ++n)
+    if (p.blocks % n == 0) p.bg = n;
   if (a.k_cache.head_stride < a.k_cache.token_stride &&
       a.v_cache.head_stride < a.v_cache.token_stride)
-    for (int n = 2; n <= std::min(8, sms); ++n)
+    for (int n = 2; n <= most / p.bg; ++n)
       if (a.Hkv % n == 0) p.hg = n;
   p.sets = a.Hkv / p.hg;
-  p.workers = sms / p.hg;
-  const int64_t items = (int64_t)a.B * p.sets * p.blocks;
+  p.block_sets = p.blocks / p.bg;
+  p.side = p.hg * p.bg;
+  p.workers = sms / p.side;
+  const int64_t items = (int64_t)a.B * p.sets * p.block_sets;
   const int64_t tiles = ((int64_t)a.cols * a.page_size + tile - 1) / tile + (a.N + tile - 1) / tile;
-  if (items * p.hg > 0x7fffffff || items > 0x7fffffff / (tiles + 1)) return false;
-  // boxes have to tile a page and a tile alike, and lie on the copy's grid
-  p.boxes = a.page_size % 8 == 0 && (tile % a.page_size == 0 || a.page_size % tile == 0) &&
-            box_strides(a.k_cache, a.Hkv, a.page_size, a.num_pages) &&
-            box_strides(a.v_cache, a.Hkv, a.page_size, a.num_pages) &&
-            box_strides(a.k, a.Hkv, a.N, a.B) && box_strides(a.v, a.Hkv, a.N, a.B);
+  if (items * p.side > 0x7fffffff || items > 0x7fffffff / (tiles + 1)) return false;
+  // A box's tokens are of one page and one tile.  Small boxes take longer than 16-byte copies:
+  // 64 x 11 nodes over pages of 20 tokens, so boxes of four, 307 us instead of 350 (D = 128)
+  // and 187 instead of 288 (64), but 585 instead of 490 at D = 256, where they are more.
+  p.box_rows = std::gcd(a.page_size, tile);
+  if (p.box_rows < (a.D == 256 ? 8 : 4) || !box_strides(a.k_cache, a.Hkv, a.page_size, a.num_pages) ||
+      !box_strides(a.v_cache, a.Hkv, a.page_size, a.num_pages) ||
+      !box_strides(a.k, a.Hkv, a.N, a.B) || !box_strides(a.v, a.Hkv, a.N, a.B))
+    p.box_rows = 0;
   p.node_rows = std::min(tile, (a.N + 7) / 8 * 8);
   // a block's queries are whole nodes, or all there are
   const ssd_paged q{a.q, a.q_seq_stride, a.q_node_stride, a.q_head_stride};
@@ -101,7 +112,7 @@ bool plan(const ssd_tree_attn& a, TreeAttnParams& p, Layout& L) {
     at += align256(bytes);
     return here;
   };
-  const size_t ctas = (size_t)p.workers * p.hg;
+  const size_t ctas = (size_t)p.workers * p.side;
   L.po = take(2 * ctas * rows * a.D * 4);
   L.pml = take(2 * ctas * rows * 8);
   L.begun = take(ctas * 8);

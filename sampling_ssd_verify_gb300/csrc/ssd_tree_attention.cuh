@@ -22,8 +22,10 @@ struct TreeAttnParams {
   int pairs;               // (node, head) pairs of a sequence's key/value head
   int blocks;              // items of a sequence's key/value head
   int hg, sets;            // key/value heads of a set, sets
-  int workers;             // of hg CTAs each
-  int boxes;               // tiles come by TMA
+  int bg, block_sets;      // items of a head side by side, sets of those
+  int side;                // CTAs of a worker: hg * bg
+  int workers;
+  int box_rows;            // tokens of a box of the cache (0: tiles do not come by TMA)
   int node_rows;           // rows of a box of nodes
   int q_nodes;             // nodes of a box of queries (0: copied row by row)
   int chain;               // the tree is one
@@ -88,7 +90,7 @@ template <int NT>
 __device__ __forceinline__ TreeSplit tree_starts(const TreeAttnParams& p, int w, TreeStart* s_start,
                                              int2* s_warp) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int B = p.a.B, items = p.sets * p.blocks;
+  const int B = p.a.B, items = p.sets * p.block_sets;
   TreeSplit all{0, 0};
   for (int pass = 0; pass < 2; ++pass) {
     int base = 0;
@@ -139,10 +141,10 @@ struct TreeStretch {
 struct TreeWalk {
   int u, u1;               // units still to do
   int b, unit;
-  int w, hh;               // worker, head of a set
+  int w, x;                // worker, its CTA: head of a set, block of a set
 };
 __device__ __forceinline__ bool next_stretch(const TreeAttnParams& p, TreeWalk& k, TreeStretch& s) {
-  const int items = p.sets * p.blocks;
+  const int items = p.sets * p.block_sets;
   while (k.u < k.u1) {
     Seq q = seq_of(p, k.b);
     int n = items * (q.tiles + 1);
@@ -158,15 +160,15 @@ __device__ __forceinline__ bool next_stretch(const TreeAttnParams& p, TreeWalk& 
     k.u += take;
     s.q = q;
     s.b = k.b;
-    const int set = local / p.blocks;
-    s.h = set * p.hg + k.hh;
-    s.mb = local - set * p.blocks;
+    const int set = local / p.block_sets, bb = k.x / p.hg;
+    s.h = set * p.hg + k.x - bb * p.hg;
+    s.mb = (local - set * p.block_sets) * p.bg + bb;
     s.tile0 = max(at - 1, 0);
     s.tile1 = at + take - 1;
     s.end = k.unit + (local + 1) * cost;
-    s.item = (k.b * items + local) * p.hg + k.hh;
+    s.item = (k.b * items + local) * p.side + k.x;
     s.slot = s.tile0 == 0 && s.tile1 == q.tiles
-                 ? -1 : 2 * (k.w * p.hg + k.hh) + (s.tile0 == 0);
+                 ? -1 : 2 * (k.w * p.side + k.x) + (s.tile0 == 0);
     if (s.tile1 > s.tile0) return true;  // not only the unit of the item's start
   }
   return false;

@@ -78,7 +78,8 @@ struct TreeHeader {
   uint64_t q_full, q_empty;         // a stretch's job and queries; its scores are all done
   uint64_t job_read;                // its job is known to the exponentials' threads
   uint64_t s_full[2];               // scores of a tile are there
-  uint64_t p_full[2];               // its weights are
+  uint64_t p_half[2];               // its weights of the first half of the tokens are
+  uint64_t p_full[2];               // all of them are
   uint64_t o_done[2];               // its part of the sums is (by stream, block or parity)
   uint64_t ml_full;                 // both streams' maxima and weights are in place
   uint64_t o_empty;                 // the sums of a stretch have been read
@@ -147,14 +148,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
   start_next();
   if (warp == kMmaWarp) tmem_alloc(&sh.tmem);
-  if (p.boxes && warp == kQueryWarp && lane < 4)
+  if (p.box_rows > 0 && warp == kQueryWarp && lane < 4)
     prefetch_map(lane == 0 ? &kmap : lane == 1 ? &vmap : lane == 2 ? &knodes : &vnodes);
   if (p.q_nodes > 0 && warp == kQueryWarp && lane == 4) prefetch_map(&qmap);
   if (tid == 0) {
     sh.err = 0;
     sh.odd[0] = sh.odd[1] = 0;
     // a tile by boxes: one arrival and its bytes; by copies of the lanes: theirs
-    const int copies = p.boxes ? 1 : 32;
+    const int copies = p.box_rows > 0 ? 1 : 32;
     for (int i = 0; i < S::kSlotsK; ++i) {
       mbar_init(&sh.k_full[i], copies);
       mbar_init(&sh.k_empty[i], 1);
@@ -167,6 +168,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     mbar_init(&sh.q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_half[i], kRows);
       mbar_init(&sh.p_full[i], kRows);
       mbar_init(&sh.o_done[i], 1);
     }
@@ -177,7 +179,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     fence_barrier_init();
   }
   if (tid < a.N) sh.parent[tid] = p.parent[tid];
-  const int w = blockIdx.x / p.hg;
+  const int w = blockIdx.x / p.side;
   const TreeSplit all = tree_starts<kTreeThreads>(p, w, &sh.start, sh.warp_sums);
   fence_before();
   __syncthreads();
@@ -189,7 +191,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   k.u = all.first(w);
   k.u1 = all.first(w + 1);
   k.w = w;
-  k.hh = blockIdx.x - w * p.hg;
+  k.x = blockIdx.x - w * p.side;
   if (k.u < k.u1) {
     k.b = sh.start.b;
     k.unit = sh.start.unit;
@@ -213,10 +215,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           ++use;
         }
       };
-      if (p.boxes) {
-        // a lane per page of a tile: a box of its tokens and 64 dimensions
-        const int rows = min(P, kTile);          // tokens of a box
-        const int boxes = kTile / rows;          // boxes of a whole tile, at most 16
+      if (p.box_rows > 0) {
+        // a lane per box: some tokens of a page, 64 dimensions
+        const int rows = p.box_rows, boxes = kTile / rows;  // tokens; of a whole tile, at most 32
         // Tokens that one block reads are not read again: they leave L2 first.
         uint64_t once, again;
         asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
@@ -246,7 +247,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               }
               const int here = min(kTile, s.q.len - tile * kTile);
               const int n = (here + rows - 1) / rows;  // boxes with tokens
-              const int in_page = boxes == 1 ? tile * kTile % P : 0;
+              const int t = tile * kTile + lane * rows;
+              const int in_page = t - p.by_page.quotient(t) * P;
               if (lane == 0)
                 mbar_arrive_expect_tx(&full[slot], (uint32_t)(n * rows * 128 * S::kPanels));
               __syncwarp();
@@ -464,12 +466,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                  q_op + (((e / 4) * S::kQueryPanel + (e % 4) * 32) >> 4),
                  k_op + (((e / 4) * S::kPanel + (e % 4) * 32) >> 4), score, e > 0);
       };
-      auto sums = [&](uint32_t weights, uint32_t col, bool add) {
+      // half a tile's tokens at a time: the first while the weights of the others are computed
+      auto sums = [&](uint32_t weights, uint32_t col, int half, bool add) {
         const uint64_t v_op = operand(vring + vs * S::kSlot, S::kPanel);
+        constexpr int kSteps = kTile / 32;
 #pragma unroll
-        for (int e = 0; e < kTile / 16; ++e)
+        for (int i = 0; i < kSteps; ++i) {
+          const int e = half * kSteps + i;
           mma_ts(tmem + kColO + col * kColStep, tmem + kColS + weights * kColStep + e * 8,
                  v_op + ((e * 16 * 128) >> 4), sum, add || e > 0);
+        }
       };
       auto turn = [](uint32_t& slot, uint32_t& use, int n) {
         if (++slot == (uint32_t)n) {
@@ -494,11 +500,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               if (j > 0) {
                 if (x == 0 && j == 1 && i > 0)
                   mbar_wait(&sh.o_empty, (i - 1) & 1, &sh.err, p.status);
-                mbar_wait(&sh.p_full[x], (t - 1) & 1, &sh.err, p.status);
+                mbar_wait(&sh.p_half[x], (t - 1) & 1, &sh.err, p.status);
                 if (x == 0) mbar_wait(&sh.v_full[vs], v_use & 1, &sh.err, p.status);
                 fence_after();
+                if (elected()) sums(x, x, 0, j > 1);
+                __syncwarp();
+                mbar_wait(&sh.p_full[x], (t - 1) & 1, &sh.err, p.status);
+                fence_after();
                 if (elected()) {
-                  sums(x, x, j > 1);
+                  sums(x, x, 1, j > 1);
                   commit(&sh.o_done[x]);
                   if (end) commit(&sh.v_empty[vs]);
                 }
@@ -540,11 +550,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             if (j > 0) {
               const uint32_t t = c + j - 1, b = t & 1, o = S::kOne ? 0 : b;
               if (j == 1 && i > 0) mbar_wait(&sh.o_empty, (i - 1) & 1, &sh.err, p.status);
-              mbar_wait(&sh.p_full[b], t >> 1 & 1, &sh.err, p.status);
+              mbar_wait(&sh.p_half[b], t >> 1 & 1, &sh.err, p.status);
               mbar_wait(&sh.v_full[vs], v_use & 1, &sh.err, p.status);
               fence_after();
+              const bool add = j > (S::kOne ? 1 : 2);
+              if (elected()) sums(b, o, 0, add);
+              __syncwarp();
+              mbar_wait(&sh.p_full[b], t >> 1 & 1, &sh.err, p.status);
+              fence_after();
               if (elected()) {
-                sums(b, o, j > (S::kOne ? 1 : 2));
+                sums(b, o, 1, add);
                 commit(&sh.v_empty[vs]);
                 commit(&sh.o_done[b]);
               }
@@ -611,6 +626,45 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         mbar_wait(&sh.s_full[buf], turn, &sh.err, p.status);
         __syncwarp();
         fence_after();
+        if (some && (!S::kByBlocks || b == 0)) {
+          // Zero weights must not meet what is no number (0 * NaN): rows of V past the
+          // last token are whatever the page or the slot held, and a node's values may be
+          // off the path of others.  Those that are no numbers are put aside, and
+          // added at the end to the nodes below theirs.  (Not before the tile's scores: they
+          // follow the sums that had this slot's tile before, so its barrier is at this turn.)
+          const uint32_t nth = all_tiles + (uint32_t)j, slot = nth % S::kSlotsV;
+          mbar_wait(&sh.v_full[slot], nth / S::kSlotsV & 1, &sh.err, p.status);
+          const uint32_t vs = vring + slot * S::kSlot;
+          for (int e = here * 8 + (int)m; e < kTile * 8; e += kRows)
+#pragma unroll
+            for (int d = 0; d < S::kPanels; ++d)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vs + d * S::kPanel +
+                                                                           e * 16),
+                           "r"(0)
+                           : "memory");
+          if (nodes) {
+            for (int e = (int)m; e < here * 8; e += kRows)
+#pragma unroll
+              for (int d = 0; d < S::kPanels; ++d) {
+                const uint32_t where = vs + d * S::kPanel + e * 16;
+                uint32_t y[4], bad = 0;
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                             : "r"(where)
+                             : "memory");
+#pragma unroll
+                for (int z = 0; z < 4; ++z) bad |= odd_mask<T>(y[z]);
+                if (bad) {
+                  sh.odd[i & 1] = (int)i + 1;
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(where),
+                               "r"(y[0] & ~odd_mask<T>(y[0])), "r"(y[1] & ~odd_mask<T>(y[1])),
+                               "r"(y[2] & ~odd_mask<T>(y[2])), "r"(y[3] & ~odd_mask<T>(y[3]))
+                               : "memory");
+                }
+              }
+          }
+          fence_async();
+        }
         if (busy) {
           uint32_t x[kTile / 32][32];
 #pragma unroll
@@ -676,47 +730,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               z[e / 2] = pack2<T>(y.x, y.y);
             }
             tmem_st16(ts + q * 16, z);
+            if (q == kTile / 64 - 1) {
+              tmem_wait_st();
+              fence_before();
+              mbar_arrive(&sh.p_half[buf]);
+            }
           }
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           tmem_wait_st();
-        }
-        if (some && (!S::kByBlocks || b == 0)) {
-          // Zero weights must not meet what is no number (0 * NaN): rows of V past the
-          // last token are whatever the page or the slot held, and a node's values may be
-          // off the path of others.  Those that are no numbers are put aside, and
-          // added at the end to the nodes below theirs.
-          const uint32_t nth = all_tiles + (uint32_t)j, slot = nth % S::kSlotsV;
-          mbar_wait(&sh.v_full[slot], nth / S::kSlotsV & 1, &sh.err, p.status);
-          const uint32_t vs = vring + slot * S::kSlot;
-          for (int e = here * 8 + (int)m; e < kTile * 8; e += kRows)
-#pragma unroll
-            for (int d = 0; d < S::kPanels; ++d)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vs + d * S::kPanel +
-                                                                           e * 16),
-                           "r"(0)
-                           : "memory");
-          if (nodes) {
-            for (int e = (int)m; e < here * 8; e += kRows)
-#pragma unroll
-              for (int d = 0; d < S::kPanels; ++d) {
-                const uint32_t where = vs + d * S::kPanel + e * 16;
-                uint32_t y[4], bad = 0;
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
-                             : "r"(where)
-                             : "memory");
-#pragma unroll
-                for (int z = 0; z < 4; ++z) bad |= odd_mask<T>(y[z]);
-                if (bad) {
-                  sh.odd[i & 1] = (int)i + 1;
-                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(where),
-                               "r"(y[0] & ~odd_mask<T>(y[0])), "r"(y[1] & ~odd_mask<T>(y[1])),
-                               "r"(y[2] & ~odd_mask<T>(y[2])), "r"(y[3] & ~odd_mask<T>(y[3]))
-                               : "memory");
-                }
-              }
-          }
-          fence_async();
+        } else {
+          mbar_arrive(&sh.p_half[buf]);
         }
         fence_before();
         mbar_arrive(&sh.p_full[buf]);
@@ -857,18 +880,19 @@ __global__ void __launch_bounds__(D) tree_join_kernel(const __grid_constant__ Tr
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   wait_previous();
   const int2 begun = p.begun[cta];
-  const int item = begun.x, np = begun.y, hh = cta % p.hg;
+  const int item = begun.x, np = begun.y;
   if (item < 0) return;
   const int i = group * 8 + (lane & 7);
-  int rest = item / p.hg;
-  const int mb = rest % p.blocks;
-  rest /= p.blocks;
-  const int h = rest % p.sets * p.hg + hh, seq = rest / p.sets;
+  const int x = cta % p.side, bb = x / p.hg;
+  int rest = item / p.side;
+  const int mb = rest % p.block_sets * p.bg + bb;
+  rest /= p.block_sets;
+  const int h = rest % p.sets * p.hg + x - bb * p.hg, seq = rest / p.sets;
   const int pair = mb * kPairs + i;
   const bool mine = i < kPairs && pair < p.pairs;
   const int at = mine ? i : 0;
   // the partial of the worker that began it, then those of workers that went on
-  auto slot_of = [&](int j) { return 2 * (cta + j * p.hg) + (j == 0); };
+  auto slot_of = [&](int j) { return 2 * (cta + j * p.side) + (j == 0); };
   // the loads of four partials are in flight together
   constexpr int kBatch = 4;
   const int d = warp * 32 + (lane >> 3) * 4;
@@ -930,10 +954,9 @@ cudaError_t launch_tree(const TreeAttnParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   CUtensorMap km{}, vm{}, kn{}, vn{}, qm{};
   const ssd_tree_attn& a = p.a;
-  if (p.boxes) {
-    const int rows = std::min(a.page_size, tree_tile(D));
-    if (!box_map(&km, a.dtype, a.k_cache, D, a.Hkv, a.page_size, a.num_pages, rows) ||
-        !box_map(&vm, a.dtype, a.v_cache, D, a.Hkv, a.page_size, a.num_pages, rows) ||
+  if (p.box_rows > 0) {
+    if (!box_map(&km, a.dtype, a.k_cache, D, a.Hkv, a.page_size, a.num_pages, p.box_rows) ||
+        !box_map(&vm, a.dtype, a.v_cache, D, a.Hkv, a.page_size, a.num_pages, p.box_rows) ||
         !box_map(&kn, a.dtype, a.k, D, a.Hkv, a.N, a.B, p.node_rows) ||
         !box_map(&vn, a.dtype, a.v, D, a.Hkv, a.N, a.B, p.node_rows))
       return cudaErrorInvalidValue;
@@ -942,14 +965,14 @@ cudaError_t launch_tree(const TreeAttnParams& p, cudaStream_t s) {
       !box_map(&qm, a.dtype, {a.q, a.q_seq_stride, a.q_node_stride, a.q_head_stride}, D, a.Hq, a.N,
                a.B, p.q_nodes, p.gqa))
     return cudaErrorInvalidValue;
-  kernel<<<p.workers * p.hg, kTreeThreads, smem, s>>>(p, km, vm, kn, vn, qm);
+  kernel<<<p.workers * p.side, kTreeThreads, smem, s>>>(p, km, vm, kn, vn, qm);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t c{};
-  c.gridDim = dim3((unsigned)(p.workers * p.hg * p.join_groups));
+  c.gridDim = dim3((unsigned)(p.workers * p.side * p.join_groups));
   c.blockDim = dim3(D);
   c.stream = s;
   c.attrs = &early;
