@@ -922,11 +922,16 @@ def tree_attention(q, k, v, k_cache, v_cache, tables, lens, parent=None, scale=N
     torch = _torch()
     i32 = torch.int32
     qs, ks, cs, dt = q.shape, k.shape, k_cache.shape, q.dtype
-    if len(qs) != 4 or len(ks) != 4 or len(cs) != 4 or v.shape != ks or v_cache.shape != cs or \
-            ks[:2] != qs[:2] or ks[3] != qs[3] or cs[2:] != ks[2:]:
+    try:
+        B, N, Hq, D = qs
+        kB, kN, Hkv, kD = ks
+        pages, page_size, cH, cD = cs
+        fits = kB == B and kN == N and kD == D and cH == Hkv and cD == D
+    except ValueError:
+        fits = False
+    if not fits or v.shape != ks or v_cache.shape != cs:
         raise SSDError("expected q [B, N, Hq, D], k and v [B, N, Hkv, D] and caches [pages, "
                        "page_size, Hkv, D]")
-    B, N, Hq, D = qs
     code = SSD_BF16 if dt is torch.bfloat16 else SSD_F16 if dt is torch.float16 else -1
     dev = q.get_device()
     if code < 0 or k.dtype is not dt or v.dtype is not dt or k_cache.dtype is not dt or \
@@ -935,7 +940,8 @@ def tree_attention(q, k, v, k_cache, v_cache, tables, lens, parent=None, scale=N
     if dev < 0 or k.get_device() != dev or v.get_device() != dev or \
             k_cache.get_device() != dev or v_cache.get_device() != dev:
         raise SSDError("q, the nodes and the caches must be on one GPU")
-    _on_current(dev)
+    if torch._C._cuda_getDevice() != dev:
+        _on_current(dev)
     o = out if out is not None else {}
     y = o.get("out")
     if y is None:
@@ -944,16 +950,17 @@ def tree_attention(q, k, v, k_cache, v_cache, tables, lens, parent=None, scale=N
         raise SSDError("out must have q's shape, type and device")
     at = 0
     if lse:
-        if o.get("lse") is None:
-            o["lse"] = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device)
-        at = _tensor(o["lse"], "lse", torch.float32, (B, N, Hq), dev)
+        z = o.get("lse")
+        if z is None:
+            z = o["lse"] = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device)
+        at = _tensor(z, "lse", torch.float32, (B, N, Hq), dev)
     qa, ya, ka, va, kc, vc = (q.stride(), y.stride(), k.stride(), v.stride(), k_cache.stride(),
                               v_cache.stride())
     if qa[3] != 1 or ya[3] != 1 or ka[3] != 1 or va[3] != 1 or kc[3] != 1 or vc[3] != 1:
         raise SSDError("the head dimension must be contiguous")
     tree, kept = (0, None) if parent is None else _parent_address(parent, N)
     table, stride, cols = _rows2d(tables, "tables", B, i32, dev)
-    a = _PACK_TREE(code, B, N, Hq, ks[2], D, cs[0], cs[1], q.data_ptr(), qa[0], qa[1], qa[2],
+    a = _PACK_TREE(code, B, N, Hq, Hkv, D, pages, page_size, q.data_ptr(), qa[0], qa[1], qa[2],
                    k.data_ptr(), ka[0], ka[1], ka[2], v.data_ptr(), va[0], va[1], va[2],
                    k_cache.data_ptr(), kc[0], kc[1], kc[2], v_cache.data_ptr(), vc[0], vc[1],
                    vc[2], table, _tensor(lens, "lens", i32, (B,), dev), stride, tree,
@@ -981,6 +988,13 @@ def _layers(t, name, dev):
     return (1, *shape), (t.data_ptr(), 0, s[0] * es, s[1] * es, s[2] * es)
 
 
+def _like(t, other, layers, name, dev):
+    """ssd_layers of a tensor of `other`'s shape and type, whose own are `layers`."""
+    if t.stride() == other.stride() and t.get_device() == dev:
+        return (t.data_ptr(), *layers[1:])
+    return _layers(t, name, dev)[1]
+
+
 _NO_LAYERS = (0, 0, 0, 0, 0)
 
 
@@ -1000,7 +1014,8 @@ def append_path(k, v, k_cache, v_cache, slots, owner, cu, path=None, dev_status=
     dev, dt = k_cache.get_device(), k_cache.dtype
     if dev < 0:
         raise SSDError("expected caches on the GPU")
-    _on_current(dev)
+    if torch._C._cuda_getDevice() != dev:
+        _on_current(dev)
     ks, kl = _layers(k, "k", dev)
     cs, cl = _layers(k_cache, "k_cache", dev)
     L, B, N, H, D = ks
@@ -1008,10 +1023,10 @@ def append_path(k, v, k_cache, v_cache, slots, owner, cu, path=None, dev_status=
         raise SSDError("nodes and caches must share the layers, heads and type")
     vl = wl = _NO_LAYERS
     if v is not None and v_cache is not None:
-        vs, vl = _layers(v, "v", dev)
-        ws, wl = _layers(v_cache, "v_cache", dev)
-        if vs != ks or ws != cs or v.dtype is not dt or v_cache.dtype is not dt:
+        if v.shape != k.shape or v_cache.shape != k_cache.shape or v.dtype is not dt or \
+                v_cache.dtype is not dt:
             raise SSDError("v and v_cache must have the shapes and type of k and k_cache")
+        vl, wl = _like(v, k, kl, "v", dev), _like(v_cache, k_cache, cl, "v_cache", dev)
     elif v is not v_cache:
         raise SSDError("v and v_cache go together")
     if slots.dim() != 1:
@@ -1052,8 +1067,10 @@ def _fork_pointers(o, counts, i32, dev):
     memory = t.untyped_storage()
     first = at = memory.data_ptr()
     ptrs = []
+    get = o.get
     for name, n in zip(_FORK, counts):
-        if name not in o or o[name].data_ptr() != at:
+        t = get(name)
+        if t is None or t.data_ptr() != at:
             raise SSDError(f"out: {name} is not that of an earlier call with these sizes")
         ptrs.append(at)
         at += (n + 15 & ~15) * 4
@@ -1079,10 +1096,11 @@ def fork_rows(src, lens, held, tables, shares, free_pages, free_count, page_size
     torch = _torch()
     i32 = torch.int32
     dev = src.get_device()
-    if dev < 0 or src.dim() != 1 or lens.dim() != 1 or shares.dim() != 1 or free_pages.dim() != 1:
-        raise SSDError("expected src [B], lens [S], shares [pages] and free_pages [n] on the GPU")
-    _on_current(dev)
     row, old, pool, stack = src.shape, lens.shape, shares.shape, free_pages.shape
+    if dev < 0 or not len(row) == len(old) == len(pool) == len(stack) == 1:
+        raise SSDError("expected src [B], lens [S], shares [pages] and free_pages [n] on the GPU")
+    if torch._C._cuda_getDevice() != dev:
+        _on_current(dev)
     B, S, pages = row[0], old[0], pool[0]
     table, stride, cols = _rows2d(tables, "tables", S, i32, dev)
     kl = vl = _NO_LAYERS
@@ -1094,9 +1112,9 @@ def fork_rows(src, lens, held, tables, shares, free_pages, free_count, page_size
             raise SSDError("the caches must have one page for each entry of shares, of page_size "
                            "tokens")
         if v_cache is not None:
-            vs, vl = _layers(v_cache, "v_cache", dev)
-            if vs != ks or v_cache.dtype is not k_cache.dtype:
+            if v_cache.shape != k_cache.shape or v_cache.dtype is not k_cache.dtype:
                 raise SSDError("the caches must have one shape and type")
+            vl = _like(v_cache, k_cache, kl, "v_cache", dev)
     elif v_cache is not None:
         raise SSDError("v_cache goes with k_cache")
     o = out if out is not None else {}

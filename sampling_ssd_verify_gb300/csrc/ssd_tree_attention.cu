@@ -100,6 +100,8 @@ bool plan(const ssd_tree_attn& a, TreeAttnParams& p, Layout& L) {
       !box_strides(a.v_cache, a.Hkv, a.page_size, a.num_pages) ||
       !box_strides(a.k, a.Hkv, a.N, a.B) || !box_strides(a.v, a.Hkv, a.N, a.B))
     p.box_rows = 0;
+  p.wide_rows = ((uintptr_t)a.out | 2 * (uintptr_t)(a.out_seq_stride | a.out_node_stride |
+                                                    a.out_head_stride)) % 32 == 0;
   p.node_rows = std::min(tile, (a.N + 7) / 8 * 8);
   // a block's queries are whole nodes, or all there are
   const ssd_paged q{a.q, a.q_seq_stride, a.q_node_stride, a.q_head_stride};

@@ -18,6 +18,7 @@ struct TreeAttnParams {
   float scale_log2;        // |scale| * log2(e): scores in base 2
   uint32_t q_and, q_xor;   // of pairs of the queries' elements, which have the scale's sign
   int q_plain;             // they change nothing
+  int wide_rows;           // rows of the output are on 32-byte boundaries
   int gqa;                 // query heads per key/value head
   int pairs;               // (node, head) pairs of a sequence's key/value head
   int blocks;              // items of a sequence's key/value head

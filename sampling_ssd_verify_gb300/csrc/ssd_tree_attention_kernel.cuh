@@ -109,6 +109,13 @@ __device__ __forceinline__ uint32_t odd_mask(uint32_t x) {
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 
+// 32 bytes, a whole sector, to an address of that alignment.
+__device__ __forceinline__ void store32(void* to, const uint32_t (&z)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(z[0]),
+               "r"(z[1]), "r"(z[2]), "r"(z[3]), "r"(z[4]), "r"(z[5]), "r"(z[6]), "r"(z[7])
+               : "memory");
+}
+
 // Leaves in ok (a bit per node, from node `at` on) those on node u's path.
 template <int TILE>
 __device__ __forceinline__ void on_path(uint32_t (&ok)[TILE / 32], const uint8_t* parent,
@@ -836,13 +843,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             T* out = static_cast<T*>(a.out) + job.seq * a.out_seq_stride +
                      node * a.out_node_stride + head * a.out_head_stride + col;
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t z[4];
+            for (int e = 0; e < 32; e += 16) {
+              uint32_t z[8];
 #pragma unroll
-              for (int g = 0; g < 4; ++g)
+              for (int g = 0; g < 8; ++g)
                 z[g] = pack2<T>(__uint_as_float(y[e + 2 * g]) * inv,
                                 __uint_as_float(y[e + 2 * g + 1]) * inv);
-              *reinterpret_cast<uint4*>(out + e) = make_uint4(z[0], z[1], z[2], z[3]);
+              if (p.wide_rows) {
+                store32(out + e, z);
+              } else {
+                *reinterpret_cast<uint4*>(out + e) = make_uint4(z[0], z[1], z[2], z[3]);
+                *reinterpret_cast<uint4*>(out + e + 8) = make_uint4(z[4], z[5], z[6], z[7]);
+              }
             }
           } else {
             float* out = p.po + part_at<D>(job.slot, BLOCKS * kRows, row, col);
