@@ -62,7 +62,7 @@ bool plan(const ssd_tree_attn& a, TreeAttnParams& p, Layout& L) {
   p.pairs = a.N * p.gqa;
   const int rows = 128 * tree_blocks(a.D, p.pairs);
   p.blocks = (p.pairs + rows - 1) / rows;
-  p.join_groups = (std::min(p.pairs, rows) + 7) / 8;
+  p.part_rows = (std::min(p.pairs, rows) + 7) / 8 * 8;
   // -q for a negative scale, 0 for none: the maximum is taken before the scale
   p.scale_log2 = (float)(std::fabs((double)a.scale) * 1.4426950408889634);
   p.q_and = ~0u;
@@ -115,8 +115,8 @@ bool plan(const ssd_tree_attn& a, TreeAttnParams& p, Layout& L) {
     return here;
   };
   const size_t ctas = (size_t)p.workers * p.side;
-  L.po = take(2 * ctas * rows * a.D * 4);
-  L.pml = take(2 * ctas * rows * 8);
+  L.po = take(2 * ctas * p.part_rows * a.D * 4);
+  L.pml = take(2 * ctas * p.part_rows * 8);
   L.begun = take(ctas * 8);
   L.total = at;
   return true;

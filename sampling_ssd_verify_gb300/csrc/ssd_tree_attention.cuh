@@ -30,9 +30,9 @@ struct TreeAttnParams {
   int node_rows;           // rows of a box of nodes
   int q_nodes;             // nodes of a box of queries (0: copied row by row)
   int chain;               // the tree is one
-  int join_groups;         // groups of eight pairs of an item
-  float* po;               // [2 * CTAs, D / 4, pairs of an item, 4] sums (part_at)
-  float2* pml;             // [2 * CTAs, pairs of an item] largest score (base 2), weight
+  int part_rows;           // pairs of an item, in eights: rows of a partial
+  float* po;               // [2 * CTAs, D / 4, part_rows, 4] sums (part_at)
+  float2* pml;             // [2 * CTAs, part_rows] largest score (base 2), weight
   int2* begun;             // [CTAs] item that it began and did not end, or -1, and its partials
   int32_t* status;
   uint8_t parent[kTreeNodes];  // of node u > 0; 0 for node 0

@@ -794,7 +794,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const bool whole = job.slot < 0;
       if (mine && (S::kByBlocks || b == 0)) {
         if (!whole)
-          p.pml[(int64_t)job.slot * (BLOCKS * kRows) + row] = make_float2(mx, sum);
+          p.pml[(int64_t)job.slot * p.part_rows + row] = make_float2(mx, sum);
         else if (a.lse)
           a.lse[((int64_t)job.seq * a.N + node) * a.Hq + head] =
               (mx + log2f(sum)) * 0.6931471805599453f;
@@ -857,10 +857,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               }
             }
           } else {
-            float* out = p.po + part_at<D>(job.slot, BLOCKS * kRows, row, col);
+            float* out = p.po + part_at<D>(job.slot, p.part_rows, row, col);
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(out + e * (BLOCKS * kRows)) =
+              *reinterpret_cast<uint4*>(out + e * p.part_rows) =
                   make_uint4(y[e], y[e + 1], y[e + 2], y[e + 3]);
           }
         }
@@ -886,9 +886,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // eight pairs at a time.
 template <typename T, int D, int BLOCKS>
 __global__ void __launch_bounds__(D) tree_join_kernel(const __grid_constant__ TreeAttnParams p) {
-  constexpr int kPairs = BLOCKS * kRows;
   const ssd_tree_attn& a = p.a;
-  const int cta = blockIdx.x / p.join_groups, group = blockIdx.x - cta * p.join_groups;
+  const int groups = p.part_rows / 8;
+  const int cta = blockIdx.x / groups, group = blockIdx.x - cta * groups;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   wait_previous();
   const int2 begun = p.begun[cta];
@@ -900,9 +900,8 @@ __global__ void __launch_bounds__(D) tree_join_kernel(const __grid_constant__ Tr
   const int mb = rest % p.block_sets * p.bg + bb;
   rest /= p.block_sets;
   const int h = rest % p.sets * p.hg + x - bb * p.hg, seq = rest / p.sets;
-  const int pair = mb * kPairs + i;
-  const bool mine = i < kPairs && pair < p.pairs;
-  const int at = mine ? i : 0;
+  const int pair = mb * (BLOCKS * kRows) + i;
+  const bool mine = pair < p.pairs;
   // the partial of the worker that began it, then those of workers that went on
   auto slot_of = [&](int j) { return 2 * (cta + j * p.side) + (j == 0); };
   // the loads of four partials are in flight together
@@ -915,12 +914,15 @@ __global__ void __launch_bounds__(D) tree_join_kernel(const __grid_constant__ Tr
     float4 x[kBatch][2];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const int slot = slot_of(min(j0 + j, np - 1));
-      ml[j] = p.pml[(int64_t)slot * kPairs + at];
-      if (j0 + j >= np) ml[j] = make_float2(-INFINITY, 0.f);
+      ml[j] = make_float2(-INFINITY, 0.f);
+      if (j0 + j < np) {
+        const int slot = slot_of(j0 + j);
+        ml[j] = p.pml[(int64_t)slot * p.part_rows + i];
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        x[j][e] = *reinterpret_cast<const float4*>(p.po + part_at<D>(slot, kPairs, at, d + e * 16));
+        for (int e = 0; e < 2; ++e)
+          x[j][e] =
+              *reinterpret_cast<const float4*>(p.po + part_at<D>(slot, p.part_rows, i, d + e * 16));
+      }
     }
     float now = top;
 #pragma unroll
@@ -984,7 +986,7 @@ cudaError_t launch_tree(const TreeAttnParams& p, cudaStream_t s) {
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t c{};
-  c.gridDim = dim3((unsigned)(p.workers * p.side * p.join_groups));
+  c.gridDim = dim3((unsigned)(p.workers * p.side * (p.part_rows / 8)));
   c.blockDim = dim3(D);
   c.stream = s;
   c.attrs = &early;
