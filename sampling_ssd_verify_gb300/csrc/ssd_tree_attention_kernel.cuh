@@ -38,6 +38,8 @@ constexpr int kCopyK = 8, kCopyV = 9, kMmaWarp = 10, kQueryWarp = 11;
 constexpr int kRegsSoftmax = 208, kRegsOther = 88;
 constexpr float kRise = 8.f;              // scores may pass the kept maximum by this (base 2)
 
+constexpr int kColS = 0, kColStep = 128;  // scores (and weights) of a buffer in tensor memory
+
 // BLOCKS: of an item.  The rings and the queries take 224 KB, one CTA per SM.
 template <int D, int BLOCKS> struct TreeShape {
   static constexpr int kTile = tree_tile(D);
@@ -46,8 +48,11 @@ template <int D, int BLOCKS> struct TreeShape {
   static constexpr int kSlot = kPanels * kPanel;      // K or V of a tile
   static constexpr int kQueryPanel = kRows * 128;
   static constexpr int kQueries = kPanels * kQueryPanel;  // of a block
-  static constexpr int kSlotsK = D == 64 ? 6 : 3;
-  static constexpr int kSlotsV = D == 64 ? 6 : D == 128 && BLOCKS == 1 ? 3 : 2;
+  // V stays until its weights are there, K not: two contexts of 131072 tokens in pages of 64
+  // take 162 us with 2 and 4, 172 with 3 and 3 (16 tokens: 169 and 168).  At D = 256 copies of
+  // 16 bytes want it the other way: 548 us with 2 and 3, 492 with 3 and 2 (boxes 359, 363).
+  static constexpr int kSlotsK = D == 64 ? 5 : D == 128 ? 2 : 3;
+  static constexpr int kSlotsV = D == 64 ? 7 : D == 128 ? (BLOCKS == 1 ? 4 : 3) : 2;
   static constexpr int kSmem = kHeaderBytes + (kSlotsK + kSlotsV) * kSlot + BLOCKS * kQueries;
   static_assert(kSmem <= 227 << 10, "shared memory");
   // How the two warpgroups of exponentials share the work:
@@ -57,10 +62,12 @@ template <int D, int BLOCKS> struct TreeShape {
   static constexpr bool kByBlocks = BLOCKS == 2;
   static constexpr bool kOne = D == 256;
   static constexpr bool kByTiles = !kByBlocks && !kOne;
+  // Buffers of scores, and where the sums are.  Where the sums leave room for three, the scores
+  // are two tiles ahead of the sums, and the exponentials need not wait for them.
+  static constexpr int kBuffers = kByTiles && D == 64 ? 3 : 2;
+  static constexpr int kLead = kBuffers - 1;
+  static constexpr int kColO = kColS + kBuffers * kColStep, kStepO = kBuffers == 3 ? 64 : 128;
 };
-
-// tensor memory columns: scores (and weights) of two streams or tiles, their sums
-constexpr int kColS = 0, kColO = 256, kColStep = 128;
 
 // What the product and exponential warps know of a stretch.
 struct TreeJob {
@@ -73,14 +80,14 @@ struct TreeJob {
 
 struct TreeHeader {
   float2 ml[2][kRows];              // the streams' maxima and weights, handed over at the end
-  uint64_t k_full[6], k_empty[6];   // ring slots
-  uint64_t v_full[6], v_empty[6];
+  uint64_t k_full[7], k_empty[7];   // ring slots
+  uint64_t v_full[7], v_empty[7];
   uint64_t q_full, q_empty;         // a stretch's job and queries; its scores are all done
   uint64_t job_read;                // its job is known to the exponentials' threads
-  uint64_t s_full[2];               // scores of a tile are there
-  uint64_t p_half[2];               // its weights of the first half of the tokens are
-  uint64_t p_full[2];               // all of them are
-  uint64_t o_done[2];               // its part of the sums is (by stream, block or parity)
+  uint64_t s_full[3];               // scores of a tile are there, by buffer
+  uint64_t p_half[3];               // its weights of the first half of the tokens are
+  uint64_t p_full[3];               // all of them are
+  uint64_t o_done[4];               // its part of the sums is, by block or by tile
   uint64_t ml_full;                 // both streams' maxima and weights are in place
   uint64_t o_empty;                 // the sums of a stretch have been read
   uint64_t drained;
@@ -173,12 +180,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
     mbar_init(&sh.q_full, 32);
     mbar_init(&sh.q_empty, 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 3; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_half[i], kRows);
       mbar_init(&sh.p_full[i], kRows);
-      mbar_init(&sh.o_done[i], 1);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.o_done[i], 1);
     mbar_init(&sh.job_read, kSoftmax);
     mbar_init(&sh.ml_full, kSoftmax);
     mbar_init(&sh.o_empty, kSoftmax);
@@ -480,7 +487,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
           const int e = half * kSteps + i;
-          mma_ts(tmem + kColO + col * kColStep, tmem + kColS + weights * kColStep + e * 8,
+          mma_ts(tmem + S::kColO + col * S::kStepO, tmem + kColS + weights * kColStep + e * 8,
                  v_op + ((e * 16 * 128) >> 4), sum, add || e > 0);
         }
       };
@@ -496,7 +503,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (n == 0) break;
         const bool two = S::kByBlocks && sh.job[i & 1].pairs > kRows;
         fence_after();
-        for (int j = 0; j <= n; ++j) {
+        // a step more for each tile that the sums are behind; n tiles may be fewer than that
+        for (int j = 0; j < n + S::kLead; ++j) {
           if constexpr (S::kByBlocks) {
             // a block's weights, then its next scores in their place
 #pragma unroll
@@ -537,38 +545,40 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
           } else {
             auto next_scores = [&] {
-              const uint32_t t = c + j;
+              const uint32_t t = c + j, buf = t % S::kBuffers;
               mbar_wait(&sh.k_full[ks], k_use & 1, &sh.err, p.status);
               fence_after();
               if (elected()) {
-                scores(0, t & 1);
-                commit(&sh.s_full[t & 1]);
+                scores(0, buf);
+                commit(&sh.s_full[buf]);
                 commit(&sh.k_empty[ks]);
                 if (j == n - 1) commit(&sh.q_empty);
               }
               __syncwarp();
               turn(ks, k_use, S::kSlotsK);
             };
-            // the scores of a tile go before the sums of the one before, but where they
+            // the scores of a tile go before the sums of an earlier one, but where they
             // have to wait for its keys
-            const bool late = j > 0 && j < n &&
+            const bool late = j >= S::kLead && j < n &&
                               !__any_sync(0xffffffffu, mbar_try_wait(&sh.k_full[ks], k_use & 1));
             if (j < n && !late) next_scores();
-            if (j > 0) {
-              const uint32_t t = c + j - 1, b = t & 1, o = S::kOne ? 0 : b;
-              if (j == 1 && i > 0) mbar_wait(&sh.o_empty, (i - 1) & 1, &sh.err, p.status);
-              mbar_wait(&sh.p_half[b], t >> 1 & 1, &sh.err, p.status);
+            if (j >= S::kLead) {
+              const int jj = j - S::kLead;
+              const uint32_t t = c + jj, buf = t % S::kBuffers, o = S::kOne ? 0 : t & 1;
+              const uint32_t at = t / S::kBuffers & 1;
+              if (jj == 0 && i > 0) mbar_wait(&sh.o_empty, (i - 1) & 1, &sh.err, p.status);
+              mbar_wait(&sh.p_half[buf], at, &sh.err, p.status);
               mbar_wait(&sh.v_full[vs], v_use & 1, &sh.err, p.status);
               fence_after();
-              const bool add = j > (S::kOne ? 1 : 2);
-              if (elected()) sums(b, o, 0, add);
+              const bool add = jj >= (S::kOne ? 1 : 2);
+              if (elected()) sums(buf, o, 0, add);
               __syncwarp();
-              mbar_wait(&sh.p_full[b], t >> 1 & 1, &sh.err, p.status);
+              mbar_wait(&sh.p_full[buf], at, &sh.err, p.status);
               fence_after();
               if (elected()) {
-                sums(b, o, 1, add);
+                sums(buf, o, 1, add);
                 commit(&sh.v_empty[vs]);
-                commit(&sh.o_done[b]);
+                commit(&sh.o_done[t & 3]);
               }
               __syncwarp();
               turn(vs, v_use, S::kSlotsV);
@@ -590,7 +600,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     const uint32_t b = warp >> 2, m = tid & (kRows - 1);
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
     const uint32_t acc = S::kOne ? 0 : b;        // its sums
-    const uint32_t to = tmem + lanes + kColO + acc * kColStep;
+    const uint32_t to = tmem + lanes + S::kColO + acc * S::kStepO;
     uint32_t c = 0;                              // tiles before the stretch (its block's)
     uint32_t all_tiles = 0;                      // before the stretch, of any block
     for (uint32_t i = 0;; ++i) {
@@ -614,8 +624,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       for (int j = j0; j < n; j += step) {
         const uint32_t t = c + j;
         // where its scores are, and the parity of their turn
-        const uint32_t buf = S::kOne ? t & 1 : b;
-        const uint32_t turn = (S::kByBlocks ? t : t >> 1) & 1;
+        const uint32_t buf = S::kByBlocks ? b : t % S::kBuffers;
+        const uint32_t turn = (S::kByBlocks ? t : t / S::kBuffers) & 1;
         const uint32_t ts = tmem + lanes + kColS + buf * kColStep;
         const bool nodes = j >= cached;
         const int at = nodes ? (j - cached) * kTile : j * kTile;
@@ -706,9 +716,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           if (j > j0 && __any_sync(0xffffffffu, move)) {
             const float f = move ? exp2_fast(old - off) : 1.f;
             l *= f;
-            const uint32_t done = S::kOne ? (t - 1) & 1 : b;  // of the tile before
-            const uint32_t turns = S::kByTiles ? (t >> 1) - 1 : S::kOne ? (t - 1) >> 1 : t - 1;
-            mbar_wait(&sh.o_done[done], turns & 1, &sh.err, p.status);
+            // the sums of the tile before are done; of the four barriers each tile's was at
+            // this turn when its scores came, two or three tiles after an earlier one's sums
+            const uint32_t before = t - (S::kByTiles ? 2 : 1);
+            mbar_wait(&sh.o_done[S::kByBlocks ? b : before & 3],
+                      (S::kByBlocks ? before : before >> 2) & 1, &sh.err, p.status);
             fence_after();
 #pragma unroll 1
             for (int q = 0; q < D; q += 8) {     // few registers: the scores have 128
@@ -760,11 +772,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (b == 0) sh.ml[0][m] = make_float2(top, l);
         mbar_arrive(&sh.ml_full);
         mbar_wait(&sh.ml_full, i & 1, &sh.err, p.status);
-        mbar_wait(&sh.o_done[(c + n - 1) & 1], (c + n - 1) >> 1 & 1, &sh.err, p.status);
+        mbar_wait(&sh.o_done[(c + n - 1) & 3], (c + n - 1) >> 2 & 1, &sh.err, p.status);
       } else {
         if (j0 < n) {
-          const uint32_t last = S::kByTiles ? (c + j0 + ((n - 1 - j0) & ~1)) >> 1 : c + n - 1;
-          mbar_wait(&sh.o_done[b], last & 1, &sh.err, p.status);
+          const uint32_t last = c + (S::kByTiles ? j0 + ((n - 1 - j0) & ~1) : n - 1);
+          mbar_wait(&sh.o_done[S::kByBlocks ? b : last & 3],
+                    (S::kByBlocks ? last : last >> 2) & 1, &sh.err, p.status);
         }
         if (i > 0) mbar_wait(&sh.o_empty, (i - 1) & 1, &sh.err, p.status);  // ml has been read
         sh.ml[b][m] = make_float2(top, l);
@@ -803,7 +816,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
       constexpr int kCols = S::kByBlocks ? D : D / 2;  // of this warpgroup
       const uint32_t first = S::kByBlocks ? 0 : b * kCols;
-      const uint32_t other = tmem + lanes + kColO + (b ^ 1) * kColStep;
+      const uint32_t other = tmem + lanes + S::kColO + (b ^ 1) * S::kStepO;
       if (busy && mine_has | other_has) {
 #pragma unroll 1
         for (int q = 0; q < kCols; q += 32) {
