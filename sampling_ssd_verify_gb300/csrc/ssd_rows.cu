@@ -83,11 +83,13 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int page = (int)(slot / a.page_size), in_page = (int)(slot - (int64_t)page * a.page_size);
   const char* from[PLANES];
   char* to[PLANES];
+  int side[PLANES];                  // the plane that keys or values are told by
 #pragma unroll
   for (int x = 0; x < PLANES; ++x) {
     const int j = min(group * PLANES + x, p.g.planes - 1);
     const ssd_layers& k = side_of(a.k, a.v, p.g, j);
     const ssd_layers& c = side_of(a.k_cache, a.v_cache, p.g, j);
+    side[x] = j;
     from[x] = plane_of(k, p.g, j) + b * k.page_stride + node * k.token_stride;
     to[x] = plane_of(c, p.g, j) + page * c.page_stride + in_page * c.token_stride;
   }
@@ -99,7 +101,7 @@ __global__ void __launch_bounds__(kWarps * 32)
       for (int i = 0; i < FLIGHT; ++i)
         if (c0 + i * 32 < p.g.chunks)
           z[x][i] = __ldcs(reinterpret_cast<const uint4*>(
-              from[x] + chunk_at(x & 1 && p.g.pair ? a.v : a.k, p.g, c0 + i * 32)));
+              from[x] + chunk_at(side_of(a.k, a.v, p.g, side[x]), p.g, c0 + i * 32)));
 #pragma unroll
     for (int x = 0; x < PLANES; ++x)
       if (x == 0 || group * PLANES + x < p.g.planes)
@@ -107,7 +109,7 @@ __global__ void __launch_bounds__(kWarps * 32)
         for (int i = 0; i < FLIGHT; ++i)
           if (c0 + i * 32 < p.g.chunks)
             *reinterpret_cast<uint4*>(
-                to[x] + chunk_at(x & 1 && p.g.pair ? a.v_cache : a.k_cache, p.g, c0 + i * 32)) =
+                to[x] + chunk_at(side_of(a.k_cache, a.v_cache, p.g, side[x]), p.g, c0 + i * 32)) =
                 z[x][i];
   }
 }

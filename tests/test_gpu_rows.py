@@ -128,6 +128,21 @@ def test_append_of_one_layer_and_of_keys_alone():
     assert torch.equal(raw(s["v_cache"]), raw(before))
 
 
+@pytest.mark.parametrize("orders", [("nhd", "hnd", "last", "nhd"), ("hnd", "nhd", "nhd", "last"),
+                                    ("last", "hnd", "hnd", "nhd")])
+@pytest.mark.parametrize("B,L", [(3, 2), (200, 40)])
+def test_append_with_a_layout_each(orders, B, L):
+    """Keys, values and both caches have strides of their own."""
+    torch, dev = torch_dev()
+    s = append_case(B, 6, L, 5, 64, 16, torch.bfloat16, seed=B)
+    want = appended(s)
+    for name, order in zip(("k", "v", "k_cache", "v_cache"), orders):
+        s[name] = laid_out(s[name], order)
+    run_append(s)
+    assert torch.equal(raw(s["k_cache"]), raw(want["k_cache"]))
+    assert torch.equal(raw(s["v_cache"]), raw(want["v_cache"]))
+
+
 def test_append_with_views_of_larger_tensors():
     """Nodes that are pieces of a projection, caches that are pieces of a pool."""
     torch, dev = torch_dev()
@@ -372,6 +387,30 @@ def test_fork_of_keys_alone_and_of_one_layer():
     assert torch.equal(raw(s["k_cache"]), raw(want["k_cache"]))
     assert torch.equal(raw(s["v_cache"]), raw(before))
     np.testing.assert_array_equal(o["tables"].cpu().numpy(), want["tables"])
+
+
+def test_fork_with_a_layout_each_and_tables_in_wider_rows():
+    torch, dev = torch_dev()
+    for orders in (("nhd", "hnd"), ("hnd", "last"), ("last", "nhd")):
+        s = fork_case(40, 60, 6, 16, 50, L=3, H=3, D=32, seed=4)
+        want, _ = forked(s)
+        d = on_gpu(s)
+        wide = torch.full((40, 19), -5, dtype=torch.int32, device=dev)
+        wide[:, 7:13] = d["tables"]
+        d.update(tables=wide[:, 7:13], k_cache=laid_out(s["k_cache"], orders[0]),
+                 v_cache=laid_out(s["v_cache"], orders[1]))
+        o = run_fork(d)
+        np.testing.assert_array_equal(o["tables"].cpu().numpy(), want["tables"])
+        np.testing.assert_array_equal(o["shares"].cpu().numpy(), want["shares"])
+        for name in ("k_cache", "v_cache"):
+            assert torch.equal(raw(d[name]), raw(want[name]))
+        assert bool((wide[:, :7] == -5).all()) and bool((wide[:, 13:] == -5).all())
+
+
+def test_fork_of_tables_of_many_pages():
+    """More pages than a warp has in flight, over one CTA and over a cluster."""
+    check_fork(fork_case(3, 2, 900, 1, 5, src=[1, 1], seed=2, shared=False))
+    check_fork(fork_case(3, 2, 30000, 1, 5, src=[2, 2], seed=3))
 
 
 def test_fork_chained_on_streams_and_in_a_graph():

@@ -191,6 +191,38 @@ def test_cache_layouts(order, page, D):
     check(s, call(s))
 
 
+@pytest.mark.parametrize("Hq,Hkv,N,lens", [(160, 1, 3, [700, 0]), (144, 1, 1, [5000]), (48, 3, 30, [90]),
+                                          (64, 1, 256, [300]), (7, 7, 200, [1000, 2]),
+                                          (33, 11, 5, [64] * 9)])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 48), (256, 32)])
+def test_head_counts(Hq, Hkv, N, lens, D, page):
+    """Groups of heads of any size, more blocks of pairs than stand side by side."""
+    s = make(lens, N, Hq, Hkv, D, page, dtype_of("bfloat16"), "random", seed=Hq)
+    poison(s)
+    check(s, call(s))
+
+
+def test_keys_and_values_with_a_layout_each_and_tables_in_wider_rows():
+    torch, dev = torch_dev()
+    s = make([200, 77, 500], 7, 8, 4, 128, 16, torch.bfloat16, "binary")
+    poison(s)
+    want = {k: v.clone() for k, v in call(s).items()}
+    wide = torch.full((3, 60), 3, dtype=torch.int32, device=dev)
+    wide[:, 9:9 + s["t"].shape[1]] = s["t"]
+    vc = s["vc"].permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3)
+    k = s["k"].permute(2, 0, 1, 3).contiguous().permute(1, 2, 0, 3)
+    got = call(dict(s, vc=vc, k=k, t=wide[:, 9:9 + s["t"].shape[1]]))
+    assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
+
+
+@pytest.mark.parametrize("page", [4, 6, 24, 40, 192, 384])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_pages_of_any_size(page, D):
+    s = make([1000, 7, 385], 6, 8, 2, D, page, dtype_of("float16"), "random", seed=page)
+    poison(s)
+    check(s, call(s))
+
+
 @pytest.mark.parametrize("N", [1, 5])
 def test_pieces_of_one_projection_and_strided_outputs(N):
     torch, dev = torch_dev()
@@ -365,6 +397,76 @@ def test_same_twice_streams_and_graphs():
         out["out"].zero_()
         g.replay()
         check(s, out)
+
+
+def test_graphs_with_one_workspace_take_turns():
+    torch, dev = torch_dev()
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device=dev)
+    cases = [make([3000, 500], 12, 8, 2, 128, 16, torch.bfloat16, "random"),
+             make([70] * 40, 3, 8, 4, 64, 20, torch.float16)]
+    outs, graphs = [{}, {}], []
+    for s, o in zip(cases, outs):
+        call(s, workspace=ws, out=o)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(s, workspace=ws, out=o)
+        graphs.append(g)
+    for _ in range(3):
+        for s, o, g in zip(cases, outs, graphs):
+            o["out"].zero_()
+            g.replay()
+            check(s, o)
+
+
+def test_threads_at_once():
+    """Calls of several threads, each on a stream of its own."""
+    import threading
+
+    torch, dev = torch_dev()
+    cases = [make([900, 20 * i], 3 + i, 8, 2, (64, 128, 256)[i % 3], 16, torch.bfloat16, "random",
+                  seed=i) for i in range(6)]
+    want = [call(s) for s in cases]
+    torch.cuda.synchronize()
+    got, errors = [None] * 6, []
+
+    def work(i):
+        try:
+            st = torch.cuda.Stream()
+            for _ in range(20):
+                got[i] = call(cases[i], stream=st)
+            st.synchronize()
+        except Exception as e:   # shown by the main thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(6)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for g, w in zip(got, want):
+        assert torch.equal(g["out"], w["out"]) and torch.equal(g["lse"], w["lse"])
+
+
+def test_offsets_beyond_32_bits():
+    """A cache of more than 2^32 elements: pages at its end."""
+    torch, dev = torch_dev()
+    s = make([100, 33], 4, 8, 2, 128, 16, torch.bfloat16, "random")
+    want = {k: v.clone() for k, v in call(s).items()}
+    pages = s["kc"].shape[0]
+    last = (1 << 32) // (16 * 2 * 128) + 7
+    for page in (16, None):
+        big = {}
+        for name in ("kc", "vc"):
+            big[name] = torch.zeros((last + pages, 16, 2, 128), dtype=torch.bfloat16, device=dev)
+            big[name][last:] = s[name]
+        if page is None:                # strides that no box takes
+            big["k"] = s["k"][:1].expand_as(s["k"])
+            want = {k: v.clone() for k, v in call(dict(s, k=big["k"])).items()}
+        t = torch.where(s["t"] >= 0, s["t"] + last, s["t"])
+        got = call(dict(s, t=t, **big))
+        assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
+        del big
 
 
 def test_dict_of_an_earlier_call():
