@@ -917,8 +917,8 @@ __global__ void __launch_bounds__(D) tree_join_kernel(const __grid_constant__ Tr
   const bool mine = pair < p.pairs;
   // the partial of the worker that began it, then those of workers that went on
   auto slot_of = [&](int j) { return 2 * (cta + j * p.side) + (j == 0); };
-  // the loads of four partials are in flight together
-  constexpr int kBatch = 4;
+  // the loads of so many partials are in flight together: items of many pairs have few
+  constexpr int kBatch = BLOCKS == 2 ? 4 : 8;
   const int d = warp * 32 + (lane >> 3) * 4;
   float top = -INFINITY, l = 0.f;
   float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
