@@ -973,26 +973,28 @@ def tree_attention(q, k, v, k_cache, v_cache, tables, lens, parent=None, scale=N
 
 
 def _layers(t, name, dev):
-    """The shape [L, X, Y, H, D] of a tensor, and ssd_layers of it (its address, strides in
-    bytes); [X, Y, H, D] is one layer."""
-    s, shape = t.stride(), t.shape
-    n = len(shape)
-    if (n != 5 and n != 4) or t.get_device() != dev:
+    """The shape [L, X, Y, H, D] of a tensor, its bytes of an element, and ssd_layers of it (its
+    address, strides in bytes); [X, Y, H, D] is one layer."""
+    shape = t.shape
+    n, es = len(shape), t.element_size()
+    if n == 5 and t.get_device() == dev:
+        s0, s1, s2, s3, s4 = t.stride()
+    elif n == 4 and t.get_device() == dev:
+        s1, s2, s3, s4 = t.stride()
+        s0, shape = 0, (1, *shape)
+    else:
         raise SSDError(f"{name}: expected a tensor of 4 dimensions, or 5 with the layers, on "
                        f"cuda:{dev}")
-    es = t.element_size()
-    if s[-1] != 1 or shape[-1] * es % 16 != 0:
+    if s4 != 1 or shape[4] * es % 16 != 0:
         raise SSDError(f"{name}: a head must be contiguous, and a multiple of 16 bytes")
-    if n == 5:
-        return tuple(shape), (t.data_ptr(), s[0] * es, s[1] * es, s[2] * es, s[3] * es)
-    return (1, *shape), (t.data_ptr(), 0, s[0] * es, s[1] * es, s[2] * es)
+    return shape, es, (t.data_ptr(), s0 * es, s1 * es, s2 * es, s3 * es)
 
 
 def _like(t, other, layers, name, dev):
     """ssd_layers of a tensor of `other`'s shape and type, whose own are `layers`."""
     if t.stride() == other.stride() and t.get_device() == dev:
         return (t.data_ptr(), *layers[1:])
-    return _layers(t, name, dev)[1]
+    return _layers(t, name, dev)[2]
 
 
 _NO_LAYERS = (0, 0, 0, 0, 0)
@@ -1016,10 +1018,9 @@ def append_path(k, v, k_cache, v_cache, slots, owner, cu, path=None, dev_status=
         raise SSDError("expected caches on the GPU")
     if torch._C._cuda_getDevice() != dev:
         _on_current(dev)
-    ks, kl = _layers(k, "k", dev)
-    cs, cl = _layers(k_cache, "k_cache", dev)
-    L, B, N, H, D = ks
-    if L != cs[0] or H != cs[3] or D != cs[4] or k.dtype is not dt:
+    (L, B, N, H, D), es, kl = _layers(k, "k", dev)
+    (cL, pages, page_size, cH, cD), _, cl = _layers(k_cache, "k_cache", dev)
+    if L != cL or H != cH or D != cD or k.dtype is not dt:
         raise SSDError("nodes and caches must share the layers, heads and type")
     vl = wl = _NO_LAYERS
     if v is not None and v_cache is not None:
@@ -1029,18 +1030,19 @@ def append_path(k, v, k_cache, v_cache, slots, owner, cu, path=None, dev_status=
         vl, wl = _like(v, k, kl, "v", dev), _like(v_cache, k_cache, cl, "v_cache", dev)
     elif v is not v_cache:
         raise SSDError("v and v_cache go together")
-    if slots.dim() != 1:
-        raise SSDError("expected slots [T]")
     row = slots.shape
+    if len(row) != 1:
+        raise SSDError("expected slots [T]")
     p = p_stride = p_cols = 0
     if path is not None:
         p, p_stride, p_cols = _rows2d(path, "path", B, i32, dev)
-    a = _PACK_APPEND(L, B, N, H, D * k.element_size(), cs[1], cs[2], row[0], p_cols, 0, *kl, *vl,
-                     *cl, *wl, _tensor(slots, "slots", torch.int64, row, dev),
+    a = _PACK_APPEND(L, B, N, H, D * es, pages, page_size, row[0], p_cols, 0, *kl, *vl, *cl, *wl,
+                     _tensor(slots, "slots", torch.int64, row, dev),
                      _tensor(owner, "owner", i32, row, dev), _tensor(cu, "cu", i32, (B + 1,), dev),
                      p, p_stride)
     st = lib().ssd_append_path(a, None if dev_status is None else _dev_ptr(dev_status),
-                               _use_stream(stream, dev, ()))
+                               torch._C._cuda_getCurrentRawStream(dev) if stream is None
+                               else stream.cuda_stream)
     if st:
         _check(st, "ssd_append_path")
 
@@ -1106,8 +1108,8 @@ def fork_rows(src, lens, held, tables, shares, free_pages, free_count, page_size
     kl = vl = _NO_LAYERS
     L = H = size = 0
     if k_cache is not None:
-        ks, kl = _layers(k_cache, "k_cache", dev)
-        L, H, size = ks[0], ks[3], ks[4] * k_cache.element_size()
+        ks, es, kl = _layers(k_cache, "k_cache", dev)
+        L, H, size = ks[0], ks[3], ks[4] * es
         if ks[1] != pages or ks[2] != page_size:
             raise SSDError("the caches must have one page for each entry of shares, of page_size "
                            "tokens")
