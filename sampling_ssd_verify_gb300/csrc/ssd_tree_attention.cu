@@ -75,8 +75,10 @@ bool plan(const ssd_tree_attn& a, TreeAttnParams& p, Layout& L) {
   }
   p.q_plain = a.scale > 0.f && p.q_and != 0u;
   // A worker's CTAs go through the same stretches side by side, up to eight of them: for the
-  // items of a head, which read the same tiles, and for the heads of a set where a token's
-  // heads lie closer than its neighbour.
+  // items of a head, which read the same tiles (32 sequences with two items a head at D = 256
+  // 288 us instead of 371, at D = 128 230 instead of 245), and for the heads of a set where a
+  // token's heads lie closer than its neighbour (64 x 11 nodes 185 us instead of 188, at D = 64
+  // 107 instead of 152; 32 x 64 129 instead of 143; two contexts of 131072 160 instead of 166).
   const int most = std::min(8, sms);
   p.bg = p.hg = 1;
   for (int n = 2; n <= most; ++n)
@@ -103,7 +105,8 @@ bool plan(const ssd_tree_attn& a, TreeAttnParams& p, Layout& L) {
   p.wide_rows = ((uintptr_t)a.out | 2 * (uintptr_t)(a.out_seq_stride | a.out_node_stride |
                                                     a.out_head_stride)) % 32 == 0;
   p.node_rows = std::min(tile, (a.N + 7) / 8 * 8);
-  // a block's queries are whole nodes, or all there are
+  // Queries by TMA, where a block's are whole nodes, or all there are (32 x 64 nodes 129 us
+  // instead of 162: copied row by row they take the first scores to 16 us, not 9).
   const ssd_paged q{a.q, a.q_seq_stride, a.q_node_stride, a.q_head_stride};
   p.q_nodes = p.q_plain && p.gqa <= 128 && (p.pairs <= 128 || 128 % p.gqa == 0) &&
                       box_strides(q, a.Hq, a.N, a.B)
