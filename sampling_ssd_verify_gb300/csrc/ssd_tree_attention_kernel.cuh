@@ -839,6 +839,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         for (int q = 0; q < kCols; q += 32) {
           const int col = (int)first + q;
           uint32_t y[32];
+          __syncwarp();                          // the loads are the whole warp's
           if (mine_has) tmem_ld32(y, to + col);
           if constexpr (S::kByTiles) {
             uint32_t z[32];
@@ -868,8 +869,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               if (v == 0) break;
             }
           }
-          if (!mine) continue;
-          if (whole) {
+          if (mine && whole) {
             T* out = static_cast<T*>(a.out) + job.seq * a.out_seq_stride +
                      node * a.out_node_stride + head * a.out_head_stride + col;
 #pragma unroll
@@ -886,7 +886,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 *reinterpret_cast<uint4*>(out + e + 8) = make_uint4(z[4], z[5], z[6], z[7]);
               }
             }
-          } else {
+          } else if (mine) {
             float* out = p.po + part_at<D>(job.slot, p.part_rows, row, col);
 #pragma unroll
             for (int e = 0; e < 32; e += 4)

@@ -399,6 +399,32 @@ def test_same_twice_streams_and_graphs():
         check(s, out)
 
 
+@pytest.mark.parametrize("N,Hq,D,lens", [(5, 8, 128, [900] * 60), (40, 8, 128, [700, 1500] * 20),
+                                         (7, 8, 256, [500] * 40), (9, 4, 64, [1100] * 50)])
+def test_same_bits_beside_other_work(N, Hq, D, lens):
+    """Items of two stretches, whose workers begin and end at any time."""
+    torch, dev = torch_dev()
+    s = make(lens, N, Hq, 2, D, 16, torch.bfloat16, "random", seed=N)
+    first = {k: v.clone() for k, v in call(s).items()}
+    check(s, first, seqs=range(0, len(lens), 9))
+    out, busy = {}, torch.randn((4096, 4096), device=dev)
+    side = torch.cuda.Stream()
+    for i in range(60):
+        if i % 3 == 0:      # work beside it, so that its CTAs begin at other times
+            with torch.cuda.stream(side):
+                busy = (busy @ busy).clamp(-1, 1)
+        out.get("out", first["out"][:0]).zero_()
+        call(s, out=out)
+        assert torch.equal(out["out"], first["out"]) and torch.equal(out["lse"], first["lse"]), i
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(s, out=out)
+    for i in range(30):
+        out["out"].zero_()
+        g.replay()
+        assert torch.equal(out["out"], first["out"]) and torch.equal(out["lse"], first["lse"]), i
+
+
 def test_graphs_with_one_workspace_take_turns():
     torch, dev = torch_dev()
     ws = torch.empty(1 << 26, dtype=torch.uint8, device=dev)
