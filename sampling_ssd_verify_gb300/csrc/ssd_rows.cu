@@ -61,6 +61,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   const ssd_append& a = p.a;
   const int lane = threadIdx.x & 31;
   const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  wait_previous();
   if (w >= p.warps) return;
   const int t = p.by_group.quotient((int)w), group = (int)w - t * p.groups;
   const int64_t slot = a.slots[t];
@@ -119,9 +120,17 @@ cudaError_t launch_append(AppendParams& p, cudaStream_t s) {
   p.groups = (p.g.planes + PLANES - 1) / PLANES;
   p.by_group = divisor(p.groups);
   p.warps = (int64_t)p.a.rows * p.groups;
-  append_kernel<PLANES, FLIGHT>
-      <<<(unsigned)((p.warps + kWarps - 1) / kWarps), kWarps * 32, 0, s>>>(p);
-  return cudaGetLastError();
+  // begins while the kernel before it ends, and waits for it
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((unsigned)((p.warps + kWarps - 1) / kWarps));
+  c.blockDim = dim3(kWarps * 32);
+  c.stream = s;
+  c.attrs = &early;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, append_kernel<PLANES, FLIGHT>, p);
 }
 
 // ---- rows of the tables ----------------------------------------------------------------
@@ -202,6 +211,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
   const int warps = threads / 32, warp = gtid / 32;
   int bad = 0;
   start_next();
+  wait_previous();
   auto barrier = [&] {
     if (p.ctas > 1) cluster_barrier();
     else __syncthreads();
@@ -627,26 +637,27 @@ ssd_status ssd_fork_rows(const ssd_fork* f, void* workspace, size_t workspace_by
     e = cudaFuncSetAttribute(fork_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              plan_ints(kMaxRows, kMaxRows) * (int)sizeof(int));
   if (e != cudaSuccess) return status_of(e);
-  cudaLaunchAttribute attr{};
+  // both begin while the kernel before them ends, and wait for it
+  cudaLaunchAttribute attr[2] = {};
   cudaLaunchConfig_t c{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)p.ctas;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   c.gridDim = dim3((unsigned)p.ctas);
   c.blockDim = dim3(kPlanThreads);
   c.dynamicSmemBytes = (size_t)smem;
   c.stream = s;
-  c.attrs = &attr;
-  c.numAttrs = 1;
+  c.attrs = attr;
+  c.numAttrs = 2;
   e = cudaLaunchKernelEx(&c, fork_plan_kernel, p);
   if (e != cudaSuccess) return status_of(e);
   const int64_t work =
       (int64_t)f->B * ((f->cols + kTableCols - 1) / kTableCols + (int64_t)p.g.planes * p.groups);
   const int grid = (int)std::min<int64_t>((work + kWarps - 1) / kWarps,
                                           (int64_t)std::max(num_sms(), 1) * 8);
-  attr = cudaLaunchAttribute{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  c.numAttrs = 1;
   c.gridDim = dim3((unsigned)grid);
   c.blockDim = dim3(kWarps * 32);
   c.dynamicSmemBytes = 0;
