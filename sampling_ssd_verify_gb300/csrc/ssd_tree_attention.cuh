@@ -21,6 +21,7 @@ struct TreeAttnParams {
   int wide_rows;           // rows of the output are on 32-byte boundaries
   int gqa;                 // query heads per key/value head
   int pairs;               // (node, head) pairs of a sequence's key/value head
+  int block_pairs;         // of a block: 128, or fewer that are whole nodes
   int blocks;              // items of a sequence's key/value head
   int hg, sets;            // key/value heads of a set, sets
   int bg, block_sets;      // items of a head side by side, sets of those

@@ -402,9 +402,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(q_policy));
       if (lane == 0) p.begun[blockIdx.x] = make_int2(-1, 0);
       while (next_stretch(p, k, s)) {
-        const int pair0 = s.mb * BLOCKS * kRows, pairs = min(BLOCKS * kRows, p.pairs - pair0);
+        const int rows = BLOCKS * p.block_pairs;  // of an item
+        const int pair0 = s.mb * rows, pairs = min(rows, p.pairs - pair0);
         auto query = [&](const TreeStretch& z, int row) {
-          const int pair = z.mb * BLOCKS * kRows + row, node = p.by_gqa.quotient(pair);
+          const int pair = z.mb * rows + row, node = p.by_gqa.quotient(pair);
           return static_cast<const T*>(a.q) + z.b * a.q_seq_stride + node * a.q_node_stride +
                  (int64_t)(z.h * p.gqa + pair - node * p.gqa) * a.q_head_stride;
         };
@@ -413,22 +414,34 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         if (p.q_nodes == 0) {
           constexpr int kLanes = D / 8;          // lanes of a row, 16 bytes each
           const int ch = lane % kLanes;
+          auto place = [&](int row) {
+            const int block = BLOCKS == 2 && row >= p.block_pairs, r = row - block * p.block_pairs;
+            return qs + block * S::kQueries + (ch / 8) * S::kQueryPanel + r * 128 +
+                   (((ch & 7) ^ (r & 7)) << 4);
+          };
+          for (int r0 = 0; r0 < pairs; r0 += 32) {  // the rows' places dealt to the lanes
+            const int64_t at = query(s, min(r0 + lane, pairs - 1)) - static_cast<const T*>(a.q);
 #pragma unroll 8
-          for (int r0 = 0; r0 < pairs; r0 += 32 / kLanes) {
-            const int row = r0 + lane / kLanes;
-            if (row < pairs) {
-              const uint32_t dst = qs + (row / kRows) * S::kQueries + (ch / 8) * S::kQueryPanel +
-                                   (row % kRows) * 128 + (((ch & 7) ^ (row & 7)) << 4);
-              const T* from = query(s, row) + ch * 8;
-              if (p.q_plain) {
-                copy16(dst, from, true);
-              } else {                           // a scale that is not positive: -q, or 0
-                const uint4 x = *reinterpret_cast<const uint4*>(from);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst),
-                             "r"((x.x & p.q_and) ^ p.q_xor), "r"((x.y & p.q_and) ^ p.q_xor),
-                             "r"((x.z & p.q_and) ^ p.q_xor), "r"((x.w & p.q_and) ^ p.q_xor)
-                             : "memory");
-              }
+            for (int j = 0; j < kLanes; ++j) {
+              const int r = j * (32 / kLanes) + lane / kLanes, row = r0 + r;
+              const int64_t x = __shfl_sync(0xffffffffu, at, r);
+              if (row < pairs) copy16(place(row), static_cast<const T*>(a.q) + x + ch * 8, true);
+            }
+          }
+          if (!p.q_plain) {                      // a scale that is not positive: -q, or 0
+            copies_commit();
+            copies_wait<0>();
+#pragma unroll 4
+            for (int row = lane / kLanes; row < pairs; row += 32 / kLanes) {
+              uint32_t x[4];                     // which this lane copied
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                           : "r"(place(row))
+                           : "memory");
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(place(row)),
+                           "r"((x[0] & p.q_and) ^ p.q_xor), "r"((x[1] & p.q_and) ^ p.q_xor),
+                           "r"((x[2] & p.q_and) ^ p.q_xor), "r"((x[3] & p.q_and) ^ p.q_xor)
+                           : "memory");
             }
           }
         }
@@ -441,7 +454,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         // 32 arrivals: lane 0's follows the job
         if (p.q_nodes > 0) {
           // boxes of a block's nodes, their heads side by side, and 64 dimensions
-          const int boxes = (pairs > kRows ? 2 : 1) * S::kPanels;
+          const int boxes = (pairs > p.block_pairs ? 2 : 1) * S::kPanels;
           if (lane == 0)
             mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(boxes * p.q_nodes * p.gqa * 128));
           __syncwarp();
@@ -465,7 +478,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         TreeWalk k1 = k;
         TreeStretch s1;
         if (next_stretch(p, k1, s1)) {
-          const int n = min(BLOCKS * kRows, p.pairs - s1.mb * BLOCKS * kRows);
+          const int n = min(rows, p.pairs - s1.mb * rows);
           for (int row = lane; row < n; row += 32)
 #pragma unroll
             for (int d = 0; d < D; d += 64)
@@ -518,7 +531,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         mbar_wait(&sh.q_full, i & 1, &sh.err, p.status);
         const int n = gave_up(sh) ? 0 : sh.job[i & 1].tiles;
         if (n == 0) break;
-        const bool two = S::kByBlocks && sh.job[i & 1].pairs > kRows;
+        const bool two = S::kByBlocks && sh.job[i & 1].pairs > p.block_pairs;
         fence_after();
         // a step more for each tile that the sums are behind; n tiles may be fewer than that
         for (int j = 0; j < n + S::kLead; ++j) {
@@ -626,10 +639,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       // one's is read
       const TreeJob& job = sh.job[i & 1];
       const int n = gave_up(sh) ? 0 : job.tiles, cached = job.cached, tokens = job.tokens;
-      const int row = (S::kByBlocks ? (int)b * kRows : 0) + (int)m;  // of the item's pairs
-      const bool mine = row < job.pairs;
+      // of the item's pairs; in a block's rows past its pairs there is none
+      const int row = (S::kByBlocks ? (int)b * p.block_pairs : 0) + (int)m;
+      const bool mine = (int)m < p.block_pairs && row < job.pairs;
       const bool busy = __any_sync(0xffffffffu, mine);
-      const bool second = job.pairs > kRows;     // two blocks
+      const bool second = job.pairs > p.block_pairs;  // two blocks
       const int mine_node = p.by_gqa.quotient(job.pair0 + min(row, job.pairs - 1));
       mbar_arrive(&sh.job_read);
       if (n == 0) break;
@@ -976,8 +990,8 @@ __global__ void __launch_bounds__(D) tree_join_kernel(const __grid_constant__ Tr
   const int mb = rest % p.block_sets * p.bg + bb;
   rest /= p.block_sets;
   const int h = rest % p.sets * p.hg + x - bb * p.hg, seq = rest / p.sets;
-  const int pair = mb * (BLOCKS * kRows) + i;
-  const bool mine = pair < p.pairs;
+  const int pair = mb * (BLOCKS * p.block_pairs) + i;
+  const bool mine = i < BLOCKS * p.block_pairs && pair < p.pairs;
   // the partial of the worker that began it, then those of workers that went on
   auto slot_of = [&](int j) { return 2 * (cta + j * p.side) + (j == 0); };
   // the loads of so many partials are in flight together (one stream of 4000 tokens 16.2 us

@@ -202,6 +202,24 @@ def test_head_counts(Hq, Hkv, N, lens, D, page):
     check(s, call(s))
 
 
+@pytest.mark.parametrize("Hq,Hkv,N,lens", [(56, 8, 57, [3, 900, 0]), (15, 3, 52, [4000]), (9, 3, 100, [70, 1]),
+                                          (24, 2, 23, [260, 5, 0]), (40, 2, 13, [33] * 5), (96, 2, 9, [500]),
+                                          (200, 2, 4, [100, 2000]), (127, 1, 2, [64])])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 16), (128, 20), (256, 64)])
+@pytest.mark.parametrize("scale", [None, -0.11, 0.0])
+def test_groups_that_do_not_divide_a_block(Hq, Hkv, N, lens, D, page, scale):
+    """Blocks of whole nodes with rows left empty, or nodes shared by two blocks; queries by boxes and row
+    by row; the output in the queries' place."""
+    s = make(lens, N, Hq, Hkv, D, page, dtype_of("bfloat16"), "random", seed=N)
+    poison(s)
+    kw = {} if scale is None else {"scale": scale}
+    o = call(s, **kw)
+    check(s, o, **kw)
+    q = s["q"].clone()
+    again = call(dict(s, q=q), out={"out": q}, **kw)
+    assert (again["out"] == o["out"]).all() and (again["lse"] == o["lse"]).all()
+
+
 def test_keys_and_values_with_a_layout_each_and_tables_in_wider_rows():
     torch, dev = torch_dev()
     s = make([200, 77, 500], 7, 8, 4, 128, 16, torch.bfloat16, "binary")
