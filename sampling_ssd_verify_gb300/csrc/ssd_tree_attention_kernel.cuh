@@ -77,6 +77,14 @@ template <int D, int BLOCKS> struct TreeShape {
   static constexpr bool kByBlocks = BLOCKS == 2;
   static constexpr bool kOne = D == 256;
   static constexpr bool kByTiles = !kByBlocks && !kOne;
+  // Of a tile, the 32s of tokens whose weights and sums are computed: those with some of
+  // the `left` from its first on (256 sequences of 10 to 200 tokens 75 us instead of 82, 32 of 100
+  // to 1500 28.9 instead of 30.6).  With two blocks and at D = 256 the test before each product
+  // costs more than that gives (32 x 64 nodes 133 us instead of 129, at D = 256 303
+  // instead of 289): all.
+  static __device__ __forceinline__ int parts(int left) {
+    return kByTiles ? (min(kTile, left) + 31) / 32 : kTile / 32;
+  }
   // Buffers of scores, and where the sums are.  Where the sums leave room for three, the scores
   // are two tiles ahead of the sums, and the exponentials need not wait for them (64 x 11 nodes
   // 107 us instead of 113).
@@ -511,14 +519,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                  k_op + (((e / 4) * S::kPanel + (e % 4) * 32) >> 4), score, e > 0);
       };
       // half a tile's tokens at a time: the first while the weights of the others are computed
-      auto sums = [&](uint32_t weights, uint32_t col, int half, bool add) {
+      auto sums = [&](uint32_t weights, uint32_t col, int half, bool add, int steps) {
         const uint64_t v_op = operand(vring + vs * S::kSlot, S::kPanel);
         constexpr int kSteps = kTile / 32;
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
           const int e = half * kSteps + i;
-          mma_ts(tmem + S::kColO + col * S::kStepO, tmem + kColS + weights * kColStep + e * 8,
-                 v_op + ((e * 16 * 128) >> 4), sum, add || e > 0);
+          if (e < steps)
+            mma_ts(tmem + S::kColO + col * S::kStepO, tmem + kColS + weights * kColStep + e * 8,
+                   v_op + ((e * 16 * 128) >> 4), sum, add || e > 0);
         }
       };
       auto turn = [](uint32_t& slot, uint32_t& use, int n) {
@@ -532,6 +541,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const int n = gave_up(sh) ? 0 : sh.job[i & 1].tiles;
         if (n == 0) break;
         const bool two = S::kByBlocks && sh.job[i & 1].pairs > p.block_pairs;
+        const int cached = sh.job[i & 1].cached, tokens = sh.job[i & 1].tokens;
+        auto steps_of = [&](int j) {             // 16 tokens each
+          return 2 * S::parts(j < cached ? tokens - j * kTile : a.N - (j - cached) * kTile);
+        };
         fence_after();
         // a step more for each tile that the sums are behind; n tiles may be fewer than that
         for (int j = 0; j < n + S::kLead; ++j) {
@@ -548,12 +561,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 mbar_wait(&sh.p_half[x], (t - 1) & 1, &sh.err, p.status);
                 if (x == 0) mbar_wait(&sh.v_full[vs], v_use & 1, &sh.err, p.status);
                 fence_after();
-                if (elected()) sums(x, x, 0, j > 1);
+                if (elected()) sums(x, x, 0, j > 1, kTile / 16);
                 __syncwarp();
                 mbar_wait(&sh.p_full[x], (t - 1) & 1, &sh.err, p.status);
                 fence_after();
                 if (elected()) {
-                  sums(x, x, 1, j > 1);
+                  sums(x, x, 1, j > 1, kTile / 16);
                   commit(&sh.o_done[x]);
                   if (end) commit(&sh.v_empty[vs]);
                 }
@@ -601,12 +614,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               mbar_wait(&sh.v_full[vs], v_use & 1, &sh.err, p.status);
               fence_after();
               const bool add = jj >= (S::kOne ? 1 : 2);
-              if (elected()) sums(buf, o, 0, add);
+              const int steps = steps_of(jj);
+              if (elected()) sums(buf, o, 0, add, steps);
               __syncwarp();
               mbar_wait(&sh.p_full[buf], at, &sh.err, p.status);
               fence_after();
               if (elected()) {
-                sums(buf, o, 1, add);
+                sums(buf, o, 1, add, steps);
                 commit(&sh.v_empty[vs]);
                 commit(&sh.o_done[t & 3]);
               }
@@ -662,6 +676,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const int at = nodes ? (j - cached) * kTile : j * kTile;
         const int here = min(kTile, (nodes ? a.N : tokens) - at);
         const bool some = nodes || here < kTile; // not all of the tile's tokens count
+        const int parts = S::parts(here);
         uint32_t ok[kTile / 32];                 // those that do, for this pair
         if (some && busy) {
 #pragma unroll
@@ -683,7 +698,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const uint32_t nth = all_tiles + (uint32_t)j, slot = nth % S::kSlotsV;
           mbar_wait(&sh.v_full[slot], nth / S::kSlotsV & 1, &sh.err, p.status);
           const uint32_t vs = vring + slot * S::kSlot;
-          for (int e = here * 8 + (int)m; e < kTile * 8; e += kRows)
+          for (int e = here * 8 + (int)m; e < parts * 32 * 8; e += kRows)
 #pragma unroll
             for (int d = 0; d < S::kPanels; ++d)
               asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vs + d * S::kPanel +
@@ -752,7 +767,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           // Weights of 32 tokens in the type of V, as the product takes them: each is off by at
           // most half a step, which an output averages over its tokens; their sum is of
           // the unrounded ones.
-          auto weights = [&](const uint32_t (&x)[32], int q, float off) {
+          auto weights = [&](const uint32_t (&x)[32], int q, float off, bool half) {
             const float2 less = make_float2(-off, -off);
             uint32_t z[16];
 #pragma unroll
@@ -763,7 +778,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               z[e / 2] = pack2<T>(y.x, y.y);
             }
             tmem_st16(ts + q * 16, z);
-            if (q == kParts / 2 - 1) {
+            if (half) {
               tmem_wait_st();
               fence_before();
               mbar_arrive(&sh.p_half[buf]);
@@ -784,12 +799,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll
                 for (int y = 1; y < kParts; ++y)
                   if (q == y) word = ok[y];
-                mask(x, word);
+                if (!__all_sync(0xffffffffu, word == ~0u)) mask(x, word);
               }
             };
             float now = -INFINITY;
 #pragma unroll 1
-            for (int q = 0; q < kParts; ++q) {
+            for (int q = 0; q < parts; ++q) {
               load(q);
               float high[4] = {now, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -801,9 +816,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             }
             const float off = raise(now * p.scale_log2);
 #pragma unroll 1
-            for (int q = 0; q < kParts; ++q) {
+            for (int q = 0; q < parts; ++q) {
               load(q);
-              weights(x, q, off);
+              weights(x, q, off, q == min(kParts / 2, parts) - 1);
             }
           } else {
             uint32_t x[kParts][32];
@@ -827,7 +842,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 raise(max3(max3(high[0], high[1], high[2]), max3(high[3], high[4], high[5]),
                            fmaxf(high[6], high[7])) * p.scale_log2);
 #pragma unroll
-            for (int q = 0; q < kParts; ++q) weights(x[q], q, off);
+            for (int q = 0; q < kParts; ++q) weights(x[q], q, off, q == kParts / 2 - 1);
           }
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           tmem_wait_st();

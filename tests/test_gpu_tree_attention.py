@@ -220,6 +220,16 @@ def test_groups_that_do_not_divide_a_block(Hq, Hkv, N, lens, D, page, scale):
     assert (again["out"] == o["out"]).all() and (again["lse"] == o["lse"]).all()
 
 
+@pytest.mark.parametrize("N", [1, 31, 32, 33, 64, 65, 97, 129])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 16), (128, 20), (256, 64)])
+def test_lengths_about_multiples_of_32(N, D, page):
+    """Tiles of which some of the 32s hold no token; the slots' other rows are those of earlier tiles."""
+    lens = [0, 1, 31, 32, 33, 63, 64, 65, 95, 96, 97, 127, 128, 129, 160, 161, 224, 255, 257, 300] * 4
+    s = make(lens, N, 4, 4, D, page, dtype_of("float16"), "random", seed=D)
+    poison(s)
+    check(s, call(s))
+
+
 def test_keys_and_values_with_a_layout_each_and_tables_in_wider_rows():
     torch, dev = torch_dev()
     s = make([200, 77, 500], 7, 8, 4, 128, 16, torch.bfloat16, "binary")
