@@ -870,6 +870,7 @@ def prefix_attention(q, k_cache, v_cache, prefix_tables, prefix_len, group_off, 
 _PACK_TREE = struct.Struct("@8i" + "Q3q" + "Q3q" * 4 + "QQqQ" + "Q3q" + "Qif").pack
 _PACK_APPEND = struct.Struct("@10i" + "Q4q" * 4 + "4Qq").pack
 _PACK_FORK = struct.Struct("@10i" + "4Qq3Q" + "Q4q" * 2 + "6Q").pack
+_UNPACKED = (struct.error, OverflowError)  # sizes beyond 32 bits, a scale beyond float32
 _parents = {}  # trees by their bytes: the library reads them by address
 
 
@@ -960,12 +961,15 @@ def tree_attention(q, k, v, k_cache, v_cache, tables, lens, parent=None, scale=N
         raise SSDError("the head dimension must be contiguous")
     tree, kept = (0, None) if parent is None else _parent_address(parent, N)
     table, stride, cols = _rows2d(tables, "tables", B, i32, dev)
-    a = _PACK_TREE(code, B, N, Hq, Hkv, D, pages, page_size, q.data_ptr(), qa[0], qa[1], qa[2],
-                   k.data_ptr(), ka[0], ka[1], ka[2], v.data_ptr(), va[0], va[1], va[2],
-                   k_cache.data_ptr(), kc[0], kc[1], kc[2], v_cache.data_ptr(), vc[0], vc[1],
-                   vc[2], table, _tensor(lens, "lens", i32, (B,), dev), stride, tree,
-                   y.data_ptr(), ya[0], ya[1], ya[2], at, cols,
-                   D ** -0.5 if scale is None else scale)
+    try:
+        a = _PACK_TREE(code, B, N, Hq, Hkv, D, pages, page_size, q.data_ptr(), qa[0], qa[1], qa[2],
+                       k.data_ptr(), ka[0], ka[1], ka[2], v.data_ptr(), va[0], va[1], va[2],
+                       k_cache.data_ptr(), kc[0], kc[1], kc[2], v_cache.data_ptr(), vc[0], vc[1],
+                       vc[2], table, _tensor(lens, "lens", i32, (B,), dev), stride, tree,
+                       y.data_ptr(), ya[0], ya[1], ya[2], at, cols,
+                       D ** -0.5 if scale is None else scale)
+    except _UNPACKED as e:
+        raise SSDError(f"ssd_tree_attention: {e}") from None
     L = lib()
     _launch(L.ssd_tree_attention, L.ssd_tree_attention_workspace_size, "ssd_tree_attention", a, o,
             workspace, dev, q.device, dev_status, stream)
@@ -1036,10 +1040,13 @@ def append_path(k, v, k_cache, v_cache, slots, owner, cu, path=None, dev_status=
     p = p_stride = p_cols = 0
     if path is not None:
         p, p_stride, p_cols = _rows2d(path, "path", B, i32, dev)
-    a = _PACK_APPEND(L, B, N, H, D * es, pages, page_size, row[0], p_cols, 0, *kl, *vl, *cl, *wl,
-                     _tensor(slots, "slots", torch.int64, row, dev),
-                     _tensor(owner, "owner", i32, row, dev), _tensor(cu, "cu", i32, (B + 1,), dev),
-                     p, p_stride)
+    try:
+        a = _PACK_APPEND(L, B, N, H, D * es, pages, page_size, row[0], p_cols, 0, *kl, *vl, *cl,
+                         *wl, _tensor(slots, "slots", torch.int64, row, dev),
+                         _tensor(owner, "owner", i32, row, dev),
+                         _tensor(cu, "cu", i32, (B + 1,), dev), p, p_stride)
+    except _UNPACKED as e:
+        raise SSDError(f"ssd_append_path: {e}") from None
     st = lib().ssd_append_path(a, None if dev_status is None else _dev_ptr(dev_status),
                                torch._C._cuda_getCurrentRawStream(dev) if stream is None
                                else stream.cuda_stream)
@@ -1126,12 +1133,15 @@ def fork_rows(src, lens, held, tables, shares, free_pages, free_count, page_size
             raise SSDError("the tables must have columns")
         o.update(_fork_views(torch, counts, cols, src.device))
     ptrs = _fork_pointers(o, counts, i32, dev)
-    a = _PACK_FORK(S, B, cols, int(page_size), pages, stack[0], L, H, size, 0,
-                   _tensor(src, "src", i32, row, dev), _tensor(lens, "lens", i32, old, dev),
-                   _tensor(held, "held", i32, old, dev), table, stride,
-                   _tensor(shares, "shares", i32, pool, dev),
-                   _tensor(free_pages, "free_pages", i32, stack, dev),
-                   _tensor(free_count, "free_count", i32, (1,), dev), *kl, *vl, *ptrs)
+    try:
+        a = _PACK_FORK(S, B, cols, int(page_size), pages, stack[0], L, H, size, 0,
+                       _tensor(src, "src", i32, row, dev), _tensor(lens, "lens", i32, old, dev),
+                       _tensor(held, "held", i32, old, dev), table, stride,
+                       _tensor(shares, "shares", i32, pool, dev),
+                       _tensor(free_pages, "free_pages", i32, stack, dev),
+                       _tensor(free_count, "free_count", i32, (1,), dev), *kl, *vl, *ptrs)
+    except _UNPACKED as e:
+        raise SSDError(f"ssd_fork_rows: {e}") from None
     f = lib()
     _launch(f.ssd_fork_rows, f.ssd_fork_rows_workspace_size, "ssd_fork_rows", a, o, workspace, dev,
             src.device, dev_status, stream)

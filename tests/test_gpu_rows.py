@@ -534,3 +534,10 @@ def test_refusals():
                     v_cache=a["v_cache"][..., :4])):
         with pytest.raises(ssd.SSDError):
             run_append(dict(a, **kw))
+
+
+@pytest.mark.parametrize("page", [2 ** 31, 2 ** 40, -2 ** 40])
+def test_page_sizes_beyond_32_bits_are_refused(page):
+    s = on_gpu(fork_case(4, 5, 6, 8, 9, L=2))
+    with pytest.raises(ssd.SSDError):
+        run_fork(dict(s, page=page, k_cache=None, v_cache=None))

@@ -555,3 +555,10 @@ def test_refusals():
     big = make([40], 257, 2, 2, 64, 16, torch.bfloat16)
     with pytest.raises(ssd.SSDError):
         call(big)
+
+
+@pytest.mark.parametrize("scale", [1e39, -1e300, float("inf")])
+def test_scales_beyond_float32_are_refused(scale):
+    s = make([40, 3], 3, 4, 2, 64, 16, dtype_of("bfloat16"), "binary")
+    with pytest.raises(ssd.SSDError):
+        call(s, scale=scale)
