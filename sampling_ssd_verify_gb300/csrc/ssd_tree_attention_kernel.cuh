@@ -925,7 +925,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           } else {
             tmem_wait_ld();
           }
-          if (odd && mine) {
+          if (odd && mine && !(whole && sum == 0.f)) {
             // values that are no numbers, of the nodes on the path whose tiles were here
             const int v0 = max(0, -cached) * kTile, v1 = (n - cached) * kTile;
             for (int v = node;; v = sh.parent[v]) {
@@ -1056,6 +1056,7 @@ __global__ void __launch_bounds__(D) tree_join_kernel(const __grid_constant__ Tr
   if (!mine) return;
   const int node = p.by_gqa.quotient(pair), head = h * p.gqa + pair - node * p.gqa;
   const float inv = l == 0.f ? 0.f : 1.f / l;
+  if (l == 0.f) o[0] = o[1] = make_float4(0.f, 0.f, 0.f, 0.f);  // of values that are no numbers too
   T* out = static_cast<T*>(a.out) + seq * a.out_seq_stride + node * a.out_node_stride +
            head * a.out_head_stride + d;
 #pragma unroll

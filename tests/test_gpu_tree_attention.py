@@ -360,6 +360,21 @@ def test_queries_that_are_no_numbers_stay_in_their_row():
     assert not bool(torch.isfinite(got[~keep]).any())
 
 
+@pytest.mark.parametrize("N", [3, 200])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_no_scores_and_values_that_are_no_numbers(N, D):
+    """Every score of a row is -inf, and a value on its path is no number: zeros."""
+    torch, dev = torch_dev()
+    s = make([0, 0], N, 4, 2, D, 16, torch.bfloat16, "chain")
+    s["q"].fill_(1.0)
+    s["k"][0].fill_(-math.inf)
+    s["v"][0, 1, 0, ::3] = math.inf
+    s["v"][0, 2, 1, 5] = math.nan
+    o = call(s)
+    assert bool((o["out"][0] == 0).all()) and bool((o["lse"][0] == -math.inf).all())
+    check(s, o, seqs=[1])
+
+
 def test_infinite_keys_of_every_token():
     """Scores of -inf alone: zeros, and -inf."""
     torch, dev = torch_dev()
