@@ -910,20 +910,28 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 #pragma unroll 1
         for (int q = 0; q < kCols; q += 32) {
           const int col = (int)first + q;
-          uint32_t y[32];
+          uint32_t y[32], z[S::kByTiles ? 32 : 1];
           __syncwarp();                          // the loads are the whole warp's
-          if (mine_has) tmem_ld32(y, to + col);
-          if constexpr (S::kByTiles) {
-            uint32_t z[32];
-            if (other_has) tmem_ld32(z, other + col);
-            tmem_wait_ld();
-            // the sums of a stream without tiles are whatever the columns held
+          // the sums of a stream without tiles are whatever the columns held
+          auto load = [&](uint32_t (&x)[32], bool has, uint32_t from) {
+            if (has) {
+              tmem_ld32(x, from);
+            } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              y[e] = __float_as_uint((mine_has ? __uint_as_float(y[e]) * f0 : 0.f) +
-                                     (other_has ? __uint_as_float(z[e]) * f1 : 0.f));
-          } else {
-            tmem_wait_ld();
+              for (int e = 0; e < 32; ++e) x[e] = 0u;
+            }
+          };
+          load(y, mine_has, to + col);
+          if constexpr (S::kByTiles) load(z, other_has, other + col);
+          tmem_wait_ld();
+          const float2 by0 = make_float2(f0 * inv, f0 * inv), by1 = make_float2(f1 * inv, f1 * inv);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float2 x = mul2(make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), by0);
+            if constexpr (S::kByTiles)
+              x = fma2(make_float2(__uint_as_float(z[e]), __uint_as_float(z[e + 1])), by1, x);
+            y[e] = __float_as_uint(x.x);
+            y[e + 1] = __float_as_uint(x.y);
           }
           if (odd && mine && !(whole && sum == 0.f)) {
             // values that are no numbers, of the nodes on the path whose tiles were here
@@ -949,8 +957,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               uint32_t z[8];
 #pragma unroll
               for (int g = 0; g < 8; ++g)
-                z[g] = pack2<T>(__uint_as_float(y[e + 2 * g]) * inv,
-                                __uint_as_float(y[e + 2 * g + 1]) * inv);
+                z[g] = pack2<T>(__uint_as_float(y[e + 2 * g]), __uint_as_float(y[e + 2 * g + 1]));
               if (p.wide_rows) {
                 store32(out + e, z);
               } else {
