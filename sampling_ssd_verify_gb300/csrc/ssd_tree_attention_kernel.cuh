@@ -658,6 +658,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const bool mine = (int)m < p.block_pairs && row < job.pairs;
       const bool busy = __any_sync(0xffffffffu, mine);
       const bool second = job.pairs > p.block_pairs;  // two blocks
+      // who looks after a tile's values: warps without pairs where there are any (256 sequences
+      // of 10 to 200 tokens 64.9 us instead of 66.8)
+      const int taken = S::kByBlocks ? 0 : (job.pairs + 31 & ~31) % kRows;
+      const int fixer = (int)m - taken, fixers = kRows - taken;
+      const bool fixes = (!S::kByBlocks || b == 0) && fixer >= 0;
       const int mine_node = p.by_gqa.quotient(job.pair0 + min(row, job.pairs - 1));
       mbar_arrive(&sh.job_read);
       if (n == 0) break;
@@ -689,7 +694,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         mbar_wait(&sh.s_full[buf], turn, &sh.err, p.status);
         __syncwarp();
         fence_after();
-        if (some && (!S::kByBlocks || b == 0)) {
+        if (some && fixes) {
           // Zero weights must not meet what is no number (0 * NaN): rows of V past the
           // last token are whatever the page or the slot held, and a node's values may be
           // off the path of others.  Those that are no numbers are put aside, and
@@ -698,7 +703,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const uint32_t nth = all_tiles + (uint32_t)j, slot = nth % S::kSlotsV;
           mbar_wait(&sh.v_full[slot], nth / S::kSlotsV & 1, &sh.err, p.status);
           const uint32_t vs = vring + slot * S::kSlot;
-          for (int e = here * 8 + (int)m; e < parts * 32 * 8; e += kRows)
+          for (int e = here * 8 + fixer; e < parts * 32 * 8; e += fixers)
 #pragma unroll
             for (int d = 0; d < S::kPanels; ++d)
               asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vs + d * S::kPanel +
@@ -706,7 +711,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                            "r"(0)
                            : "memory");
           if (nodes) {
-            for (int e = (int)m; e < here * 8; e += kRows)
+            for (int e = fixer; e < here * 8; e += fixers)
 #pragma unroll
               for (int d = 0; d < S::kPanels; ++d) {
                 const uint32_t where = vs + d * S::kPanel + e * 16;
