@@ -6,6 +6,10 @@
 // row_bytes, a few KB that mostly lie side by side, and copying is all there is
 // to it.  A warp takes a token (append) or a few tokens (fork) of one layer's
 // keys or values, with its loads in flight together before the first store.
+//
+// Measured in a graph: accepted nodes of 64 trees of 11 into 32 layers 5.7 us (5.6 at a
+// copy's rate), of one tree 2.2; 8 samples of one prompt over 32 layers 9.7, 512 rows
+// over 4 layers 20.7 (4.4), 12 of them the plan's chain of loads and barriers.
 
 #include <cuda_runtime.h>
 #include <limits.h>

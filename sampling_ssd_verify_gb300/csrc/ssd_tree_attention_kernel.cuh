@@ -1,7 +1,7 @@
 // ssd_tree_attention_kernel.cuh -- attention of drafted nodes over a paged cache and
 // the nodes on their paths, on the 5th-generation tensor cores.
 //
-// A block is 128 (node, head) pairs of one sequence and key/value head, a tile kTile
+// A block is up to 128 (node, head) pairs of one sequence and key/value head, a tile kTile
 // tokens: of the cache, and after those of the sequence's nodes, where each pair's
 // weights of nodes off its path are zero.  S = Q K^T, P = exp2(S * scale - m), O += P V,
 // out = O / sum P.  An item is a sequence's key/value head and one or two blocks, and
@@ -20,13 +20,15 @@
 // exponentials of different tiles overlap (warps of their own, barriers between them), and
 // no barrier gets two phases ahead of a waiter.
 //
-// Measured, 32 heads on 8, D = 128: 256 sequences of 200 to 8000 tokens, one node each, 606 us
-// (7.1 TB/s; a copy has 6.8); two contexts of 131072 for 16 nodes 157 (6.8 TB/s); 64
-// sequences of 500 to 8191 in pages of 16 for trees of 11 178 (6.5 TB/s); 32 of them for 64
-// nodes 126 (1.16 PFLOP/s: the tensor cores are busy for 58% of the cycles; their operands come
+// Measured, 32 heads on 8, D = 128: 256 sequences of 200 to 8000 tokens, one node each, 603 us
+// (7.1 TB/s; a copy has 6.8); two contexts of 131072 for 16 nodes 158 (6.8 TB/s); 64
+// sequences of 500 to 8191 in pages of 16 for trees of 11 176 (6.5 TB/s); 32 of them for 64
+// nodes 124 (1.18 PFLOP/s: the tensor cores are busy for 57% of the cycles; their operands come
 // from shared memory at its rate, and a block's next scores wait for its weights).  One
-// stream of 700 tokens and 5 nodes 11.8: 4.6 until the first scores, 3 for the
-// stretch, 4 for the join.
+// stream of 700 tokens and 5 nodes 11.1: 5.5 until a tile's weights are there, 7.6 until
+// the last partials are, and the join from 8.6 on.  256 sequences of 10 to 200 tokens 65, where memory would take 17: an
+// item of one or two tiles is a chain of 3.4 us (scores, weights, sums, output) in the threads
+// of the exponentials.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -169,8 +171,8 @@ __device__ __forceinline__ void on_path(uint32_t (&ok)[TILE / 32], const uint8_t
 
 template <typename T, int D, int BLOCKS>
 __global__ void __launch_bounds__(kTreeThreads, 1)
-    tree_tc_kernel(const __grid_constant__ TreeAttnParams p, const __grid_constant__ CUtensorMap kmap,
-                   const __grid_constant__ CUtensorMap vmap,
+    tree_tc_kernel(const __grid_constant__ TreeAttnParams p,
+                   const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ CUtensorMap knodes,
                    const __grid_constant__ CUtensorMap vnodes,
                    const __grid_constant__ CUtensorMap qmap) {
