@@ -1069,9 +1069,11 @@ def _fork_views(torch, counts, cols, device):
 
 
 def _fork_pointers(o, counts, i32, dev):
-    """Addresses of fork_rows' outputs: views of one buffer, one after the other."""
+    """Addresses of fork_rows' outputs: views of one buffer, one after the other.  Their sizes
+    are looked at too: others may take the same places."""
     t = o.get("tables")
-    if t is None or t.dtype is not i32 or t.get_device() != dev or t.numel() != counts[0]:
+    if t is None or t.dtype is not i32 or t.get_device() != dev or t.shape[0] != counts[1] or \
+            not t.is_contiguous():
         raise SSDError("out: expected the dict of an earlier call with these sizes")
     memory = t.untyped_storage()
     first = at = memory.data_ptr()
@@ -1079,7 +1081,7 @@ def _fork_pointers(o, counts, i32, dev):
     get = o.get
     for name, n in zip(_FORK, counts):
         t = get(name)
-        if t is None or t.data_ptr() != at:
+        if t is None or t.data_ptr() != at or t.numel() != n:
             raise SSDError(f"out: {name} is not that of an earlier call with these sizes")
         ptrs.append(at)
         at += (n + 15 & ~15) * 4

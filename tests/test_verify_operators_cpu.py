@@ -273,3 +273,32 @@ def test_outputs_of_a_fork_are_known_again_and_come_whole():
             for other in ((4 * 7, 4, 4, 4, 49, 1), (5 * 7, 5, 5, 5, 33, 1), (4 * 7, 20, 4, 4, 33, 1)):
                 with pytest.raises(ssd.SSDError):
                     ssd._fork_pointers(o, other, torch.int32, -1)
+
+
+@pytest.mark.parametrize("made,asked", [
+    ((4, 7, 33), (7, 4, 33)), ((4, 7, 33), (14, 2, 48)), ((4, 7, 33), (4, 7, 40)),
+    ((4, 6, 30), (6, 4, 30)), ((8, 10, 97), (10, 8, 112)), ((2, 3, 100), (2, 3, 110)),
+    ((16, 16, 16), (16, 16, 15)), ((3, 5, 20), (5, 3, 20)),
+])
+def test_outputs_of_a_fork_of_other_sizes_are_refused(made, asked):
+    """Rows, columns and pages that take the same room in the buffer are told apart."""
+    import torch
+
+    def counts(B, cols, pages):
+        return B * cols, B, B, B, pages, 1
+
+    o = ssd._fork_views(torch, counts(*made), made[1], torch.device("cpu"))
+    assert ssd._fork_pointers(o, counts(*made), torch.int32, -1) == [o[k].data_ptr() for k in ssd._FORK]
+    with pytest.raises(ssd.SSDError, match="earlier call"):
+        ssd._fork_pointers(o, counts(*asked), torch.int32, -1)
+
+
+def test_outputs_of_a_fork_seen_otherwise_are_refused():
+    import torch
+
+    counts = (4 * 4, 4, 4, 4, 33, 1)
+    o = ssd._fork_views(torch, counts, 4, torch.device("cpu"))
+    for bad in (dict(tables=o["tables"].t()), dict(tables=o["tables"].view(-1)),
+                dict(lens=o["lens"][:3]), dict(shares=o["shares"][:32])):
+        with pytest.raises(ssd.SSDError, match="earlier call"):
+            ssd._fork_pointers(dict(o, **bad), counts, torch.int32, -1)
