@@ -710,9 +710,11 @@ ssd_status ssd_tree_attention(const ssd_tree_attn* a, void* workspace, size_t wo
  *             page_size are passed over and set SSD_DEV_BAD_PAGE; no two rows
  *             have one slot.
  * path        device int32, sequence b's row of path_cols starts at b *
- *             path_stride: accepted nodes as ssd_tree_verify writes them.  A row
- *             whose owner, place or node is out of range is passed over and
- *             sets SSD_DEV_BAD_LENGTH.
+ *             path_stride: accepted nodes as ssd_tree_verify writes them.  NULL:
+ *             a chain, whatever path_cols is; a path of no columns, with a
+ *             place for node 0 alone, has an address.  A row whose owner, place
+ *             or node is out of range is passed over and sets
+ *             SSD_DEV_BAD_LENGTH.
  * One launch, no workspace.
  * ------------------------------------------------------------------------- */
 typedef struct {

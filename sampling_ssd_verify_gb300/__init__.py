@@ -1037,14 +1037,15 @@ def append_path(k, v, k_cache, v_cache, slots, owner, cu, path=None, dev_status=
     row = slots.shape
     if len(row) != 1:
         raise SSDError("expected slots [T]")
+    at = _tensor(cu, "cu", i32, (B + 1,), dev)
     p = p_stride = p_cols = 0
     if path is not None:
         p, p_stride, p_cols = _rows2d(path, "path", B, i32, dev)
+        p = p or at  # one of no columns has no memory, but no address would mean a chain
     try:
         a = _PACK_APPEND(L, B, N, H, D * es, pages, page_size, row[0], p_cols, 0, *kl, *vl, *cl,
                          *wl, _tensor(slots, "slots", torch.int64, row, dev),
-                         _tensor(owner, "owner", i32, row, dev),
-                         _tensor(cu, "cu", i32, (B + 1,), dev), p, p_stride)
+                         _tensor(owner, "owner", i32, row, dev), at, p, p_stride)
     except _UNPACKED as e:
         raise SSDError(f"ssd_append_path: {e}") from None
     st = lib().ssd_append_path(a, None if dev_status is None else _dev_ptr(dev_status),

@@ -541,3 +541,21 @@ def test_page_sizes_beyond_32_bits_are_refused(page):
     s = on_gpu(fork_case(4, 5, 6, 8, 9, L=2))
     with pytest.raises(ssd.SSDError):
         run_fork(dict(s, page=page, k_cache=None, v_cache=None))
+
+
+def test_append_with_a_path_of_no_columns():
+    """Only node 0 has a place; rows past it are passed over and flagged, as with a path that is
+    too short."""
+    torch, dev = torch_dev()
+    gen = torch.Generator(device=dev).manual_seed(0)
+    k, c = filled((2, 3, 4, 2, 64), torch.bfloat16, gen), filled((2, 9, 16, 2, 64), torch.bfloat16, gen)
+    slots = torch.tensor([5, 20, 21, 40, -1], device=dev)
+    owner, cu = i32([0, 1, 1, 2, -1]), i32([0, 1, 3, 4])
+    for path in (torch.empty((3, 0), dtype=torch.int32, device=dev), i32([[1], [2], [3]])[:, :0]):
+        cache, status = c.clone(), torch.zeros(1, dtype=torch.int32, device=dev)
+        ssd.append_path(k, None, cache, None, slots, owner, cu, path, dev_status=status)
+        want = c.clone()
+        for slot, b in ((5, 0), (20, 1), (40, 2)):
+            want[:, slot // 16, slot % 16] = k[:, b, 0]
+        assert torch.equal(raw(cache), raw(want))
+        assert int(status.item()) == ssd.DEV_BAD_LENGTH

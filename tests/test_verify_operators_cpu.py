@@ -302,3 +302,52 @@ def test_outputs_of_a_fork_seen_otherwise_are_refused():
                 dict(lens=o["lens"][:3]), dict(shares=o["shares"][:32])):
         with pytest.raises(ssd.SSDError, match="earlier call"):
             ssd._fork_pointers(dict(o, **bad), counts, torch.int32, -1)
+
+
+class _Library:
+    """Keeps the descriptors of its calls."""
+
+    def __init__(self):
+        self.seen = []
+
+    def __getattr__(self, name):
+        def call(a, *rest):
+            self.seen.append((name, a))
+            return 256 if name.endswith("workspace_size") else 0
+        return call
+
+
+@pytest.fixture
+def here(monkeypatch):
+    """The binding with a library that launches nothing, and CPU tensors that pass for the current
+    GPU's."""
+    import torch
+
+    class Here(torch.Tensor):
+        is_cuda = True
+
+        def get_device(self):
+            return 0
+
+    library = _Library()
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
+    monkeypatch.setattr(ssd, "lib", lambda: library)
+    monkeypatch.setattr(ssd, "_torch_module", torch)
+    return library, lambda t: t.as_subclass(Here)
+
+
+def test_a_path_of_no_columns_is_a_path(here):
+    import torch
+
+    library, on = here
+    k, c = (on(torch.zeros(shape, dtype=torch.bfloat16)) for shape in ((2, 3, 2, 64), (9, 16, 2, 64)))
+    slots, owner, cu = on(torch.zeros(4, dtype=torch.int64)), on(torch.zeros(4, dtype=torch.int32)), \
+        on(torch.tensor([0, 2, 4], dtype=torch.int32))
+    for path in (None, on(torch.zeros((2, 0), dtype=torch.int32)),
+                 on(torch.zeros((2, 2), dtype=torch.int32)[:, :0]),
+                 on(torch.zeros((2, 2), dtype=torch.int32))):
+        ssd.append_path(k, None, c, None, slots, owner, cu, path)
+        a = _Append.from_buffer_copy(library.seen.pop()[1])
+        assert a.path_cols == (0 if path is None else path.shape[1])
+        assert bool(a.path) == (path is not None)  # without an address: a chain
