@@ -666,7 +666,10 @@ ssd_status ssd_prefix_attention(const ssd_attention* a, void* workspace, size_t 
  *             same descriptor.
  * N <= 256.  Scores, their maxima and sums and the outputs' sums are held in
  * float32; the weights exp(s_j - max) are rounded to dtype for the matrix
- * product.
+ * product (SSD_F16: to 2^-32 at least, so that the small weights of a long
+ * cache add up beside a large one).  A row whose largest score times log2 e is
+ * beyond +-2^28 (SSD_F16) or +-2^31 (SSD_BF16), where float32 has steps of 32
+ * and 256, is undefined.
  * ------------------------------------------------------------------------- */
 typedef struct {
   int32_t dtype; /* ssd_dtype */

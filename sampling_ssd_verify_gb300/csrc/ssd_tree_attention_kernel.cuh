@@ -54,6 +54,13 @@ constexpr int kCopyK = 8, kCopyV = 9, kMmaWarp = 10, kQueryWarp = 11;
 // gives up 80 and the others take 40 each: 8 * 208 + 4 * 88 = 12 * 168.
 constexpr int kRegsSoftmax = 208, kRegsOther = 88;
 constexpr float kRise = 8.f;              // scores may pass the kept maximum by this (base 2)
+// Half has no weights below 2^-24: beside one that is the largest the many small ones of a long
+// cache would be lost from the sums.  So all of a half's weights are 2^kLift larger, up to
+// 2^(kRise + kLift) of the 2^16 that there are: what is lost then is at most 2^-32 of the largest
+// weight for each token (2^-15 for 131072 of them).  Large scores are rounded when they are
+// scaled, by 2^4 from 2^27 on; half's maxima are rounded up, so that no weight grows by it.
+template <typename T>
+constexpr float kLift = __is_same(T, __half) ? 7.f : 0.f;
 
 constexpr int kColS = 0, kColStep = 128;  // scores (and weights) of a buffer in tensor memory
 
@@ -742,7 +749,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             for (int e = 0; e < 32; ++e)
               if (!(word & 1u << e)) x[e] = 0xff800000u;  // -inf
           };
-          // The kept maximum moves when a score passes it by 2^kRise; gives the weights' offset.
+          auto scaled = [&](float x) {
+            return kLift<T> > 0.f ? __fmul_ru(x, p.scale_log2) : x * p.scale_log2;
+          };
+          // The kept maximum moves when a score passes it by kRise; gives the weights' offset.
           auto raise = [&](float now) {
             const bool move = now > top + kRise;
             const float old = top;
@@ -772,10 +782,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const float2 by = make_float2(p.scale_log2, p.scale_log2);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           // Weights of 32 tokens in the type of V, as the product takes them: each is off by at
-          // most half a step, which an output averages over its tokens; their sum is of
-          // the unrounded ones.
+          // most half a step (bf16 2^-8, half 2^-11, or 2^-32 of the largest where that is more), and
+          // an output by at most that part of sum p |v|: by less where the steps are of both
+          // signs, by all of it where many weights are equal.  Their sum is of the unrounded ones.
           auto weights = [&](const uint32_t (&x)[32], int q, float off, bool half) {
-            const float2 less = make_float2(-off, -off);
+            const float2 less = make_float2(kLift<T> - off, kLift<T> - off);
             uint32_t z[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
@@ -821,7 +832,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                   high[y] = max3(high[y], __uint_as_float(x[e + y]), __uint_as_float(x[e + 4 + y]));
               now = max3(fmaxf(high[0], high[1]), high[2], high[3]);
             }
-            const float off = raise(now * p.scale_log2);
+            const float off = raise(scaled(now));
 #pragma unroll 1
             for (int q = 0; q < parts; ++q) {
               load(q);
@@ -846,8 +857,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                 high[y] = max3(high[y], __uint_as_float(x[e / 32][e % 32 + y]),
                                __uint_as_float(x[e / 32][e % 32 + 8 + y]));
             const float off =
-                raise(max3(max3(high[0], high[1], high[2]), max3(high[3], high[4], high[5]),
-                           fmaxf(high[6], high[7])) * p.scale_log2);
+                raise(scaled(max3(max3(high[0], high[1], high[2]), max3(high[3], high[4], high[5]),
+                                  fmaxf(high[6], high[7]))));
 #pragma unroll
             for (int q = 0; q < kParts; ++q) weights(x[q], q, off, q == kParts / 2 - 1);
           }
@@ -866,7 +877,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       // 32 x 64 nodes 126 instead of 129).
       const bool mine_has = S::kOne || j0 < n, other_has = S::kByTiles && (j0 ^ 1) < n;
       if (i > 0) mbar_wait(&sh.o_empty, (i - 1) & 1, &sh.err, p.status);  // ml has been read
-      if (!S::kOne || b == 0) sh.ml[b][m] = make_float2(top, l);
+      if (!S::kOne || b == 0) sh.ml[b][m] = make_float2(top - kLift<T>, l);
       mbar_arrive(&sh.ml_full);
       mbar_wait(&sh.ml_full, i & 1, &sh.err, p.status);
       __syncwarp();

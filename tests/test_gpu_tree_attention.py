@@ -577,3 +577,85 @@ def test_scales_beyond_float32_are_refused(scale):
     s = make([40, 3], 3, 4, 2, 64, 16, dtype_of("bfloat16"), "binary")
     with pytest.raises(ssd.SSDError):
         call(s, scale=scale)
+
+
+@pytest.mark.parametrize("below", [20.3, 24.45, 25.1, 27.0])
+@pytest.mark.parametrize("D,N,Hq", [(64, 1, 1), (128, 5, 4), (64, 40, 4), (128, 40, 4), (256, 3, 2)])
+def test_many_small_weights_beside_a_large_one(below, D, N, Hq):
+    """Two tokens with the largest score and values of 0, and 131072 whose weights are 2^-below of
+    theirs and whose values are 1: what these add up to is the output.  Each worker goes through
+    whole sequences, so that the largest score is kept beside the others.
+
+    Tolerance: as above, where a half's step is at least 2^-24 beside a largest weight of at least
+    2^7: with W = sum |v| (n + N at most), 2^-25 W / 2^7.
+    """
+    torch, dev = torch_dev()
+    n, page, B = 131072, 64, 320
+    kc = torch.zeros((n // page, page, 1, D), dtype=torch.float16, device=dev)
+    vc = torch.ones_like(kc)
+    for t in (0, 128):                   # of both streams of tiles
+        kc[t // page, t % page, 0, 0], vc[t // page, t % page] = 1.0, 0.0
+    q = torch.zeros((B, N, Hq, D), dtype=torch.float16, device=dev)
+    q[..., 0] = 1.0
+    k = torch.zeros((B, N, 1, D), dtype=torch.float16, device=dev)
+    tables = torch.arange(n // page, dtype=torch.int32, device=dev).expand(B, -1).contiguous()
+    scale = float(np.float32(below * math.log(2)))
+    o = ssd.tree_attention(q, k, torch.ones_like(k), kc, vc, tables, i32([n] * B), scale=scale)
+    w = math.exp(-scale)
+    for u in {0, N - 1}:
+        small = (n - 2 + u + 1) * w
+        want, A = small / (2 + small), small / (2 + small)
+        rs = (D + 4) * 2.0 ** -23 * scale + 2.0 ** -21
+        eps = torch.finfo(torch.float16).eps
+        tol = A * (eps / 2 + 2 * rs + (n + N + 8) * 2.0 ** -23) + eps / 2 * want + 2.0 ** -32 * (n + N)
+        got = o["out"][:, u].double()
+        assert float((got - want).abs().max()) <= tol, (float(got.min()), float(got.max()), want, tol)
+        lse = scale + math.log(2 + small)
+        assert float((o["lse"][:, u].double() - lse).abs().max()) <= \
+            rs + (n + N) * 2.0 ** -24 + 2.0 ** -21 + 2.0 ** -23 * lse
+
+
+@pytest.mark.parametrize("dt,top", [("float16", 20.4), ("float16", 24.3), ("float16", 26.7),
+                                    ("float16", 27.95), ("bfloat16", 24.3), ("bfloat16", 30.95)])
+@pytest.mark.parametrize("D,N,Hq", [(64, 2, 4), (128, 2, 4), (128, 70, 4), (256, 2, 4)])
+@pytest.mark.parametrize("cached", [0, 700])
+def test_large_scores(dt, top, D, N, Hq, cached):
+    """Scores of 2^top (base 2), which float32 rounds to multiples of up to 128, equal ones alike: nodes
+    with one key share their row equally, beside cached tokens that come nowhere near.
+
+    Each row has one weight w, which the type rounds by eps / 2 and their sum does not; the sum of
+    the values is off by N 2^-23 in float32, the reciprocal and its product by 2^-23 each, and the
+    output is rounded by eps / 2, or a half's 2^-25:
+      |out - mean| <= (eps / 2) |mean| + (eps / 2 + (N + 4) 2^-23) mean |v| + 2^-25.
+    A row's weight is 2^-16 to 1 (bf16: 2^-64 to 2^64), beyond what either type rounds otherwise
+    (half: normal from 2^-14, and 2^7 more here)."""
+    torch, dev = torch_dev()
+    t = dtype_of(dt)
+    B, eps = 100, torch.finfo(t).eps
+    s = make([cached] * B, N, Hq, 2, D, 16, t, seed=D)
+    s["q"].fill_(200.0)
+    s["k"].fill_(300.0)
+    s["kc"].fill_(150.0)
+    scale = 2.0 ** top / math.log2(math.e) / (200.0 * 300.0 * D)
+    for sign in (1, -1):
+        o = call(dict(s, q=s["q"] * sign), scale=sign * scale)
+        v = s["v"].double()[:, :, torch.arange(Hq, device=dev) // (Hq // 2)]
+        n = torch.arange(1, N + 1, device=dev)[:, None, None]
+        mean, A = v.cumsum(1) / n, v.abs().cumsum(1) / n
+        tol = eps / 2 * mean.abs() + (eps / 2 + (N + 4) * 2.0 ** -23) * A + 2.0 ** -25
+        assert bool(((o["out"].double() - mean).abs() <= tol).all())
+        lse = 2.0 ** top / math.log2(math.e)
+        assert bool(((o["lse"] - lse).abs() <= (D + 8) * 2.0 ** -23 * lse + math.log(N)).all())
+
+
+def test_large_scores_of_a_row_leave_the_others_bits():
+    torch, dev = torch_dev()
+    for t, N in ((torch.float16, 9), (torch.bfloat16, 40)):
+        s = make([500, 40], N, 16, 4, 128, 16, t, "random")
+        want = {k: call(s)[k].clone() for k in ("out", "lse")}
+        s["q"][0, 3, 5] = 3e4
+        keep = torch.ones((2, N, 16), dtype=torch.bool, device=dev)
+        keep[0, 3, 5] = False
+        got = call(s)
+        for k in want:
+            assert torch.equal(got[k][keep], want[k][keep])
