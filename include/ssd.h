@@ -776,7 +776,9 @@ ssd_status ssd_append_path(const ssd_append* a, int32_t* dev_status, void* strea
  * shares      device [num_pages] int32, not negative.
  * free_pages  device [free_cap] int32; free_count device int32 in [0,
  *             free_cap] (clamped otherwise, SSD_DEV_BAD_LENGTH).  Pages past
- *             its end: as in ssd_page_plan.
+ *             its end: as in ssd_page_plan.  An entry taken that is outside [0,
+ *             num_pages) sets SSD_DEV_BAD_PAGE; it is off the stack, and the
+ *             row is left empty, served[b] = 0.
  * tables_out  device [B, cols] int32 out, -1 past a row's pages; lens_out,
  *             held_out, served device [B] int32 out; shares_out device
  *             [num_pages] int32 out; free_out device int32 out.  Outputs are not

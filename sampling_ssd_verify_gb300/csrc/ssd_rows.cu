@@ -398,10 +398,16 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
         if (take) {
           given = nth < back;              // its page is put down where it is given back
           if (!given) row.w = f.free_pages[top - 1 - nth];
+          const bool none = !given && (unsigned)row.w >= (unsigned)f.num_pages;
           int* copy = reinterpret_cast<int*>(p.copies + nth);
           copy[0] = b == gtid ? early_page : last_page(b);
           if (!given) copy[1] = row.w;
-          copy[2] = len - full * f.page_size;
+          copy[2] = none ? 0 : len - full * f.page_size;
+          if (none) {                      // off the stack, and no page: the row is left empty
+            bad |= SSD_DEV_BAD_PAGE;
+            ok = len = 0;
+            row = make_int4(-1, 0, 0, -1);
+          }
         }
       } else {
         bad |= SSD_DEV_NO_PAGES;

@@ -559,3 +559,64 @@ def test_append_with_a_path_of_no_columns():
             want[:, slot // 16, slot % 16] = k[:, b, 0]
         assert torch.equal(raw(cache), raw(want))
         assert int(status.item()) == ssd.DEV_BAD_LENGTH
+
+
+@pytest.mark.parametrize("L", [0, 3])
+@pytest.mark.parametrize("x", [-1, 40, -9, 2 ** 31 - 1, -2 ** 31])
+@pytest.mark.parametrize("W", [6, 900])
+def test_fork_passes_over_stack_entries_that_are_no_pages(L, x, W):
+    """The row that would take one is left empty and not served, and the entry is off the stack;
+    rows after it take the next."""
+    torch, dev = torch_dev()
+    s = fork_case(5, 5, W, 8, 9, src=[0, 0, 1, 0, 1], shared=False, seed=1)
+    s["lens"][:] = 13
+    s["held"][:] = 2
+    s["tables"][:, :2] = np.arange(10).reshape(5, 2)
+    s["free_pages"][:9] = np.arange(10, 19)
+    s["shares"] = np.zeros(40, dtype=int)
+    s["free_count"][0] = 2               # below the six pages that rows 2 to 4 give back
+    gen = torch.Generator(device=dev).manual_seed(2)
+    for name in ("k_cache", "v_cache"):
+        s[name] = filled((L, 40, 8, 1, 16), torch.bfloat16, gen) if L else None
+
+    def call(src):
+        s["src"] = np.array(src)
+        d = on_gpu(s)
+        for name in ("k_cache", "v_cache"):
+            d[name] = s[name].clone() if L else None
+        status = torch.zeros(1, dtype=torch.int32, device=dev)
+        o = {k: v.cpu().numpy() for k, v in run_fork(d, dev_status=status).items()}
+        for k in ("tables", "lens", "held", "served", "shares"):
+            o[k] = o[k].tolist()
+        o["tables"] = [[p for p in r if p != -1] for r in o["tables"]]
+        return o, int(status.item()), d
+
+    # no row gives pages back: the stack alone, of which an entry is no page
+    for bad, pages in ((1, (None, 10)), (0, (11, None))):
+        s["free_pages"][:2] = [10, 11]
+        s["free_pages"][bad] = x
+        o, status, d = call([0, 1, 2, 3, 4, 0, 1])
+        assert status == ssd.DEV_BAD_PAGE
+        want = [[0, 1], [2, 3], [4, 5], [6, 7], [8, 9]]
+        for row, page in zip((0, 2), pages):
+            want.append([] if page is None else [row, page])
+        assert o["tables"] == want
+        assert o["served"] == [1] * 5 + [int(p is not None) for p in pages]
+        assert o["held"] == [len(r) for r in want] and o["lens"] == [13 if r else 0 for r in want]
+        assert sum(o["shares"]) == 1 and o["shares"][0 if pages[0] else 2] == 1
+        assert o["free_count"][0] == 0
+        for name in ("k_cache", "v_cache"):
+            if L:
+                c = s[name].clone()
+                old, new = (1, pages[0]) if pages[0] else (3, pages[1])
+                c[:, new, :5] = c[:, old, :5]
+                assert torch.equal(raw(d[name]), raw(c))
+    # pages given back are taken first: the entry below them is reached by the last row alone
+    s["free_pages"][:2] = [10, x]
+    o, status, d = call([0, 0, 0, 0, 0, 0, 0, 0, 0, 0])
+    assert status == ssd.DEV_BAD_PAGE
+    assert o["tables"] == [[0, 1]] + [[0, p] for p in (9, 8, 7, 6, 5, 4, 3, 2)] + [[]]
+    assert o["served"] == [1] * 9 + [0] and o["free_count"][0] == 1 and o["shares"][0] == 8
+    # and where no row takes it, it stays
+    o, status, d = call([0, 0, -1])
+    assert status == 0 and o["free_count"][0] == 9 and int(d["free_pages"][1]) == x
