@@ -875,9 +875,15 @@ _parents = {}  # trees by their bytes: the library reads them by address
 
 
 def _parent_address(parent, N):
-    if len(parent) != N:
-        raise SSDError("parent must have N entries")
-    key = np.asarray(parent, dtype=np.int32).tobytes()
+    try:
+        par = np.asarray(parent, dtype=np.int32)
+        good = par.shape == (N,) and (par is parent or par.tolist() == (
+            parent.tolist() if hasattr(parent, "tolist") else list(parent)))
+    except (TypeError, ValueError, OverflowError):
+        good = False
+    if not good:
+        raise SSDError("parent must have N entries, whole numbers of 32 bits")
+    key = par.tobytes()
     kept = _parents.get(key)
     if kept is None:
         if len(_parents) >= 256:

@@ -351,3 +351,43 @@ def test_a_path_of_no_columns_is_a_path(here):
         a = _Append.from_buffer_copy(library.seen.pop()[1])
         assert a.path_cols == (0 if path is None else path.shape[1])
         assert bool(a.path) == (path is not None)  # without an address: a chain
+
+
+def _drafts(on, N):
+    import torch
+
+    q, k = (on(torch.zeros((2, N, H, 64), dtype=torch.bfloat16)) for H in (4, 2))
+    c = on(torch.zeros((9, 16, 2, 64), dtype=torch.bfloat16))
+    return q, k, k, c, c, on(torch.zeros((2, 4), dtype=torch.int32)), \
+        on(torch.zeros(2, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("parent", [
+    [-1, 0, 2 ** 31], [-1, 0, -2 ** 40], [-1, 0, 2 ** 70], [-1, 0.5, 1], np.array([-1.0, 0.0, 0.9]),
+    np.array([[-1, 5], [0, 5], [1, 5]]), [[-1], [0], [1]], [-1, 0], [-1, 0, 1, 1], [-1, None, 0],
+    ["-1", "0", "1"], [-1, [0], 0], 3, np.int64(3), np.array([2 ** 40, 0, 0]),
+    np.array([2 ** 64 - 1, 0, 0], dtype=np.uint64),
+])
+def test_parents_that_are_no_tree_of_the_nodes_are_refused(here, parent):
+    library, on = here
+    with pytest.raises(ssd.SSDError, match="parent"):
+        ssd.tree_attention(*_drafts(on, 3), parent=parent, lse=False)
+    assert not library.seen
+
+
+def test_parents_of_any_whole_type(here):
+    import torch
+
+    library, on = here
+    for parent in ([-1, 0, 0], (-1, 0, 0), np.array([-1, 0, 0]), np.array([-1, 0, 0], dtype=np.int8),
+                   np.array([[-1, 0, 0]] * 2)[0], torch.tensor([-1, 0, 0]), [np.int64(-1), 0, 0],
+                   [-1.0, 0.0, 0.0], np.array([-1, 0, 0], dtype=object),
+                   np.array([-1, 7, 0, 7, 0])[::2]):
+        ssd.tree_attention(*_drafts(on, 3), parent=parent, lse=False)
+        name, a = library.seen.pop()
+        library.seen.clear()
+        assert name == "ssd_tree_attention"
+        at = type("T", (ctypes.Structure,), {"_fields_": [
+            (n, ctypes.c_void_p if f is ctypes.c_char_p else f) for n, f in _TreeAttn._fields_]}) \
+            .from_buffer_copy(a).parent
+        assert np.frombuffer(ctypes.string_at(at, 12), dtype=np.int32).tolist() == [-1, 0, 0]
