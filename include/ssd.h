@@ -647,7 +647,8 @@ ssd_status ssd_prefix_attention(const ssd_attention* a, void* workspace, size_t 
  *             contiguous, strides are in elements, multiples of 8 and not
  *             negative, bases 16-byte aligned.  D: 64, 128 or 256.  Hkv
  *             divides Hq.  out is q itself (same pointer and strides) or does
- *             not overlap it, nor any key or value.
+ *             not overlap it, nor any key or value, and none of its rows lies on
+ *             another (strides below D are SSD_ERR_INVALID_ARG).
  * k, v        [B, N, Hkv, D] of dtype, the nodes': page_stride is a
  *             sequence's, token_stride a node's.
  * k_cache, v_cache  [num_pages, page_size, Hkv, D] of dtype, any order of the
@@ -706,8 +707,9 @@ ssd_status ssd_tree_attention(const ssd_tree_attn* a, void* workspace, size_t wo
  *             bytes (page_stride: a sequence's); k_cache, v_cache: [L,
  *             num_pages, page_size, H] rows.  row_bytes, strides and bases are
  *             multiples of 16, strides not negative; the caches overlap
- *             neither one another nor the nodes.  v and v_cache may both be
- *             NULL.
+ *             neither one another nor the nodes, and none of their rows lies on
+ *             another (strides below row_bytes are SSD_ERR_INVALID_ARG).  v and
+ *             v_cache may both be NULL.
  * slots       device [rows] int64, owner [rows] and cu [B + 1] device int32, as
  *             ssd_page_plan writes them.  Slots at or past num_pages *
  *             page_size are passed over and set SSD_DEV_BAD_PAGE; no two rows

@@ -501,6 +501,12 @@ bool layers_ok(const ssd_layers& x) {
     if (s < 0 || s % 16 != 0) return false;
   return true;
 }
+// Whether no two rows of [L, X, Y, H] lie on one another by a stride alone.
+bool rows_apart(const ssd_layers& x, int L, int X, int Y, int H, int row_bytes) {
+  auto ok = [&](int n, int64_t stride) { return n == 1 || stride >= row_bytes; };
+  return ok(L, x.layer_stride) && ok(X, x.page_stride) && ok(Y, x.token_stride) &&
+         ok(H, x.head_stride);
+}
 // Heads side by side in all of them are one row.
 Geometry geometry(int L, int H, int row_bytes, bool pair,
                   std::initializer_list<const ssd_layers*> all) {
@@ -580,6 +586,9 @@ ssd_status ssd_append_path(const ssd_append* a, int32_t* dev_status, void* strea
   if (pair && (a->k.ptr == a->v_cache.ptr || a->v.ptr == a->v_cache.ptr))
     return SSD_ERR_INVALID_ARG;
   if (!rows_fit(a->H, a->row_bytes, a->L)) return SSD_ERR_UNSUPPORTED;
+  for (const ssd_layers* c : {&a->k_cache, &a->v_cache})
+    if (c->ptr && !rows_apart(*c, a->L, a->num_pages, a->page_size, a->H, a->row_bytes))
+      return SSD_ERR_INVALID_ARG;
   AppendParams p{};
   p.a = *a;
   p.g = geometry(a->L, a->H, a->row_bytes, pair, {&a->k, &a->v, &a->k_cache, &a->v_cache});

@@ -26,6 +26,9 @@ bool view_ok(const ssd_paged& x) {
   return view_ok(x.ptr, {x.page_stride, x.token_stride, x.head_stride});
 }
 
+// Whether rows of D elements that a dimension of n lies apart by a stride are apart.
+bool apart(int n, int64_t stride, int D) { return n == 1 || stride >= D; }
+
 // Tokens and (node, head) pairs are counted in 32 bits.
 constexpr int64_t kMaxCount = 0x7fffffff - (1 << 20);
 
@@ -151,6 +154,9 @@ ssd_status ssd_tree_attention(const ssd_tree_attn* a, void* workspace, size_t wo
   if (!view_ok(a->q, {a->q_seq_stride, a->q_node_stride, a->q_head_stride}) ||
       !view_ok(a->out, {a->out_seq_stride, a->out_node_stride, a->out_head_stride}) ||
       !view_ok(a->k) || !view_ok(a->v) || !view_ok(a->k_cache) || !view_ok(a->v_cache))
+    return SSD_ERR_INVALID_ARG;
+  if (!apart(a->B, a->out_seq_stride, a->D) || !apart(a->N, a->out_node_stride, a->D) ||
+      !apart(a->Hq, a->out_head_stride, a->D))
     return SSD_ERR_INVALID_ARG;
   if (a->out == a->q &&
       (a->out_seq_stride != a->q_seq_stride || a->out_node_stride != a->q_node_stride ||

@@ -391,3 +391,27 @@ def test_parents_of_any_whole_type(here):
             (n, ctypes.c_void_p if f is ctypes.c_char_p else f) for n, f in _TreeAttn._fields_]}) \
             .from_buffer_copy(a).parent
         assert np.frombuffer(ctypes.string_at(at, 12), dtype=np.int32).tolist() == [-1, 0, 0]
+
+
+@pytest.mark.parametrize("kw,status", [
+    *[({f"out_{d}_stride": x}, INVALID) for d in ("seq", "node", "head") for x in (0, 8, 56)],
+    ({"out_head_stride": 64}, WORKSPACE),
+    ({"B": 1, "out_seq_stride": 0}, WORKSPACE), ({"N": 1, "out_node_stride": 0}, WORKSPACE),
+    ({"Hq": 1, "Hkv": 1, "out_head_stride": 0}, WORKSPACE),
+])
+def test_outputs_that_lie_on_one_another_are_refused(L, kw, status):
+    assert L.ssd_tree_attention(ctypes.byref(_tree(**kw)), None, 0, None, None) == status
+
+
+@pytest.mark.parametrize("at,n", list(enumerate(("L", "num_pages", "page_size", "H"))))
+@pytest.mark.parametrize("name", ["k_cache", "v_cache"])
+def test_caches_that_lie_on_themselves_are_refused(L, at, n, name):
+    """An expanded cache, or one whose rows overlap, takes several tokens in one place."""
+    for x in (0, 16, 112):
+        row = [*ROW]
+        row[at] = x
+        kw = {name: ((3 if name == "k_cache" else 4) * PTR, *row)}
+        assert L.ssd_append_path(ctypes.byref(_append(**kw)), None, None) == INVALID
+        assert L.ssd_append_path(ctypes.byref(_append(**kw, **{n: 1})), None, None) == 0
+        # nodes are only read
+        assert L.ssd_append_path(ctypes.byref(_append(k=(PTR, *row))), None, None) == 0
