@@ -663,6 +663,7 @@ ssd_status ssd_prefix_attention(const ssd_attention* a, void* workspace, size_t 
  *             work beyond 32-bit counts are SSD_ERR_UNSUPPORTED.
  * parent      HOST [N] int32 as in ssd_tree_verify, or NULL for a chain.
  * lse         device [B, N, Hq] float out (or NULL).
+ * scale       finite, also times log2 e; of any sign, or 0.
  * workspace   256-byte aligned, >= ssd_tree_attention_workspace_size of the
  *             same descriptor.
  * N <= 256.  Scores, their maxima and sums and the outputs' sums are held in

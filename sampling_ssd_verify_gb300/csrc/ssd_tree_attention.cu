@@ -32,10 +32,13 @@ bool apart(int n, int64_t stride, int D) { return n == 1 || stride >= D; }
 // Tokens and (node, head) pairs are counted in 32 bits.
 constexpr int64_t kMaxCount = 0x7fffffff - (1 << 20);
 
+// The scale of scores in base 2.
+float base_2(float scale) { return (float)((double)scale * 1.4426950408889634); }
+
 ssd_status check(const ssd_tree_attn* a) {
   if (!a || (a->dtype != SSD_BF16 && a->dtype != SSD_F16)) return SSD_ERR_INVALID_ARG;
   if (a->B < 1 || a->N < 1 || a->Hq < 1 || a->Hkv < 1 || a->Hq % a->Hkv != 0 ||
-      a->num_pages < 1 || a->page_size < 1 || a->cols < 0 || !std::isfinite(a->scale))
+      a->num_pages < 1 || a->page_size < 1 || a->cols < 0 || !std::isfinite(base_2(a->scale)))
     return SSD_ERR_INVALID_ARG;
   // tables of no columns may have no address
   if ((!a->tables && a->cols > 0) || !a->lens || a->table_stride < a->cols)
@@ -73,7 +76,7 @@ bool plan(const ssd_tree_attn& a, TreeAttnParams& p, Layout& L) {
   p.blocks = (p.pairs + rows - 1) / rows;
   p.part_rows = (std::min(p.pairs, rows) + 7) / 8 * 8;
   // -q for a negative scale, 0 for none: the maximum is taken before the scale
-  p.scale_log2 = (float)(std::fabs((double)a.scale) * 1.4426950408889634);
+  p.scale_log2 = std::fabs(base_2(a.scale));
   p.q_and = ~0u;
   p.q_xor = 0u;
   if (p.scale_log2 == 0.f) {

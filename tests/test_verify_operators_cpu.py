@@ -415,3 +415,12 @@ def test_caches_that_lie_on_themselves_are_refused(L, at, n, name):
         assert L.ssd_append_path(ctypes.byref(_append(**kw, **{n: 1})), None, None) == 0
         # nodes are only read
         assert L.ssd_append_path(ctypes.byref(_append(k=(PTR, *row))), None, None) == 0
+
+
+@pytest.mark.parametrize("scale", [2.4e38, -2.4e38, 3.4e38])
+def test_scales_that_pass_float32_in_base_2_are_refused(L, scale):
+    a = _tree(scale=scale)
+    assert L.ssd_tree_attention(ctypes.byref(a), None, 0, None, None) == INVALID
+    assert L.ssd_tree_attention_workspace_size(ctypes.byref(a)) == 0
+    assert L.ssd_tree_attention(ctypes.byref(_tree(scale=scale * 0.9)), None, 0, None, None) == \
+        (WORKSPACE if abs(scale) < 2.5e38 else INVALID)
