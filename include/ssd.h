@@ -527,6 +527,10 @@ ssd_status ssd_process_logits(const ssd_logits* in, const ssd_logits* out, int B
  * A request is not served, and SSD_DEV_BAD_LENGTH set, when lens, new or held
  * are negative, held > cols, lens + new > cols * page, or held pages do not
  * hold lens tokens; it keeps its pages and has no rows.
+ * Pages are taken to have one holder: what step 1 pushes is free, whoever
+ * else's table names it.  So where rows share pages (ssd_fork_rows), a row
+ * that holds some ends through ssd_fork_rows and not here, and lens + new do
+ * not fall below the tokens that it shares; the pages behind those are its own.
  *
  * Outputs are not inputs, but arrays of their own (SSD_ERR_INVALID_ARG where
  * an output has an input's address).
@@ -761,7 +765,9 @@ ssd_status ssd_append_path(const ssd_append* a, int32_t* dev_status, void* strea
  *      layers are copied.  When the stack is empty, it and every later one
  *      that needs a page are left empty: served[b] = 0 (SSD_DEV_NO_PAGES).
  * A page that holds tokens at or past lens[s] is not to be shared: 3 never
- * does.
+ * does.  ssd_page_plan does not know shares: rows with shared pages end here
+ * alone, and never fall below the tokens that they share (a rollback behind
+ * their fork), or other rows' pages would be given out again.
  * The inputs are left as they are but for entries of free_pages at or past
  * *free_count and the copied tokens, so a call repeated on the same inputs
  * gives the same results; the next call passes the outputs.

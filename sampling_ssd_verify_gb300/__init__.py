@@ -762,7 +762,9 @@ def page_plan(lens, new, held, tables, free_pages, free_count, page_size, max_ro
     Returns a dict of device tensors: slots int64, positions and owner int32
     [max_rows]; cu int32 [B + 1]; kv_len, held, served int32 [B]; free_count
     int32 [1].  `out`: the dict of an earlier call, to use its tensors again
-    (not while one of them is this call's input)."""
+    (not while one of them is this call's input).
+    What it gives back is free whoever else holds it: rows with pages that they
+    share end through fork_rows, and do not fall below the tokens shared."""
     torch = _torch()
     i32 = torch.int32
     dev = lens.get_device()
@@ -1108,6 +1110,8 @@ def fork_rows(src, lens, held, tables, shares, free_pages, free_count, page_size
     continues one keeps its pages, the others share the full ones and get a copy of the tokens
     of the last in a page from the stack.  k_cache, v_cache [L, pages, page_size, H, D] (or of
     one layer) hold those tokens (None: nothing is copied; v_cache alone may be None too).
+    page_plan does not know shares: rows with shared pages end here alone, and their lengths
+    never fall below the tokens that they share.
     Returns a dict of device tensors: tables [B, W], lens, held, served [B], shares [pages],
     free_count [1], all int32.  `out`: the dict of an earlier call of these sizes, to use its
     tensors and workspace again (not while one of them is this call's input)."""
