@@ -782,8 +782,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const float2 by = make_float2(p.scale_log2, p.scale_log2);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           // Weights of 32 tokens in the type of V, as the product takes them: each is off by at
-          // most half a step (bf16 2^-8, half 2^-11, or 2^-32 of the largest where that is more), and
-          // an output by at most that part of sum p |v|: by less where the steps are of both
+          // most half a step (bf16 2^-8, half 2^-11, or 2^-32 of the largest where that is more),
+          // and an output by at most that part of sum p |v|: by less where the steps are of both
           // signs, by all of it where many weights are equal.  Their sum is of the unrounded ones.
           auto weights = [&](const uint32_t (&x)[32], int q, float off, bool half) {
             const float2 less = make_float2(kLift<T> - off, kLift<T> - off);
@@ -829,8 +829,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               for (int e = 0; e < 32; e += 8)
 #pragma unroll
                 for (int y = 0; y < 4; ++y)
-                  high[y] = max3(high[y], __uint_as_float(x[e + y]), __uint_as_float(x[e + 4 + y]));
-              now = max3(fmaxf(high[0], high[1]), high[2], high[3]);
+                  high[y] = fmax3(high[y], __uint_as_float(x[e + y]), __uint_as_float(x[e + 4 + y]));
+              now = fmax3(fmaxf(high[0], high[1]), high[2], high[3]);
             }
             const float off = raise(scaled(now));
 #pragma unroll 1
@@ -854,11 +854,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             for (int e = 0; e < kTile; e += 16)
 #pragma unroll
               for (int y = 0; y < 8; ++y)
-                high[y] = max3(high[y], __uint_as_float(x[e / 32][e % 32 + y]),
+                high[y] = fmax3(high[y], __uint_as_float(x[e / 32][e % 32 + y]),
                                __uint_as_float(x[e / 32][e % 32 + 8 + y]));
             const float off =
-                raise(scaled(max3(max3(high[0], high[1], high[2]), max3(high[3], high[4], high[5]),
-                                  fmaxf(high[6], high[7]))));
+                raise(scaled(fmax3(fmax3(high[0], high[1], high[2]),
+                                   fmax3(high[3], high[4], high[5]), fmaxf(high[6], high[7]))));
 #pragma unroll
             for (int q = 0; q < kParts; ++q) weights(x[q], q, off, q == kParts / 2 - 1);
           }
