@@ -7,9 +7,12 @@
 // to it.  A warp takes a token (append) or a few tokens (fork) of one layer's
 // keys or values, with its loads in flight together before the first store.
 //
-// Measured in a graph: accepted nodes of 64 trees of 11 into 32 layers 5.7 us (5.6 at a
-// copy's rate), of one tree 2.2; 8 samples of one prompt over 32 layers 9.7, 512 rows
-// over 4 layers 20.7 (4.4), 12 of them the plan's chain of loads and barriers.
+// Measured in a graph, over inputs that together pass L2 (in brackets at a copy's rate):
+// accepted nodes of 64 trees of 11 into 32 layers 9.0 us (5.6), of twice as many 15.5 (11.2),
+// of one tree 2.4: 6.4 for the bytes beside 2.6 for the launch and the loads of places.  8
+// samples of one prompt over 32 layers 12.2 (4.1), 64 beams over 8 layers 16.7 (1.7), 512
+// rows over 4 layers 25 (4.4): most of it the plan's chain of loads and barriers.  From L2
+// they take 5.5, 10.3, 13.4 and 20.6.
 
 #include <cuda_runtime.h>
 #include <limits.h>
@@ -597,9 +600,11 @@ ssd_status ssd_append_path(const ssd_append* a, int32_t* dev_status, void* strea
   if (a->rows == 0) return SSD_OK;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   // With more tokens and planes than the GPU has warps a warp takes two planes, and its
-  // loads of places serve both: 64 x 4 rows of 2 KB in 32 layers 5.7 us instead of 6.5, 256 x
-  // 4 of 1.25 KB in 12 layers 5.3 instead of 5.6 (4 loads in flight of each, which short
-  // rows leave idle, 6.2); 5 rows in 32 layers 2.9 instead of 2.3.  (From L2.)
+  // loads of places serve both.  From memory: 64 x 4 rows of 2 KB in 32 layers 9.1 us instead of
+  // 9.5, 256 x 4 of 1.25 KB in 12 layers 8.1 instead of 8.9 (4 loads in flight of each, which
+  // short rows leave idle, 8.3; in 6 layers 6.0 instead of 5.3), 256 x 4 of 128 bytes in 32
+  // layers 10.1 instead of 17.7; 32 x 4 rows of 2 KB in 32 layers 6.0 instead of 5.9, 5 of them
+  // 2.8 instead of 2.3.
   if ((int64_t)a->rows * p.g.planes <= (int64_t)64 * std::max(num_sms(), 1))
     return status_of(launch_append<1, 4>(p, s));
   return status_of(p.g.chunks >= 128 ? launch_append<2, 4>(p, s) : launch_append<2, 2>(p, s));
@@ -646,9 +651,9 @@ ssd_status ssd_fork_rows(const ssd_fork* f, void* workspace, size_t workspace_by
     p.groups = (f->page_size + p.group - 1) / p.group;
   }
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // Several CTAs share the tables' rows and the counts of shares when there are many: 64 rows
-  // of 77 pages 15.0 us with 8 instead of 17.0 with one, 512 of 143 23.9 instead of 74.7; one
-  // row of 97 10.9 instead of 10.1.
+  // Several CTAs share the tables' rows and the counts of shares when there are many.  From
+  // memory: 128 rows of 77 pages 18.2 us with 8 instead of 23.2 with one, 512 of 143 25 instead of
+  // 91; 64 of 77 16.7 instead of 16.4, 32 of 77 15.9 instead of 14.2, one of 97 13.1 instead of 12.1.
   p.ctas = (int64_t)f->S * f->cols + f->num_pages > 4096 ? kPlanCtas : 1;
   const int smem = plan_ints(f->S, f->B) * (int)sizeof(int);
   cudaError_t e = cudaSuccess;

@@ -13,22 +13,24 @@
 // stretches at most, one that goes on with an item and one that begins one, so
 // partials have places by the CTA.
 //
-// A tile's 64 KB (D = 128) take an SM 1.25 us at the memory's rate for reads, its products
+// A tile's 64 KB (D = 128) take an SM 1.4 us of the memory's time (7.1 TB/s below), its products
 // 2 x 512 cycles of the tensor cores for each block of pairs and its exponentials 512 of
 // the four units of an SM: with one block the memory is the bound, and padding a few pairs to 128
 // costs nothing; with two, which share the tile, both are near.  Copies, products and
 // exponentials of different tiles overlap (warps of their own, barriers between them), and
 // no barrier gets two phases ahead of a waiter.
 //
-// Measured, 32 heads on 8, D = 128: 256 sequences of 200 to 8000 tokens, one node each, 603 us
-// (7.1 TB/s; a copy has 6.8); two contexts of 131072 for 16 nodes 158 (6.8 TB/s); 64
-// sequences of 500 to 8191 in pages of 16 for trees of 11 176 (6.5 TB/s); 32 of them for 64
-// nodes 124 (1.18 PFLOP/s: the tensor cores are busy for 57% of the cycles; their operands come
-// from shared memory at its rate, and a block's next scores wait for its weights).  One
-// stream of 700 tokens and 5 nodes 11.1: 5.5 until a tile's weights are there, 7.6 until
-// the last partials are, and the join from 8.6 on.  256 sequences of 10 to 200 tokens 65, where memory would take 17: an
-// item of one or two tiles is a chain of 3.4 us (scores, weights, sums, output) in the threads
-// of the exponentials.
+// Measured in a graph, 32 heads on 8, D = 128: 256 sequences of 200 to 8000 tokens, one node
+// each, 593 to 603 us (7.1 TB/s; a copy has 6.8); two contexts of 131072 for 16 nodes 157
+// (6.8 TB/s); 64 sequences of 500 to 8191 in pages of 16 for trees of 11 177 (6.5 TB/s); 32 of
+// them for 64 nodes 126 (1.16 PFLOP/s: the tensor cores are busy for 57% of the cycles; their
+// operands come from shared memory at its rate, and a block's next scores wait for its weights).
+// One stream of 700 tokens and 5 nodes 11.7, from L2 11.1: 5.5 until a tile's weights are there,
+// 7.6 until the last partials are, and the join from 8.6 on.  256 sequences of 10 to 200 tokens
+// 65, where memory would take 17: an item of one or two tiles is a chain of 3.4 us (scores,
+// weights, sums, output) in the threads of the exponentials.  Float16 takes as long.
+// A figure "instead of" another, here and below, is of the step that made the choice: with it and
+// without it then, when other steps were still to come.
 #pragma once
 
 #include <cuda_bf16.h>
