@@ -599,6 +599,8 @@ ssd_status ssd_page_plan(const int32_t* lens, const int32_t* new_tokens, const i
  *             same descriptor.
  * Scores, their maxima and sums and the outputs' sums are held in float32;
  * the weights exp(s_j - max) are rounded to dtype for the matrix product.
+ * SSD_F16 has no weights below 2^-24: tokens far below the largest score of
+ * their stretch (2^-25 of its weight) count in lse, but not in out.
  * ------------------------------------------------------------------------- */
 typedef struct {
   const void* ptr;
